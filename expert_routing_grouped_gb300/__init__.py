@@ -18,6 +18,8 @@ MOE_OPT_WAIT_LIMIT_US = 6
 REGIME_AUTO, REGIME_GEMV, REGIME_TC, REGIME_TC_EXACT = 0, 1, 2, 3
 ROUTER_SOFTMAX, ROUTER_SIGMOID, ROUTER_SOFTMAX_RAW = 0, 1, 2
 X_F32, X_BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU = 0, 1, 2, 3
 
 MOE_DBG_IDX, MOE_DBG_W, MOE_DBG_COUNTS, MOE_DBG_OFFSETS, MOE_DBG_PERM, MOE_DBG_INV = range(6)
 
@@ -26,7 +28,8 @@ EXPORTS = ("moe_init", "moe_route", "moe_forward", "moe_forward_residual",
            "moe_rmsnorm_bf16", "moe_set_option", "moe_debug_view", "moe_debug_read",
            "moe_stage_times", "moe_status", "moe_device_bytes", "moe_free", "moe_strerror",
            "moe_route_noalloc", "moe_usage_read", "moe_usage_reset", "moe_engine_id",
-           "moe_route_trace_write", "moe_route_trace_read", "moe_set_next_layer")
+           "moe_route_trace_write", "moe_route_trace_read", "moe_set_next_layer",
+           "moe_add_rmsnorm", "moe_linear", "moe_balance_loss", "moe_balance_workspace")
 
 
 class MoeLayout(ctypes.Structure):
@@ -59,6 +62,7 @@ def _load():
                           "the MoE layer has no other implementation")
     lib = ctypes.CDLL(LIB_PATH)
     P, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    q, z = ctypes.c_int64, ctypes.c_size_t
     sig = {
         "moe_init": (i, [P, P, P]),
         "moe_forward": (i, [P, P, i, P, P]),
@@ -80,6 +84,11 @@ def _load():
         "moe_usage_reset": (i, [P]),
         "moe_set_next_layer": (i, [P, P]),
         "moe_engine_id": (ctypes.c_uint32, [ctypes.c_char_p]),
+        "moe_add_rmsnorm": (i, [P, P, P, P, i, i, f, i, i, i, i, P, P, q, q, q, q, P]),
+        "moe_linear": (i, [P, P, P, P, P, P, P, i, i, i, i, i, i, q, q, q, q, P, P]),
+        "moe_balance_loss": (i, [P, P, P, P, P, i, i, i, i, i, i, f, P, q, P, P, P, P, P, q, P, z,
+                                 P]),
+        "moe_balance_workspace": (z, [i, i, i]),
         "moe_route_trace_write": (i, [ctypes.c_char_p, i, i, ctypes.c_uint32, P]),
         "moe_route_trace_read": (i, [ctypes.c_char_p, i, i, ctypes.c_uint32, P, P]),
     }
@@ -224,6 +233,47 @@ class MoELayer:
 def rmsnorm_bf16(x, T, H, eps, out, stream=None):
     return _check(lib.moe_rmsnorm_bf16(_ptr(x), T, H, eps, _ptr(out), _stream(stream)),
                   "moe_rmsnorm_bf16")
+
+
+def add_rmsnorm(x, T, H, eps, out, resid=None, resid_out=None, gain=None, scale=None, group=0,
+                x_dtype=BF16, resid_dtype=F32, out_dtype=BF16, x_stride=0, resid_stride=0,
+                resid_out_stride=0, out_stride=0, stream=None):
+    """moe_add_rmsnorm: resid_out = resid + x, out = rmsnorm(resid_out) * gain in
+    bf16, or in e4m3 with a scale per row or per group of values."""
+    return _check(lib.moe_add_rmsnorm(_ptr(x), _ptr(resid), _ptr(resid_out), _ptr(gain), T, H, eps,
+                                      x_dtype, resid_dtype, out_dtype, group, _ptr(out),
+                                      _ptr(scale), x_stride, resid_stride, resid_out_stride,
+                                      out_stride, _stream(stream)), "moe_add_rmsnorm")
+
+
+def linear(x, w, T, N, K, out, dtype=BF16, out_dtype=F32, act=ACT_NONE, x_scale=None,
+           w_scale=None, bias=None, resid=None, x_stride=0, w_stride=0, resid_stride=0,
+           out_stride=0, status=None, stream=None):
+    """moe_linear: out = act(x . w^T (scaled) + bias) + resid; ACT_SWIGLU takes
+    2N rows of w."""
+    return _check(lib.moe_linear(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias),
+                                 _ptr(resid), _ptr(out), T, N, K, dtype, out_dtype, act, x_stride,
+                                 w_stride, resid_stride, out_stride, _ptr(status),
+                                 _stream(stream)), "moe_linear")
+
+
+def balance_workspace(T, num_experts, n_seq=1):
+    """Bytes of scratch that balance_loss needs."""
+    return lib.moe_balance_workspace(T, num_experts, n_seq)
+
+
+def balance_loss(z, idx, T, num_experts, top_k, loss, counts, tokens, prob, workspace, bias=None,
+                 mask=None, seq_off=None, n_seq=1, z_dtype=F32, router_mode=ROUTER_SOFTMAX,
+                 alpha=1.0, dz=None, grad=None, z_stride=0, dz_stride=0, stream=None):
+    """moe_balance_loss: the router's balance loss, per-expert counts and (with
+    dz) the gradient of the logits, per segment.  workspace is a tensor or
+    array of at least balance_workspace(...) bytes."""
+    return _check(lib.moe_balance_loss(_ptr(z), _ptr(bias), _ptr(idx), _ptr(mask), _ptr(seq_off),
+                                       T, num_experts, top_k, n_seq, z_dtype, router_mode, alpha,
+                                       _ptr(grad), z_stride, _ptr(loss), _ptr(counts),
+                                       _ptr(tokens), _ptr(prob), _ptr(dz), dz_stride,
+                                       _ptr(workspace), workspace.nbytes, _stream(stream)),
+                  "moe_balance_loss")
 
 
 def layout_for(wl, max_tokens):

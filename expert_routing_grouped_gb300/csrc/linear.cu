@@ -1,0 +1,182 @@
+// linear.cu -- the matrix product with bias, activation and residual in its
+// epilogue (moe_linear in include/moe.h).
+//
+//   y[t][n] = act(sx[t] sw[n] sum_k x[t][k] w[n][k] + bias[n]) + resid[t][n]
+//
+// x and w both bf16, or both e4m3 with one f32 scale per row; f32 accumulation.
+// SwiGLU takes 2N rows of w: y = silu(row n) * (row N + n).
+#include <algorithm>
+
+#include "linear.cuh"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------ few tokens --
+// Warp-level MMAs with the weights as the B operand (8 rows) and the tokens as
+// A (16 rows).  K order inside an MMA is free as long as both operands agree,
+// so each lane takes 16 consecutive bytes of its row -- lane 4 g + q piece q of
+// every 64 bytes of row g -- straight from memory into two MMAs' fragments.
+// A block owns 8 outputs and splits K over its warps, 128 bytes of each row at
+// a time; partial sums meet in shared memory in warp order.
+constexpr int kFewWarps = 4;
+constexpr int kFewTokens = 16;
+
+template <int DT>
+__device__ __forceinline__ void mma_m16n8(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (DT == MOE_BF16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+__device__ __forceinline__ uint4 load_piece(const uint8_t *row, int off, int bytes) {
+  if (off >= bytes) return make_uint4(0u, 0u, 0u, 0u);
+  return *reinterpret_cast<const uint4 *>(row + off);
+}
+
+// NB: row blocks of 8 per warp -- 1, or 2 (SwiGLU: the gate rows, then the up rows).
+template <int DT, int NB>
+__global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const LinearParams p) {
+  __shared__ float red[kFewWarps][kFewTokens][8 * NB];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int n0 = blockIdx.x * 8, t0 = blockIdx.y * kFewTokens;
+  constexpr int es = DT == MOE_BF16 ? 2 : 1;
+  const int kb = p.K * es;                       // bytes of a row, a multiple of 16
+  const bool row_ok = n0 + g < p.N, t_lo = t0 + g < p.T, t_hi = t0 + g + 8 < p.T;
+  const uint8_t *wr[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+    wr[b] = reinterpret_cast<const uint8_t *>(p.w) + ((size_t)(n0 + g) + (size_t)b * p.N) * p.ldw * es;
+  const uint8_t *xl = reinterpret_cast<const uint8_t *>(p.x) + (size_t)(t0 + g) * p.ldx * es;
+  const uint8_t *xh = xl + (size_t)8 * p.ldx * es;
+  float c[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[b][i] = 0.f;
+  constexpr int U = 4;                           // 64-byte units in flight
+  for (int u = warp * U; u * 64 < kb; u += kFewWarps * U) {
+    uint4 wv[NB][U], lo[U], hi[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int off = (u + i) * 64 + q * 16;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) wv[b][i] = load_piece(wr[b], off, row_ok ? kb : 0);
+      lo[i] = load_piece(xl, off, t_lo ? kb : 0);
+      hi[i] = load_piece(xh, off, t_hi ? kb : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        mma_m16n8<DT>(c[b], lo[i].x, hi[i].x, lo[i].y, hi[i].y, wv[b][i].x, wv[b][i].y);
+        mma_m16n8<DT>(c[b], lo[i].z, hi[i].z, lo[i].w, hi[i].w, wv[b][i].z, wv[b][i].w);
+      }
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    red[warp][g][b * 8 + 2 * q] = c[b][0];
+    red[warp][g][b * 8 + 2 * q + 1] = c[b][1];
+    red[warp][g + 8][b * 8 + 2 * q] = c[b][2];
+    red[warp][g + 8][b * 8 + 2 * q + 1] = c[b][3];
+  }
+  __syncthreads();
+  const int r = threadIdx.x >> 3, col = threadIdx.x & 7;   // 16 tokens x 8 outputs
+  const int t = t0 + r, n = n0 + col;
+  if (t >= p.T || n >= p.N) return;
+  float acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    acc[b] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) acc[b] += red[w][r][b * 8 + col];
+  }
+  const float sx = p.x_scale ? p.x_scale[t] : 1.f;
+  const float res = load_resid(p, t, n);
+  float y;
+  if constexpr (NB == 2)
+    y = swiglu(finish_acc(p, acc[0], sx, n), finish_acc(p, acc[1], sx, p.N + n));
+  else
+    y = activate(p.act, finish_acc(p, acc[0], sx, n));
+  store_out(p, t, n, y + res);
+}
+
+template <int DT>
+cudaError_t launch_few(const LinearParams &p, cudaStream_t st) {
+  const dim3 grid((p.N + 7) / 8, (p.T + kFewTokens - 1) / kFewTokens);
+  return launch_k(false, p.act == MOE_ACT_SWIGLU ? linear_few_kernel<DT, 2> : linear_few_kernel<DT, 1>,
+                  grid, dim3(kFewWarps * 32), 0, st, p);
+}
+
+size_t span(int rows, int cols, long long ld, size_t elem) {
+  return ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * elem;
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" __attribute__((visibility("default"))) int moe_linear(
+    const void *x, const float *x_scale, const void *w, const float *w_scale, const float *bias,
+    const void *resid, void *out, int T, int N, int K, int dtype, int out_dtype, int act,
+    int64_t x_stride, int64_t w_stride, int64_t resid_stride, int64_t out_stride, int32_t *status,
+    moe_stream_t stream) {
+  using namespace moe;
+  constexpr int kMaxDim = 1 << 19;
+  if ((dtype != MOE_BF16 && dtype != MOE_E4M3) || (out_dtype != MOE_F32 && out_dtype != MOE_BF16) ||
+      act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU)
+    return MOE_ERR_ARG;
+  const size_t es = dtype == MOE_BF16 ? 2 : 1, os = out_dtype == MOE_F32 ? 4 : 2;
+  if (T < 0 || T > kMaxDim || N < 1 || N > kMaxDim || K < 1 || K > kMaxDim || (size_t)K * es % 16)
+    return MOE_ERR_ARG;
+  if (act == MOE_ACT_SWIGLU && N % 16) return MOE_ERR_ARG;
+  const int rows = act == MOE_ACT_SWIGLU ? 2 * N : N;
+  const long long ldx = x_stride ? x_stride : K, ldw = w_stride ? w_stride : K,
+                  ldr = resid_stride ? resid_stride : N, ldo = out_stride ? out_stride : N;
+  constexpr long long kMaxStride = 1LL << 31;
+  if (ldx < K || ldw < K || ldr < N || ldo < N || ldx > kMaxStride || ldw > kMaxStride ||
+      ldr > kMaxStride || ldo > kMaxStride)
+    return MOE_ERR_ARG;
+  // Rows of x and w are read 16 bytes at a time.
+  if (((size_t)ldx * es | (size_t)ldw * es) & 15) return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !out) return MOE_ERR_ARG;
+  if ((dtype == MOE_E4M3) != (x_scale != nullptr) || (dtype == MOE_E4M3) != (w_scale != nullptr))
+    return MOE_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) return MOE_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(x_scale) | reinterpret_cast<uintptr_t>(w_scale) |
+       reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(status)) & 3)
+    return MOE_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(resid)) & (os - 1))
+    return MOE_ERR_ARG;
+  // Blocks run in any order: out is apart from everything they read, but for
+  // resid, which may be out itself (each element is read by the thread that
+  // writes it).
+  const size_t no = span(T, N, ldo, os);
+  if (overlap(out, no, x, span(T, K, ldx, es)) || overlap(out, no, w, span(rows, K, ldw, es)) ||
+      (x_scale && overlap(out, no, x_scale, (size_t)T * 4)) ||
+      (w_scale && overlap(out, no, w_scale, (size_t)rows * 4)) ||
+      (bias && overlap(out, no, bias, (size_t)rows * 4)) ||
+      (status && overlap(out, no, status, 4)))
+    return MOE_ERR_ARG;
+  if (resid && !(resid == out && ldr == ldo) && overlap(out, no, resid, span(T, N, ldr, os)))
+    return MOE_ERR_ARG;
+  LinearParams p{x, w, x_scale, w_scale, bias, resid, out, T, N, K, act, out_dtype,
+                 ldx, ldw, ldr, ldo, status};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t err = dtype == MOE_BF16 ? launch_few<MOE_BF16>(p, st) : launch_few<MOE_E4M3>(p, st);
+  return err == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}

@@ -310,6 +310,136 @@ int moe_route_noalloc(const void *x, int T, int hidden, int num_experts, int top
                       int router_mode, float routed_scaling_factor, const float *router_w_eh,
                       const float *router_bias, int32_t *idx, float *w, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Dense operators around the MoE layer.  They need no handle: every call
+ * works on the caller's device memory and stream, allocates nothing, never
+ * synchronises, and can be captured into a graph.  Calls share no scratch, so
+ * any number may overlap on different streams.  The current device must be
+ * the one that owns the pointers.  Strides are in elements, 0 for contiguous
+ * rows.  Results are bitwise identical from run to run.
+ */
+
+/* Element types of these operators (x_dtype of moe_layout uses the first two). */
+#define MOE_F32 0
+#define MOE_BF16 1
+#define MOE_E4M3 2 /* 8 bits: 4 of exponent, 3 of mantissa, largest 448, no infinity */
+
+/*
+ * The RMS norm with the residual's addition, the pre-norm of moe_rmsnorm_bf16
+ * (tutorial cf-1.com §2.1 step 1) for any stream:
+ *
+ *   r[t]   = resid[t] + x[t] in f32, rounded to resid's type (r = x when resid is NULL)
+ *   resid_out[t] = r[t]
+ *   n[t]   = r[t] / sqrt(mean(r[t]^2) + eps) * gain          (in f32)
+ *   out[t] = bf16(n[t]), or in 8 bits with one f32 scale per group of values:
+ *            scale[t][g] = max(max |n| of the group / 448, 2^-126),
+ *            out[t][i] = e4m3(n[t][i] / scale[t][g])
+ *
+ *   x          [T][H] MOE_F32 or MOE_BF16 (x_dtype), row stride x_stride
+ *   resid      [T][H] MOE_F32 or MOE_BF16 (resid_dtype), or NULL
+ *   resid_out  [T][H] of resid's type; may be resid itself (the same rows and
+ *              stride); NULL exactly when resid is
+ *   gain       [H] f32, or NULL (1)
+ *   out        [T][H] MOE_BF16 or MOE_E4M3 (out_dtype)
+ *   group      values per scale: 0 (one scale a row), 32, 64 or 128, a divisor
+ *              of H; 0 with bf16 output
+ *   scale      [T][H / group] f32, contiguous ([T] with group 0); unused
+ *              (may be NULL) with bf16 output
+ * H a multiple of 8 (16 for e4m3), at most 32768; x, resid, resid_out, gain
+ * and out 16-byte aligned with row strides of a multiple of 16 bytes.  out and
+ * scale must not overlap anything else, resid_out nothing but resid.  A NaN or
+ * an infinity makes its whole row of out NaN or 0 as the formula does (e4m3: a
+ * group with a NaN has a NaN scale).  T == 0 checks what it can and launches
+ * nothing.  Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
+ */
+int moe_add_rmsnorm(const void *x, const void *resid, void *resid_out, const float *gain, int T,
+                    int H, float eps, int x_dtype, int resid_dtype, int out_dtype, int group,
+                    void *out, float *scale, int64_t x_stride, int64_t resid_stride,
+                    int64_t resid_out_stride, int64_t out_stride, moe_stream_t stream);
+
+/* Activations of moe_linear. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU 1   /* v / (1 + exp(-v)) */
+#define MOE_ACT_GELU 2   /* v / 2 (1 + erf(v / sqrt 2)) */
+#define MOE_ACT_SWIGLU 3 /* silu(row n) * (row N + n): w has 2N rows */
+
+/*
+ * Matrix product with bias, activation and residual in its epilogue -- the
+ * dense products next to the experts' (a dense FFN, a projection, an
+ * unquantised shared expert, the logits of a router):
+ *
+ *   a[t][n]   = x_scale[t] w_scale[n] sum_k x[t][k] w[n][k] + bias[n]
+ *   out[t][n] = act(a[t][n]) + resid[t][n]
+ *   SwiGLU:     silu(a[t][n]) * a[t][N + n] + resid[t][n]
+ *
+ *   x        [T][K], w [N][K] ([2N][K] for SwiGLU: the gate rows, then the up
+ *            rows): both MOE_BF16 or both MOE_E4M3 (dtype)
+ *   x_scale  [T], w_scale [rows of w] f32: required for e4m3 (the scales of
+ *            moe_add_rmsnorm with group 0 are an x_scale), NULL for bf16
+ *   bias     [rows of w] f32, or NULL
+ *   resid    [T][N] of out's type, or NULL; may be out itself (the same stride)
+ *   out      [T][N] MOE_F32 or MOE_BF16 (out_dtype)
+ *   status   int32 on the device, or NULL: set to 2 when a bounded wait of the
+ *            kernel gave up (out is then not complete); otherwise left alone
+ * Sums are f32; out is rounded once.  T, N and K are at most 2^19; K and the
+ * strides of x and w are multiples of 16 bytes, x and w 16-byte aligned; N is
+ * any number (a multiple of 16 for SwiGLU).  out must not overlap anything
+ * else.  T == 0 checks what it can and launches nothing.
+ * Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
+ */
+int moe_linear(const void *x, const float *x_scale, const void *w, const float *w_scale,
+               const float *bias, const void *resid, void *out, int T, int N, int K, int dtype,
+               int out_dtype, int act, int64_t x_stride, int64_t w_stride, int64_t resid_stride,
+               int64_t out_stride, int32_t *status, moe_stream_t stream);
+
+/*
+ * The router's balance loss, per-expert counts and the gradient of its logits.
+ * With p[t] the router's probabilities over all experts -- softmax(z[t] + bias)
+ * for router_mode 0 and 2, sigmoid(z[t]) / sum sigmoid(z[t]) for mode 1, where
+ * the bias enters selection only -- and, per segment s (a sequence), over its
+ * T_s kept tokens:
+ *
+ *   counts[s][e] = assignments of expert e
+ *   prob[s][e]   = 1/T_s sum_t p[t][e]
+ *   loss[s]      = alpha sum_e f_e prob[s][e],  f_e = E / (k T_s) counts[s][e]
+ *   dz[t][i]     = grad[s] d loss[s] / d z[t][i]   (counts are constants)
+ *
+ * A balanced segment has loss alpha.  A segment without kept tokens has loss,
+ * counts and prob 0.
+ *
+ *   z        [T][E] MOE_F32 or MOE_BF16 logits, row stride z_stride
+ *   bias     [E] f32 or NULL; not read in mode 1
+ *   idx      [T][k] int32, as moe_debug.idx or moe_route_noalloc give it; an
+ *            id outside [0, E) (a slot that the top-p trim dropped) is no
+ *            assignment
+ *   mask     [T] bytes or NULL: a token whose byte is 0 is padding: not
+ *            counted, its z not used, its dz 0
+ *   seq_off  [n_seq + 1] int32, non-decreasing: segment s is the tokens
+ *            seq_off[s] .. seq_off[s+1] - 1; NULL (n_seq 1): all T.  Tokens in
+ *            no segment are not read and their dz is left as it was
+ *   grad     [n_seq] f32 or NULL (1): the gradient of each segment's loss
+ *   loss     [n_seq], prob [n_seq][E] f32; counts [n_seq][E], tokens [n_seq]
+ *            (T_s) int32
+ *   dz       [T][E] of z's type, row stride dz_stride, or NULL (no gradient);
+ *            may be z itself (the same stride)
+ *   workspace  at least moe_balance_workspace(T, num_experts, n_seq) bytes,
+ *            not shared with a call that may overlap this one
+ * A row whose logits are all -infinity has p = 0.  num_experts <= 1024, top_k
+ * <= 32, T * top_k <= 2^26, n_seq <= 65535.  Loss and gradient together read z
+ * once.  Outputs and workspace must not overlap anything else.  T == 0 checks
+ * what it can, launches nothing and writes nothing.  Returns MOE_OK,
+ * MOE_ERR_NOMEM (workspace too small), MOE_ERR_ROUTING, MOE_ERR_ARG or
+ * MOE_ERR_DEVICE.
+ */
+int moe_balance_loss(const void *z, const float *bias, const int32_t *idx, const uint8_t *mask,
+                     const int32_t *seq_off, int T, int num_experts, int top_k, int n_seq,
+                     int z_dtype, int router_mode, float alpha, const float *grad,
+                     int64_t z_stride, float *loss, int32_t *counts, int32_t *tokens, float *prob,
+                     void *dz, int64_t dz_stride, void *workspace, size_t workspace_bytes,
+                     moe_stream_t stream);
+/* Bytes of scratch that moe_balance_loss needs (0 for sizes it refuses or T < 1). */
+size_t moe_balance_workspace(int T, int num_experts, int n_seq);
+
 /* Fields of moe_debug_read. */
 #define MOE_DBG_IDX 0      /* int32 [T][k]  */
 #define MOE_DBG_W 1        /* f32   [T][k]  */
