@@ -11,13 +11,22 @@
 // The counts come from the selection alone, so they are taken first, and then
 // ONE pass over the logits gives both the sums of p and the gradient: z is
 // read once and dz written once, which is what the operator cannot do without.
-// Counts are integers (their atomics commute); every floating sum runs in a
-// fixed order: rows of a chunk by warp, warps of a block, chunks of a segment.
+// Counts are integers; every floating sum runs in a fixed order: rows of a
+// chunk by warp, warps of a block, chunks of a segment.
 //
-// A chunk is a run of consecutive tokens, one block's work.  Chunk c and
-// segment s meet in at most one run of tokens, and along the tokens both only
-// grow, so c + s names each meeting once: the block writes its partial sums of
-// a segment to slot c + s, and no slot has two writers.
+// Three kernels, chained by programmatic dependent launch:
+//   count   a cluster per segment: histograms in shared memory, added across
+//           the cluster (no zeroing, no global atomics);
+//   pass    a block per chunk of consecutive tokens; its first rows of z are
+//           on their way before it waits for the counts, and without a
+//           gradient it waits only at its end;
+//   finish  a cluster per segment: P and the loss from the chunks' sums.
+// Chunk c and segment s meet in at most one run of tokens, and along the
+// tokens both only grow, so c + s names each meeting once: a block writes its
+// partial sums of a segment to slot c + s, and no slot has two writers.
+//
+// Up to kSmallElems logits one kernel does all three steps, a cluster per
+// segment with cluster barriers between them: there the launches are the time.
 #include <algorithm>
 
 #include "moe_internal.cuh"
@@ -27,7 +36,10 @@ namespace {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBalChunks = 3 * 1024;   // most chunks of a call
+constexpr int kBalBlocks = 608;          // most chunks of a call: 4 blocks on each of 152 SMs
+constexpr int kCountThreads = 512;
+constexpr int kCluster = 8;
+constexpr long long kSmallElems = 1 << 18;
 
 struct BalParams {
   const void *z;
@@ -44,8 +56,35 @@ struct BalParams {
   float *part;                // [chunks + S][E] partial sums of p
   long long ldz, lddz;
   int T, E, k, S, chunk;      // chunk: tokens per block
+  int idx_vec;                // idx rows are whole 16-byte pieces
   float alpha;
 };
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Called by all threads of all CTAs of the cluster, converged.
+__device__ __forceinline__ void cluster_sync() {
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// The 32-bit word at p (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t ld_peer(const void *p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 
 // First and past-the-last token of segment s, inside [0, T] whatever seq_off holds.
 __device__ __forceinline__ int seg_begin(const BalParams &p, int s) {
@@ -55,219 +94,523 @@ __device__ __forceinline__ int seg_end(const BalParams &p, int s) {
   return p.seq_off ? min(max(p.seq_off[s + 1], 0), p.T) : p.T;
 }
 
-// The first segment that ends past token t (S if there is none): by halving,
-// seq_off being non-decreasing.
+// The first segment that ends past token t (S if there is none), for a whole
+// warp: seq_off is non-decreasing, so each step tests 32 segments at once.
 __device__ __forceinline__ int seg_of(const BalParams &p, int t) {
-  int lo = 0, hi = p.S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seg_end(p, mid) > t) hi = mid;
-    else lo = mid + 1;
+  if (!p.seq_off) return 0;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.S;                       // the answer is in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int s = lo + min((lane + 1) * step, n) - 1;   // last of this lane's piece
+    const int ended = __popc(__ballot_sync(0xffffffffu, seg_end(p, s) <= t));
+    if (ended == 32) return lo + n;
+    const int hi = lo + n;
+    lo += ended * step;
+    n = min(step, hi - lo) - 1;              // that piece's last one ends past t
   }
   return lo;
 }
 
 // ---------------------------------------------------------------- counts --
-// Block = chunk of tokens: a histogram in shared memory per segment that the
-// chunk meets, added to the segment's counts.
-__global__ void __launch_bounds__(kBalThreads) balance_count_kernel(const BalParams p, int chunk) {
-  extern __shared__ int32_t hist[];   // [E + 1]: counts, then the kept tokens
-  const int t0 = blockIdx.x * chunk, t1 = min(p.T, t0 + chunk);
-  for (int s = seg_of(p, t0); s < p.S; ++s) {
-    const int a = max(t0, seg_begin(p, s)), b = min(t1, seg_end(p, s));
-    if (seg_begin(p, s) >= t1) break;
-    if (a >= b) continue;
-    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
-    __syncthreads();
-    const int32_t *idx = p.idx + (size_t)a * p.k;
-    const int n = (b - a) * p.k;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int row = i / p.k;
-      if (p.mask && !p.mask[a + row]) continue;
-      const int e = idx[i];
-      if (e >= 0 && e < p.E) atomicAdd(&hist[e], 1);
-      if (i == row * p.k) atomicAdd(&hist[p.E], 1);
+
+// Adds the assignments of tokens [a, b) that the mask keeps, this thread's
+// share of them (thread i of n takes rows a + i, a + i + n, ..), to hist[E]
+// and the kept tokens to hist[E].
+__device__ __forceinline__ void count_rows(const BalParams &p, int a, int b, int i, int n, int32_t *hist) {
+  int kept = 0;
+  for (int t = a + i; t < b; t += n) {
+    if (p.mask && !p.mask[t]) continue;
+    ++kept;
+    const int32_t *row = p.idx + (size_t)t * p.k;
+    if (p.idx_vec) {
+      for (int j = 0; j < p.k; j += 4) {
+        const int4 v = __ldg(reinterpret_cast<const int4 *>(row + j));
+        if ((uint32_t)v.x < (uint32_t)p.E) atomicAdd(&hist[v.x], 1);
+        if ((uint32_t)v.y < (uint32_t)p.E) atomicAdd(&hist[v.y], 1);
+        if ((uint32_t)v.z < (uint32_t)p.E) atomicAdd(&hist[v.z], 1);
+        if ((uint32_t)v.w < (uint32_t)p.E) atomicAdd(&hist[v.w], 1);
+      }
+    } else {
+      for (int j = 0; j < p.k; ++j) {
+        const int e = __ldg(row + j);
+        if ((uint32_t)e < (uint32_t)p.E) atomicAdd(&hist[e], 1);
+      }
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x)
-      if (hist[e]) atomicAdd(&p.counts[(size_t)s * p.E + e], hist[e]);
-    if (threadIdx.x == 0 && hist[p.E]) atomicAdd(&p.tokens[s], hist[p.E]);
-    __syncthreads();
+  }
+  kept = __reduce_add_sync(0xffffffffu, kept);
+  if ((threadIdx.x & 31) == 0 && kept) atomicAdd(&hist[p.E], kept);
+}
+
+// One cluster per segment.
+__global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const BalParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int32_t hist[kMaxExperts + 1];
+  const int ranks = cluster_size(), rank = cluster_rank(), s = blockIdx.x / ranks;
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  count_rows(p, seg_begin(p, s), seg_end(p, s), rank * blockDim.x + threadIdx.x, ranks * blockDim.x,
+             hist);
+  cluster_sync();
+  for (int e = rank + ranks * threadIdx.x; e <= p.E; e += ranks * blockDim.x) {
+    int c = 0;
+    for (int r = 0; r < ranks; ++r) c += (int)ld_peer(&hist[e], r);
+    if (e < p.E) p.counts[(size_t)s * p.E + e] = c;
+    else p.tokens[s] = c;
+  }
+  cluster_sync();   // no CTA leaves while a peer reads its histogram
+}
+
+// -------------------------------------------------------------- one token --
+
+// A token's logits over LPR lanes (a power of two) of a warp, 32 / LPR tokens
+// at a time: VPL vectors of VEC neighbouring experts per lane.
+template <int DT_, int VEC_, int VPL_, int LPR_, bool kSig_>
+struct Lay {
+  static constexpr int DT = DT_, VEC = VEC_, VPL = VPL_, LPR = LPR_, NE = VEC * VPL;
+  static constexpr bool kSig = kSig_;
+  // First expert of vector i in this lane.
+  static __device__ __forceinline__ int first(int i) {
+    return (i * LPR + (int)(threadIdx.x & (LPR - 1))) * VEC;
+  }
+  static __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  static __device__ __forceinline__ float max(float v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+  // Raw registers of one lane's logits.
+  struct Raw {
+    uint32_t w[DT == MOE_F32 ? NE : (VEC == 1 ? NE : NE / 2)];
+  };
+  static __device__ __forceinline__ void load(const BalParams &p, int t, bool valid, Raw &r) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = first(i);
+      const bool in = valid && e < p.E;
+      const size_t at = (size_t)t * p.ldz + e;
+      if constexpr (VEC == 1) {
+        r.w[i] = 0u;
+        if (in) {
+          if constexpr (DT == MOE_F32) r.w[i] = __float_as_uint(__ldcs(reinterpret_cast<const float *>(p.z) + at));
+          else r.w[i] = __ldcs(reinterpret_cast<const unsigned short *>(p.z) + at);
+        }
+      } else {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (in)
+          u = __ldcs(reinterpret_cast<const uint4 *>(
+              reinterpret_cast<const char *>(p.z) + at * (DT == MOE_F32 ? 4 : 2)));
+        r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
+      }
+    }
+  }
+  static __device__ __forceinline__ float get(const Raw &r, int j) {   // logit j of the lane
+    if constexpr (DT == MOE_F32) return __uint_as_float(r.w[j]);
+    if constexpr (VEC == 1) return __uint_as_float(r.w[j] << 16);
+    const uint32_t w = r.w[j / 2];
+    return __uint_as_float((j & 1) ? (w & 0xFFFF0000u) : (w << 16));
+  }
+  static __device__ __forceinline__ void store(const BalParams &p, int t, const float (&d)[NE]) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = first(i);
+      if (e >= p.E) continue;
+      const size_t at = (size_t)t * p.lddz + e;
+      if constexpr (VEC == 1) {
+        if constexpr (DT == MOE_F32) __stcs(reinterpret_cast<float *>(p.dz) + at, d[i]);
+        else reinterpret_cast<__nv_bfloat16 *>(p.dz)[at] = __float2bfloat16_rn(d[i]);
+      } else if constexpr (DT == MOE_F32) {
+        __stcs(reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.dz) + at),
+               make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]));
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(d[8 * i + 2 * c], d[8 * i + 2 * c + 1]);
+          w[c] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        __stcs(reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.dz) + at),
+               make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+  }
+};
+
+// p of the lane's token added to acc, and the token's gradient written when
+// `coef` (the counts less their mean, in shared memory) is given.  valid: the
+// token exists and the mask keeps it; write: it exists (a masked token's
+// gradient is 0).  Every lane of the warp takes part.
+//
+// The mean taken off the counts cancels in a_i - sum_e p_e a_e, and small
+// differences keep their digits.
+template <class L>
+__device__ __forceinline__ void one_token(const BalParams &p, const typename L::Raw &raw, int t,
+                                          bool valid, bool write, const float *bias,
+                                          const float *coef, float scale, float (&acc)[L::NE]) {
+  float v[L::NE], om[L::NE];
+  float tot = 0.f;
+  if constexpr (L::kSig) {
+#pragma unroll
+    for (int j = 0; j < L::NE; ++j) {
+      // 1 - sigmoid is taken as exp(-z) sigmoid, which keeps its digits where
+      // the sigmoid is near 1.  The quotient is the fast one (2 units): p is
+      // a sum's share, so f32 rounding is what counts.
+      const float ex = expf(-L::get(raw, j));
+      const float sg = __fdividef(1.0f, 1.0f + ex);
+      const bool in = L::first(j / L::VEC) + j % L::VEC < p.E;
+      v[j] = in && !(ex > 8e37f) ? sg : 0.f;   // below 2^-126: 0
+      om[j] = ex > 8e37f ? 1.0f : ex * sg;
+      tot += v[j];
+    }
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < L::NE; ++j) {
+      const int e = L::first(j / L::VEC) + j % L::VEC;
+      const bool in = e < p.E;
+      v[j] = in ? L::get(raw, j) : -INFINITY;
+      if (bias && in) v[j] += bias[e];
+      m = fmaxf(m, v[j]);
+    }
+    m = L::max(m);
+    if (m == -INFINITY) m = 0.f;   // a row with nothing left: p = 0
+#pragma unroll
+    for (int j = 0; j < L::NE; ++j) {
+      v[j] = expf(v[j] - m);
+      tot += v[j];
+    }
+  }
+  tot = L::sum(tot);
+  const float inv = valid ? (tot == 0.f ? 0.f : 1.0f / tot) : 0.f;
+  float dot = 0.f;
+#pragma unroll
+  for (int j = 0; j < L::NE; ++j) {
+    v[j] *= inv;
+    acc[j] += valid ? v[j] : 0.f;
+  }
+  if (!coef) return;
+#pragma unroll
+  for (int j = 0; j < L::NE; ++j)
+    dot = fmaf(v[j], coef[L::first(j / L::VEC) + j % L::VEC], dot);
+  dot = L::sum(dot);
+#pragma unroll
+  for (int j = 0; j < L::NE; ++j) {
+    float d = scale * v[j] * (coef[L::first(j / L::VEC) + j % L::VEC] - dot);
+    if constexpr (L::kSig) d *= om[j];
+    v[j] = valid ? d : 0.f;
+  }
+  if (write) L::store(p, t, v);
+}
+
+// Rows [a, b), rows a + w0 .. in steps of the warps' rows, into acc; one row's
+// load runs ahead of the row at work.
+template <class L>
+struct Rows {
+  static constexpr int RPW = 32 / L::LPR;   // rows per warp and step
+  typename L::Raw next;
+  int t;
+  bool valid;
+  __device__ __forceinline__ void fetch(const BalParams &p, int row, int b) {
+    t = row + (int)(threadIdx.x & 31) / L::LPR;
+    valid = t < b && (!p.mask || p.mask[t]);
+    L::load(p, t, valid, next);
+  }
+};
+
+// Shared memory of a block of the pass: the warps' sums, the coefficients and
+// the bias, each over the padded experts of the layout.
+template <class L>
+__device__ __forceinline__ void stage_bias(const BalParams &p, float *bias) {
+  if (p.bias)
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) bias[e] = __ldg(p.bias + e);
+}
+
+__device__ __forceinline__ float grad_scale(const BalParams &p, int s, int tokens) {
+  const float n = (float)tokens;
+  return n > 0.f ? (p.grad ? p.grad[s] : 1.f) * p.alpha * (float)p.E / (float)p.k / n / n : 0.f;
+}
+
+// Adds the subgroups of a warp (the same experts) and leaves the warp's sums
+// in sums[warp][NE * LPR].
+template <class L>
+__device__ __forceinline__ void warp_sums(float (&acc)[L::NE], float *sums) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < L::NE; ++j) {
+#pragma unroll
+    for (int o = 16; o >= L::LPR; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+    if (lane < L::LPR) sums[warp * (L::NE * L::LPR) + L::first(j / L::VEC) + j % L::VEC] = acc[j];
   }
 }
 
 // -------------------------------------------------------------- main pass --
 
-template <int DT>
-__device__ __forceinline__ float load_z(const void *z, size_t i) {
-  if constexpr (DT == MOE_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(z)[i]);
-  return reinterpret_cast<const float *>(z)[i];
-}
-
-template <int DT>
-__device__ __forceinline__ void store_z(void *z, size_t i, float v) {
-  if constexpr (DT == MOE_BF16) reinterpret_cast<__nv_bfloat16 *>(z)[i] = __float2bfloat16_rn(v);
-  else reinterpret_cast<float *>(z)[i] = v;
-}
-
-// One warp per token; expert e lives in lane e % 32, slot e / 32 (EPL slots).
-template <int DT, int EPL, bool kSigmoid>
+template <class L>
 __global__ void __launch_bounds__(kBalThreads) balance_pass_kernel(const BalParams p) {
-  pdl_enter();
-  extern __shared__ float sums[];   // [kBalWarps][E]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int EP = L::NE * L::LPR;   // experts of the layout, >= E
+  __shared__ float sums[kBalWarps * EP];
+  __shared__ float coef[EP], bias[EP];
+  const int warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
-  for (int s = seg_of(p, t0); s < p.S; ++s) {
-    const int a = max(t0, seg_begin(p, s)), b = min(t1, seg_end(p, s));
-    if (seg_begin(p, s) >= t1) break;
+  constexpr int kStep = kBalWarps * Rows<L>::RPW;
+  bool waited = false;
+  stage_bias<L>(p, bias);
+  for (int at = t0; at < t1;) {
+    const int s = seg_of(p, at);
+    if (s >= p.S) break;
+    const int a = max(at, seg_begin(p, s)), b = min(t1, seg_end(p, s));
+    if (a >= t1) break;
+    at = b;                                  // past `at`: the segment ends after it
     if (a >= b) continue;
-    float acc[EPL], ce[EPL];
-    const int32_t *counts = p.counts + (size_t)s * p.E;
+    const int first = a + warp * Rows<L>::RPW;
+    Rows<L> rows;
+    rows.fetch(p, first, b);
     float scale = 0.f;
     if (p.dz) {
-      // Gradient coefficients with the mean taken off the counts: the term
-      // it adds cancels in a_i - sum_e p_e a_e, and small differences keep
-      // their digits.
-      const float n = (float)__ldcg(p.tokens + s);
-      scale = n > 0.f ? (p.grad ? p.grad[s] : 1.f) * p.alpha * (float)p.E / (float)p.k / n / n : 0.f;
-      int sum = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (lane + 32 * i < p.E) sum += __ldcg(counts + lane + 32 * i);
-      sum = __reduce_add_sync(0xffffffffu, sum);
-      const float mean = (float)sum / (float)p.E;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        ce[i] = lane + 32 * i < p.E ? (float)__ldcg(counts + lane + 32 * i) - mean : 0.f;
+      if (!waited) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // the counts
+        waited = true;
+      }
+      const int32_t *counts = p.counts + (size_t)s * p.E;
+      scale = grad_scale(p, s, __ldcg(p.tokens + s));
+      int sum = 0;   // every warp for itself: all assignments of the segment
+      for (int e = threadIdx.x & 31; e < p.E; e += 32) sum += __ldcg(counts + e);
+      const float mean = (float)__reduce_add_sync(0xffffffffu, sum) / (float)p.E;
+      for (int e = threadIdx.x; e < EP; e += blockDim.x)
+        coef[e] = e < p.E ? (float)__ldcg(counts + e) - mean : 0.f;
     }
+    __syncthreads();
+    float acc[L::NE];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
-    for (int t = a + warp; t < b; t += kBalWarps) {
-      const bool keep = !p.mask || p.mask[t];
-      if (!keep) {
-        if (p.dz) {
-#pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (lane + 32 * i < p.E) store_z<DT>(p.dz, (size_t)t * p.lddz + lane + 32 * i, 0.f);
-        }
-        continue;
-      }
-      float v[EPL], om[EPL];
-      float tot = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = e < p.E ? load_z<DT>(p.z, (size_t)t * p.ldz + e) : -INFINITY;
-      }
-      if constexpr (kSigmoid) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          // 0 past E: expf(inf) = inf.  1 - sigmoid is taken as e sigmoid,
-          // which keeps its digits where the sigmoid is near 1.
-          const float ex = expf(-v[i]);
-          v[i] = 1.0f / (1.0f + ex);
-          om[i] = ex < 1e30f ? ex * v[i] : 1.0f - v[i];
-          tot += v[i];
-        }
-      } else {
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          if (p.bias && lane + 32 * i < p.E) v[i] += p.bias[lane + 32 * i];
-          m = fmaxf(m, v[i]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (m == -INFINITY) m = 0.f;   // a row with nothing left: p = 0
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          v[i] = lane + 32 * i < p.E ? expf(v[i] - m) : 0.f;
-          tot += v[i];
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-      const float inv = tot == 0.f ? 0.f : 1.0f / tot;
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        v[i] *= inv;
-        acc[i] += v[i];
-        if (p.dz) dot = fmaf(v[i], ce[i], dot);
-      }
-      if (p.dz) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const int e = lane + 32 * i;
-          float d = scale * v[i] * (ce[i] - dot);
-          if constexpr (kSigmoid) d *= om[i];
-          if (e < p.E) store_z<DT>(p.dz, (size_t)t * p.lddz + e, d);
-        }
-      }
+    for (int j = 0; j < L::NE; ++j) acc[j] = 0.f;
+    for (int row = first; row < b; row += kStep) {
+      const typename L::Raw raw = rows.next;
+      const int t = rows.t;
+      const bool valid = rows.valid;
+      rows.fetch(p, row + kStep, b);
+      one_token<L>(p, raw, t, valid, t < b, p.bias ? bias : nullptr, p.dz ? coef : nullptr, scale, acc);
     }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + 32 * i < p.E) sums[warp * p.E + lane + 32 * i] = acc[i];
+    warp_sums<L>(acc, sums);
     __syncthreads();
     float *dst = p.part + (size_t)(blockIdx.x + s) * p.E;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
       float tsum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) tsum += sums[w * p.E + e];
+      for (int w = 0; w < kBalWarps; ++w) tsum += sums[w * EP + e];
       dst[e] = tsum;
     }
     __syncthreads();
   }
+  // The finish kernel waits for this grid alone: leave only after the counts.
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // -------------------------------------------------------------- finish ----
-// Block = segment: P from the chunks' partial sums in chunk order, then loss.
-__global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p) {
-  pdl_enter();
-  __shared__ float red[32];
-  const int s = blockIdx.x;
-  const int a = seg_begin(p, s), b = seg_end(p, s);
-  const int n = __ldcg(p.tokens + s);
-  const float inv = n > 0 ? 1.0f / (float)n : 0.f;
-  float dot = 0.f;
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-    float sum = 0.f;
-    if (a < b)
-      for (int c = a / p.chunk; c <= (b - 1) / p.chunk; ++c)
-        sum += __ldcg(p.part + (size_t)(c + s) * p.E + e);
-    sum *= inv;
-    p.prob[(size_t)s * p.E + e] = sum;
-    dot = fmaf((float)__ldcg(p.counts + (size_t)s * p.E + e), sum, dot);
-  }
+
+// The loss of a segment from each CTA's share of sum_e c_e P_e: red is shared,
+// one float per warp, and slot one float.
+__device__ __forceinline__ void finish_loss(const BalParams &p, int s, float dot, float inv, float *red,
+                                            float *slot) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
+  if (lane == 0) red[warp] = dot;
   __syncthreads();
   if (threadIdx.x == 0) {
     float tot = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) tot += red[w];
+    for (int w = 0; w < nw; ++w) tot += red[w];
+    *slot = tot;
+  }
+  cluster_sync();
+  if (cluster_rank() == 0 && threadIdx.x == 0) {
+    const int ranks = cluster_size();
+    float tot = 0.f;
+    for (int r = 0; r < ranks; ++r) tot += __uint_as_float(ld_peer(slot, r));
     p.loss[s] = p.alpha * (float)p.E / (float)p.k * inv * tot;
   }
+  cluster_sync();
+}
+
+// A cluster per segment: rank r takes experts 32 r .. 32 r + 31, 32 (r +
+// ranks) .., a lane each; the warps share the segment's chunks, and their sums
+// are added in warp order.
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float part[32][33];
+  __shared__ float red[32], slot;
+  const int ranks = cluster_size(), rank = cluster_rank(), s = blockIdx.x / ranks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int a = seg_begin(p, s), b = seg_end(p, s);
+  const int c0 = a / p.chunk, c1 = a < b ? (b - 1) / p.chunk + 1 : c0;
+  const int n = __ldcg(p.tokens + s);
+  const float inv = n > 0 ? 1.0f / (float)n : 0.f;
+  float dot = 0.f;
+  for (int e0 = rank * 32; e0 < p.E; e0 += ranks * 32) {
+    const int e = e0 + lane;
+    float sum = 0.f;
+    if (e < p.E) {
+#pragma unroll 8
+      for (int c = c0 + warp; c < c1; c += nw) sum += __ldcg(p.part + (size_t)(c + s) * p.E + e);
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && e < p.E) {
+      float tot = 0.f;
+      for (int w = 0; w < nw; ++w) tot += part[w][lane];
+      tot *= inv;
+      p.prob[(size_t)s * p.E + e] = tot;
+      dot = fmaf((float)__ldcg(p.counts + (size_t)s * p.E + e), tot, dot);
+    }
+    __syncthreads();
+  }
+  finish_loss(p, s, dot, inv, red, &slot);
+}
+
+// ---------------------------------------------------------- small batches --
+
+template <class L>
+__global__ void __launch_bounds__(kBalThreads) balance_small_kernel(const BalParams p) {
+  constexpr int EP = L::NE * L::LPR;
+  __shared__ float sums[kBalWarps * EP];
+  __shared__ float coef[EP], bias[EP];
+  float *mine = sums;   // the block's sums, in place of warp 0's
+  __shared__ int32_t hist[EP + 1];
+  __shared__ float red[kBalWarps], slot;
+  __shared__ int total;
+  const int ranks = cluster_size(), rank = cluster_rank(), s = blockIdx.x / ranks;
+  const int warp = threadIdx.x >> 5;
+  const int a = seg_begin(p, s), b = seg_end(p, s);
+  constexpr int kStep = kBalWarps * Rows<L>::RPW;
+  const int first = a + (rank * kBalWarps + warp) * Rows<L>::RPW;
+  Rows<L> rows;
+  rows.fetch(p, first, b);
+  stage_bias<L>(p, bias);
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
+  if (threadIdx.x == 0) total = 0;
+  __syncthreads();
+  count_rows(p, a, b, rank * blockDim.x + threadIdx.x, ranks * blockDim.x, hist);
+  cluster_sync();
+  // Every CTA adds up the whole segment's counts for itself (coef: as floats).
+  int sum = 0, n = 0;
+  for (int e = threadIdx.x; e < EP; e += blockDim.x) {
+    int c = 0;
+    if (e < p.E)
+      for (int r = 0; r < ranks; ++r) c += (int)ld_peer(&hist[e], r);
+    coef[e] = (float)c;
+    sum += c;
+    if (rank == 0 && e < p.E) p.counts[(size_t)s * p.E + e] = c;
+  }
+  for (int r = 0; r < ranks; ++r) n += (int)ld_peer(&hist[p.E], r);
+  if (rank == 0 && threadIdx.x == 0) p.tokens[s] = n;
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&total, sum);
+  __syncthreads();
+  const float mean = (float)total / (float)p.E;
+  const float scale = grad_scale(p, s, n), inv = n > 0 ? 1.0f / (float)n : 0.f;
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) coef[e] -= mean;
+  __syncthreads();
+  float acc[L::NE];
+#pragma unroll
+  for (int j = 0; j < L::NE; ++j) acc[j] = 0.f;
+  for (int row = first; row < b; row += ranks * kStep) {
+    const typename L::Raw raw = rows.next;
+    const int t = rows.t;
+    const bool valid = rows.valid;
+    rows.fetch(p, row + ranks * kStep, b);
+    one_token<L>(p, raw, t, valid, t < b, p.bias ? bias : nullptr, p.dz ? coef : nullptr, scale, acc);
+  }
+  warp_sums<L>(acc, sums);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    float tsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBalWarps; ++w) tsum += sums[w * EP + e];
+    mine[e] = tsum;
+  }
+  cluster_sync();
+  float dot = 0.f;
+  for (int e = rank + ranks * threadIdx.x; e < p.E; e += ranks * blockDim.x) {
+    float tot = 0.f;
+    for (int r = 0; r < ranks; ++r) tot += __uint_as_float(ld_peer(&mine[e], r));
+    tot *= inv;
+    p.prob[(size_t)s * p.E + e] = tot;
+    dot = fmaf(coef[e] + mean, tot, dot);
+  }
+  finish_loss(p, s, dot, inv, red, &slot);
+}
+
+// ----------------------------------------------------------------- launch --
+
+template <typename... KArgs>
+cudaError_t launch_cluster(bool pdl, void (*kernel)(KArgs...), int blocks, int threads, int ranks,
+                           cudaStream_t st, const BalParams &p) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 int balance_chunk(int T) {
-  // One block's tokens: 32 (four per warp) until that makes kBalChunks blocks.
-  return std::max(32, (T + kBalChunks - 1) / kBalChunks);
+  // One block's tokens: 32 (four per warp) until that makes kBalBlocks blocks.
+  return std::max(32, (T + kBalBlocks - 1) / kBalBlocks);
 }
 
-template <int DT, bool kSigmoid>
-cudaError_t launch_pass(const BalParams &p, int chunks, cudaStream_t st) {
-  const size_t smem = (size_t)kBalWarps * p.E * sizeof(float);
-  const int epl = (p.E + 31) / 32;
-  auto k = epl <= 1    ? balance_pass_kernel<DT, 1, kSigmoid>
-           : epl <= 2  ? balance_pass_kernel<DT, 2, kSigmoid>
-           : epl <= 4  ? balance_pass_kernel<DT, 4, kSigmoid>
-           : epl <= 8  ? balance_pass_kernel<DT, 8, kSigmoid>
-           : epl <= 16 ? balance_pass_kernel<DT, 16, kSigmoid>
-                       : balance_pass_kernel<DT, 32, kSigmoid>;
-  return launch_k(true, k, dim3(chunks), dim3(kBalThreads), smem, st, p);
+bool is_small(int T, int E) { return (long long)T * E <= kSmallElems; }
+
+template <class L>
+cudaError_t launch_layout(const BalParams &p, cudaStream_t st) {
+  if (is_small(p.T, p.E)) {
+    // CTAs of a segment: one for every two steps of its share of the rows
+    // (four times the mean segment: they differ in length).
+    const int rows = std::min<long long>(p.T, 4LL * ((p.T + p.S - 1) / p.S));
+    const int step = 2 * kBalWarps * Rows<L>::RPW;
+    int ranks = 1;
+    while (ranks < kCluster && ranks * step < rows) ranks *= 2;
+    return launch_cluster(false, balance_small_kernel<L>, p.S * ranks, kBalThreads, ranks, st, p);
+  }
+  const int chunks = (p.T + p.chunk - 1) / p.chunk;
+  cudaError_t err =
+      launch_cluster(false, balance_count_kernel, p.S * kCluster, kCountThreads, kCluster, st, p);
+  if (err == cudaSuccess)
+    err = launch_k(true, balance_pass_kernel<L>, dim3(chunks), dim3(kBalThreads), 0, st, p);
+  // A warp of the finish kernel for every few chunks of a segment.
+  const int per = (chunks + p.S - 1) / p.S;
+  const int threads = std::min(1024, std::max(64, (per / 4 + 1) * 32));
+  if (err == cudaSuccess)
+    err = launch_cluster(true, balance_finish_kernel, p.S * kCluster, threads, kCluster, st, p);
+  return err;
+}
+
+// Vectors where rows are whole 16-byte pieces, as few lanes a row as hold it.
+template <int DT, bool kSig>
+cudaError_t launch_balance(const BalParams &p, bool vec, cudaStream_t st) {
+  constexpr int V = DT == MOE_F32 ? 4 : 8;
+  if (vec) {
+    if (p.E <= 8 * V) return launch_layout<Lay<DT, V, 1, 8, kSig>>(p, st);
+    if (p.E <= 16 * V) return launch_layout<Lay<DT, V, 1, 16, kSig>>(p, st);
+    if (p.E <= 32 * V) return launch_layout<Lay<DT, V, 1, 32, kSig>>(p, st);
+    if (p.E <= 64 * V) return launch_layout<Lay<DT, V, 2, 32, kSig>>(p, st);
+    if (p.E <= 128 * V) return launch_layout<Lay<DT, V, 4, 32, kSig>>(p, st);
+    if constexpr (DT == MOE_F32) return launch_layout<Lay<DT, V, 8, 32, kSig>>(p, st);
+  }
+  if (p.E <= 64) return launch_layout<Lay<DT, 1, 2, 32, kSig>>(p, st);
+  if (p.E <= 256) return launch_layout<Lay<DT, 1, 8, 32, kSig>>(p, st);
+  return launch_layout<Lay<DT, 1, 32, 32, kSig>>(p, st);
 }
 
 }  // namespace
@@ -343,23 +686,15 @@ extern "C" __attribute__((visibility("default"))) int moe_balance_loss(
     }
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  BalParams p{z, router_mode == 1 ? nullptr : bias, idx, mask, seq_off, grad, loss,
-              counts, tokens, prob, dz, static_cast<float *>(workspace), ldz, lddz, T, E, top_k,
-              n_seq, balance_chunk(T), alpha};
-  cudaError_t err = cudaMemsetAsync(counts, 0, (size_t)n_seq * E * sizeof(int32_t), st);
-  if (err == cudaSuccess) err = cudaMemsetAsync(tokens, 0, (size_t)n_seq * sizeof(int32_t), st);
-  if (err == cudaSuccess) {
-    const int cc = std::max(64, (T + 1023) / 1024);   // count kernel: at most 1024 blocks
-    err = launch_k(false, balance_count_kernel, dim3((T + cc - 1) / cc), dim3(kBalThreads),
-                   (size_t)(E + 1) * sizeof(int32_t), st, p, cc);
-    const int chunks = (T + p.chunk - 1) / p.chunk;
-    const bool sig = router_mode == 1;
-    if (err == cudaSuccess)
-      err = z_dtype == MOE_F32
-                ? (sig ? launch_pass<MOE_F32, true>(p, chunks, st) : launch_pass<MOE_F32, false>(p, chunks, st))
-                : (sig ? launch_pass<MOE_BF16, true>(p, chunks, st) : launch_pass<MOE_BF16, false>(p, chunks, st));
-  }
-  if (err == cudaSuccess)
-    err = launch_k(true, balance_finish_kernel, dim3(n_seq), dim3(E <= 256 ? 256 : 1024), 0, st, p);
+  BalParams p{z, router_mode == 1 ? nullptr : bias, idx, mask, seq_off, grad, loss, counts, tokens,
+              prob, dz, static_cast<float *>(workspace), ldz, lddz, T, E, top_k, n_seq,
+              balance_chunk(T), top_k % 4 == 0 && !(reinterpret_cast<uintptr_t>(idx) & 15), alpha};
+  const long long v = z_dtype == MOE_F32 ? 4 : 8;
+  const bool vec = E % v == 0 && ldz % v == 0 && !(reinterpret_cast<uintptr_t>(z) & 15) &&
+                   (!dz || (lddz % v == 0 && !(reinterpret_cast<uintptr_t>(dz) & 15)));
+  const bool sig = router_mode == 1;
+  const cudaError_t err =
+      z_dtype == MOE_F32 ? (sig ? launch_balance<MOE_F32, true>(p, vec, st) : launch_balance<MOE_F32, false>(p, vec, st))
+                         : (sig ? launch_balance<MOE_BF16, true>(p, vec, st) : launch_balance<MOE_BF16, false>(p, vec, st));
   return err == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }

@@ -17,11 +17,9 @@ namespace {
 // A (16 rows).  K order inside an MMA is free as long as both operands agree,
 // so each lane takes 16 consecutive bytes of its row -- lane 4 g + q piece q of
 // every 64 bytes of row g -- straight from memory into two MMAs' fragments.
-// A block owns 8 outputs and splits K over its warps, 128 bytes of each row at
-// a time; partial sums meet in shared memory in warp order.
-constexpr int kFewWarps = 4;
-constexpr int kFewTokens = 16;
-
+// A block owns 8 outputs and splits K over its warps, 64 U bytes of each row
+// at a time; partial sums meet in shared memory in warp order.
+//
 template <int DT>
 __device__ __forceinline__ void mma_m16n8(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -38,41 +36,56 @@ __device__ __forceinline__ void mma_m16n8(float c[4], uint32_t a0, uint32_t a1, 
   }
 }
 
+// 16 bytes at `off` of a row of `bytes` (0: no row); w is read once and passes
+// L1 by.
+template <bool kOnce>
 __device__ __forceinline__ uint4 load_piece(const uint8_t *row, int off, int bytes) {
-  if (off >= bytes) return make_uint4(0u, 0u, 0u, 0u);
-  return *reinterpret_cast<const uint4 *>(row + off);
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (off < bytes) {
+    if constexpr (kOnce)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "l"(row + off));
+    else
+      v = __ldg(reinterpret_cast<const uint4 *>(row + off));
+  }
+  return v;
 }
 
-// NB: row blocks of 8 per warp -- 1, or 2 (SwiGLU: the gate rows, then the up rows).
-template <int DT, int NB>
-__global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const LinearParams p) {
-  __shared__ float red[kFewWarps][kFewTokens][8 * NB];
+// NB: row blocks of 8 per warp -- 1, or 2 (SwiGLU: the gate rows, then the up
+// rows).  HI: more than 8 tokens.  W: warps.  Each lane has four 16-byte
+// pieces of w in flight whatever NB.
+template <int DT, int NB, bool HI, int W>
+__global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const LinearParams p) {
+  constexpr int TT = HI ? 16 : 8;
+  __shared__ float red[W][TT][8 * NB];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int n0 = blockIdx.x * 8, t0 = blockIdx.y * kFewTokens;
+  const int n0 = blockIdx.x * 8;
   constexpr int es = DT == MOE_BF16 ? 2 : 1;
   const int kb = p.K * es;                       // bytes of a row, a multiple of 16
-  const bool row_ok = n0 + g < p.N, t_lo = t0 + g < p.T, t_hi = t0 + g + 8 < p.T;
+  const int row_kb = n0 + g < p.N ? kb : 0;
+  const int lo_kb = g < p.T ? kb : 0, hi_kb = HI && g + 8 < p.T ? kb : 0;
   const uint8_t *wr[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
     wr[b] = reinterpret_cast<const uint8_t *>(p.w) + ((size_t)(n0 + g) + (size_t)b * p.N) * p.ldw * es;
-  const uint8_t *xl = reinterpret_cast<const uint8_t *>(p.x) + (size_t)(t0 + g) * p.ldx * es;
+  const uint8_t *xl = reinterpret_cast<const uint8_t *>(p.x) + (size_t)g * p.ldx * es;
   const uint8_t *xh = xl + (size_t)8 * p.ldx * es;
   float c[NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[b][i] = 0.f;
-  constexpr int U = 4;                           // 64-byte units in flight
-  for (int u = warp * U; u * 64 < kb; u += kFewWarps * U) {
+  constexpr int U = 4 / NB;
+  for (int u = warp * U; u * 64 < kb; u += W * U) {
     uint4 wv[NB][U], lo[U], hi[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int off = (u + i) * 64 + q * 16;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) wv[b][i] = load_piece(wr[b], off, row_ok ? kb : 0);
-      lo[i] = load_piece(xl, off, t_lo ? kb : 0);
-      hi[i] = load_piece(xh, off, t_hi ? kb : 0);
+      for (int b = 0; b < NB; ++b) wv[b][i] = load_piece<true>(wr[b], off, row_kb);
+      lo[i] = load_piece<false>(xl, off, lo_kb);
+      hi[i] = HI ? load_piece<false>(xh, off, hi_kb) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i)
@@ -84,21 +97,19 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    red[warp][g][b * 8 + 2 * q] = c[b][0];
-    red[warp][g][b * 8 + 2 * q + 1] = c[b][1];
-    red[warp][g + 8][b * 8 + 2 * q] = c[b][2];
-    red[warp][g + 8][b * 8 + 2 * q + 1] = c[b][3];
+    *reinterpret_cast<float2 *>(&red[warp][g][b * 8 + 2 * q]) = make_float2(c[b][0], c[b][1]);
+    if constexpr (HI)
+      *reinterpret_cast<float2 *>(&red[warp][g + 8][b * 8 + 2 * q]) = make_float2(c[b][2], c[b][3]);
   }
   __syncthreads();
-  const int r = threadIdx.x >> 3, col = threadIdx.x & 7;   // 16 tokens x 8 outputs
-  const int t = t0 + r, n = n0 + col;
-  if (t >= p.T || n >= p.N) return;
+  const int t = threadIdx.x >> 3, col = threadIdx.x & 7, n = n0 + col;
+  if (t >= TT || t >= p.T || n >= p.N) return;
   float acc[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     acc[b] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) acc[b] += red[w][r][b * 8 + col];
+    for (int w = 0; w < W; ++w) acc[b] += red[w][t][b * 8 + col];
   }
   const float sx = p.x_scale ? p.x_scale[t] : 1.f;
   const float res = load_resid(p, t, n);
@@ -110,11 +121,20 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
   store_out(p, t, n, y + res);
 }
 
+// Warps per block: 8 where there are four blocks for every SM (short-lived
+// blocks overlap better), 16 where there are fewer (more bytes in flight).
+template <int DT, int NB, bool HI>
+cudaError_t launch_few_w(const LinearParams &p, cudaStream_t st) {
+  const int blocks = (p.N + 7) / 8;
+  return blocks >= 608 ? launch_k(false, linear_few_kernel<DT, NB, HI, 8>, dim3(blocks), dim3(256), 0, st, p)
+                       : launch_k(false, linear_few_kernel<DT, NB, HI, 16>, dim3(blocks), dim3(512), 0, st, p);
+}
+
 template <int DT>
 cudaError_t launch_few(const LinearParams &p, cudaStream_t st) {
-  const dim3 grid((p.N + 7) / 8, (p.T + kFewTokens - 1) / kFewTokens);
-  return launch_k(false, p.act == MOE_ACT_SWIGLU ? linear_few_kernel<DT, 2> : linear_few_kernel<DT, 1>,
-                  grid, dim3(kFewWarps * 32), 0, st, p);
+  if (p.act == MOE_ACT_SWIGLU)
+    return p.T > 8 ? launch_few_w<DT, 2, true>(p, st) : launch_few_w<DT, 2, false>(p, st);
+  return p.T > 8 ? launch_few_w<DT, 1, true>(p, st) : launch_few_w<DT, 1, false>(p, st);
 }
 
 size_t span(int rows, int cols, long long ld, size_t elem) {
@@ -177,6 +197,8 @@ extern "C" __attribute__((visibility("default"))) int moe_linear(
   LinearParams p{x, w, x_scale, w_scale, bias, resid, out, T, N, K, act, out_dtype,
                  ldx, ldw, ldr, ldo, status};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = dtype == MOE_BF16 ? launch_few<MOE_BF16>(p, st) : launch_few<MOE_E4M3>(p, st);
+  const cudaError_t err = T > kFewTokens      ? launch_linear_tc(p, dtype, st)
+                          : dtype == MOE_BF16 ? launch_few<MOE_BF16>(p, st)
+                                              : launch_few<MOE_E4M3>(p, st);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }

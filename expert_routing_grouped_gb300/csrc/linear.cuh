@@ -17,6 +17,10 @@ struct LinearParams {
   int32_t *status;
 };
 
+// linear_tc.cu: more than kFewTokens tokens.
+constexpr int kFewTokens = 16;
+cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st);
+
 // sx sw acc + bias, the pre-activation of row n of w.
 static __device__ __forceinline__ float finish_acc(const LinearParams &p, float acc, float sx, int n) {
   if (p.w_scale) acc *= sx * p.w_scale[n];

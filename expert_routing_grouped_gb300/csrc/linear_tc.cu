@@ -1,0 +1,548 @@
+// linear_tc.cu -- moe_linear above 16 tokens, on the 5th-gen tensor cores.
+//
+// D[128 rows of w][BN tokens] = w_tile . x_tile^T: the weights are the MMA's M
+// side, so a short batch wastes no tensor rows on absent tokens (BN follows T
+// in steps of 32) and an epilogue lane owns one output feature, whose bias and
+// scale it loads once.  Both operands come by TMA, 128 bytes of K a row and
+// stage (64 bf16 or 128 e4m3 values), 128-byte swizzled.
+//
+// Per CTA: warp 0 the TMA producer, warp 1 the MMA issuer (tcgen05.mma, M = 128,
+// N = BN, f32 accumulators in TMEM), warps 4-11 the epilogue (a lane quadrant
+// and half of the columns each).  Two accumulators in TMEM: the epilogue of one
+// tile runs under the main loop of the next.
+//
+// Sums: the tensor cores truncate when they add to an accumulator, measured
+// 1.8e-8 of the result per addition (16 bf16 products): 1.6e-5 at K = 14336.
+// That is nothing beside a bf16 output's 2^-9, but for f32 output the
+// accumulator is handed over every kSegBlocks K blocks and the epilogue adds
+// the segments in f32 to nearest, in registers (kSegs).
+//
+// Few tiles (short batches, narrow outputs) leave SMs idle, so K is split over
+// a cluster of 2 to 8 CTAs: each writes its partial tile to its own shared
+// memory, and after a cluster barrier each finishes its share of the columns,
+// reading the peers' partials over distributed shared memory in rank order --
+// no workspace, no atomics, the same bits on every call.
+//
+// Every mbarrier wait is bounded: one that gives up sets the status word, and
+// the roles stop, drain their copies and MMAs, and return.
+#include <algorithm>
+#include <atomic>
+#include <cuda.h>
+
+#include "linear.cuh"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BM = 128;             // rows of w per tile
+constexpr int kRowBytes = 128;      // K bytes per row and stage
+constexpr int kMaxStages = 8;
+constexpr int kThreads = 384;
+constexpr int kEpiWarp0 = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kSegBlocks = 8;       // K blocks per accumulator segment (f32 output)
+constexpr int kMaxBN = 256;
+constexpr int kSegMaxBN = 192;      // with segment sums in registers: 96 of an epilogue thread's
+constexpr size_t kSmemMax = 227 * 1024;
+
+struct TcLinear {
+  CUtensorMap map_w;       // [rows][K], box 128 x 128 bytes; SwiGLU: [N/16][2][16][K]
+  CUtensorMap map_x;       // [T][K], box BN x 128 bytes
+  LinearParams p;
+  int bn;                  // tokens per tile, a multiple of 32
+  int n_fb, n_tb;          // tiles along the outputs and the tokens
+  int group_tb;            // token tiles per raster group
+  int nkb;                 // K blocks of the whole product
+  int stages;
+};
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int32_t status;          // used when the caller gave no status word
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t linear_idesc(int n) {
+  // kind::f8f6f4: format fields 0 = e4m3 for A and B, f32 accumulator
+  if constexpr (DT == MOE_BF16) return idesc_bf16(BM, n);
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+
+template <int DT>
+__device__ __forceinline__ void linear_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                           uint32_t acc) {
+  if constexpr (DT == MOE_BF16) {
+    mma_bf16(d, da, db, idesc, acc);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(acc)
+        : "memory");
+  }
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            int w, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Token tiles run fastest within groups of group_tb, so the CTAs of a wave
+// share few w and x tiles and both stay in L2.
+__device__ __forceinline__ void tile_at(const TcLinear &q, int t, int &fb, int &tb) {
+  const int per = q.group_tb * q.n_fb;
+  const int g = t / per, r = t - g * per;
+  const int width = min(q.group_tb, q.n_tb - g * q.group_tb);
+  fb = r / width;
+  tb = g * q.group_tb + (r - fb * width);
+}
+
+// One lane's accumulator column block: W values of columns (tokens) t0 ..,
+// its own row's sums in v.  Rows of w: lane r of the tile holds row
+// fb * 128 + r; for SwiGLU, quadrant q's lanes 0-15 the gate rows of features
+// fb * 64 + 16 q + lane, lanes 16-31 their up rows.
+template <bool kSwiglu>
+struct LaneRow {
+  int n;          // output feature of this lane
+  bool ok;        // inside N
+  float sw, b;    // scale and bias of this lane's row of w
+};
+
+template <bool kSwiglu>
+__device__ __forceinline__ LaneRow<kSwiglu> lane_row(const LinearParams &p, int fb, int quad, int lane) {
+  LaneRow<kSwiglu> r;
+  int row;
+  if constexpr (kSwiglu) {
+    r.n = fb * 64 + quad * 16 + (lane & 15);
+    row = r.n + (lane >= 16 ? p.N : 0);
+  } else {
+    r.n = fb * BM + quad * 32 + lane;
+    row = r.n;
+  }
+  r.ok = r.n < p.N;
+  r.sw = r.ok && p.w_scale ? __ldg(p.w_scale + row) : 1.f;
+  r.b = r.ok && p.bias ? __ldg(p.bias + row) : 0.f;
+  return r;
+}
+
+template <bool kSwiglu, int W>
+__device__ __forceinline__ void finish_columns(const LinearParams &p, const LaneRow<kSwiglu> &r,
+                                               float (&v)[W], int t0, int n_cols) {
+  static_assert(W <= 32 && W % 2 == 0, "columns of one block");
+  const int lane = threadIdx.x & 31;
+  if (p.x_scale) {
+    const float sx = lane < W && t0 + lane < p.T ? __ldg(p.x_scale + t0 + lane) : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] *= r.sw * __shfl_sync(0xffffffffu, sx, j);
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) v[j] += r.b;
+  if constexpr (kSwiglu) {
+    // One exchange per column pair: lanes 0-15 finish token j (their gate,
+    // the partner's up), lanes 16-31 token j + 1.
+    const bool lo = lane < 16;
+#pragma unroll
+    for (int j = 0; j < W; j += 2) {
+      const float recv = __shfl_xor_sync(0xffffffffu, lo ? v[j + 1] : v[j], 16);
+      const int jc = j + (lo ? 0 : 1);
+      if (r.ok && jc < n_cols && t0 + jc < p.T) {
+        const float y = swiglu(lo ? v[j] : recv, lo ? recv : v[j + 1]);
+        store_out(p, t0 + jc, r.n, y + load_resid(p, t0 + jc, r.n));
+      }
+    }
+  } else {
+    float res[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      res[j] = r.ok && j < n_cols && t0 + j < p.T ? load_resid(p, t0 + j, r.n) : 0.f;
+    if (p.act == MOE_ACT_SILU) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[j] = silu(v[j]);
+    } else if (p.act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[j] = activate(MOE_ACT_GELU, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (r.ok && j < n_cols && t0 + j < p.T) store_out(p, t0 + j, r.n, v[j] + res[j]);
+  }
+}
+
+// kSplit: one tile per cluster, its K split over the CTAs; otherwise a
+// persistent CTA per SM walks the tiles.
+template <int DT, bool kSwiglu, bool kSplit, bool kSegs>
+__global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ TcLinear q) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars sm;
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const LinearParams &p = q.p;
+  int32_t *status = p.status ? p.status : &sm.status;
+  constexpr int kBlockElems = kRowBytes / (DT == MOE_BF16 ? 2 : 1);
+  const uint32_t stage_bytes = (BM + q.bn) * kRowBytes;
+  const uint32_t acc_cols = q.bn <= 32 ? 32 : q.bn <= 64 ? 64 : q.bn <= 128 ? 128 : 256;
+  const int S = q.stages;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.acc_full[i], 1);
+      mbar_init(&sm.acc_empty[i], kEpiWarps);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sm.tmem_base)),
+                 "r"(2 * acc_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  // This CTA's tiles and its share of K.
+  const int n_tiles = q.n_fb * q.n_tb;
+  int ranks = 1, rank = 0;
+  if constexpr (kSplit) {
+    asm volatile("mov.u32 %0, %cluster_nctarank;" : "=r"(ranks));
+    rank = cluster_rank();
+  }
+  const int t_first = blockIdx.x / ranks, t_step = gridDim.x / ranks;
+  const int kb0 = (int)((long long)q.nkb * rank / ranks);
+  const int kb1 = (int)((long long)q.nkb * (rank + 1) / ranks);
+  const int n_seg = kSegs ? (kb1 - kb0 + kSegBlocks - 1) / kSegBlocks : 1;
+  auto seg_at = [&](int s) { return kb0 + (int)((long long)(kb1 - kb0) * s / n_seg); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    int s = 0;
+    uint32_t ph = 0, armed = 0, par = 0;
+    bool ok = true;
+    for (int t = t_first; ok && t < n_tiles; t += t_step) {
+      int fb, tb;
+      tile_at(q, t, fb, tb);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = wait_bar(&sm.empty[s], ph ^ 1, &sm.abort, status))) break;
+        if (elect_one()) {
+          uint8_t *a = smem + s * stage_bytes;
+          mbar_expect_tx(&sm.full[s], stage_bytes);
+          if constexpr (kSwiglu) tma_load_4d(a, &q.map_w, kb * kBlockElems, 0, 0, fb * 4, &sm.full[s]);
+          else tma_load_2d(a, &q.map_w, kb * kBlockElems, fb * BM, &sm.full[s]);
+          tma_load_2d(a + BM * kRowBytes, &q.map_x, kb * kBlockElems, tb * q.bn, &sm.full[s]);
+        }
+        __syncwarp();
+        armed |= 1u << s;
+        par = (par & ~(1u << s)) | (ph << s);
+        if (++s == S) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    // Every copy that was issued has landed before the CTA goes on.
+    const unsigned long long t0 = globaltimer();
+    for (int i = 0; i < S; ++i)
+      if ((armed >> i) & 1) drain_bar(&sm.full[i], (par >> i) & 1, t0);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    int s = 0;
+    uint32_t ph = 0, it = 0;
+    const uint32_t idesc = linear_idesc<DT>(q.bn);
+    const uint64_t da0 = sw128_desc(smem_u32(smem));
+    const uint32_t stage_desc = stage_bytes >> 4;
+    bool ok = true;
+    for (int t = t_first; ok && t < n_tiles; t += t_step) {
+      for (int sg = 0; ok && sg < n_seg; ++sg, ++it) {
+        const int buf = it & 1;
+        if (!(ok = wait_bar(&sm.acc_empty[buf], ((it >> 1) & 1) ^ 1, &sm.abort, status))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * acc_cols;
+        const int ka = seg_at(sg), ke = seg_at(sg + 1);
+        for (int kb = ka; kb < ke; ++kb) {
+          if (!(ok = wait_bar(&sm.full[s], ph, &sm.abort, status))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t da = da0 + (uint64_t)(s * stage_desc);
+            const uint64_t db = da + ((BM * kRowBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              linear_mma<DT>(d, da + 2 * kk, db + 2 * kk, idesc, kb > ka || kk > 0);
+            mma_commit(&sm.empty[s]);
+          }
+          __syncwarp();
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit(&sm.acc_full[buf]);
+        __syncwarp();
+      }
+    }
+    // One more commit covers every MMA issued, also those of a tile that was
+    // left in the middle; TMEM is freed only after it has arrived.
+    if (elect_one()) mma_commit(&sm.drain);
+    __syncwarp();
+    drain_bar(&sm.drain, 0, globaltimer());
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    const int c_lo = half * (q.bn / 2), c_n = q.bn / 2;   // this warp's columns: a multiple of 16
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = t_first; ok && t < n_tiles; t += t_step) {
+      int fb, tb;
+      tile_at(q, t, fb, tb);
+      const LaneRow<kSwiglu> row = lane_row<kSwiglu>(p, fb, quad, lane);
+      constexpr int kChunks = kSegs ? kSegMaxBN / 32 : 1;
+      float acc[kChunks][16];
+      if constexpr (kSegs) {
+        for (int sg = 0; sg + 1 < n_seg; ++sg, ++it) {
+          const int buf = it & 1;
+          if (!(ok = wait_bar(&sm.acc_full[buf], (it >> 1) & 1, &sm.abort, status))) break;
+          tc_fence_after();
+          const uint32_t col = tmem + lane_base + buf * acc_cols + c_lo;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (c * 16 < c_n) {
+              float v[16];
+              tmem_ld16(col + c * 16, v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) acc[c][j] = sg > 0 ? acc[c][j] + v[j] : v[j];
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
+        }
+        if (!ok) break;
+      }
+      {
+        const int buf = it & 1;
+        if (!(ok = wait_bar(&sm.acc_full[buf], (it >> 1) & 1, &sm.abort, status))) break;
+        tc_fence_after();
+        const uint32_t col = tmem + lane_base + buf * acc_cols + c_lo;
+        auto chunk = [&](int c, const float *more) {
+          float v[16];
+          tmem_ld16(col + c * 16, v);
+          if (more) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += more[j];
+          }
+          if constexpr (kSplit) {
+            float *dst = reinterpret_cast<float *>(smem) + (c_lo + c * 16) * BM + quad * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dst[j * BM] = v[j];
+          } else {
+            finish_columns<kSwiglu>(p, row, v, tb * q.bn + c_lo + c * 16, 16);
+          }
+        };
+        if constexpr (kSegs) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c * 16 < c_n) chunk(c, n_seg > 1 ? acc[c] : nullptr);
+        } else {
+          for (int c = 0; c * 16 < c_n; ++c) chunk(c, nullptr);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
+        ++it;
+      }
+    }
+  }
+
+  if constexpr (kSplit) {
+    __syncthreads();          // the roles are reconverged for the aligned barrier
+    cluster_sync();           // every CTA's partial tile is in its shared memory
+    if (warp >= kEpiWarp0 && !*reinterpret_cast<volatile int *>(&sm.abort)) {
+      const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
+      int fb, tb;
+      tile_at(q, t_first, fb, tb);
+      const LaneRow<kSwiglu> row = lane_row<kSwiglu>(p, fb, quad, lane);
+      const int share = ((q.bn + ranks - 1) / ranks + 1) & ~1;   // columns per rank, even
+      const int cols = min(share, q.bn - rank * share);
+      for (int c = half * 4; c < cols; c += 8) {
+        const int n_cols = min(4, cols - c), col = rank * share + c;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t src = smem_u32(smem) + ((uint32_t)col * BM + quad * 32 + lane) * 4;
+        for (int r = 0; r < ranks; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < n_cols) v[j] += ld_peer(src + j * BM * 4, r);
+        finish_columns<kSwiglu>(p, row, v, tb * q.bn + col, n_cols);
+      }
+    }
+    __syncthreads();
+    cluster_sync();           // no CTA leaves while a peer reads its partials
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(2 * acc_cols)
+                 : "memory");
+  }
+}
+
+// ----------------------------------------------------------------- launch --
+
+struct Plan {
+  int bn, split;
+};
+
+int device_sms(int *dev) {
+  int sms = 0;
+  if (cudaGetDevice(dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// Tile width and K split with the least estimated time.  A K block costs the
+// larger of its MMAs (4 of BN / 2 clocks, not under 59 each) and its operand
+// bytes at an SM's share of the memory system; a tile adds a start and, split,
+// the exchange.
+Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
+  const int n_fb = (rows + BM - 1) / BM;
+  Plan best{32, 1};
+  double best_cost = 1e300;
+  for (int bn = 32; bn <= max_bn; bn += 32) {
+    const long long n_tb = (T + bn - 1) / bn;
+    if (bn > 32 && (long long)(bn - 32) >= T) break;   // wider than the batch
+    for (int split = 1; split <= 8; ++split) {
+      if (split > 1 && nkb / split < 4) break;
+      const long long ctas = n_fb * n_tb * split;
+      const double mma = 4.0 * std::max(bn / 2.0, 59.0);
+      const double mem = (BM + bn) * (double)kRowBytes / 64.0;
+      const long long waves = (ctas + sms - 1) / sms;
+      const double kblocks = (double)(nkb + split - 1) / split;
+      double cost = waves * kblocks * std::max(mma, mem) + 1500.0 + 8.0 * bn;
+      if (split > 1) cost += waves * (2000.0 + 16.0 * bn);   // a start and an exchange per wave
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = Plan{bn, split};
+      }
+    }
+  }
+  return best;
+}
+
+template <int DT, bool kSwiglu, bool kSplit, bool kSegs>
+cudaError_t launch(const TcLinear &q, int grid, int split, int dev, cudaStream_t st) {
+  auto kernel = linear_tc_kernel<DT, kSwiglu, kSplit, kSegs>;
+  // The shared-memory limit is raised once per device.
+  static std::atomic<unsigned long long> ready{0};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t err = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemMax - sizeof(Bars) - 64));
+    if (err != cudaSuccess) return err;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)q.stages * (BM + q.bn) * kRowBytes + 1024;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = kSplit ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, q);
+}
+
+template <int DT, bool kSwiglu, bool kSegs>
+cudaError_t launch_split(const TcLinear &q, int sms, int split, int dev, cudaStream_t st) {
+  const int tiles = q.n_fb * q.n_tb;
+  return split > 1 ? launch<DT, kSwiglu, true, kSegs>(q, tiles * split, split, dev, st)
+                   : launch<DT, kSwiglu, false, kSegs>(q, std::min(tiles, sms), 1, dev, st);
+}
+
+template <int DT>
+cudaError_t launch_type(const TcLinear &q, int sms, int split, bool segs, int dev, cudaStream_t st) {
+  if (q.p.act == MOE_ACT_SWIGLU)
+    return segs ? launch_split<DT, true, true>(q, sms, split, dev, st)
+                : launch_split<DT, true, false>(q, sms, split, dev, st);
+  return segs ? launch_split<DT, false, true>(q, sms, split, dev, st)
+              : launch_split<DT, false, false>(q, sms, split, dev, st);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) {
+  int dev = 0;
+  const int sms = device_sms(&dev);
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const bool sw = p.act == MOE_ACT_SWIGLU;
+  const int es = dtype == MOE_BF16 ? 2 : 1, rows = sw ? 2 * p.N : p.N;
+  const CUtensorMapDataType dt =
+      dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  TcLinear q;
+  q.p = p;
+  q.nkb = (p.K * es + kRowBytes - 1) / kRowBytes;
+  const bool segs = p.out_dtype == MOE_F32 && q.nkb > kSegBlocks;
+  const Plan plan = plan_of(p.T, rows, q.nkb, sms, segs ? kSegMaxBN : kMaxBN);
+  q.bn = plan.bn;
+  q.n_fb = (rows + BM - 1) / BM;
+  q.n_tb = (p.T + q.bn - 1) / q.bn;
+  q.group_tb = std::min(q.n_tb, 16);
+  const size_t stage = (size_t)(BM + q.bn) * kRowBytes;
+  q.stages = (int)std::min<size_t>(kMaxStages, (kSmemMax - sizeof(Bars) - 64 - 1024) / stage);
+  if (sw) {
+    if (!make_map_4d(&q.map_w, p.w, dt, p.K, 16, 2, p.N / 16, (uint64_t)p.ldw * es,
+                     (uint64_t)p.ldw * es * p.N, (uint64_t)p.ldw * es * 16, kRowBytes / es, 16, 2, 4))
+      return cudaErrorInvalidValue;
+  } else if (!make_map(&q.map_w, p.w, dt, es, p.K, rows, p.ldw, kRowBytes / es, BM)) {
+    return cudaErrorInvalidValue;
+  }
+  if (!make_map(&q.map_x, p.x, dt, es, p.K, p.T, p.ldx, kRowBytes / es, q.bn))
+    return cudaErrorInvalidValue;
+  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, sms, plan.split, segs, dev, st)
+                           : launch_type<MOE_E4M3>(q, sms, plan.split, segs, dev, st);
+}
+
+}  // namespace moe

@@ -278,6 +278,11 @@ cudaError_t launch_router_tc(const moe_handle *h, const void *x, int T, float *z
 bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, size_t elem, uint64_t cols,
               uint64_t rows, uint64_t row_stride_elems, uint32_t box_cols, uint32_t box_rows,
               bool swizzle = true);
+// 4D map: extents d0..d3 (d0 innermost), byte strides of dimensions 1-3, box
+// b0..b3; 128-byte swizzle.
+bool make_map_4d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t d0, uint64_t d1,
+                 uint64_t d2, uint64_t d3, uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b0,
+                 uint32_t b1, uint32_t b2, uint32_t b3);
 // Grouped x of a decode-sized batch as bf16 operand planes (xe) and the
 // per-row routing weights (wperm).
 cudaError_t launch_gather_exact(const moe_handle *h, const void *x, int T, cudaStream_t st);

@@ -316,7 +316,8 @@ int moe_route_noalloc(const void *x, int T, int hidden, int num_experts, int top
  * synchronises, and can be captured into a graph.  Calls share no scratch, so
  * any number may overlap on different streams.  The current device must be
  * the one that owns the pointers.  Strides are in elements, 0 for contiguous
- * rows.  Results are bitwise identical from run to run.
+ * rows.  The same call gives the same bits on every run (sizes, strides and
+ * alignment choose among kernels that sum in different orders).
  */
 
 /* Element types of these operators (x_dtype of moe_layout uses the first two). */
@@ -424,7 +425,8 @@ int moe_linear(const void *x, const float *x_scale, const void *w, const float *
  *            may be z itself (the same stride)
  *   workspace  at least moe_balance_workspace(T, num_experts, n_seq) bytes,
  *            not shared with a call that may overlap this one
- * A row whose logits are all -infinity has p = 0.  num_experts <= 1024, top_k
+ * A row whose logits are all -infinity (in mode 1: whose sigmoids are all
+ * below 2^-126) has p = 0.  num_experts <= 1024, top_k
  * <= 32, T * top_k <= 2^26, n_seq <= 65535.  Loss and gradient together read z
  * once.  Outputs and workspace must not overlap anything else.  T == 0 checks
  * what it can, launches nothing and writes nothing.  Returns MOE_OK,
