@@ -112,13 +112,15 @@ __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const Linear
     for (int w = 0; w < W; ++w) acc[b] += red[w][t][b * 8 + col];
   }
   const float sx = p.x_scale ? p.x_scale[t] : 1.f;
-  const float res = load_resid(p, t, n);
+  const bool bf = p.out_dtype == MOE_BF16;
+  const float res = !p.resid ? 0.f : bf ? load_resid<true>(p, t, n) : load_resid<false>(p, t, n);
   float y;
   if constexpr (NB == 2)
     y = swiglu(finish_acc(p, acc[0], sx, n), finish_acc(p, acc[1], sx, p.N + n));
   else
     y = activate(p.act, finish_acc(p, acc[0], sx, n));
-  store_out(p, t, n, y + res);
+  if (bf) store_out<true>(p, t, n, y + res);
+  else store_out<false>(p, t, n, y + res);
 }
 
 // Warps per block: 8 where there are four blocks for every SM (short-lived

@@ -27,7 +27,13 @@ static __device__ __forceinline__ float finish_acc(const LinearParams &p, float 
   return p.bias ? acc + p.bias[n] : acc;
 }
 
-static __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// kFast, for a bf16 output: the hardware exponential (2 units and |v| 2^-24),
+// far below the 2^-9 of the rounding that follows.  The quotient is the fast
+// one (2 units of f32) either way.
+template <bool kFast = false>
+static __device__ __forceinline__ float silu(float v) {
+  return __fdividef(v, 1.0f + (kFast ? __expf(-v) : expf(-v)));
+}
 
 static __device__ __forceinline__ float activate(int act, float v) {
   if (act == MOE_ACT_SILU) return silu(v);
@@ -35,19 +41,24 @@ static __device__ __forceinline__ float activate(int act, float v) {
   return v;
 }
 
-static __device__ __forceinline__ float swiglu(float gate, float up) { return silu(gate) * up; }
-
-static __device__ __forceinline__ float load_resid(const LinearParams &p, int t, int n) {
-  if (!p.resid) return 0.f;
-  const size_t i = (size_t)t * p.ldr + n;
-  return p.out_dtype == MOE_BF16
-             ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.resid)[i])
-             : reinterpret_cast<const float *>(p.resid)[i];
+template <bool kFast = false>
+static __device__ __forceinline__ float swiglu(float gate, float up) {
+  return silu<kFast>(gate) * up;
 }
 
+// Residual and output elements, kBf16 the output type (of the whole kernel: a
+// branch at each element would make every residual load wait for itself).
+template <bool kBf16>
+static __device__ __forceinline__ float load_resid(const LinearParams &p, int t, int n) {
+  const size_t i = (size_t)t * p.ldr + n;
+  if constexpr (kBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.resid)[i]);
+  return reinterpret_cast<const float *>(p.resid)[i];
+}
+
+template <bool kBf16>
 static __device__ __forceinline__ void store_out(const LinearParams &p, int t, int n, float y) {
   const size_t i = (size_t)t * p.ldo + n;
-  if (p.out_dtype == MOE_BF16) reinterpret_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(y);
+  if constexpr (kBf16) reinterpret_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(y);
   else reinterpret_cast<float *>(p.out)[i] = y;
 }
 

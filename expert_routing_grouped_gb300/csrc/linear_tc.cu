@@ -7,15 +7,15 @@
 // stage (64 bf16 or 128 e4m3 values), 128-byte swizzled.
 //
 // Per CTA: warp 0 the TMA producer, warp 1 the MMA issuer (tcgen05.mma, M = 128,
-// N = BN, f32 accumulators in TMEM), warps 4-11 the epilogue (a lane quadrant
-// and half of the columns each).  Two accumulators in TMEM: the epilogue of one
+// N = BN, f32 accumulators in TMEM), warps 4 and up the epilogue (two or three
+// to a lane quadrant).  Two accumulators in TMEM: the epilogue of one
 // tile runs under the main loop of the next.
 //
 // Sums: the tensor cores truncate when they add to an accumulator, measured
 // 1.8e-8 of the result per addition (16 bf16 products): 1.6e-5 at K = 14336.
 // That is nothing beside a bf16 output's 2^-9, but for f32 output the
 // accumulator is handed over every kSegBlocks K blocks and the epilogue adds
-// the segments in f32 to nearest, in registers (kSegs).
+// the segments in f32 to nearest, in registers.
 //
 // Few tiles (short batches, narrow outputs) leave SMs idle, so K is split over
 // a cluster of 2 to 8 CTAs: each writes its partial tile to its own shared
@@ -39,12 +39,17 @@ namespace {
 constexpr int BM = 128;             // rows of w per tile
 constexpr int kRowBytes = 128;      // K bytes per row and stage
 constexpr int kMaxStages = 8;
-constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4;
-constexpr int kEpiWarps = 8;
-constexpr int kSegBlocks = 8;       // K blocks per accumulator segment (f32 output)
+constexpr int kSegBlocks = 16;      // K blocks per accumulator segment (f32 output)
 constexpr int kMaxBN = 256;
-constexpr int kSegMaxBN = 192;      // with segment sums in registers: 96 of an epilogue thread's
+constexpr int kSegMaxBN = 192;      // with segment sums in registers
+// Epilogue warps per lane quadrant: they take turns at blocks of 16 columns.
+// f32 output has three, so that a thread's segment sums (64 at BN = 192) fit
+// its registers: spilled, they share the path that feeds the MMAs operands.
+template <bool kBf16>
+constexpr int kEpiGroups = kBf16 ? 2 : 3;
+template <bool kBf16>
+constexpr int kThreads = (kEpiWarp0 + 4 * kEpiGroups<kBf16>) * 32;
 constexpr size_t kSmemMax = 227 * 1024;
 
 struct TcLinear {
@@ -153,9 +158,33 @@ __device__ __forceinline__ LaneRow<kSwiglu> lane_row(const LinearParams &p, int 
   return r;
 }
 
-template <bool kSwiglu, int W>
+// The residual of a block of W columns, raw, loaded ahead of its use.  SwiGLU:
+// the lane's own token of each column pair.  Tokens and features past the end
+// take the last one's address (their columns are not stored): a branch or a
+// conversion at each load would make it wait for itself.
+template <bool kSwiglu, bool kBf16, int W>
+struct Resid {
+  uint32_t v[kSwiglu ? W / 2 : W];
+  __device__ __forceinline__ void load(const LinearParams &p, const LaneRow<kSwiglu> &r, int t0) {
+    if (!p.resid) return;
+    const int up = kSwiglu && (threadIdx.x & 31) >= 16 ? 1 : 0;
+    const size_t n = min(r.n, p.N - 1);
+#pragma unroll
+    for (int j = 0; j < W; j += kSwiglu ? 2 : 1) {
+      const size_t i = (size_t)min(t0 + j + up, p.T - 1) * p.ldr + n;
+      v[kSwiglu ? j / 2 : j] = kBf16 ? reinterpret_cast<const unsigned short *>(p.resid)[i]
+                                     : reinterpret_cast<const uint32_t *>(p.resid)[i];
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(kBf16 ? v[i] << 16 : v[i]);
+  }
+};
+
+template <bool kSwiglu, bool kBf16, int W>
 __device__ __forceinline__ void finish_columns(const LinearParams &p, const LaneRow<kSwiglu> &r,
-                                               float (&v)[W], int t0, int n_cols) {
+                                               float (&v)[W], const Resid<kSwiglu, kBf16, W> &res,
+                                               int t0, int n_cols) {
   static_assert(W <= 32 && W % 2 == 0, "columns of one block");
   const int lane = threadIdx.x & 31;
   if (p.x_scale) {
@@ -174,32 +203,55 @@ __device__ __forceinline__ void finish_columns(const LinearParams &p, const Lane
       const float recv = __shfl_xor_sync(0xffffffffu, lo ? v[j + 1] : v[j], 16);
       const int jc = j + (lo ? 0 : 1);
       if (r.ok && jc < n_cols && t0 + jc < p.T) {
-        const float y = swiglu(lo ? v[j] : recv, lo ? recv : v[j + 1]);
-        store_out(p, t0 + jc, r.n, y + load_resid(p, t0 + jc, r.n));
+        float y = swiglu<kBf16>(lo ? v[j] : recv, lo ? recv : v[j + 1]);
+        if (p.resid) y += res.get(j / 2);
+        store_out<kBf16>(p, t0 + jc, r.n, y);
       }
     }
   } else {
-    float res[W];
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      res[j] = r.ok && j < n_cols && t0 + j < p.T ? load_resid(p, t0 + j, r.n) : 0.f;
     if (p.act == MOE_ACT_SILU) {
 #pragma unroll
-      for (int j = 0; j < W; ++j) v[j] = silu(v[j]);
+      for (int j = 0; j < W; ++j) v[j] = silu<kBf16>(v[j]);
     } else if (p.act == MOE_ACT_GELU) {
 #pragma unroll
       for (int j = 0; j < W; ++j) v[j] = activate(MOE_ACT_GELU, v[j]);
     }
+    if (p.resid) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[j] += res.get(j);
+    }
 #pragma unroll
     for (int j = 0; j < W; ++j)
-      if (r.ok && j < n_cols && t0 + j < p.T) store_out(p, t0 + j, r.n, v[j] + res[j]);
+      if (r.ok && j < n_cols && t0 + j < p.T) store_out<kBf16>(p, t0 + j, r.n, v[j]);
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void prefetch_resid(const LinearParams &p, int t, int n) {
+  const char *a = reinterpret_cast<const char *>(p.resid) + ((size_t)t * p.ldr + n) * (kBf16 ? 2 : 4);
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+}
+
+// wait_bar without the call: the epilogue holds sums in registers across it.
+__device__ __forceinline__ bool wait_inline(uint64_t *bar, uint32_t parity, int *abort, int32_t *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int *>(abort)) return false;
+    if (globaltimer() - t0 > kWaitNs) {
+      atomicExch(abort, 1);
+      atomicExch(status, kStatusTimeout);
+      return false;
+    }
   }
 }
 
 // kSplit: one tile per cluster, its K split over the CTAs; otherwise a
 // persistent CTA per SM walks the tiles.
-template <int DT, bool kSwiglu, bool kSplit, bool kSegs>
-__global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ TcLinear q) {
+// kBf16: the output type; f32 output sums K in segments.
+template <int DT, bool kSwiglu, bool kSplit, bool kBf16>
+__global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __grid_constant__ TcLinear q) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars sm;
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -207,6 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const LinearParams &p = q.p;
   int32_t *status = p.status ? p.status : &sm.status;
+  constexpr bool kSegs = !kBf16;
+  constexpr int G = kEpiGroups<kBf16>;
   constexpr int kBlockElems = kRowBytes / (DT == MOE_BF16 ? 2 : 1);
   const uint32_t stage_bytes = (BM + q.bn) * kRowBytes;
   const uint32_t acc_cols = q.bn <= 32 ? 32 : q.bn <= 64 ? 64 : q.bn <= 128 ? 128 : 256;
@@ -219,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.acc_full[i], 1);
-      mbar_init(&sm.acc_empty[i], kEpiWarps);
+      mbar_init(&sm.acc_empty[i], 4 * G);
     }
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -324,8 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     drain_bar(&sm.drain, 0, globaltimer());
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
-    const int c_lo = half * (q.bn / 2), c_n = q.bn / 2;   // this warp's columns: a multiple of 16
+    const int quad = warp & 3, turn = (warp - kEpiWarp0) >> 2;
+    // Block c of this warp: columns (c G + turn) 16 .. + 15.
+    auto col_of = [&](int c) { return (c * G + turn) * 16; };
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     uint32_t it = 0;
     bool ok = true;
@@ -333,21 +388,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
       int fb, tb;
       tile_at(q, t, fb, tb);
       const LaneRow<kSwiglu> row = lane_row<kSwiglu>(p, fb, quad, lane);
-      constexpr int kChunks = kSegs ? kSegMaxBN / 32 : 1;
+      if constexpr (!kSplit) {
+        // The tile's residual comes to L2 under the main loop.
+        if (p.resid && row.ok)
+          for (int c = turn; c < q.bn; c += G)
+            if (tb * q.bn + c < p.T && (lane & 7) == 0) prefetch_resid<kBf16>(p, tb * q.bn + c, row.n);
+      }
+      constexpr int kChunks = kSegs ? kSegMaxBN / 16 / G : 1;
       float acc[kChunks][16];
       if constexpr (kSegs) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c][j] = 0.f;
         for (int sg = 0; sg + 1 < n_seg; ++sg, ++it) {
           const int buf = it & 1;
-          if (!(ok = wait_bar(&sm.acc_full[buf], (it >> 1) & 1, &sm.abort, status))) break;
+          if (!(ok = wait_inline(&sm.acc_full[buf], (it >> 1) & 1, &sm.abort, status))) break;
           tc_fence_after();
-          const uint32_t col = tmem + lane_base + buf * acc_cols + c_lo;
+          const uint32_t col = tmem + lane_base + buf * acc_cols;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            if (c * 16 < c_n) {
+            if (col_of(c) < q.bn) {
               float v[16];
-              tmem_ld16(col + c * 16, v);
+              tmem_ld16(col + col_of(c), v);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) acc[c][j] = sg > 0 ? acc[c][j] + v[j] : v[j];
+              for (int j = 0; j < 16; ++j) acc[c][j] += v[j];
             }
           }
           tc_fence_before();
@@ -358,30 +423,32 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
       }
       {
         const int buf = it & 1;
-        if (!(ok = wait_bar(&sm.acc_full[buf], (it >> 1) & 1, &sm.abort, status))) break;
+        if (!(ok = wait_inline(&sm.acc_full[buf], (it >> 1) & 1, &sm.abort, status))) break;
         tc_fence_after();
-        const uint32_t col = tmem + lane_base + buf * acc_cols + c_lo;
+        const uint32_t col = tmem + lane_base + buf * acc_cols;
         auto chunk = [&](int c, const float *more) {
           float v[16];
-          tmem_ld16(col + c * 16, v);
+          Resid<kSwiglu, kBf16, 16> res;
+          if constexpr (!kSplit) res.load(p, row, tb * q.bn + col_of(c));
+          tmem_ld16(col + col_of(c), v);
           if (more) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] += more[j];
           }
           if constexpr (kSplit) {
-            float *dst = reinterpret_cast<float *>(smem) + (c_lo + c * 16) * BM + quad * 32 + lane;
+            float *dst = reinterpret_cast<float *>(smem) + col_of(c) * BM + quad * 32 + lane;
 #pragma unroll
             for (int j = 0; j < 16; ++j) dst[j * BM] = v[j];
           } else {
-            finish_columns<kSwiglu>(p, row, v, tb * q.bn + c_lo + c * 16, 16);
+            finish_columns<kSwiglu, kBf16>(p, row, v, res, tb * q.bn + col_of(c), 16);
           }
         };
         if constexpr (kSegs) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
-            if (c * 16 < c_n) chunk(c, n_seg > 1 ? acc[c] : nullptr);
+            if (col_of(c) < q.bn) chunk(c, acc[c]);
         } else {
-          for (int c = 0; c * 16 < c_n; ++c) chunk(c, nullptr);
+          for (int c = 0; col_of(c) < q.bn; ++c) chunk(c, nullptr);
         }
         tc_fence_before();
         __syncwarp();
@@ -395,21 +462,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     __syncthreads();          // the roles are reconverged for the aligned barrier
     cluster_sync();           // every CTA's partial tile is in its shared memory
     if (warp >= kEpiWarp0 && !*reinterpret_cast<volatile int *>(&sm.abort)) {
-      const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
+      const int quad = warp & 3, turn = (warp - kEpiWarp0) >> 2;
       int fb, tb;
       tile_at(q, t_first, fb, tb);
       const LaneRow<kSwiglu> row = lane_row<kSwiglu>(p, fb, quad, lane);
       const int share = ((q.bn + ranks - 1) / ranks + 1) & ~1;   // columns per rank, even
       const int cols = min(share, q.bn - rank * share);
-      for (int c = half * 4; c < cols; c += 8) {
+      for (int c = turn * 4; c < cols; c += 4 * G) {
         const int n_cols = min(4, cols - c), col = rank * share + c;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
+        Resid<kSwiglu, kBf16, 4> res;
+        res.load(p, row, tb * q.bn + col);
         const uint32_t src = smem_u32(smem) + ((uint32_t)col * BM + quad * 32 + lane) * 4;
         for (int r = 0; r < ranks; ++r)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (j < n_cols) v[j] += ld_peer(src + j * BM * 4, r);
-        finish_columns<kSwiglu>(p, row, v, tb * q.bn + col, n_cols);
+        finish_columns<kSwiglu, kBf16>(p, row, v, res, tb * q.bn + col, n_cols);
       }
     }
     __syncthreads();
@@ -468,9 +537,9 @@ Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
   return best;
 }
 
-template <int DT, bool kSwiglu, bool kSplit, bool kSegs>
+template <int DT, bool kSwiglu, bool kSplit, bool kBf16>
 cudaError_t launch(const TcLinear &q, int grid, int split, int dev, cudaStream_t st) {
-  auto kernel = linear_tc_kernel<DT, kSwiglu, kSplit, kSegs>;
+  auto kernel = linear_tc_kernel<DT, kSwiglu, kSplit, kBf16>;
   // The shared-memory limit is raised once per device.
   static std::atomic<unsigned long long> ready{0};
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
@@ -487,7 +556,7 @@ cudaError_t launch(const TcLinear &q, int grid, int split, int dev, cudaStream_t
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<kBf16>);
   cfg.dynamicSmemBytes = (size_t)q.stages * (BM + q.bn) * kRowBytes + 1024;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -495,19 +564,20 @@ cudaError_t launch(const TcLinear &q, int grid, int split, int dev, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, q);
 }
 
-template <int DT, bool kSwiglu, bool kSegs>
+template <int DT, bool kSwiglu, bool kBf16>
 cudaError_t launch_split(const TcLinear &q, int sms, int split, int dev, cudaStream_t st) {
   const int tiles = q.n_fb * q.n_tb;
-  return split > 1 ? launch<DT, kSwiglu, true, kSegs>(q, tiles * split, split, dev, st)
-                   : launch<DT, kSwiglu, false, kSegs>(q, std::min(tiles, sms), 1, dev, st);
+  return split > 1 ? launch<DT, kSwiglu, true, kBf16>(q, tiles * split, split, dev, st)
+                   : launch<DT, kSwiglu, false, kBf16>(q, std::min(tiles, sms), 1, dev, st);
 }
 
 template <int DT>
-cudaError_t launch_type(const TcLinear &q, int sms, int split, bool segs, int dev, cudaStream_t st) {
+cudaError_t launch_type(const TcLinear &q, int sms, int split, int dev, cudaStream_t st) {
+  const bool bf = q.p.out_dtype == MOE_BF16;
   if (q.p.act == MOE_ACT_SWIGLU)
-    return segs ? launch_split<DT, true, true>(q, sms, split, dev, st)
+    return bf ? launch_split<DT, true, true>(q, sms, split, dev, st)
                 : launch_split<DT, true, false>(q, sms, split, dev, st);
-  return segs ? launch_split<DT, false, true>(q, sms, split, dev, st)
+  return bf ? launch_split<DT, false, true>(q, sms, split, dev, st)
               : launch_split<DT, false, false>(q, sms, split, dev, st);
 }
 
@@ -524,8 +594,7 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   TcLinear q;
   q.p = p;
   q.nkb = (p.K * es + kRowBytes - 1) / kRowBytes;
-  const bool segs = p.out_dtype == MOE_F32 && q.nkb > kSegBlocks;
-  const Plan plan = plan_of(p.T, rows, q.nkb, sms, segs ? kSegMaxBN : kMaxBN);
+  const Plan plan = plan_of(p.T, rows, q.nkb, sms, p.out_dtype == MOE_F32 ? kSegMaxBN : kMaxBN);
   q.bn = plan.bn;
   q.n_fb = (rows + BM - 1) / BM;
   q.n_tb = (p.T + q.bn - 1) / q.bn;
@@ -541,8 +610,8 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   }
   if (!make_map(&q.map_x, p.x, dt, es, p.K, p.T, p.ldx, kRowBytes / es, q.bn))
     return cudaErrorInvalidValue;
-  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, sms, plan.split, segs, dev, st)
-                           : launch_type<MOE_E4M3>(q, sms, plan.split, segs, dev, st);
+  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, sms, plan.split, dev, st)
+                           : launch_type<MOE_E4M3>(q, sms, plan.split, dev, st);
 }
 
 }  // namespace moe
