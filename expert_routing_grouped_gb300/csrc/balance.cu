@@ -14,16 +14,17 @@
 // Counts are integers; every floating sum runs in a fixed order: rows of a
 // chunk by warp, warps of a block, chunks of a segment.
 //
-// Three kernels, chained by programmatic dependent launch:
-//   count   a cluster per segment: histograms in shared memory, added across
-//           the cluster (no zeroing, no global atomics);
-//   pass    a block per chunk of consecutive tokens; its first rows of z are
-//           on their way before it waits for the counts, and without a
-//           gradient it waits only at its end;
-//   finish  a cluster per segment: P and the loss from the chunks' sums.
+// Up to three kernels, chained by programmatic dependent launch:
+//   count   (gradient only) a block per long chunk of consecutive tokens: a
+//           histogram in shared memory for each segment that it meets;
+//   pass    a block per short chunk; its first rows of z are on their way
+//           before it waits for the histograms.  Without a gradient it counts
+//           its own tokens and there is no count kernel;
+//   finish  a cluster per segment: counts, P and the loss from the partials.
 // Chunk c and segment s meet in at most one run of tokens, and along the
 // tokens both only grow, so c + s names each meeting once: a block writes its
-// partial sums of a segment to slot c + s, and no slot has two writers.
+// partials of a segment to slot c + s, and no slot has two writers.  Nothing
+// needs clearing before a call, and no atomic leaves a block.
 //
 // Up to kSmallElems logits one kernel does all three steps, a cluster per
 // segment with cluster barriers between them: there the launches are the time.
@@ -36,8 +37,8 @@ namespace {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBalBlocks = 608;          // most chunks of a call: 4 blocks on each of 152 SMs
-constexpr int kCountThreads = 512;
+constexpr int kBalBlocks = 456;          // most chunks of a call: 3 blocks on each of 152 SMs
+constexpr int kCountThreads = 1024;
 constexpr int kCluster = 8;
 constexpr long long kSmallElems = 1 << 18;
 
@@ -53,9 +54,12 @@ struct BalParams {
   int32_t *tokens;            // [S]
   float *prob;                // [S][E]
   void *dz;                   // [T][E] or nullptr
-  float *part;                // [chunks + S][E] partial sums of p
+  float *part;                // [chunks + S][E4] partial sums of p
+  int32_t *cnt;               // [count chunks + S][E4 + 4] partial counts, kept tokens at E4
   long long ldz, lddz;
-  int T, E, k, S, chunk;      // chunk: tokens per block
+  int T, E, k, S;
+  int E4;                     // E rounded up to 4: whole 16-byte pieces
+  int chunk, cchunk;          // tokens per block of the pass, and of what counts
   int idx_vec;                // idx rows are whole 16-byte pieces
   float alpha;
 };
@@ -142,23 +146,71 @@ __device__ __forceinline__ void count_rows(const BalParams &p, int a, int b, int
   if ((threadIdx.x & 31) == 0 && kept) atomicAdd(&hist[p.E], kept);
 }
 
-// One cluster per segment.
+// The histogram of tokens [a, b) of segment s into slot blockIdx.x + s, by the
+// whole block; hist[E + 1] is shared memory.
+__device__ __forceinline__ void count_chunk(const BalParams &p, int s, int a, int b, int32_t *hist) {
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  count_rows(p, a, b, threadIdx.x, blockDim.x, hist);
+  __syncthreads();
+  int32_t *dst = p.cnt + (size_t)(blockIdx.x + s) * (p.E4 + 4);
+  for (int e = threadIdx.x; e < p.E4; e += blockDim.x) dst[e] = e < p.E ? hist[e] : 0;
+  if (threadIdx.x == 0) dst[p.E4] = hist[p.E];
+}
+
+// Calls f(s, a, b) for every segment s and its tokens [a, b) inside [t0, t1).
+template <class F>
+__device__ __forceinline__ void each_segment(const BalParams &p, int t0, int t1, F f) {
+  for (int at = t0; at < t1;) {
+    const int s = seg_of(p, at);
+    if (s >= p.S) break;
+    const int a = max(at, seg_begin(p, s)), b = min(t1, seg_end(p, s));
+    if (a >= t1) break;
+    at = b;                                  // past `at`: the segment ends after it
+    if (a < b) f(s, a, b);
+  }
+}
+
 __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const BalParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int32_t hist[kMaxExperts + 1];
-  const int ranks = cluster_size(), rank = cluster_rank(), s = blockIdx.x / ranks;
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
+  const int t0 = blockIdx.x * p.cchunk, t1 = min(p.T, t0 + p.cchunk);
+  each_segment(p, t0, t1, [&](int s, int a, int b) {
+    count_chunk(p, s, a, b, hist);
+    __syncthreads();
+  });
+}
+
+// The slots that hold segment s's partial counts: first and past the last.
+__device__ __forceinline__ int2 count_slots(const BalParams &p, int s) {
+  const int a = seg_begin(p, s), b = seg_end(p, s);
+  const int c0 = a / p.cchunk;
+  return make_int2(c0 + s, a < b ? (b - 1) / p.cchunk + 1 + s : c0 + s);
+}
+
+// Segment s's counts added up into sum[E4 + 4] (shared memory, kept tokens at
+// E4) by the whole block: a warp per slot, integer atomics.
+__device__ __forceinline__ void total_counts(const BalParams &p, int s, int32_t *sum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  for (int e = threadIdx.x; e < p.E4 + 4; e += blockDim.x) sum[e] = 0;
   __syncthreads();
-  count_rows(p, seg_begin(p, s), seg_end(p, s), rank * blockDim.x + threadIdx.x, ranks * blockDim.x,
-             hist);
-  cluster_sync();
-  for (int e = rank + ranks * threadIdx.x; e <= p.E; e += ranks * blockDim.x) {
-    int c = 0;
-    for (int r = 0; r < ranks; ++r) c += (int)ld_peer(&hist[e], r);
-    if (e < p.E) p.counts[(size_t)s * p.E + e] = c;
-    else p.tokens[s] = c;
+  const int2 sl = count_slots(p, s);
+  const int row = p.E4 + 4;
+  for (int e = 4 * lane; e <= p.E4; e += 128) {   // the piece at E4: kept tokens, rest unused
+    int4 c = make_int4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int i = sl.x + warp; i < sl.y; i += nw) {
+      const int4 v = __ldcg(reinterpret_cast<const int4 *>(p.cnt + (size_t)i * row + e));
+      c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
+    }
+    if (c.x) atomicAdd(&sum[e], c.x);
+    if (e < p.E4) {
+      if (c.y) atomicAdd(&sum[e + 1], c.y);
+      if (c.z) atomicAdd(&sum[e + 2], c.z);
+      if (c.w) atomicAdd(&sum[e + 3], c.w);
+    }
   }
-  cluster_sync();   // no CTA leaves while a peer reads its histogram
+  __syncthreads();
 }
 
 // -------------------------------------------------------------- one token --
@@ -247,83 +299,113 @@ struct Lay {
 //
 // The mean taken off the counts cancels in a_i - sum_e p_e a_e, and small
 // differences keep their digits.
-template <class L>
+//
+// expf is the hardware one (2 units and |z| 2^-24) and the reciprocal good to
+// a unit: p is a sum's share, held in f32.
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+template <class L, bool kGrad>
 __device__ __forceinline__ void one_token(const BalParams &p, const typename L::Raw &raw, int t,
                                           bool valid, bool write, const float *bias,
                                           const float *coef, float scale, float (&acc)[L::NE]) {
-  float v[L::NE], om[L::NE];
+  float v[L::NE], om[L::kSig && kGrad ? L::NE : 1];
   float tot = 0.f;
   if constexpr (L::kSig) {
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      // 1 - sigmoid is taken as exp(-z) sigmoid, which keeps its digits where
-      // the sigmoid is near 1.  The quotient is the fast one (2 units): p is
-      // a sum's share, so f32 rounding is what counts.
-      const float ex = expf(-L::get(raw, j));
-      const float sg = __fdividef(1.0f, 1.0f + ex);
-      const bool in = L::first(j / L::VEC) + j % L::VEC < p.E;
-      v[j] = in && !(ex > 8e37f) ? sg : 0.f;   // below 2^-126: 0
-      om[j] = ex > 8e37f ? 1.0f : ex * sg;
+      const float ex = __expf(-L::get(raw, j));
+      const float sg = rcp_fast(1.0f + ex);   // 0 from 2^126 on
+      v[j] = L::first(j / L::VEC) < p.E ? sg : 0.f;
+      // 1 - sigmoid keeps its digits as exp(-z) sigmoid where the sigmoid is
+      // near 1.
+      if constexpr (kGrad) om[j] = ex < 1.0f ? ex * sg : 1.0f - sg;
       tot += v[j];
     }
   } else {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      const int e = L::first(j / L::VEC) + j % L::VEC;
-      const bool in = e < p.E;
+      const bool in = L::first(j / L::VEC) < p.E;
       v[j] = in ? L::get(raw, j) : -INFINITY;
-      if (bias && in) v[j] += bias[e];
+      if (bias && in) v[j] += bias[L::first(j / L::VEC) + j % L::VEC];
       m = fmaxf(m, v[j]);
     }
     m = L::max(m);
     if (m == -INFINITY) m = 0.f;   // a row with nothing left: p = 0
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      v[j] = expf(v[j] - m);
+      v[j] = __expf(v[j] - m);
       tot += v[j];
     }
   }
   tot = L::sum(tot);
+  // A token that is not there or masked has raw 0: its p is 0 from here on.
   const float inv = valid ? (tot == 0.f ? 0.f : 1.0f / tot) : 0.f;
   float dot = 0.f;
 #pragma unroll
   for (int j = 0; j < L::NE; ++j) {
-    v[j] *= inv;
-    acc[j] += valid ? v[j] : 0.f;
+    v[j] = __fmul_rn(v[j], inv);   // not fused into the sum: the same bits with and without dz
+    acc[j] += v[j];
+    if constexpr (kGrad) dot = fmaf(v[j], coef[L::first(j / L::VEC) + j % L::VEC], dot);
   }
-  if (!coef) return;
+  if constexpr (kGrad) {
+    dot = L::sum(dot);
 #pragma unroll
-  for (int j = 0; j < L::NE; ++j)
-    dot = fmaf(v[j], coef[L::first(j / L::VEC) + j % L::VEC], dot);
-  dot = L::sum(dot);
-#pragma unroll
-  for (int j = 0; j < L::NE; ++j) {
-    float d = scale * v[j] * (coef[L::first(j / L::VEC) + j % L::VEC] - dot);
-    if constexpr (L::kSig) d *= om[j];
-    v[j] = valid ? d : 0.f;
+    for (int j = 0; j < L::NE; ++j) {
+      float d = scale * v[j] * (coef[L::first(j / L::VEC) + j % L::VEC] - dot);
+      if constexpr (L::kSig) d *= om[j];
+      v[j] = d;
+    }
+    if (write) L::store(p, t, v);
   }
-  if (write) L::store(p, t, v);
 }
 
-// Rows [a, b), rows a + w0 .. in steps of the warps' rows, into acc; one row's
-// load runs ahead of the row at work.
+// A warp's rows first, first + step, .. below b, with the loads of kAhead steps
+// under way: enough bytes in flight to cover the memory's latency where a
+// lane's share is short.
 template <class L>
 struct Rows {
   static constexpr int RPW = 32 / L::LPR;   // rows per warp and step
-  typename L::Raw next;
-  int t;
-  bool valid;
-  __device__ __forceinline__ void fetch(const BalParams &p, int row, int b) {
-    t = row + (int)(threadIdx.x & 31) / L::LPR;
-    valid = t < b && (!p.mask || p.mask[t]);
-    L::load(p, t, valid, next);
+  static constexpr int kAhead = L::NE <= 8 ? 3 : L::NE <= 16 ? 2 : 1;
+  typename L::Raw raw[kAhead];
+  bool valid[kAhead];
+  static __device__ __forceinline__ int token(int row) {
+    return row + (int)(threadIdx.x & 31) / L::LPR;
+  }
+  __device__ __forceinline__ void fetch(const BalParams &p, int i, int row, int b) {
+    const int t = token(row);
+    valid[i] = t < b && (!p.mask || p.mask[t]);
+    L::load(p, t, valid[i], raw[i]);
+  }
+  __device__ __forceinline__ void start(const BalParams &p, int first, int step, int b) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(p, i, first + i * step, b);
+  }
+  template <bool kGrad>
+  __device__ __forceinline__ void run(const BalParams &p, int first, int step, int b, const float *bias,
+                                      const float *coef, float scale, float (&acc)[L::NE]) {
+    for (int row0 = first; row0 < b; row0 += kAhead * step) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int row = row0 + i * step;
+        if (row < b) {
+          const typename L::Raw now = raw[i];
+          const bool ok = valid[i];
+          fetch(p, i, row + kAhead * step, b);
+          const int t = token(row);
+          one_token<L, kGrad>(p, now, t, ok, t < b, bias, coef, scale, acc);
+        }
+      }
+    }
   }
 };
 
 // Shared memory of a block of the pass: the warps' sums, the coefficients and
 // the bias, each over the padded experts of the layout.
-template <class L>
 __device__ __forceinline__ void stage_bias(const BalParams &p, float *bias) {
   if (p.bias)
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) bias[e] = __ldg(p.bias + e);
@@ -349,55 +431,46 @@ __device__ __forceinline__ void warp_sums(float (&acc)[L::NE], float *sums) {
 
 // -------------------------------------------------------------- main pass --
 
-template <class L>
-__global__ void __launch_bounds__(kBalThreads) balance_pass_kernel(const BalParams p) {
+template <class L, bool kGrad>
+__global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_pass_kernel(const BalParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int EP = L::NE * L::LPR;   // experts of the layout, >= E
   __shared__ float sums[kBalWarps * EP];
-  __shared__ float coef[EP], bias[EP];
+  __shared__ float coef[kGrad ? EP : 1], bias[EP];
+  int32_t *ints = reinterpret_cast<int32_t *>(sums);   // counts, before sums holds anything
   const int warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   constexpr int kStep = kBalWarps * Rows<L>::RPW;
   bool waited = false;
-  stage_bias<L>(p, bias);
-  for (int at = t0; at < t1;) {
-    const int s = seg_of(p, at);
-    if (s >= p.S) break;
-    const int a = max(at, seg_begin(p, s)), b = min(t1, seg_end(p, s));
-    if (a >= t1) break;
-    at = b;                                  // past `at`: the segment ends after it
-    if (a >= b) continue;
+  if (!L::kSig) stage_bias(p, bias);
+  each_segment(p, t0, t1, [&](int s, int a, int b) {
     const int first = a + warp * Rows<L>::RPW;
     Rows<L> rows;
-    rows.fetch(p, first, b);
+    rows.start(p, first, kStep, b);
     float scale = 0.f;
-    if (p.dz) {
+    if constexpr (kGrad) {
       if (!waited) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // the counts
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial counts
         waited = true;
       }
-      const int32_t *counts = p.counts + (size_t)s * p.E;
-      scale = grad_scale(p, s, __ldcg(p.tokens + s));
+      total_counts(p, s, ints);
+      scale = grad_scale(p, s, ints[p.E4]);
       int sum = 0;   // every warp for itself: all assignments of the segment
-      for (int e = threadIdx.x & 31; e < p.E; e += 32) sum += __ldcg(counts + e);
+      for (int e = threadIdx.x & 31; e < p.E; e += 32) sum += ints[e];
       const float mean = (float)__reduce_add_sync(0xffffffffu, sum) / (float)p.E;
       for (int e = threadIdx.x; e < EP; e += blockDim.x)
-        coef[e] = e < p.E ? (float)__ldcg(counts + e) - mean : 0.f;
+        coef[e] = e < p.E ? (float)ints[e] - mean : 0.f;
+    } else {
+      count_chunk(p, s, a, b, ints);
     }
     __syncthreads();
     float acc[L::NE];
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) acc[j] = 0.f;
-    for (int row = first; row < b; row += kStep) {
-      const typename L::Raw raw = rows.next;
-      const int t = rows.t;
-      const bool valid = rows.valid;
-      rows.fetch(p, row + kStep, b);
-      one_token<L>(p, raw, t, valid, t < b, p.bias ? bias : nullptr, p.dz ? coef : nullptr, scale, acc);
-    }
+    rows.template run<kGrad>(p, first, kStep, b, p.bias ? bias : nullptr, coef, scale, acc);
     warp_sums<L>(acc, sums);
     __syncthreads();
-    float *dst = p.part + (size_t)(blockIdx.x + s) * p.E;
+    float *dst = p.part + (size_t)(blockIdx.x + s) * p.E4;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
       float tsum = 0.f;
 #pragma unroll
@@ -405,9 +478,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_pass_kernel(const BalPara
       dst[e] = tsum;
     }
     __syncthreads();
-  }
+  });
   // The finish kernel waits for this grid alone: leave only after the counts.
-  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kGrad && !waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // -------------------------------------------------------------- finish ----
@@ -443,28 +516,47 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float part[32][33];
   __shared__ float red[32], slot;
+  __shared__ int32_t counts[32], kept;
   const int ranks = cluster_size(), rank = cluster_rank(), s = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int a = seg_begin(p, s), b = seg_end(p, s);
   const int c0 = a / p.chunk, c1 = a < b ? (b - 1) / p.chunk + 1 : c0;
-  const int n = __ldcg(p.tokens + s);
+  const int2 sl = count_slots(p, s);
+  const int row = p.E4 + 4;
+  if (threadIdx.x == 0) kept = 0;
+  __syncthreads();
+  int n = 0;
+  for (int i = sl.x + (int)threadIdx.x; i < sl.y; i += blockDim.x)
+    n += __ldcg(p.cnt + (size_t)i * row + p.E4);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0 && n) atomicAdd(&kept, n);
+  __syncthreads();
+  n = kept;
   const float inv = n > 0 ? 1.0f / (float)n : 0.f;
+  if (rank == 0 && threadIdx.x == 0) p.tokens[s] = n;
   float dot = 0.f;
   for (int e0 = rank * 32; e0 < p.E; e0 += ranks * 32) {
     const int e = e0 + lane;
+    if (warp == 0) counts[lane] = 0;
+    __syncthreads();
     float sum = 0.f;
+    int c = 0;
     if (e < p.E) {
-#pragma unroll 8
-      for (int c = c0 + warp; c < c1; c += nw) sum += __ldcg(p.part + (size_t)(c + s) * p.E + e);
+#pragma unroll 10
+      for (int i = c0 + warp; i < c1; i += nw) sum += __ldcg(p.part + (size_t)(i + s) * p.E4 + e);
+#pragma unroll 10
+      for (int i = sl.x + warp; i < sl.y; i += nw) c += __ldcg(p.cnt + (size_t)i * row + e);
     }
     part[warp][lane] = sum;
+    if (c) atomicAdd(&counts[lane], c);
     __syncthreads();
     if (warp == 0 && e < p.E) {
       float tot = 0.f;
       for (int w = 0; w < nw; ++w) tot += part[w][lane];
       tot *= inv;
       p.prob[(size_t)s * p.E + e] = tot;
-      dot = fmaf((float)__ldcg(p.counts + (size_t)s * p.E + e), tot, dot);
+      p.counts[(size_t)s * p.E + e] = counts[lane];
+      dot = fmaf((float)counts[lane], tot, dot);
     }
     __syncthreads();
   }
@@ -474,7 +566,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p)
 // ---------------------------------------------------------- small batches --
 
 template <class L>
-__global__ void __launch_bounds__(kBalThreads) balance_small_kernel(const BalParams p) {
+__global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small_kernel(const BalParams p) {
   constexpr int EP = L::NE * L::LPR;
   __shared__ float sums[kBalWarps * EP];
   __shared__ float coef[EP], bias[EP];
@@ -488,8 +580,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_small_kernel(const BalPar
   constexpr int kStep = kBalWarps * Rows<L>::RPW;
   const int first = a + (rank * kBalWarps + warp) * Rows<L>::RPW;
   Rows<L> rows;
-  rows.fetch(p, first, b);
-  stage_bias<L>(p, bias);
+  rows.start(p, first, ranks * kStep, b);
+  if (!L::kSig) stage_bias(p, bias);
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
   if (threadIdx.x == 0) total = 0;
   __syncthreads();
@@ -517,13 +609,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_small_kernel(const BalPar
   float acc[L::NE];
 #pragma unroll
   for (int j = 0; j < L::NE; ++j) acc[j] = 0.f;
-  for (int row = first; row < b; row += ranks * kStep) {
-    const typename L::Raw raw = rows.next;
-    const int t = rows.t;
-    const bool valid = rows.valid;
-    rows.fetch(p, row + ranks * kStep, b);
-    one_token<L>(p, raw, t, valid, t < b, p.bias ? bias : nullptr, p.dz ? coef : nullptr, scale, acc);
-  }
+  const float *sb = p.bias ? bias : nullptr;
+  if (p.dz) rows.template run<true>(p, first, ranks * kStep, b, sb, coef, scale, acc);
+  else rows.template run<false>(p, first, ranks * kStep, b, sb, coef, scale, acc);
   warp_sums<L>(acc, sums);
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
@@ -570,6 +658,13 @@ int balance_chunk(int T) {
   return std::max(32, (T + kBalBlocks - 1) / kBalBlocks);
 }
 
+// Tokens per histogram: what a block of the pass has when it counts for itself;
+// the count kernel's blocks take 2048, or more to stay at 128 blocks (each
+// block of the pass reads every histogram of its segment).
+int balance_count_chunk(int T, bool grad) {
+  return grad ? std::max(2048, (T + 127) / 128) : balance_chunk(T);
+}
+
 bool is_small(int T, int E) { return (long long)T * E <= kSmallElems; }
 
 template <class L>
@@ -584,10 +679,15 @@ cudaError_t launch_layout(const BalParams &p, cudaStream_t st) {
     return launch_cluster(false, balance_small_kernel<L>, p.S * ranks, kBalThreads, ranks, st, p);
   }
   const int chunks = (p.T + p.chunk - 1) / p.chunk;
-  cudaError_t err =
-      launch_cluster(false, balance_count_kernel, p.S * kCluster, kCountThreads, kCluster, st, p);
-  if (err == cudaSuccess)
-    err = launch_k(true, balance_pass_kernel<L>, dim3(chunks), dim3(kBalThreads), 0, st, p);
+  cudaError_t err = cudaSuccess;
+  if (p.dz) {
+    err = launch_k(false, balance_count_kernel, dim3((p.T + p.cchunk - 1) / p.cchunk),
+                   dim3(kCountThreads), 0, st, p);
+    if (err == cudaSuccess)
+      err = launch_k(true, balance_pass_kernel<L, true>, dim3(chunks), dim3(kBalThreads), 0, st, p);
+  } else {
+    err = launch_k(false, balance_pass_kernel<L, false>, dim3(chunks), dim3(kBalThreads), 0, st, p);
+  }
   // A warp of the finish kernel for every few chunks of a segment.
   const int per = (chunks + p.S - 1) / p.S;
   const int threads = std::min(1024, std::max(64, (per / 4 + 1) * 32));
@@ -620,9 +720,10 @@ extern "C" __attribute__((visibility("default"))) size_t moe_balance_workspace(i
                                                                               int n_seq) {
   using namespace moe;
   if (T < 1 || num_experts < 1 || num_experts > kMaxExperts || n_seq < 1) return 0;
+  // Partial sums of p, and partial counts in the form that has more of them.
   const int chunk = balance_chunk(T);
-  const size_t slots = (size_t)(T + chunk - 1) / chunk + n_seq;
-  return slots * num_experts * sizeof(float);
+  const size_t slots = (size_t)(T + chunk - 1) / chunk + n_seq, E4 = (num_experts + 3) / 4 * 4;
+  return slots * (2 * E4 + 4) * sizeof(float);
 }
 
 extern "C" __attribute__((visibility("default"))) int moe_balance_loss(
@@ -652,7 +753,8 @@ extern "C" __attribute__((visibility("default"))) int moe_balance_loss(
         reinterpret_cast<uintptr_t>(seq_off) | reinterpret_cast<uintptr_t>(grad) |
         reinterpret_cast<uintptr_t>(loss) | reinterpret_cast<uintptr_t>(counts) |
         reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(prob) |
-        reinterpret_cast<uintptr_t>(workspace)) & 3))
+        0) & 3) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 15))
     return MOE_ERR_ARG;
   // What the kernels write is apart from everything else that the call
   // touches; dz may be z itself (a row is read whole before it is written).
@@ -687,8 +789,9 @@ extern "C" __attribute__((visibility("default"))) int moe_balance_loss(
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   BalParams p{z, router_mode == 1 ? nullptr : bias, idx, mask, seq_off, grad, loss, counts, tokens,
-              prob, dz, static_cast<float *>(workspace), ldz, lddz, T, E, top_k, n_seq,
-              balance_chunk(T), top_k % 4 == 0 && !(reinterpret_cast<uintptr_t>(idx) & 15), alpha};
+              prob, dz, static_cast<float *>(workspace), nullptr, ldz, lddz, T, E, top_k, n_seq,
+              (E + 3) / 4 * 4, balance_chunk(T), balance_count_chunk(T, dz != nullptr), top_k % 4 == 0 && !(reinterpret_cast<uintptr_t>(idx) & 15), alpha};
+  p.cnt = reinterpret_cast<int32_t *>(p.part + ((size_t)(T + p.chunk - 1) / p.chunk + n_seq) * p.E4);
   const long long v = z_dtype == MOE_F32 ? 4 : 8;
   const bool vec = E % v == 0 && ldz % v == 0 && !(reinterpret_cast<uintptr_t>(z) & 15) &&
                    (!dz || (lddz % v == 0 && !(reinterpret_cast<uintptr_t>(dz) & 15)));

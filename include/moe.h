@@ -424,7 +424,8 @@ int moe_linear(const void *x, const float *x_scale, const void *w, const float *
  *   dz       [T][E] of z's type, row stride dz_stride, or NULL (no gradient);
  *            may be z itself (the same stride)
  *   workspace  at least moe_balance_workspace(T, num_experts, n_seq) bytes,
- *            not shared with a call that may overlap this one
+ *            16-byte aligned, not shared with a call that may overlap this one;
+ *            nothing in it needs clearing
  * A row whose logits are all -infinity (in mode 1: whose sigmoids are all
  * below 2^-126) has p = 0.  num_experts <= 1024, top_k
  * <= 32, T * top_k <= 2^26, n_seq <= 65535.  Loss and gradient together read z
