@@ -17,11 +17,21 @@
 // accumulator is handed over every kSegBlocks K blocks and the epilogue adds
 // the segments in f32 to nearest, in registers.
 //
-// Few tiles (short batches, narrow outputs) leave SMs idle, so K is split over
-// a cluster of 2 to 8 CTAs: each writes its partial tile to its own shared
-// memory, and after a cluster barrier each finishes its share of the columns,
-// reading the peers' partials over distributed shared memory in rank order --
-// no workspace, no atomics, the same bits on every call.
+// Three forms (kMode):
+//   pair   large products: two CTAs on neighbouring SMs form one 256-row tile
+//          (cta_group::2): each loads its 128 rows of w and half of the
+//          tokens, and the leader's MMAs read both halves, so a K block costs
+//          each SM (128 + BN / 2) rows of operand traffic in place of
+//          128 + BN -- what bounds the solo form: 0.00091 us a row;
+//   solo   one CTA per tile;
+//   split  few tiles (short batches, narrow outputs): K is split over a cluster
+//          of 2 to 8 CTAs; each writes its partial tile to its own shared
+//          memory, and after a cluster barrier each finishes its share of the
+//          columns, reading the peers' partials over distributed shared memory
+//          in rank order -- no workspace, no atomics, the same bits on every
+//          call.
+// The tokens are cut into n_tb nearly equal tiles (a difference of one unit of
+// 16, in pairs 32), so that the tiles fill whole waves of the SMs.
 //
 // Every mbarrier wait is bounded: one that gives up sets the status word, and
 // the roles stop, drain their copies and MMAs, and return.
@@ -52,12 +62,16 @@ template <bool kBf16>
 constexpr int kThreads = (kEpiWarp0 + 4 * kEpiGroups<kBf16>) * 32;
 constexpr size_t kSmemMax = 227 * 1024;
 
+enum Mode { kSolo, kPair, kSplit };
+
 struct TcLinear {
   CUtensorMap map_w;       // [rows][K], box 128 x 128 bytes; SwiGLU: [N/16][2][16][K]
-  CUtensorMap map_x;       // [T][K], box BN x 128 bytes
+  CUtensorMap map_x;       // [T][K], box of a CTA's tokens x 128 bytes
   LinearParams p;
-  int bn;                  // tokens per tile, a multiple of 32
-  int n_fb, n_tb;          // tiles along the outputs and the tokens
+  int unit, units;         // tokens come in `units` units of 16 (pairs: 32)
+  int bn;                  // most tokens of a tile
+  int x_rows;              // tokens a CTA loads per tile (bn, in pairs bn / 2)
+  int n_fb, n_tb;          // tiles along the outputs (in pairs: of 256 rows) and the tokens
   int group_tb;            // token tiles per raster group
   int nkb;                 // K blocks of the whole product
   int stages;
@@ -73,34 +87,84 @@ struct Bars {
 };
 
 template <int DT>
-__device__ __forceinline__ uint32_t linear_idesc(int n) {
+__device__ __forceinline__ uint32_t linear_idesc(int m, int n) {
   // kind::f8f6f4: format fields 0 = e4m3 for A and B, f32 accumulator
-  if constexpr (DT == MOE_BF16) return idesc_bf16(BM, n);
-  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+  if constexpr (DT == MOE_BF16) return idesc_bf16(m, n);
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-template <int DT>
+#define MOE_LINEAR_MMA(GROUP, KIND)                                                       \
+  asm volatile(                                                                           \
+      "{\n\t.reg .pred p;\n\t"                                                            \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                         \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d), \
+      "l"(da), "l"(db), "r"(idesc), "r"(acc)                                              \
+      : "memory")
+template <int DT, int kMode>
 __device__ __forceinline__ void linear_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
                                            uint32_t acc) {
   if constexpr (DT == MOE_BF16) {
-    mma_bf16(d, da, db, idesc, acc);
+    if constexpr (kMode == kPair) MOE_LINEAR_MMA("2", "f16");
+    else MOE_LINEAR_MMA("1", "f16");
   } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(da), "l"(db), "r"(idesc), "r"(acc)
-        : "memory");
+    if constexpr (kMode == kPair) MOE_LINEAR_MMA("2", "f8f6f4");
+    else MOE_LINEAR_MMA("1", "f8f6f4");
   }
 }
+#undef MOE_LINEAR_MMA
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z,
-                                            int w, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
+// Arrives on `bar` when the MMAs issued so far are done; in pairs on the
+// barrier at the same place in both CTAs.
+template <int kMode>
+__device__ __forceinline__ void linear_commit(uint64_t *bar) {
+  if constexpr (kMode == kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    mma_commit(bar);
+}
+
+// The address of p in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+
+// TMA loads into this CTA's shared memory; in pairs the bytes are counted on
+// the leader's barrier (`bar` its cluster address).
+template <int kMode>
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  if constexpr (kMode == kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int kMode>
+__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x, int w, uint32_t bar) {
+  if constexpr (kMode == kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(w), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(w), "r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -120,14 +184,23 @@ __device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// Token tiles run fastest within groups of group_tb, so the CTAs of a wave
-// share few w and x tiles and both stay in L2.
-__device__ __forceinline__ void tile_at(const TcLinear &q, int t, int &fb, int &tb) {
+// Tile t of the raster: output tile fb, tokens c0 .. c0 + w - 1.  Token tiles
+// run fastest within groups of group_tb, so the CTAs of a wave share few w and
+// x tiles and both stay in L2.
+struct Tile {
+  int fb, c0, w;
+};
+__device__ __forceinline__ Tile tile_at(const TcLinear &q, int t) {
   const int per = q.group_tb * q.n_fb;
   const int g = t / per, r = t - g * per;
   const int width = min(q.group_tb, q.n_tb - g * q.group_tb);
-  fb = r / width;
-  tb = g * q.group_tb + (r - fb * width);
+  Tile tl;
+  tl.fb = r / width;
+  const int tb = g * q.group_tb + (r - tl.fb * width);
+  const int u0 = (int)((long long)q.units * tb / q.n_tb);
+  tl.c0 = u0 * q.unit;
+  tl.w = (int)((long long)q.units * (tb + 1) / q.n_tb) * q.unit - tl.c0;
+  return tl;
 }
 
 // One lane's accumulator column block: W values of columns (tokens) t0 ..,
@@ -247,13 +320,13 @@ __device__ __forceinline__ bool wait_inline(uint64_t *bar, uint32_t parity, int 
   }
 }
 
-// kSplit: one tile per cluster, its K split over the CTAs; otherwise a
-// persistent CTA per SM walks the tiles.
+// A persistent CTA (pair) walks the tiles; kSplit: one tile per cluster.
 // kBf16: the output type; f32 output sums K in segments.
-template <int DT, bool kSwiglu, bool kSplit, bool kBf16>
+template <int DT, bool kSwiglu, int kMode, bool kBf16>
 __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __grid_constant__ TcLinear q) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars sm;
+  // Pairs: the buffers lie at the same place in both CTAs (the same launch).
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -262,9 +335,14 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
   constexpr bool kSegs = !kBf16;
   constexpr int G = kEpiGroups<kBf16>;
   constexpr int kBlockElems = kRowBytes / (DT == MOE_BF16 ? 2 : 1);
-  const uint32_t stage_bytes = (BM + q.bn) * kRowBytes;
+  const uint32_t stage_bytes = (BM + q.x_rows) * kRowBytes;
   const uint32_t acc_cols = q.bn <= 32 ? 32 : q.bn <= 64 ? 64 : q.bn <= 128 ? 128 : 256;
   const int S = q.stages;
+  int ranks = 1, rank = 0;
+  if constexpr (kMode != kSolo) {
+    asm volatile("mov.u32 %0, %cluster_nctarank;" : "=r"(ranks));
+    rank = cluster_rank();
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -273,36 +351,43 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.acc_full[i], 1);
-      mbar_init(&sm.acc_empty[i], 4 * G);
+      mbar_init(&sm.acc_empty[i], (kMode == kPair ? 2 : 1) * 4 * G);
     }
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&sm.tmem_base)),
-                 "r"(2 * acc_cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (kMode == kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&sm.tmem_base)),
+                   "r"(2 * acc_cols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&sm.tmem_base)),
+                   "r"(2 * acc_cols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kMode == kPair) cluster_sync();   // the peer's barriers are ready too
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
   // This CTA's tiles and its share of K.
   const int n_tiles = q.n_fb * q.n_tb;
-  int ranks = 1, rank = 0;
-  if constexpr (kSplit) {
-    asm volatile("mov.u32 %0, %cluster_nctarank;" : "=r"(ranks));
-    rank = cluster_rank();
-  }
   const int t_first = blockIdx.x / ranks, t_step = gridDim.x / ranks;
-  const int kb0 = (int)((long long)q.nkb * rank / ranks);
-  const int kb1 = (int)((long long)q.nkb * (rank + 1) / ranks);
+  const int kb0 = kMode == kSplit ? (int)((long long)q.nkb * rank / ranks) : 0;
+  const int kb1 = kMode == kSplit ? (int)((long long)q.nkb * (rank + 1) / ranks) : q.nkb;
   const int n_seg = kSegs ? (kb1 - kb0 + kSegBlocks - 1) / kSegBlocks : 1;
   auto seg_at = [&](int s) { return kb0 + (int)((long long)(kb1 - kb0) * s / n_seg); };
+  // The 128-row block of w and the tokens that this CTA loads of a tile.
+  auto block_of = [&](const Tile &tl) { return kMode == kPair ? 2 * tl.fb + rank : tl.fb; };
+  auto x_row_of = [&](const Tile &tl) { return kMode == kPair ? tl.c0 + rank * (tl.w / 2) : tl.c0; };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -310,16 +395,20 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
     uint32_t ph = 0, armed = 0, par = 0;
     bool ok = true;
     for (int t = t_first; ok && t < n_tiles; t += t_step) {
-      int fb, tb;
-      tile_at(q, t, fb, tb);
+      const Tile tl = tile_at(q, t);
+      const int fb = block_of(tl), x_row = x_row_of(tl);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = wait_bar(&sm.empty[s], ph ^ 1, &sm.abort, status))) break;
         if (elect_one()) {
           uint8_t *a = smem + s * stage_bytes;
-          mbar_expect_tx(&sm.full[s], stage_bytes);
-          if constexpr (kSwiglu) tma_load_4d(a, &q.map_w, kb * kBlockElems, 0, 0, fb * 4, &sm.full[s]);
-          else tma_load_2d(a, &q.map_w, kb * kBlockElems, fb * BM, &sm.full[s]);
-          tma_load_2d(a + BM * kRowBytes, &q.map_x, kb * kBlockElems, tb * q.bn, &sm.full[s]);
+          uint32_t bar = smem_u32(&sm.full[s]);
+          if constexpr (kMode == kPair) bar = peer_addr(&sm.full[s], 0);
+          // The leader expects both CTAs' bytes.
+          if (kMode != kPair || rank == 0)
+            mbar_expect_tx(&sm.full[s], kMode == kPair ? 2 * stage_bytes : stage_bytes);
+          if constexpr (kSwiglu) load_4d<kMode>(a, &q.map_w, kb * kBlockElems, fb * 4, bar);
+          else load_2d<kMode>(a, &q.map_w, kb * kBlockElems, fb * BM, bar);
+          load_2d<kMode>(a + BM * kRowBytes, &q.map_x, kb * kBlockElems, x_row, bar);
         }
         __syncwarp();
         armed |= 1u << s;
@@ -330,19 +419,28 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
         }
       }
     }
-    // Every copy that was issued has landed before the CTA goes on.
+    // Every copy that was issued has landed before the CTA goes on.  A pair's
+    // second CTA cannot watch the leader's barriers: its copies are done when
+    // the leader's MMAs have read them; if it stopped early it gives them a
+    // millisecond.
     const unsigned long long t0 = globaltimer();
-    for (int i = 0; i < S; ++i)
-      if ((armed >> i) & 1) drain_bar(&sm.full[i], (par >> i) & 1, t0);
-  } else if (warp == 1) {
+    if (kMode != kPair || rank == 0) {
+      for (int i = 0; i < S; ++i)
+        if ((armed >> i) & 1) drain_bar(&sm.full[i], (par >> i) & 1, t0);
+    } else if (!ok) {
+      while (globaltimer() - t0 < 1000000ull) {
+      }
+    }
+  } else if (warp == 1 && (kMode != kPair || rank == 0)) {
     // ---------------------------------------------------------- MMA issuer
     int s = 0;
     uint32_t ph = 0, it = 0;
-    const uint32_t idesc = linear_idesc<DT>(q.bn);
     const uint64_t da0 = sw128_desc(smem_u32(smem));
     const uint32_t stage_desc = stage_bytes >> 4;
     bool ok = true;
     for (int t = t_first; ok && t < n_tiles; t += t_step) {
+      const Tile tl = tile_at(q, t);
+      const uint32_t idesc = linear_idesc<DT>(kMode == kPair ? 2 * BM : BM, tl.w);
       for (int sg = 0; ok && sg < n_seg; ++sg, ++it) {
         const int buf = it & 1;
         if (!(ok = wait_bar(&sm.acc_empty[buf], ((it >> 1) & 1) ^ 1, &sm.abort, status))) break;
@@ -357,8 +455,8 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
             const uint64_t db = da + ((BM * kRowBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              linear_mma<DT>(d, da + 2 * kk, db + 2 * kk, idesc, kb > ka || kk > 0);
-            mma_commit(&sm.empty[s]);
+              linear_mma<DT, kMode>(d, da + 2 * kk, db + 2 * kk, idesc, kb > ka || kk > 0);
+            linear_commit<kMode>(&sm.empty[s]);
           }
           __syncwarp();
           if (++s == S) {
@@ -367,13 +465,13 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
           }
         }
         if (!ok) break;
-        if (elect_one()) mma_commit(&sm.acc_full[buf]);
+        if (elect_one()) linear_commit<kMode>(&sm.acc_full[buf]);
         __syncwarp();
       }
     }
     // One more commit covers every MMA issued, also those of a tile that was
     // left in the middle; TMEM is freed only after it has arrived.
-    if (elect_one()) mma_commit(&sm.drain);
+    if (elect_one()) linear_commit<kMode>(&sm.drain);
     __syncwarp();
     drain_bar(&sm.drain, 0, globaltimer());
   } else if (warp >= kEpiWarp0) {
@@ -381,18 +479,29 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
     const int quad = warp & 3, turn = (warp - kEpiWarp0) >> 2;
     // Block c of this warp: columns (c G + turn) 16 .. + 15.
     auto col_of = [&](int c) { return (c * G + turn) * 16; };
+    auto release = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kMode == kPair)
+          asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+                           peer_addr(&sm.acc_empty[buf], 0))
+                       : "memory");
+        else
+          mbar_arrive(&sm.acc_empty[buf]);
+      }
+    };
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     uint32_t it = 0;
     bool ok = true;
     for (int t = t_first; ok && t < n_tiles; t += t_step) {
-      int fb, tb;
-      tile_at(q, t, fb, tb);
-      const LaneRow<kSwiglu> row = lane_row<kSwiglu>(p, fb, quad, lane);
-      if constexpr (!kSplit) {
+      const Tile tl = tile_at(q, t);
+      const LaneRow<kSwiglu> row = lane_row<kSwiglu>(p, block_of(tl), quad, lane);
+      if constexpr (kMode != kSplit) {
         // The tile's residual comes to L2 under the main loop.
         if (p.resid && row.ok)
-          for (int c = turn; c < q.bn; c += G)
-            if (tb * q.bn + c < p.T && (lane & 7) == 0) prefetch_resid<kBf16>(p, tb * q.bn + c, row.n);
+          for (int c = turn; c < tl.w; c += G)
+            if (tl.c0 + c < p.T && (lane & 7) == 0) prefetch_resid<kBf16>(p, tl.c0 + c, row.n);
       }
       constexpr int kChunks = kSegs ? kSegMaxBN / 16 / G : 1;
       float acc[kChunks][16];
@@ -408,96 +517,94 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
           const uint32_t col = tmem + lane_base + buf * acc_cols;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            if (col_of(c) < q.bn) {
+            if (col_of(c) < tl.w) {
               float v[16];
               tmem_ld16(col + col_of(c), v);
 #pragma unroll
               for (int j = 0; j < 16; ++j) acc[c][j] += v[j];
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
+          release(buf);
         }
         if (!ok) break;
       }
-      {
-        const int buf = it & 1;
-        if (!(ok = wait_inline(&sm.acc_full[buf], (it >> 1) & 1, &sm.abort, status))) break;
-        tc_fence_after();
-        const uint32_t col = tmem + lane_base + buf * acc_cols;
-        auto chunk = [&](int c, const float *more) {
-          float v[16];
-          Resid<kSwiglu, kBf16, 16> res;
-          if constexpr (!kSplit) res.load(p, row, tb * q.bn + col_of(c));
-          tmem_ld16(col + col_of(c), v);
-          if (more) {
+      const int buf = it & 1;
+      if (!(ok = wait_inline(&sm.acc_full[buf], (it >> 1) & 1, &sm.abort, status))) break;
+      tc_fence_after();
+      const uint32_t col = tmem + lane_base + buf * acc_cols;
+      auto chunk = [&](int c, const float *more) {
+        float v[16];
+        Resid<kSwiglu, kBf16, 16> res;
+        if constexpr (kMode != kSplit) res.load(p, row, tl.c0 + col_of(c));
+        tmem_ld16(col + col_of(c), v);
+        if (more) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += more[j];
-          }
-          if constexpr (kSplit) {
-            float *dst = reinterpret_cast<float *>(smem) + col_of(c) * BM + quad * 32 + lane;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) dst[j * BM] = v[j];
-          } else {
-            finish_columns<kSwiglu, kBf16>(p, row, v, res, tb * q.bn + col_of(c), 16);
-          }
-        };
-        if constexpr (kSegs) {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            if (col_of(c) < q.bn) chunk(c, acc[c]);
-        } else {
-          for (int c = 0; col_of(c) < q.bn; ++c) chunk(c, nullptr);
+          for (int j = 0; j < 16; ++j) v[j] += more[j];
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
-        ++it;
+        if constexpr (kMode == kSplit) {
+          float *dst = reinterpret_cast<float *>(smem) + col_of(c) * BM + quad * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) dst[j * BM] = v[j];
+        } else {
+          finish_columns<kSwiglu, kBf16>(p, row, v, res, tl.c0 + col_of(c), 16);
+        }
+      };
+      if constexpr (kSegs) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (col_of(c) < tl.w) chunk(c, acc[c]);
+      } else {
+        for (int c = 0; col_of(c) < tl.w; ++c) chunk(c, nullptr);
       }
+      release(buf);
+      ++it;
     }
   }
 
-  if constexpr (kSplit) {
+  if constexpr (kMode == kSplit) {
     __syncthreads();          // the roles are reconverged for the aligned barrier
     cluster_sync();           // every CTA's partial tile is in its shared memory
     if (warp >= kEpiWarp0 && !*reinterpret_cast<volatile int *>(&sm.abort)) {
       const int quad = warp & 3, turn = (warp - kEpiWarp0) >> 2;
-      int fb, tb;
-      tile_at(q, t_first, fb, tb);
-      const LaneRow<kSwiglu> row = lane_row<kSwiglu>(p, fb, quad, lane);
-      const int share = ((q.bn + ranks - 1) / ranks + 1) & ~1;   // columns per rank, even
-      const int cols = min(share, q.bn - rank * share);
+      const Tile tl = tile_at(q, t_first);
+      const LaneRow<kSwiglu> row = lane_row<kSwiglu>(p, tl.fb, quad, lane);
+      const int share = ((tl.w + ranks - 1) / ranks + 1) & ~1;   // columns per rank, even
+      const int cols = min(share, tl.w - rank * share);
       for (int c = turn * 4; c < cols; c += 4 * G) {
         const int n_cols = min(4, cols - c), col = rank * share + c;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         Resid<kSwiglu, kBf16, 4> res;
-        res.load(p, row, tb * q.bn + col);
+        res.load(p, row, tl.c0 + col);
         const uint32_t src = smem_u32(smem) + ((uint32_t)col * BM + quad * 32 + lane) * 4;
         for (int r = 0; r < ranks; ++r)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (j < n_cols) v[j] += ld_peer(src + j * BM * 4, r);
-        finish_columns<kSwiglu, kBf16>(p, row, v, res, tb * q.bn + col, n_cols);
+        finish_columns<kSwiglu, kBf16>(p, row, v, res, tl.c0 + col, n_cols);
       }
     }
-    __syncthreads();
-    cluster_sync();           // no CTA leaves while a peer reads its partials
   }
   tc_fence_before();
   __syncthreads();
+  // No CTA leaves while a peer may read its shared memory or tensor memory.
+  if constexpr (kMode != kSolo) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(2 * acc_cols)
-                 : "memory");
+    if constexpr (kMode == kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(2 * acc_cols)
+                   : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(2 * acc_cols)
+                   : "memory");
   }
 }
 
 // ----------------------------------------------------------------- launch --
 
 struct Plan {
-  int bn, split;
+  int mode, n_tb, split;
 };
 
 int device_sms(int *dev) {
@@ -508,38 +615,50 @@ int device_sms(int *dev) {
   return sms;
 }
 
-// Tile width and K split with the least estimated time.  A K block costs the
-// larger of its MMAs (4 of BN / 2 clocks, not under 59 each) and its operand
-// bytes at an SM's share of the memory system; a tile adds a start and, split,
-// the exchange.
+int up(int v, int m) { return (v + m - 1) / m; }
+
+// The form and the tiles with the least estimated time, in clocks of an SM.  A
+// K block costs the larger of its MMAs (4 of w / 2 clocks for w tokens, not
+// under 59 each) and its operand rows at 1.74 clocks each (measured); a wave
+// costs its tiles; everything costs at least its bytes from memory; a split
+// adds an exchange.
 Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
-  const int n_fb = (rows + BM - 1) / BM;
-  Plan best{32, 1};
+  Plan best{kSolo, 1, 1};
   double best_cost = 1e300;
-  for (int bn = 32; bn <= max_bn; bn += 32) {
-    const long long n_tb = (T + bn - 1) / bn;
-    if (bn > 32 && (long long)(bn - 32) >= T) break;   // wider than the batch
-    for (int split = 1; split <= 8; ++split) {
-      if (split > 1 && nkb / split < 4) break;
-      const long long ctas = n_fb * n_tb * split;
-      const double mma = 4.0 * std::max(bn / 2.0, 59.0);
-      const double mem = (BM + bn) * (double)kRowBytes / 64.0;
-      const long long waves = (ctas + sms - 1) / sms;
-      const double kblocks = (double)(nkb + split - 1) / split;
-      double cost = waves * kblocks * std::max(mma, mem) + 1500.0 + 8.0 * bn;
-      if (split > 1) cost += waves * (2000.0 + 16.0 * bn);   // a start and an exchange per wave
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = Plan{bn, split};
-      }
+  auto consider = [&](int mode, int n_tb, int split) {
+    const int unit = mode == kPair ? 32 : 16, units = up(T, unit);
+    if (n_tb > units) return;
+    const int w = up(units, n_tb) * unit;
+    if (w > max_bn) return;
+    const long long tiles = (long long)up(rows, mode == kPair ? 2 * BM : BM) * n_tb;
+    const long long slots = mode == kPair ? sms / 2 : sms;
+    const long long waves = (tiles * (mode == kSplit ? split : 1) + slots - 1) / slots;
+    const double mma = 4.0 * std::max(w / 2.0, 59.0);
+    const double mem = 1.74 * (BM + (mode == kPair ? w / 2 : w));
+    // A wave of tiles of two widths: their mean, not the larger.
+    const double mean = (double)units * unit / n_tb / w;
+    const double blocks = std::max(1.0, (double)nkb / split);
+    double cost = waves * (blocks * std::max(mma * mean, mem) + (mode == kSplit ? 2500.0 : 0.0));
+    const double bytes = ((double)rows + T) * nkb * kRowBytes / 3500.0;
+    cost = std::max(cost, bytes) + 2000.0 + 12.0 * w;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = Plan{mode, n_tb, split};
     }
+  };
+  const int least = up(T, max_bn), n_fb = up(rows, BM);
+  for (int n_tb = least; n_tb <= std::min(least + 32, 2 * least + 8); ++n_tb) {
+    consider(kSolo, n_tb, 1);
+    if (n_fb >= 2) consider(kPair, n_tb, 1);
+    if ((long long)n_fb * n_tb < sms)
+      for (int split = 2; split <= 8 && nkb / split >= 4; split *= 2) consider(kSplit, n_tb, split);
   }
   return best;
 }
 
-template <int DT, bool kSwiglu, bool kSplit, bool kBf16>
-cudaError_t launch(const TcLinear &q, int grid, int split, int dev, cudaStream_t st) {
-  auto kernel = linear_tc_kernel<DT, kSwiglu, kSplit, kBf16>;
+template <int DT, bool kSwiglu, int kMode, bool kBf16>
+cudaError_t launch(const TcLinear &q, int grid, int cluster, int dev, cudaStream_t st) {
+  auto kernel = linear_tc_kernel<DT, kSwiglu, kMode, kBf16>;
   // The shared-memory limit is raised once per device.
   static std::atomic<unsigned long long> ready{0};
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
@@ -551,34 +670,37 @@ cudaError_t launch(const TcLinear &q, int grid, int split, int dev, cudaStream_t
   }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads<kBf16>);
-  cfg.dynamicSmemBytes = (size_t)q.stages * (BM + q.bn) * kRowBytes + 1024;
+  cfg.dynamicSmemBytes = (size_t)q.stages * (BM + q.x_rows) * kRowBytes + 1024;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = kSplit ? 1 : 0;
+  cfg.numAttrs = kMode == kSolo ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, q);
 }
 
 template <int DT, bool kSwiglu, bool kBf16>
-cudaError_t launch_split(const TcLinear &q, int sms, int split, int dev, cudaStream_t st) {
+cudaError_t launch_mode(const TcLinear &q, const Plan &plan, int sms, int dev, cudaStream_t st) {
   const int tiles = q.n_fb * q.n_tb;
-  return split > 1 ? launch<DT, kSwiglu, true, kBf16>(q, tiles * split, split, dev, st)
-                   : launch<DT, kSwiglu, false, kBf16>(q, std::min(tiles, sms), 1, dev, st);
+  if (plan.mode == kPair)
+    return launch<DT, kSwiglu, kPair, kBf16>(q, 2 * std::min(tiles, sms / 2), 2, dev, st);
+  if (plan.mode == kSplit)
+    return launch<DT, kSwiglu, kSplit, kBf16>(q, tiles * plan.split, plan.split, dev, st);
+  return launch<DT, kSwiglu, kSolo, kBf16>(q, std::min(tiles, sms), 1, dev, st);
 }
 
 template <int DT>
-cudaError_t launch_type(const TcLinear &q, int sms, int split, int dev, cudaStream_t st) {
+cudaError_t launch_type(const TcLinear &q, const Plan &plan, int sms, int dev, cudaStream_t st) {
   const bool bf = q.p.out_dtype == MOE_BF16;
   if (q.p.act == MOE_ACT_SWIGLU)
-    return bf ? launch_split<DT, true, true>(q, sms, split, dev, st)
-                : launch_split<DT, true, false>(q, sms, split, dev, st);
-  return bf ? launch_split<DT, false, true>(q, sms, split, dev, st)
-              : launch_split<DT, false, false>(q, sms, split, dev, st);
+    return bf ? launch_mode<DT, true, true>(q, plan, sms, dev, st)
+              : launch_mode<DT, true, false>(q, plan, sms, dev, st);
+  return bf ? launch_mode<DT, false, true>(q, plan, sms, dev, st)
+            : launch_mode<DT, false, false>(q, plan, sms, dev, st);
 }
 
 }  // namespace
@@ -593,13 +715,17 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
       dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   TcLinear q;
   q.p = p;
-  q.nkb = (p.K * es + kRowBytes - 1) / kRowBytes;
+  q.nkb = up(p.K * es, kRowBytes);
   const Plan plan = plan_of(p.T, rows, q.nkb, sms, p.out_dtype == MOE_F32 ? kSegMaxBN : kMaxBN);
-  q.bn = plan.bn;
-  q.n_fb = (rows + BM - 1) / BM;
-  q.n_tb = (p.T + q.bn - 1) / q.bn;
+  const bool pair = plan.mode == kPair;
+  q.unit = pair ? 32 : 16;
+  q.units = up(p.T, q.unit);
+  q.n_tb = plan.n_tb;
+  q.bn = up(q.units, q.n_tb) * q.unit;
+  q.x_rows = pair ? q.bn / 2 : q.bn;
+  q.n_fb = up(rows, pair ? 2 * BM : BM);
   q.group_tb = std::min(q.n_tb, 16);
-  const size_t stage = (size_t)(BM + q.bn) * kRowBytes;
+  const size_t stage = (size_t)(BM + q.x_rows) * kRowBytes;
   q.stages = (int)std::min<size_t>(kMaxStages, (kSmemMax - sizeof(Bars) - 64 - 1024) / stage);
   if (sw) {
     if (!make_map_4d(&q.map_w, p.w, dt, p.K, 16, 2, p.N / 16, (uint64_t)p.ldw * es,
@@ -608,10 +734,10 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   } else if (!make_map(&q.map_w, p.w, dt, es, p.K, rows, p.ldw, kRowBytes / es, BM)) {
     return cudaErrorInvalidValue;
   }
-  if (!make_map(&q.map_x, p.x, dt, es, p.K, p.T, p.ldx, kRowBytes / es, q.bn))
+  if (!make_map(&q.map_x, p.x, dt, es, p.K, p.T, p.ldx, kRowBytes / es, q.x_rows))
     return cudaErrorInvalidValue;
-  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, sms, plan.split, dev, st)
-                           : launch_type<MOE_E4M3>(q, sms, plan.split, dev, st);
+  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, plan, sms, dev, st)
+                           : launch_type<MOE_E4M3>(q, plan, sms, dev, st);
 }
 
 }  // namespace moe
