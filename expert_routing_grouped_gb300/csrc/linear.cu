@@ -18,7 +18,11 @@ namespace {
 // so each lane takes 16 consecutive bytes of its row -- lane 4 g + q piece q of
 // every 64 bytes of row g -- straight from memory into two MMAs' fragments.
 // A block owns 8 outputs and splits K over its warps, 64 U bytes of each row
-// at a time; partial sums meet in shared memory in warp order.
+// at a time; partial sums meet in shared memory in warp order.  Reading w is
+// the time: one bf16 token at K = 4096, SwiGLU of 14336, takes 34.9 us (6.7
+// TB/s).  A ring of cp.async pieces in shared memory in place of the registers
+// was slower at every size (K = 14336, N = 4096: 23.1 against 19.4 us), and so
+// were 16 outputs a block.
 //
 template <int DT>
 __device__ __forceinline__ void mma_m16n8(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -76,24 +80,45 @@ __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const Linear
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[b][i] = 0.f;
-  constexpr int U = 4 / NB;
-  for (int u = warp * U; u * 64 < kb; u += W * U) {
-    uint4 wv[NB][U], lo[U], hi[U];
+  // bf16: U units are fetched, then multiplied.  e4m3, whose MMAs take longer
+  // beside half the bytes: two buffers of half as many, one on its way while
+  // the other is at work (K = 14336, N = 4096: 13.1 us in place of 14.8; bf16
+  // the other way round, 23.5 in place of 19.4).
+  constexpr int B = DT == MOE_E4M3 ? 2 : 1, U = 4 / NB / B;
+  uint4 wv[B][NB][U], lo[B][U], hi[B][U];
+  auto fetch = [&](int s, int u) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int off = (u + i) * 64 + q * 16;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) wv[b][i] = load_piece<true>(wr[b], off, row_kb);
-      lo[i] = load_piece<false>(xl, off, lo_kb);
-      hi[i] = HI ? load_piece<false>(xh, off, hi_kb) : make_uint4(0u, 0u, 0u, 0u);
+      for (int b = 0; b < NB; ++b) wv[s][b][i] = load_piece<true>(wr[b], off, row_kb);
+      lo[s][i] = load_piece<false>(xl, off, lo_kb);
+      hi[s][i] = HI ? load_piece<false>(xh, off, hi_kb) : make_uint4(0u, 0u, 0u, 0u);
     }
+  };
+  auto work = [&](int s) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        mma_m16n8<DT>(c[b], lo[i].x, hi[i].x, lo[i].y, hi[i].y, wv[b][i].x, wv[b][i].y);
-        mma_m16n8<DT>(c[b], lo[i].z, hi[i].z, lo[i].w, hi[i].w, wv[b][i].z, wv[b][i].w);
+        mma_m16n8<DT>(c[b], lo[s][i].x, hi[s][i].x, lo[s][i].y, hi[s][i].y, wv[s][b][i].x, wv[s][b][i].y);
+        mma_m16n8<DT>(c[b], lo[s][i].z, hi[s][i].z, lo[s][i].w, hi[s][i].w, wv[s][b][i].z, wv[s][b][i].w);
       }
+  };
+  // The warp's units: U of every W U.
+  constexpr int kStep = W * U;
+  int u = warp * U;
+  if constexpr (B == 2) fetch(0, u);
+  while (u * 64 < kb) {
+    fetch(B - 1, u + (B - 1) * kStep);
+    work(0);
+    u += kStep;
+    if constexpr (B == 2) {
+      if (u * 64 >= kb) break;
+      fetch(0, u + kStep);
+      work(1);
+      u += kStep;
+    }
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -123,12 +148,13 @@ __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const Linear
   else store_out<false>(p, t, n, y + res);
 }
 
-// Warps per block: 8 where there are four blocks for every SM (short-lived
-// blocks overlap better), 16 where there are fewer (more bytes in flight).
+// Warps per block: 8 where there are two blocks for every SM, 16 where there
+// are fewer (more bytes in flight).  bf16, one token: N = 4096, K = 4096 6.7 us
+// with 8, 7.4 with 16; N = 256, K = 6144 3.8 us with 8, 3.1 with 16.
 template <int DT, int NB, bool HI>
 cudaError_t launch_few_w(const LinearParams &p, cudaStream_t st) {
   const int blocks = (p.N + 7) / 8;
-  return blocks >= 608 ? launch_k(false, linear_few_kernel<DT, NB, HI, 8>, dim3(blocks), dim3(256), 0, st, p)
+  return blocks > 304 ? launch_k(false, linear_few_kernel<DT, NB, HI, 8>, dim3(blocks), dim3(256), 0, st, p)
                        : launch_k(false, linear_few_kernel<DT, NB, HI, 16>, dim3(blocks), dim3(512), 0, st, p);
 }
 

@@ -2,9 +2,28 @@
 // moe_linear.
 #pragma once
 
+#include <atomic>
+
 #include "moe_internal.cuh"
 
 namespace moe {
+
+// Runs f (a function attribute that lasts as long as the context) once for
+// each device; again after an error.
+struct DeviceOnce {
+  std::atomic<unsigned long long> done{0};
+  template <class F>
+  cudaError_t run(F f) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    err = f();
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return err;
+  }
+};
 
 struct LinearParams {
   const void *x, *w;

@@ -36,7 +36,6 @@
 // Every mbarrier wait is bounded: one that gives up sets the status word, and
 // the roles stop, drain their copies and MMAs, and return.
 #include <algorithm>
-#include <atomic>
 #include <cuda.h>
 
 #include "linear.cuh"
@@ -607,21 +606,28 @@ struct Plan {
   int mode, n_tb, split;
 };
 
-int device_sms(int *dev) {
-  int sms = 0;
-  if (cudaGetDevice(dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
+int device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
   return sms;
 }
 
 int up(int v, int m) { return (v + m - 1) / m; }
 
+// Clusters of 1 .. 8 CTAs, one CTA to an SM, that run at once on 152 SMs
+// (cudaOccupancyMaxActiveClusters): a split into more takes a second wave,
+// which costs more than it gains (48 clusters of 3 for N = 6144: 28 us; of 2:
+// 18 us).
+constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+
 // The form and the tiles with the least estimated time, in clocks of an SM.  A
 // K block costs the larger of its MMAs (4 of w / 2 clocks for w tokens, not
-// under 59 each) and its operand rows at 1.74 clocks each (measured); a wave
-// costs its tiles; everything costs at least its bytes from memory; a split
-// adds an exchange.
+// under 59 each, and 12 more) and its operand rows at 1.74 clocks each; the
+// whole costs at least its bytes from memory; each form has its start and end.
+// All measured: within 15% of the best of all forms and tilings for T = 32 ..
+// 1024 and N = 256 .. 14336.
 Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
   Plan best{kSolo, 1, 1};
   double best_cost = 1e300;
@@ -631,16 +637,17 @@ Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
     const int w = up(units, n_tb) * unit;
     if (w > max_bn) return;
     const long long tiles = (long long)up(rows, mode == kPair ? 2 * BM : BM) * n_tb;
-    const long long slots = mode == kPair ? sms / 2 : sms;
-    const long long waves = (tiles * (mode == kSplit ? split : 1) + slots - 1) / slots;
-    const double mma = 4.0 * std::max(w / 2.0, 59.0);
+    if (mode == kSplit && tiles > (long long)kClusters[split] * sms / 152) return;
+    const int slots = mode == kPair ? sms / 2 : sms;
+    const double waves = mode == kSplit ? 1.0 : (double)((tiles + slots - 1) / slots);
+    // Tiles of two widths: between their mean and the larger.
+    const double we = 0.5 * (w + (double)units * unit / n_tb);
+    const double mma = 4.0 * std::max((we + 24.0) / 2.0, 59.0);
     const double mem = 1.74 * (BM + (mode == kPair ? w / 2 : w));
-    // A wave of tiles of two widths: their mean, not the larger.
-    const double mean = (double)units * unit / n_tb / w;
-    const double blocks = std::max(1.0, (double)nkb / split);
-    double cost = waves * (blocks * std::max(mma * mean, mem) + (mode == kSplit ? 2500.0 : 0.0));
     const double bytes = ((double)rows + T) * nkb * kRowBytes / 3500.0;
-    cost = std::max(cost, bytes) + 2000.0 + 12.0 * w;
+    const double start = mode == kSolo ? 8500.0 : mode == kPair ? 10500.0 : 11500.0;
+    const double cost =
+        std::max(waves * std::max(1.0, (double)nkb / split) * std::max(mma, mem), bytes) + start + 12.0 * w;
     if (cost < best_cost) {
       best_cost = cost;
       best = Plan{mode, n_tb, split};
@@ -650,24 +657,20 @@ Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
   for (int n_tb = least; n_tb <= std::min(least + 32, 2 * least + 8); ++n_tb) {
     consider(kSolo, n_tb, 1);
     if (n_fb >= 2) consider(kPair, n_tb, 1);
-    if ((long long)n_fb * n_tb < sms)
-      for (int split = 2; split <= 8 && nkb / split >= 4; split *= 2) consider(kSplit, n_tb, split);
+    for (int split = 2; split <= 8 && nkb / split >= 4; ++split) consider(kSplit, n_tb, split);
   }
   return best;
 }
 
 template <int DT, bool kSwiglu, int kMode, bool kBf16>
-cudaError_t launch(const TcLinear &q, int grid, int cluster, int dev, cudaStream_t st) {
+cudaError_t launch(const TcLinear &q, int grid, int cluster, cudaStream_t st) {
   auto kernel = linear_tc_kernel<DT, kSwiglu, kMode, kBf16>;
-  // The shared-memory limit is raised once per device.
-  static std::atomic<unsigned long long> ready{0};
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(ready.load(std::memory_order_acquire) & bit)) {
-    const cudaError_t err = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemMax - sizeof(Bars) - 64));
-    if (err != cudaSuccess) return err;
-    ready.fetch_or(bit, std::memory_order_release);
-  }
+  static DeviceOnce once;
+  const cudaError_t err = once.run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(kSmemMax - sizeof(Bars) - 64));
+  });
+  if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
@@ -684,30 +687,29 @@ cudaError_t launch(const TcLinear &q, int grid, int cluster, int dev, cudaStream
 }
 
 template <int DT, bool kSwiglu, bool kBf16>
-cudaError_t launch_mode(const TcLinear &q, const Plan &plan, int sms, int dev, cudaStream_t st) {
+cudaError_t launch_mode(const TcLinear &q, const Plan &plan, int sms, cudaStream_t st) {
   const int tiles = q.n_fb * q.n_tb;
   if (plan.mode == kPair)
-    return launch<DT, kSwiglu, kPair, kBf16>(q, 2 * std::min(tiles, sms / 2), 2, dev, st);
+    return launch<DT, kSwiglu, kPair, kBf16>(q, 2 * std::min(tiles, sms / 2), 2, st);
   if (plan.mode == kSplit)
-    return launch<DT, kSwiglu, kSplit, kBf16>(q, tiles * plan.split, plan.split, dev, st);
-  return launch<DT, kSwiglu, kSolo, kBf16>(q, std::min(tiles, sms), 1, dev, st);
+    return launch<DT, kSwiglu, kSplit, kBf16>(q, tiles * plan.split, plan.split, st);
+  return launch<DT, kSwiglu, kSolo, kBf16>(q, std::min(tiles, sms), 1, st);
 }
 
 template <int DT>
-cudaError_t launch_type(const TcLinear &q, const Plan &plan, int sms, int dev, cudaStream_t st) {
+cudaError_t launch_type(const TcLinear &q, const Plan &plan, int sms, cudaStream_t st) {
   const bool bf = q.p.out_dtype == MOE_BF16;
   if (q.p.act == MOE_ACT_SWIGLU)
-    return bf ? launch_mode<DT, true, true>(q, plan, sms, dev, st)
-              : launch_mode<DT, true, false>(q, plan, sms, dev, st);
-  return bf ? launch_mode<DT, false, true>(q, plan, sms, dev, st)
-            : launch_mode<DT, false, false>(q, plan, sms, dev, st);
+    return bf ? launch_mode<DT, true, true>(q, plan, sms, st)
+              : launch_mode<DT, true, false>(q, plan, sms, st);
+  return bf ? launch_mode<DT, false, true>(q, plan, sms, st)
+            : launch_mode<DT, false, false>(q, plan, sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) {
-  int dev = 0;
-  const int sms = device_sms(&dev);
+  const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const bool sw = p.act == MOE_ACT_SWIGLU;
   const int es = dtype == MOE_BF16 ? 2 : 1, rows = sw ? 2 * p.N : p.N;
@@ -736,8 +738,8 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   }
   if (!make_map(&q.map_x, p.x, dt, es, p.K, p.T, p.ldx, kRowBytes / es, q.x_rows))
     return cudaErrorInvalidValue;
-  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, plan, sms, dev, st)
-                           : launch_type<MOE_E4M3>(q, plan, sms, dev, st);
+  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, plan, sms, st)
+                           : launch_type<MOE_E4M3>(q, plan, sms, st);
 }
 
 }  // namespace moe

@@ -586,3 +586,33 @@ def test_ops_device_refusals_leave_outputs(moe):
     assert e.value.code == moe.MOE_ERR_NOMEM
     torch.cuda.synchronize()
     assert bool((out.float() == SENT).all())
+
+
+@pytest.mark.parametrize("T", [1, 5, 16, 40, 600])
+@pytest.mark.parametrize("act", [0, 3])
+def test_linear_e4m3_every_code(moe, T, act):
+    """Every e4m3 code on both sides, subnormals, zeros and (in single rows)
+    NaN codes among them: a NaN reaches its row of w's outputs or its token,
+    and nothing else."""
+    K, N = 512, 256
+    rows = 2 * N if act == 3 else N
+    g = gen(T)
+    codes = torch.randint(0, 256, (T + rows, K), generator=g, device="cuda", dtype=torch.int32)
+    codes[(codes & 127) == 127] = 3
+    x, w = codes[:T].to(torch.uint8), codes[T:].to(torch.uint8)
+    w[0, :256] = torch.tensor([c if c & 127 != 127 else 0 for c in range(256)], dtype=torch.uint8, device="cuda")
+    sx = 2.0 ** torch.randint(-8, 0, (T,), generator=g, device="cuda").float()
+    sw = 2.0 ** torch.randint(-12, -4, (rows,), generator=g, device="cuda").float()
+    out, st = run_linear(moe, x.view(E4M3), w.view(E4M3), sx, sw, None, None, N, 2, 0, act)
+    check_linear(out, st, x.view(E4M3), w.view(E4M3), sx, sw, None, None, N, act)
+    w[7, K - 1] = 0x7F
+    w[rows - 3, 0] = 0xFF
+    bad, st = run_linear(moe, x.view(E4M3), w.view(E4M3), sx, sw, None, None, N, 2, 0, act)
+    cols = sorted({7, (rows - 3) % N})
+    keep = [n for n in range(N) if n not in cols]
+    assert bool(bad[:, cols].isnan().all()) and torch.equal(bad[:, keep], out[:, keep])
+    w[7, K - 1] = 1
+    w[rows - 3, 0] = 1
+    x[T - 1, 3] = 0x7F
+    bad, st = run_linear(moe, x.view(E4M3), w.view(E4M3), sx, sw, None, None, N, 2, 0, act)
+    assert bool(bad[T - 1].isnan().all()) and not bool(bad[:T - 1].isnan().any())
