@@ -19,15 +19,15 @@
 //           histogram in shared memory for each segment that it meets;
 //   pass    a block per short chunk; its first rows of z are on their way
 //           before it waits for the histograms.  Without a gradient it counts
-//           its own tokens and there is no count kernel;
+//           its own tokens first and there is no count kernel;
 //   finish  a cluster per segment: counts, P and the loss from the partials.
 // Chunk c and segment s meet in at most one run of tokens, and along the
 // tokens both only grow, so c + s names each meeting once: a block writes its
 // partials of a segment to slot c + s, and no slot has two writers.  Nothing
 // needs clearing before a call, and no atomic leaves a block.
 //
-// Up to kSmallElems logits one kernel does all three steps, a cluster per
-// segment with cluster barriers between them: there the launches are the time.
+// For short segments one kernel does all three steps, a cluster per segment
+// with cluster barriers between them: there the launches are the time.
 #include <algorithm>
 
 #include "moe_internal.cuh"
@@ -40,7 +40,7 @@ constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalBlocks = 456;          // most chunks of a call: 3 blocks on each of 152 SMs
 constexpr int kCountThreads = 1024;
 constexpr int kCluster = 8;
-constexpr long long kSmallElems = 1 << 18;
+constexpr long long kSmallElems = 1 << 16, kSmallTotal = 1 << 22;
 
 struct BalParams {
   const void *z;
@@ -79,6 +79,14 @@ __device__ __forceinline__ void cluster_sync() {
   __syncthreads();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
+}
+// The same barrier in two halves: every CTA of the cluster has started once
+// the wait returns, so its shared memory may be written.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The 32-bit word at p (this CTA's shared memory) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t ld_peer(const void *p, uint32_t rank) {
@@ -235,24 +243,27 @@ struct Lay {
     for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
   }
-  // Raw registers of one lane's logits.
+  // Raw registers of one lane's logits; -infinity (p = 0) where there is none,
+  // so that nothing later asks whether an expert exists.
   struct Raw {
-    uint32_t w[DT == MOE_F32 ? NE : (VEC == 1 ? NE : NE / 2)];
+    static constexpr int N = DT == MOE_F32 ? NE : (VEC == 1 ? NE : NE / 2);
+    uint32_t w[N];
   };
-  static __device__ __forceinline__ void load(const BalParams &p, int t, bool valid, Raw &r) {
+  static constexpr uint32_t kNone = DT == MOE_F32 ? 0xFF800000u : 0xFF80FF80u;
+  static __device__ __forceinline__ void load(const BalParams &p, int t, bool there, Raw &r) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = first(i);
-      const bool in = valid && e < p.E;
+      const bool in = there && e < p.E;
       const size_t at = (size_t)t * p.ldz + e;
       if constexpr (VEC == 1) {
-        r.w[i] = 0u;
+        r.w[i] = kNone;
         if (in) {
           if constexpr (DT == MOE_F32) r.w[i] = __float_as_uint(__ldcs(reinterpret_cast<const float *>(p.z) + at));
           else r.w[i] = __ldcs(reinterpret_cast<const unsigned short *>(p.z) + at);
         }
       } else {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        uint4 u = make_uint4(kNone, kNone, kNone, kNone);
         if (in)
           u = __ldcs(reinterpret_cast<const uint4 *>(
               reinterpret_cast<const char *>(p.z) + at * (DT == MOE_F32 ? 4 : 2)));
@@ -292,16 +303,22 @@ struct Lay {
   }
 };
 
-// p of the lane's token added to acc, and the token's gradient written when
-// `coef` (the counts less their mean, in shared memory) is given.  valid: the
-// token exists and the mask keeps it; write: it exists (a masked token's
-// gradient is 0).  Every lane of the warp takes part.
+// p of the lane's token added to acc, and (kGrad) the token's gradient written
+// from coef, the counts less their mean, in shared memory.  valid: the token
+// exists and the mask keeps it; write: it exists (a masked token's gradient is
+// 0).  Every lane of the warp takes part.  bias and coef cover the layout's
+// experts (0 past E).
 //
 // The mean taken off the counts cancels in a_i - sum_e p_e a_e, and small
 // differences keep their digits.
 //
-// expf is the hardware one (2 units and |z| 2^-24) and the reciprocal good to
-// a unit: p is a sum's share, held in f32.
+// exp is the hardware one (2 units and |z| 2^-24, 0 below 2^-126) and the
+// reciprocal good to a unit: p is a sum's share, held in f32.
+__device__ __forceinline__ float exp_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+  return r;
+}
 __device__ __forceinline__ float rcp_fast(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -309,42 +326,52 @@ __device__ __forceinline__ float rcp_fast(float v) {
 }
 
 template <class L, bool kGrad>
-__device__ __forceinline__ void one_token(const BalParams &p, const typename L::Raw &raw, int t,
-                                          bool valid, bool write, const float *bias,
-                                          const float *coef, float scale, float (&acc)[L::NE]) {
+__device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &raw, int t, bool valid,
+                                          bool write, const float *bias, const float *coef, float scale,
+                                          float (&acc)[L::NE]) {
   float v[L::NE], om[L::kSig && kGrad ? L::NE : 1];
+  if constexpr (L::LPR == 32) {   // the warp's one token
+    if (!valid) {
+      if (kGrad && write) {
+#pragma unroll
+        for (int j = 0; j < L::NE; ++j) v[j] = 0.f;
+        L::store(p, t, v);
+      }
+      return;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < L::Raw::N; ++j) raw.w[j] = valid ? raw.w[j] : L::kNone;
+  }
   float tot = 0.f;
   if constexpr (L::kSig) {
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      const float ex = __expf(-L::get(raw, j));
-      const float sg = rcp_fast(1.0f + ex);   // 0 from 2^126 on
-      v[j] = L::first(j / L::VEC) < p.E ? sg : 0.f;
+      const float ex = exp_fast(-L::get(raw, j));
+      v[j] = rcp_fast(1.0f + ex);   // 0 from 2^126 on
       // 1 - sigmoid keeps its digits as exp(-z) sigmoid where the sigmoid is
       // near 1.
-      if constexpr (kGrad) om[j] = ex < 1.0f ? ex * sg : 1.0f - sg;
+      if constexpr (kGrad) om[j] = ex < 1.0f ? ex * v[j] : 1.0f - v[j];
       tot += v[j];
     }
   } else {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      const bool in = L::first(j / L::VEC) < p.E;
-      v[j] = in ? L::get(raw, j) : -INFINITY;
-      if (bias && in) v[j] += bias[L::first(j / L::VEC) + j % L::VEC];
+      v[j] = L::get(raw, j);
+      if (bias) v[j] += bias[L::first(j / L::VEC) + j % L::VEC];
       m = fmaxf(m, v[j]);
     }
     m = L::max(m);
     if (m == -INFINITY) m = 0.f;   // a row with nothing left: p = 0
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      v[j] = __expf(v[j] - m);
+      v[j] = exp_fast(v[j] - m);
       tot += v[j];
     }
   }
   tot = L::sum(tot);
-  // A token that is not there or masked has raw 0: its p is 0 from here on.
-  const float inv = valid ? (tot == 0.f ? 0.f : 1.0f / tot) : 0.f;
+  const float inv = tot == 0.f ? 0.f : 1.0f / tot;
   float dot = 0.f;
 #pragma unroll
   for (int j = 0; j < L::NE; ++j) {
@@ -376,10 +403,11 @@ struct Rows {
   static __device__ __forceinline__ int token(int row) {
     return row + (int)(threadIdx.x & 31) / L::LPR;
   }
+  // The logits' load does not wait for the mask's.
   __device__ __forceinline__ void fetch(const BalParams &p, int i, int row, int b) {
     const int t = token(row);
     valid[i] = t < b && (!p.mask || p.mask[t]);
-    L::load(p, t, valid[i], raw[i]);
+    L::load(p, t, t < b, raw[i]);
   }
   __device__ __forceinline__ void start(const BalParams &p, int first, int step, int b) {
 #pragma unroll
@@ -393,7 +421,7 @@ struct Rows {
       for (int i = 0; i < kAhead; ++i) {
         const int row = row0 + i * step;
         if (row < b) {
-          const typename L::Raw now = raw[i];
+          typename L::Raw now = raw[i];
           const bool ok = valid[i];
           fetch(p, i, row + kAhead * step, b);
           const int t = token(row);
@@ -406,9 +434,10 @@ struct Rows {
 
 // Shared memory of a block of the pass: the warps' sums, the coefficients and
 // the bias, each over the padded experts of the layout.
+template <int EP>
 __device__ __forceinline__ void stage_bias(const BalParams &p, float *bias) {
   if (p.bias)
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) bias[e] = __ldg(p.bias + e);
+    for (int e = threadIdx.x; e < EP; e += blockDim.x) bias[e] = e < p.E ? __ldg(p.bias + e) : 0.f;
 }
 
 __device__ __forceinline__ float grad_scale(const BalParams &p, int s, int tokens) {
@@ -436,13 +465,13 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_pass_
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int EP = L::NE * L::LPR;   // experts of the layout, >= E
   __shared__ float sums[kBalWarps * EP];
-  __shared__ float coef[kGrad ? EP : 1], bias[EP];
+  __shared__ __align__(16) float coef[kGrad ? EP : 1], bias[L::kSig ? 1 : EP];
   int32_t *ints = reinterpret_cast<int32_t *>(sums);   // counts, before sums holds anything
   const int warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   constexpr int kStep = kBalWarps * Rows<L>::RPW;
   bool waited = false;
-  if (!L::kSig) stage_bias(p, bias);
+  if (!L::kSig) stage_bias<EP>(p, bias);
   each_segment(p, t0, t1, [&](int s, int a, int b) {
     const int first = a + warp * Rows<L>::RPW;
     Rows<L> rows;
@@ -485,82 +514,105 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_pass_
 
 // -------------------------------------------------------------- finish ----
 
-// The loss of a segment from each CTA's share of sum_e c_e P_e: red is shared,
-// one float per warp, and slot one float.
-__device__ __forceinline__ void finish_loss(const BalParams &p, int s, float dot, float inv, float *red,
-                                            float *slot) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+// The loss of a segment from each CTA's share of sum_e c_e P_e, which warp 0
+// holds in its lanes: every rank puts its sum into rank 0's shares[], and after
+// the one cluster barrier rank 0 adds them in rank order.
+__device__ __forceinline__ void finish_loss(const BalParams &p, int s, float dot, float inv, float *shares) {
+  const int ranks = cluster_size(), rank = cluster_rank();
+  if (threadIdx.x < 32) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-  if (lane == 0) red[warp] = dot;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float tot = 0.f;
-    for (int w = 0; w < nw; ++w) tot += red[w];
-    *slot = tot;
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (threadIdx.x == 0) {
+      uint32_t a;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(a)
+                   : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(shares + rank))), "r"(0));
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(dot) : "memory");
+    }
   }
   cluster_sync();
-  if (cluster_rank() == 0 && threadIdx.x == 0) {
-    const int ranks = cluster_size();
+  if (rank == 0 && threadIdx.x == 0) {
     float tot = 0.f;
-    for (int r = 0; r < ranks; ++r) tot += __uint_as_float(ld_peer(slot, r));
+    for (int r = 0; r < ranks; ++r) tot += shares[r];
     p.loss[s] = p.alpha * (float)p.E / (float)p.k * inv * tot;
   }
-  cluster_sync();
 }
 
 // A cluster per segment: rank r takes experts 32 r .. 32 r + 31, 32 (r +
-// ranks) .., a lane each; the warps share the segment's chunks, and their sums
-// are added in warp order.
-__global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float part[32][33];
-  __shared__ float red[32], slot;
-  __shared__ int32_t counts[32], kept;
+// ranks) .., four to a lane; a warp reads four slots at a time, and the sums of
+// its quarters and of the warps are added in that order.
+constexpr int kFinishWarps = 16;
+
+__global__ void __launch_bounds__(kFinishWarps * 32) balance_finish_kernel(const BalParams p) {
+  cluster_arrive();
   const int ranks = cluster_size(), rank = cluster_rank(), s = blockIdx.x / ranks;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = lane >> 3, piece = (lane & 7) * 4;
   const int a = seg_begin(p, s), b = seg_end(p, s);
-  const int c0 = a / p.chunk, c1 = a < b ? (b - 1) / p.chunk + 1 : c0;
+  const int c0 = a / p.chunk + s, c1 = a < b ? (b - 1) / p.chunk + 1 + s : c0;
   const int2 sl = count_slots(p, s);
   const int row = p.E4 + 4;
+  __shared__ float4 part[kFinishWarps][8];
+  __shared__ int32_t counts[32], kept;
+  __shared__ float shares[kCluster];
+  if (threadIdx.x < 32) counts[threadIdx.x] = 0;
   if (threadIdx.x == 0) kept = 0;
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   int n = 0;
   for (int i = sl.x + (int)threadIdx.x; i < sl.y; i += blockDim.x)
     n += __ldcg(p.cnt + (size_t)i * row + p.E4);
-  n = __reduce_add_sync(0xffffffffu, n);
-  if (lane == 0 && n) atomicAdd(&kept, n);
-  __syncthreads();
-  n = kept;
-  const float inv = n > 0 ? 1.0f / (float)n : 0.f;
-  if (rank == 0 && threadIdx.x == 0) p.tokens[s] = n;
-  float dot = 0.f;
+  float dot = 0.f, inv = 0.f;
   for (int e0 = rank * 32; e0 < p.E; e0 += ranks * 32) {
-    const int e = e0 + lane;
-    if (warp == 0) counts[lane] = 0;
-    __syncthreads();
-    float sum = 0.f;
-    int c = 0;
-    if (e < p.E) {
-#pragma unroll 10
-      for (int i = c0 + warp; i < c1; i += nw) sum += __ldcg(p.part + (size_t)(i + s) * p.E4 + e);
-#pragma unroll 10
-      for (int i = sl.x + warp; i < sl.y; i += nw) c += __ldcg(p.cnt + (size_t)i * row + e);
+    const int e = e0 + piece;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 c = make_int4(0, 0, 0, 0);
+    if (e < p.E4) {
+#pragma unroll 8
+      for (int i = c0 + warp * 4 + quarter; i < c1; i += kFinishWarps * 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (size_t)i * p.E4 + e));
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+      }
+#pragma unroll 8
+      for (int i = sl.x + warp * 4 + quarter; i < sl.y; i += kFinishWarps * 4) {
+        const int4 v = __ldcg(reinterpret_cast<const int4 *>(p.cnt + (size_t)i * row + e));
+        c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
+      }
     }
-    part[warp][lane] = sum;
-    if (c) atomicAdd(&counts[lane], c);
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1) {
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o), sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+      sum.z += __shfl_xor_sync(0xffffffffu, sum.z, o), sum.w += __shfl_xor_sync(0xffffffffu, sum.w, o);
+    }
+    if (quarter == 0) part[warp][lane] = sum;
+    if (c.x) atomicAdd(&counts[piece], c.x);
+    if (c.y) atomicAdd(&counts[piece + 1], c.y);
+    if (c.z) atomicAdd(&counts[piece + 2], c.z);
+    if (c.w) atomicAdd(&counts[piece + 3], c.w);
+    if (e0 == rank * 32) {
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0 && n) atomicAdd(&kept, n);
+    }
     __syncthreads();
-    if (warp == 0 && e < p.E) {
+    if (warp == 0) {
+      n = kept;
+      inv = n > 0 ? 1.0f / (float)n : 0.f;
       float tot = 0.f;
-      for (int w = 0; w < nw; ++w) tot += part[w][lane];
+#pragma unroll
+      for (int w = 0; w < kFinishWarps; ++w) tot += reinterpret_cast<const float *>(part[w])[lane];
       tot *= inv;
-      p.prob[(size_t)s * p.E + e] = tot;
-      p.counts[(size_t)s * p.E + e] = counts[lane];
-      dot = fmaf((float)counts[lane], tot, dot);
+      if (e0 + lane < p.E) {
+        p.prob[(size_t)s * p.E + e0 + lane] = tot;
+        p.counts[(size_t)s * p.E + e0 + lane] = counts[lane];
+        dot = fmaf((float)counts[lane], tot, dot);
+      }
+      counts[lane] = 0;
     }
     __syncthreads();
   }
-  finish_loss(p, s, dot, inv, red, &slot);
+  if (rank == 0 && threadIdx.x == 0) p.tokens[s] = n;   // rank 0 always has experts
+  __syncthreads();
+  cluster_wait();
+  finish_loss(p, s, dot, inv, shares);
 }
 
 // ---------------------------------------------------------- small batches --
@@ -569,10 +621,10 @@ template <class L>
 __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small_kernel(const BalParams p) {
   constexpr int EP = L::NE * L::LPR;
   __shared__ float sums[kBalWarps * EP];
-  __shared__ float coef[EP], bias[EP];
+  __shared__ __align__(16) float coef[EP], bias[L::kSig ? 1 : EP];
   float *mine = sums;   // the block's sums, in place of warp 0's
   __shared__ int32_t hist[EP + 1];
-  __shared__ float red[kBalWarps], slot;
+  __shared__ float shares[kCluster];
   __shared__ int total;
   const int ranks = cluster_size(), rank = cluster_rank(), s = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5;
@@ -581,7 +633,7 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small
   const int first = a + (rank * kBalWarps + warp) * Rows<L>::RPW;
   Rows<L> rows;
   rows.start(p, first, ranks * kStep, b);
-  if (!L::kSig) stage_bias(p, bias);
+  if (!L::kSig) stage_bias<EP>(p, bias);
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
   if (threadIdx.x == 0) total = 0;
   __syncthreads();
@@ -622,14 +674,17 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small
   }
   cluster_sync();
   float dot = 0.f;
-  for (int e = rank + ranks * threadIdx.x; e < p.E; e += ranks * blockDim.x) {
+  for (int e = rank + ranks * (int)threadIdx.x; e < p.E; e += ranks * blockDim.x) {
     float tot = 0.f;
     for (int r = 0; r < ranks; ++r) tot += __uint_as_float(ld_peer(&mine[e], r));
     tot *= inv;
     p.prob[(size_t)s * p.E + e] = tot;
-    dot = fmaf(coef[e] + mean, tot, dot);
+    sums[EP + e] = (coef[e] + mean) * tot;   // past `mine`, which the peers read
   }
-  finish_loss(p, s, dot, inv, red, &slot);
+  __syncthreads();
+  if (warp == 0)   // this rank's experts, in their order
+    for (int e = rank + ranks * (int)(threadIdx.x & 31); e < p.E; e += ranks * 32) dot += sums[EP + e];
+  finish_loss(p, s, dot, inv, shares);
 }
 
 // ----------------------------------------------------------------- launch --
@@ -659,17 +714,25 @@ int balance_chunk(int T) {
 }
 
 // Tokens per histogram: what a block of the pass has when it counts for itself;
-// the count kernel's blocks take 2048, or more to stay at 128 blocks (each
-// block of the pass reads every histogram of its segment).
+// the count kernel's blocks take 256, or more to stay at 64 blocks (each block
+// of the pass reads every histogram of its segment).
 int balance_count_chunk(int T, bool grad) {
-  return grad ? std::max(2048, (T + 127) / 128) : balance_chunk(T);
+  return grad ? std::max(256, (T + 63) / 64) : balance_chunk(T);
 }
 
-bool is_small(int T, int E) { return (long long)T * E <= kSmallElems; }
+// One kernel where a mean segment has at most 2^16 logits and all have 2^22
+// (bounds what one segment that holds nearly every token costs).  With a
+// gradient, us in one kernel and in three: T = 512, E = 64, one segment 6.7 and
+// 7.8; 1024 x 256, one segment 14.8 and 10.5; 4096 x 256, 24 segments 12.7 and
+// 21.1, 8 segments 17.7 and 15.9; 16389 x 256, 64 segments 20.0 and 27.5, 24
+// segments 28.7 and 20.7.
+bool is_small(int T, int E, int S) {
+  return (long long)T * E <= kSmallElems * S && (long long)T * E <= kSmallTotal;
+}
 
 template <class L>
 cudaError_t launch_layout(const BalParams &p, cudaStream_t st) {
-  if (is_small(p.T, p.E)) {
+  if (is_small(p.T, p.E, p.S)) {
     // CTAs of a segment: one for every two steps of its share of the rows
     // (four times the mean segment: they differ in length).
     const int rows = std::min<long long>(p.T, 4LL * ((p.T + p.S - 1) / p.S));
@@ -688,11 +751,8 @@ cudaError_t launch_layout(const BalParams &p, cudaStream_t st) {
   } else {
     err = launch_k(false, balance_pass_kernel<L, false>, dim3(chunks), dim3(kBalThreads), 0, st, p);
   }
-  // A warp of the finish kernel for every few chunks of a segment.
-  const int per = (chunks + p.S - 1) / p.S;
-  const int threads = std::min(1024, std::max(64, (per / 4 + 1) * 32));
   if (err == cudaSuccess)
-    err = launch_cluster(true, balance_finish_kernel, p.S * kCluster, threads, kCluster, st, p);
+    err = launch_cluster(true, balance_finish_kernel, p.S * kCluster, kFinishWarps * 32, kCluster, st, p);
   return err;
 }
 
