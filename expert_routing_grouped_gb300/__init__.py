@@ -123,10 +123,26 @@ def _ptr(t):
     return t.ctypes.data
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """The current stream's address: where torch offers it without building a
+    Stream object, that way (0.4 us in place of 3 us a call)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    device = torch.cuda.current_device
+    return lambda: raw(device())
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     return getattr(stream, "cuda_stream", stream)
 
 

@@ -18,8 +18,8 @@
 //   count   (gradient only) a block per long chunk of consecutive tokens: a
 //           histogram in shared memory for each segment that it meets;
 //   pass    a block per short chunk; its first rows of z are on their way
-//           before it waits for the histograms.  Without a gradient it counts
-//           its own tokens first and there is no count kernel;
+//           before it waits for the histograms.  Without a gradient a
+//           ninth warp counts the block's tokens and there is no count kernel;
 //   finish  a cluster per segment: counts, P and the loss from the partials.
 // Chunk c and segment s meet in at most one run of tokens, and along the
 // tokens both only grow, so c + s names each meeting once: a block writes its
@@ -154,16 +154,19 @@ __device__ __forceinline__ void count_rows(const BalParams &p, int a, int b, int
   if ((threadIdx.x & 31) == 0 && kept) atomicAdd(&hist[p.E], kept);
 }
 
-// The histogram of tokens [a, b) of segment s into slot blockIdx.x + s, by the
-// whole block; hist[E + 1] is shared memory.
-__device__ __forceinline__ void count_chunk(const BalParams &p, int s, int a, int b, int32_t *hist) {
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
-  __syncthreads();
-  count_rows(p, a, b, threadIdx.x, blockDim.x, hist);
-  __syncthreads();
+// The histogram of tokens [a, b) of segment s into slot blockIdx.x + s, by
+// threads i of n with `sync` between them; hist[E + 1] is shared memory.
+template <class F>
+__device__ __forceinline__ void count_chunk(const BalParams &p, int s, int a, int b, int32_t *hist, int i,
+                                            int n, F sync) {
+  for (int e = i; e <= p.E; e += n) hist[e] = 0;
+  sync();
+  count_rows(p, a, b, i, n, hist);
+  sync();
   int32_t *dst = p.cnt + (size_t)(blockIdx.x + s) * (p.E4 + 4);
-  for (int e = threadIdx.x; e < p.E4; e += blockDim.x) dst[e] = e < p.E ? hist[e] : 0;
-  if (threadIdx.x == 0) dst[p.E4] = hist[p.E];
+  for (int e = i; e < p.E4; e += n) dst[e] = e < p.E ? hist[e] : 0;
+  if (i == 0) dst[p.E4] = hist[p.E];
+  sync();
 }
 
 // Calls f(s, a, b) for every segment s and its tokens [a, b) inside [t0, t1).
@@ -184,8 +187,7 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const BalP
   __shared__ int32_t hist[kMaxExperts + 1];
   const int t0 = blockIdx.x * p.cchunk, t1 = min(p.T, t0 + p.cchunk);
   each_segment(p, t0, t1, [&](int s, int a, int b) {
-    count_chunk(p, s, a, b, hist);
-    __syncthreads();
+    count_chunk(p, s, a, b, hist, threadIdx.x, blockDim.x, [] { __syncthreads(); });
   });
 }
 
@@ -461,21 +463,27 @@ __device__ __forceinline__ void warp_sums(float (&acc)[L::NE], float *sums) {
 // -------------------------------------------------------------- main pass --
 
 template <class L, bool kGrad>
-__global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_pass_kernel(const BalParams p) {
+__global__ void __launch_bounds__(kBalThreads + (kGrad ? 0 : 32), L::NE <= 8 ? 3 : 1) balance_pass_kernel(const BalParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int EP = L::NE * L::LPR;   // experts of the layout, >= E
   __shared__ float sums[kBalWarps * EP];
   __shared__ __align__(16) float coef[kGrad ? EP : 1], bias[L::kSig ? 1 : EP];
-  int32_t *ints = reinterpret_cast<int32_t *>(sums);   // counts, before sums holds anything
+  // kGrad: the segment's counts, before sums holds anything; else the ninth
+  // warp's histogram of the block's own tokens.
+  __shared__ int32_t hist[kGrad ? 1 : EP + 1];
+  int32_t *ints = kGrad ? reinterpret_cast<int32_t *>(sums) : hist;
   const int warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   constexpr int kStep = kBalWarps * Rows<L>::RPW;
   bool waited = false;
-  if (!L::kSig) stage_bias<EP>(p, bias);
+  if constexpr (!L::kSig) {
+    stage_bias<EP>(p, bias);
+    __syncthreads();
+  }
   each_segment(p, t0, t1, [&](int s, int a, int b) {
     const int first = a + warp * Rows<L>::RPW;
     Rows<L> rows;
-    rows.start(p, first, kStep, b);
+    if (kGrad || warp < kBalWarps) rows.start(p, first, kStep, b);
     float scale = 0.f;
     if constexpr (kGrad) {
       if (!waited) {
@@ -489,15 +497,17 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_pass_
       const float mean = (float)__reduce_add_sync(0xffffffffu, sum) / (float)p.E;
       for (int e = threadIdx.x; e < EP; e += blockDim.x)
         coef[e] = e < p.E ? (float)ints[e] - mean : 0.f;
-    } else {
-      count_chunk(p, s, a, b, ints);
+      __syncthreads();
     }
-    __syncthreads();
-    float acc[L::NE];
+    if (kGrad || warp < kBalWarps) {
+      float acc[L::NE];
 #pragma unroll
-    for (int j = 0; j < L::NE; ++j) acc[j] = 0.f;
-    rows.template run<kGrad>(p, first, kStep, b, p.bias ? bias : nullptr, coef, scale, acc);
-    warp_sums<L>(acc, sums);
+      for (int j = 0; j < L::NE; ++j) acc[j] = 0.f;
+      rows.template run<kGrad>(p, first, kStep, b, p.bias ? bias : nullptr, coef, scale, acc);
+      warp_sums<L>(acc, sums);
+    } else {
+      count_chunk(p, s, a, b, ints, threadIdx.x & 31, 32, [] { __syncwarp(); });
+    }
     __syncthreads();
     float *dst = p.part + (size_t)(blockIdx.x + s) * p.E4;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
@@ -749,7 +759,7 @@ cudaError_t launch_layout(const BalParams &p, cudaStream_t st) {
     if (err == cudaSuccess)
       err = launch_k(true, balance_pass_kernel<L, true>, dim3(chunks), dim3(kBalThreads), 0, st, p);
   } else {
-    err = launch_k(false, balance_pass_kernel<L, false>, dim3(chunks), dim3(kBalThreads), 0, st, p);
+    err = launch_k(false, balance_pass_kernel<L, false>, dim3(chunks), dim3(kBalThreads + 32), 0, st, p);
   }
   if (err == cudaSuccess)
     err = launch_cluster(true, balance_finish_kernel, p.S * kCluster, kFinishWarps * 32, kCluster, st, p);

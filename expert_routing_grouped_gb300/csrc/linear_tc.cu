@@ -657,7 +657,8 @@ Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
   for (int n_tb = least; n_tb <= std::min(least + 32, 2 * least + 8); ++n_tb) {
     consider(kSolo, n_tb, 1);
     if (n_fb >= 2) consider(kPair, n_tb, 1);
-    for (int split = 2; split <= 8 && nkb / split >= 4; ++split) consider(kSplit, n_tb, split);
+    for (int split = 2; split <= 8 && n_fb * n_tb <= kClusters[split] && nkb / split >= 4; ++split)
+      consider(kSplit, n_tb, split);
   }
   return best;
 }
