@@ -16,7 +16,7 @@ ROOT = os.path.dirname(HERE)
 SOURCES = ["router.cu", "dispatch.cu", "gemv.cu", "ggemm_tc.cu", "misc.cu", "moe_api.cu",
            "route_trace.cu", "decode_tc.cu", "norm.cu", "linear.cu", "linear_tc.cu",
            "balance.cu"]
-HEADERS = ["moe_internal.cuh", "ptx.cuh", "tc.cuh", "linear.cuh"]
+HEADERS = ["moe_internal.cuh", "ptx.cuh", "tc.cuh", "linear.cuh", "area.cuh"]
 
 NVCC_FLAGS = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",

@@ -30,6 +30,7 @@
 // with cluster barriers between them: there the launches are the time.
 #include <algorithm>
 
+#include "area.cuh"
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -107,18 +108,20 @@ __device__ __forceinline__ int seg_end(const BalParams &p, int s) {
 }
 
 // The first segment that ends past token t (S if there is none), for a whole
-// warp: seq_off is non-decreasing, so each step tests 32 segments at once.
+// warp: seq_off is non-decreasing, so each step tests 32 segments at once.  In
+// any order of seq_off's values, a segment that is returned ends past t (it was
+// tested itself), so a walk that goes on from its end always moves.
 __device__ __forceinline__ int seg_of(const BalParams &p, int t) {
-  if (!p.seq_off) return 0;
+  if (!p.seq_off) return t < p.T ? 0 : 1;
   const int lane = threadIdx.x & 31;
   int lo = 0, n = p.S;                       // the answer is in [lo, lo + n]
   while (n > 0) {
     const int step = (n + 31) / 32;
     const int s = lo + min((lane + 1) * step, n) - 1;   // last of this lane's piece
-    const int ended = __popc(__ballot_sync(0xffffffffu, seg_end(p, s) <= t));
-    if (ended == 32) return lo + n;
+    const unsigned open = __ballot_sync(0xffffffffu, seg_end(p, s) > t);
+    if (!open) return lo + n;
     const int hi = lo + n;
-    lo += ended * step;
+    lo += (__ffs(open) - 1) * step;
     n = min(step, hi - lo) - 1;              // that piece's last one ends past t
   }
   return lo;
@@ -829,27 +832,19 @@ extern "C" __attribute__((visibility("default"))) int moe_balance_loss(
   // What the kernels write is apart from everything else that the call
   // touches; dz may be z itself (a row is read whole before it is written).
   {
-    const size_t ze = z_dtype == MOE_F32 ? 4 : 2, SE = (size_t)n_seq * E * 4;
-    struct Area {
-      const void *p;
-      size_t n;
-    };
-    const Area in[] = {{z, ((size_t)(T - 1) * ldz + E) * ze},
-                       {idx, (size_t)T * top_k * 4},
-                       {bias, bias ? (size_t)E * 4 : 0},
-                       {mask, mask ? (size_t)T : 0},
-                       {seq_off, seq_off ? (size_t)(n_seq + 1) * 4 : 0},
-                       {grad, grad ? (size_t)n_seq * 4 : 0}};
-    const Area wr[] = {{dz, dz ? ((size_t)(T - 1) * lddz + E) * ze : 0},
-                       {loss, (size_t)n_seq * 4},
-                       {counts, SE},
-                       {tokens, (size_t)n_seq * 4},
-                       {prob, SE},
-                       {workspace, moe_balance_workspace(T, E, n_seq)}};
-    auto meet = [](const Area &a, const Area &b) {
-      const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-      return a.n && b.n && x < y + b.n && y < x + a.n;
-    };
+    const size_t ze = z_dtype == MOE_F32 ? 4 : 2, S = n_seq, SE = S * E * 4;
+    const Area in[] = {{z, (size_t)T, E * ze, (size_t)ldz * ze},
+                       area(idx, (size_t)T * top_k * 4),
+                       area(bias, (size_t)E * 4),
+                       area(mask, T),
+                       area(seq_off, (S + 1) * 4),
+                       area(grad, S * 4)};
+    const Area wr[] = {{dz, (size_t)T, E * ze, (size_t)lddz * ze},
+                       area(loss, S * 4),
+                       area(counts, SE),
+                       area(tokens, S * 4),
+                       area(prob, SE),
+                       area(workspace, moe_balance_workspace(T, E, n_seq))};
     for (int i = 0; i < 6; ++i) {
       for (int j = 0; j < 6; ++j)
         if (!(i == 0 && j == 0 && dz == z && lddz == ldz) && meet(wr[i], in[j])) return MOE_ERR_ARG;

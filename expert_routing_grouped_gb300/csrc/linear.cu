@@ -7,6 +7,7 @@
 // SwiGLU takes 2N rows of w: y = silu(row n) * (row N + n).
 #include <algorithm>
 
+#include "area.cuh"
 #include "linear.cuh"
 
 namespace moe {
@@ -165,15 +166,6 @@ cudaError_t launch_few(const LinearParams &p, cudaStream_t st) {
   return p.T > 8 ? launch_few_w<DT, 1, true>(p, st) : launch_few_w<DT, 1, false>(p, st);
 }
 
-size_t span(int rows, int cols, long long ld, size_t elem) {
-  return ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * elem;
-}
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -213,15 +205,13 @@ extern "C" __attribute__((visibility("default"))) int moe_linear(
   // Blocks run in any order: out is apart from everything they read, but for
   // resid, which may be out itself (each element is read by the thread that
   // writes it).
-  const size_t no = span(T, N, ldo, os);
-  if (overlap(out, no, x, span(T, K, ldx, es)) || overlap(out, no, w, span(rows, K, ldw, es)) ||
-      (x_scale && overlap(out, no, x_scale, (size_t)T * 4)) ||
-      (w_scale && overlap(out, no, w_scale, (size_t)rows * 4)) ||
-      (bias && overlap(out, no, bias, (size_t)rows * 4)) ||
-      (status && overlap(out, no, status, 4)))
+  const Area ao{out, (size_t)T, N * os, (size_t)ldo * os}, ar{resid, (size_t)T, N * os, (size_t)ldr * os},
+      ax{x, (size_t)T, K * es, (size_t)ldx * es}, aw{w, (size_t)rows, K * es, (size_t)ldw * es};
+  if (meet(ao, ax) || meet(ao, aw) || meet(ao, area(x_scale, (size_t)T * 4)) ||
+      meet(ao, area(w_scale, (size_t)rows * 4)) || meet(ao, area(bias, (size_t)rows * 4)) ||
+      meet(ao, area(status, 4)))
     return MOE_ERR_ARG;
-  if (resid && !(resid == out && ldr == ldo) && overlap(out, no, resid, span(T, N, ldr, os)))
-    return MOE_ERR_ARG;
+  if (!(resid == out && ldr == ldo) && meet(ao, ar)) return MOE_ERR_ARG;
   LinearParams p{x, w, x_scale, w_scale, bias, resid, out, T, N, K, act, out_dtype,
                  ldx, ldw, ldr, ldo, status};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

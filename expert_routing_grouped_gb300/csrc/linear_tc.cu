@@ -230,22 +230,24 @@ __device__ __forceinline__ LaneRow<kSwiglu> lane_row(const LinearParams &p, int 
   return r;
 }
 
-// The residual of a block of W columns, raw, loaded ahead of its use.  SwiGLU:
-// the lane's own token of each column pair.  Tokens and features past the end
-// take the last one's address (their columns are not stored): a branch or a
-// conversion at each load would make it wait for itself.
+// The residual of a block of W columns, raw, loaded ahead of its use: a
+// conversion at each load would make it wait for itself.  SwiGLU: the lane's
+// own token of each column pair.
 template <bool kSwiglu, bool kBf16, int W>
 struct Resid {
   uint32_t v[kSwiglu ? W / 2 : W];
-  __device__ __forceinline__ void load(const LinearParams &p, const LaneRow<kSwiglu> &r, int t0) {
+  __device__ __forceinline__ void load(const LinearParams &p, const LaneRow<kSwiglu> &r, int t0, int n_cols) {
     if (!p.resid) return;
     const int up = kSwiglu && (threadIdx.x & 31) >= 16 ? 1 : 0;
-    const size_t n = min(r.n, p.N - 1);
+    const int end = r.ok ? min(p.T - t0, n_cols) - up : 0;   // columns this lane stores
+    const size_t i0 = (size_t)(t0 + up) * p.ldr + r.n;
 #pragma unroll
     for (int j = 0; j < W; j += kSwiglu ? 2 : 1) {
-      const size_t i = (size_t)min(t0 + j + up, p.T - 1) * p.ldr + n;
-      v[kSwiglu ? j / 2 : j] = kBf16 ? reinterpret_cast<const unsigned short *>(p.resid)[i]
-                                     : reinterpret_cast<const uint32_t *>(p.resid)[i];
+      uint32_t u = 0u;
+      if (j < end)
+        u = kBf16 ? reinterpret_cast<const unsigned short *>(p.resid)[i0 + (size_t)j * p.ldr]
+                  : reinterpret_cast<const uint32_t *>(p.resid)[i0 + (size_t)j * p.ldr];
+      v[kSwiglu ? j / 2 : j] = u;
     }
   }
   __device__ __forceinline__ float get(int i) const {
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
       auto chunk = [&](int c, const float *more) {
         float v[16];
         Resid<kSwiglu, kBf16, 16> res;
-        if constexpr (kMode != kSplit) res.load(p, row, tl.c0 + col_of(c));
+        if constexpr (kMode != kSplit) res.load(p, row, tl.c0 + col_of(c), 16);
         tmem_ld16(col + col_of(c), v);
         if (more) {
 #pragma unroll
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
         const int n_cols = min(4, cols - c), col = rank * share + c;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         Resid<kSwiglu, kBf16, 4> res;
-        res.load(p, row, tl.c0 + col);
+        res.load(p, row, tl.c0 + col, n_cols);
         const uint32_t src = smem_u32(smem) + ((uint32_t)col * BM + quad * 32 + lane) * 4;
         for (int r = 0; r < ranks; ++r)
 #pragma unroll

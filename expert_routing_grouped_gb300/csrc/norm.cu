@@ -13,6 +13,7 @@
 // values (16 bytes of bf16, 32 of f32) per thread and step.
 #include <algorithm>
 
+#include "area.cuh"
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -222,16 +223,6 @@ cudaError_t launch_norm_r(const NormParams &p, int T, int rt, int out_dtype, cud
   return launch_norm_o<XT, kNoResid>(p, T, out_dtype, st);
 }
 
-// Bytes that T rows of H elements with a row stride of ld elements span.
-size_t span(int T, int H, long long ld, size_t elem) {
-  return ((size_t)(T - 1) * (size_t)ld + (size_t)H) * elem;
-}
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -271,26 +262,18 @@ extern "C" __attribute__((visibility("default"))) int moe_add_rmsnorm(
        reinterpret_cast<uintptr_t>(gain)) & 15)
     return MOE_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(scale) & 3) return MOE_ERR_ARG;
-  const size_t nx = span(T, H, ldx, xe), nr = span(T, H, ldr, re), nro = span(T, H, ldro, re),
-               no = span(T, H, ldo, oe), ng = (size_t)H * 4,
-               nsc = out_dtype == MOE_E4M3 ? (size_t)T * (group ? H / group : 1) * 4 : 0;
   // Blocks run in any order, so what one writes no other may read: the output
   // and the scales are apart from everything else, and resid_out is either
   // resid itself (the same rows) or apart from what is read.
-  if (overlap(out, no, x, nx)) return MOE_ERR_ARG;
-  if (gain && overlap(out, no, gain, ng)) return MOE_ERR_ARG;
-  if (nsc && (overlap(scale, nsc, out, no) || overlap(scale, nsc, x, nx) ||
-              (gain && overlap(scale, nsc, gain, ng))))
+  const size_t n = T, h = H;
+  const Area ax{x, n, h * xe, (size_t)ldx * xe}, ar{resid, n, h * re, (size_t)ldr * re},
+      aro{resid_out, n, h * re, (size_t)ldro * re}, ao{out, n, h * oe, (size_t)ldo * oe},
+      ag = area(gain, h * 4),
+      as = area(scale, out_dtype == MOE_E4M3 ? n * (group ? h / group : 1) * 4 : 0);
+  if (meet(ao, ax) || meet(ao, ar) || meet(ao, aro) || meet(ao, ag) || meet(as, ao) || meet(as, ax) ||
+      meet(as, ar) || meet(as, aro) || meet(as, ag) || meet(aro, ax) || meet(aro, ag))
     return MOE_ERR_ARG;
-  if (resid) {
-    if (overlap(out, no, resid, nr) || overlap(out, no, resid_out, nro)) return MOE_ERR_ARG;
-    if (nsc && (overlap(scale, nsc, resid, nr) || overlap(scale, nsc, resid_out, nro)))
-      return MOE_ERR_ARG;
-    const bool in_place = resid_out == resid && ldro == ldr;
-    if (!in_place && overlap(resid_out, nro, resid, nr)) return MOE_ERR_ARG;
-    if (overlap(resid_out, nro, x, nx) || (gain && overlap(resid_out, nro, gain, ng)))
-      return MOE_ERR_ARG;
-  }
+  if (!(resid_out == resid && ldro == ldr) && meet(aro, ar)) return MOE_ERR_ARG;
   NormParams p{x, resid, resid_out, gain, out, scale, H, group ? group : H, eps,
                ldx, ldr, ldro, ldo};
   const int rt = resid ? resid_dtype : kNoResid;

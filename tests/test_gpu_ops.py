@@ -616,3 +616,187 @@ def test_linear_e4m3_every_code(moe, T, act):
     x[T - 1, 3] = 0x7F
     bad, st = run_linear(moe, x.view(E4M3), w.view(E4M3), sx, sw, None, None, N, 2, 0, act)
     assert bool(bad[T - 1].isnan().all()) and not bool(bad[:T - 1].isnan().any())
+
+
+# Large products: several tiles for each CTA pair, pairs whose second half has
+# no rows, many K segments, tiles of two widths.
+@pytest.mark.parametrize("dtype", [1, 2])
+@pytest.mark.parametrize("out_dtype", [0, 1])
+@pytest.mark.parametrize("T,K,N,act", [(3001, 512, 4097, 0), (2500, 1040, 4112, 3), (4096, 272, 2048, 1),
+                                       (600, 14336, 4096, 0), (2049, 4096, 1300, 2), (8200, 128, 1024, 0)])
+def test_linear_large(moe, T, K, N, act, dtype, out_dtype):
+    g = gen(T + N)
+    x, w, sx, sw, b, r = make_linear(g, T, K, N, dtype, act, out_dtype, True, True)
+    out, st = run_linear(moe, x, w, sx, sw, b, r, N, dtype, out_dtype, act)
+    check_linear(out, st, x, w, sx, sw, b, r, N, act)
+    again, st = run_linear(moe, x, w, sx, sw, b, r, N, dtype, out_dtype, act)
+    assert torch.equal(out, again)
+
+
+def test_linear_random_shapes(moe):
+    """Sixty seeded shapes over the whole range of forms and tilings."""
+    rs = np.random.RandomState(17)
+    for i in range(60):
+        T = int(np.exp(rs.uniform(0, np.log(3000))))
+        K = 16 * int(np.exp(rs.uniform(0, np.log(260))))
+        act = int(rs.randint(4))
+        N = int(np.exp(rs.uniform(0, np.log(2500))))
+        if act == 3:
+            N = (N + 15) // 16 * 16
+        dtype, out_dtype, bias, resid = 1 + i % 2, int(rs.randint(2)), bool(rs.randint(2)), bool(rs.randint(2))
+        x, w, sx, sw, b, r = make_linear(gen(i), T, K, N, dtype, act, out_dtype, bias, resid)
+        out, st = run_linear(moe, x, w, sx, sw, b, r, N, dtype, out_dtype, act)
+        try:
+            check_linear(out, st, x, w, sx, sw, b, r, N, act)
+        except AssertionError as e:
+            raise AssertionError("T=%d K=%d N=%d act=%d dtype=%d out=%d: %s" % (T, K, N, act, dtype, out_dtype, e))
+
+
+@pytest.mark.parametrize("T", [3, 20])
+def test_ops_offsets_past_32_bits(moe, T):
+    """Row strides that put the last rows past 2^31 elements and 2^32 bytes."""
+    far = (1 << 31) // (T - 1) // 16 * 16 + 64
+    H, N, E = 256, 64, 32
+    g = gen(T)
+    big = torch.empty((T - 1) * far + 4096, dtype=torch.bfloat16, device="cuda")
+
+    def spread(t, at):
+        v = big.as_strided((T, t.shape[1]), (far, 1), at)
+        v.copy_(t)
+        return v
+
+    x = spread(randn(g, T, H).bfloat16(), 0)
+    w = (randn(g, N, H) / 16).bfloat16()
+    resid = spread(randn(g, T, N).bfloat16(), 512)
+    out = spread(torch.zeros(T, N, device="cuda"), 1024)
+    _, st = run_linear(moe, x, w, None, None, None, resid, N, 1, 1, 0, out=out)
+    check_linear(out, st, x, w, None, None, None, resid, N, 0)
+    n = spread(torch.zeros(T, H, device="cuda"), 1536)
+    rout = spread(torch.zeros(T, H, device="cuda"), 2048)
+    r = spread(randn(g, T, H).bfloat16(), 2560)
+    moe.add_rmsnorm(x, T, H, 1e-6, n, resid=r, resid_out=rout, resid_dtype=1, x_stride=far,
+                    resid_stride=far, resid_out_stride=far, out_stride=far)
+    check_norm(x, r, None, n, None, rout, 1, 0)
+    z = spread(randn(g, T, E).bfloat16(), 3072)
+    dz = spread(torch.zeros(T, E, device="cuda"), 3584)
+    idx = torch.randint(0, E, (T, 2), generator=g, device="cuda", dtype=torch.int32)
+    loss, prob = torch.empty(1, device="cuda"), torch.empty(1, E, device="cuda")
+    counts = torch.empty(1, E, dtype=torch.int32, device="cuda")
+    tokens = torch.empty(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.balance_workspace(T, E), dtype=torch.uint8, device="cuda")
+    moe.balance_loss(z, idx, T, E, 2, loss, counts, tokens, prob, ws, z_dtype=1, alpha=0.01, dz=dz,
+                     z_stride=far, dz_stride=far)
+    check_balance((loss, counts, tokens, prob, dz), z, idx, None, None, None, 2, 0)
+
+
+def test_ops_from_two_threads(moe):
+    """Calls from two host threads at once, each on its own stream."""
+    import threading
+    a, b = ops_state(moe, 5, 300), ops_state(moe, 6, 20)
+    for s in (a, b):
+        ops_call(moe, s)
+    torch.cuda.synchronize()
+    want = [{k: s[k].clone() for k in OUTS} for s in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    bad = []
+
+    def go(s, st):
+        try:
+            for _ in range(50):
+                ops_call(moe, s, stream=st)
+        except Exception as e:   # noqa: BLE001
+            bad.append(e)
+
+    ts = [threading.Thread(target=go, args=v) for v in zip((a, b), streams)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+    for s, w in zip((a, b), want):
+        for k in OUTS:
+            assert torch.equal(s[k], w[k]), k
+
+
+def test_ops_first_call_inside_a_capture():
+    """A process whose first calls are captured (no call before to set anything up)."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import torch, expert_routing_grouped_gb300 as moe, test_gpu_ops as t\n"
+            "states = [t.ops_state(moe, 1, T) for T in (1, 40, 2000)]\n"
+            "gr = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(gr):\n"
+            "    for s in states: t.ops_call(moe, s)\n"
+            "gr.replay(); torch.cuda.synchronize()\n"
+            "got = [{k: s[k].clone() for k in t.OUTS} for s in states]\n"
+            "for s in states: t.ops_call(moe, s)\n"
+            "torch.cuda.synchronize()\n"
+            "assert all(torch.equal(g[k], s[k]) for g, s in zip(got, states) for k in t.OUTS)\n"
+            % (os.path.dirname(here), here))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("S", [7, 300, 3000])
+def test_balance_many_segments(moe, S):
+    """More segments than a warp looks at once, many of them empty or of one
+    token, in each of the kernels' forms."""
+    T, E, k = 9000, 64, 4
+    g = gen(S)
+    z, idx, _, m = make_balance(g, T, E, k, 0, 1, True)
+    rs = np.random.RandomState(S)
+    cuts = [np.sort(rs.randint(0, T + 1, S + 1)), np.minimum(np.arange(S + 1) * 2, T),
+            np.concatenate([np.zeros(S // 2, int), np.full(S + 1 - S // 2, T)])]
+    for cut in cuts:
+        off = torch.tensor(cut, dtype=torch.int32, device="cuda")
+        got = run_balance(moe, z, idx, None, m, off, k, 1)
+        check_balance(got, z, idx, None, m, off, k, 1)
+        plain = run_balance(moe, z, idx, None, m, off, k, 1, want_dz=False)
+        for a, b in zip(got[:4], plain[:4]):
+            assert torch.equal(a, b)
+
+
+def test_balance_disordered_segments_stay_in_bounds(moe):
+    """seq_off that is not what the header asks for: any values, but nothing
+    outside the outputs is written."""
+    T, E, k = 5000, 64, 2
+    z, idx, _, _ = make_balance(gen(3), T, E, k, 0)
+    for bad in ([5000, 0, 9999, -7, 100], [-2 ** 31, 2 ** 31 - 1, 3, 3, 4000], [10, 5, 4, 3, 2]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        for n, dt in ((T, True), (300, False)):
+            buf = torch.full((n + 2, E), SENT, device="cuda")
+            S = len(bad) - 1
+            f = dict(device="cuda")
+            outs = [torch.full((S * c + 2,), 72, dtype=d, **f)
+                    for c, d in ((1, torch.float32), (E, torch.int32), (1, torch.int32), (E, torch.float32))]
+            nb = moe.balance_workspace(n, E, S)
+            ws = torch.full((nb + 64,), 0x55, dtype=torch.uint8, **f)
+            moe.balance_loss(z, idx, n, E, k, outs[0][1:], outs[1][1:], outs[2][1:], outs[3][1:], ws[:nb],
+                             seq_off=off, n_seq=S, dz=buf[1:] if dt else None)
+            torch.cuda.synchronize()
+            assert bool((buf[0] == SENT).all()) and bool((buf[-1] == SENT).all())
+            assert bool((ws[nb:] == 0x55).all())
+            for o in outs:
+                assert int(o[0]) == 72 and int(o[-1]) == 72
+
+
+def test_ops_on_columns_of_one_tensor(moe):
+    """Operands and results side by side in the rows of one tensor."""
+    g = gen(12)
+    T, H, N = 50, 256, 96
+    wide = torch.full((T, 4 * 1024), SENT, device="cuda").bfloat16()
+    x, out, n, rout, resid = (wide[:, a:a + c] for a, c in ((0, H), (H, N), (512, H), (1024, H), (2048, H)))
+    x.copy_(randn(g, T, H))
+    resid.copy_(randn(g, T, H))
+    w = (randn(g, N, H) / 16).bfloat16()
+    _, st = run_linear(moe, x, w, None, None, None, None, N, 1, 1, 0, out=out)
+    check_linear(out, st, x, w, None, None, None, None, N, 0)
+    moe.add_rmsnorm(x, T, H, 1e-6, n, resid=resid, resid_out=rout, resid_dtype=1, x_stride=4096,
+                    resid_stride=4096, resid_out_stride=4096, out_stride=4096)
+    check_norm(x, resid, None, n, None, rout, 1, 0)
+    for a, b in ((H + N, 512), (768, 1024), (1280, 2048), (2304, 4096)):
+        assert bool((wide[:, a:b].float() == SENT).all())

@@ -125,3 +125,18 @@ def test_balance_workspace_sizes():
 def test_balance_dry_run():
     assert balance(T=0, z=None, idx=None, loss=None, ws=None, nb=0) == 0
     assert balance(T=0, mode=5) == moe.MOE_ERR_ROUTING
+
+
+def test_columns_of_one_tensor_that_meet():
+    """Column slices of one wider tensor (one row stride) may be apart; these
+    are not: a row further, or a byte into the neighbour's columns.  (Slices
+    that are apart are accepted: the GPU tests use them.)"""
+    base, H, wide = addr(0), 512, 4 * 512
+    cols = dict(x=base, resid=base + H * 4, resid_out=base + 2 * H * 4, x_dtype=0, xs=wide, rs=wide,
+                ros=wide, os=4 * wide)
+    assert norm(out=base + wide * 4, **cols) == moe.MOE_ERR_ARG
+    assert norm(out=base + 4 * wide - 496, **cols) == moe.MOE_ERR_ARG
+    assert linear(x=base, out=base + 512 * 2, resid=base + 512 * 2 + 200, xs=2048, os=1024, rs=1024,
+                  bias=None) == moe.MOE_ERR_ARG
+    assert linear(x=base, out=base + 1000, xs=2048, os=1024, resid=None, bias=None) == moe.MOE_ERR_ARG
+    assert balance(z=base, dz=base + 60, zs=64, dzs=64) == moe.MOE_ERR_ARG
