@@ -209,20 +209,31 @@ __device__ __forceinline__ void total_counts(const BalParams &p, int s, int32_t 
   __syncthreads();
   const int2 sl = count_slots(p, s);
   const int row = p.E4 + 4;
-  for (int e = 4 * lane; e <= p.E4; e += 128) {   // the piece at E4: kept tokens, rest unused
-    int4 c = make_int4(0, 0, 0, 0);
-#pragma unroll 8
+  int n = 0;
+  for (int i = sl.x + (int)threadIdx.x; i < sl.y; i += blockDim.x)
+    n += __ldcg(p.cnt + (size_t)i * row + p.E4);
+  for (int e = 4 * lane; e < p.E4; e += 256) {   // two pieces of a slot at a time
+    int4 c = make_int4(0, 0, 0, 0), d = make_int4(0, 0, 0, 0);
+    const bool two = e + 128 < p.E4;
+#pragma unroll 4
     for (int i = sl.x + warp; i < sl.y; i += nw) {
-      const int4 v = __ldcg(reinterpret_cast<const int4 *>(p.cnt + (size_t)i * row + e));
-      c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
+      const int32_t *src = p.cnt + (size_t)i * row + e;
+      const int4 u = __ldcg(reinterpret_cast<const int4 *>(src));
+      const int4 v = two ? __ldcg(reinterpret_cast<const int4 *>(src + 128)) : make_int4(0, 0, 0, 0);
+      c.x += u.x, c.y += u.y, c.z += u.z, c.w += u.w;
+      d.x += v.x, d.y += v.y, d.z += v.z, d.w += v.w;
     }
     if (c.x) atomicAdd(&sum[e], c.x);
-    if (e < p.E4) {
-      if (c.y) atomicAdd(&sum[e + 1], c.y);
-      if (c.z) atomicAdd(&sum[e + 2], c.z);
-      if (c.w) atomicAdd(&sum[e + 3], c.w);
-    }
+    if (c.y) atomicAdd(&sum[e + 1], c.y);
+    if (c.z) atomicAdd(&sum[e + 2], c.z);
+    if (c.w) atomicAdd(&sum[e + 3], c.w);
+    if (d.x) atomicAdd(&sum[e + 128], d.x);
+    if (d.y) atomicAdd(&sum[e + 129], d.y);
+    if (d.z) atomicAdd(&sum[e + 130], d.z);
+    if (d.w) atomicAdd(&sum[e + 131], d.w);
   }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0 && n) atomicAdd(&sum[p.E4], n);
   __syncthreads();
 }
 
