@@ -266,23 +266,22 @@ struct Lay {
     uint32_t w[N];
   };
   static constexpr uint32_t kNone = DT == MOE_F32 ? 0xFF800000u : 0xFF80FF80u;
-  static __device__ __forceinline__ void load(const BalParams &p, int t, bool there, Raw &r) {
+  static constexpr int ES = DT == MOE_F32 ? 4 : 2;
+  // row: the token's first logit of this lane, i.e. of expert first(0).
+  static __device__ __forceinline__ void load(const BalParams &p, const char *row, bool there, Raw &r) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = first(i);
-      const bool in = there && e < p.E;
-      const size_t at = (size_t)t * p.ldz + e;
+      const bool in = there && first(i) < p.E;
+      const char *at = row + i * (LPR * VEC * ES);
       if constexpr (VEC == 1) {
         r.w[i] = kNone;
         if (in) {
-          if constexpr (DT == MOE_F32) r.w[i] = __float_as_uint(__ldcs(reinterpret_cast<const float *>(p.z) + at));
-          else r.w[i] = __ldcs(reinterpret_cast<const unsigned short *>(p.z) + at);
+          if constexpr (DT == MOE_F32) r.w[i] = __float_as_uint(__ldcs(reinterpret_cast<const float *>(at)));
+          else r.w[i] = __ldcs(reinterpret_cast<const unsigned short *>(at));
         }
       } else {
         uint4 u = make_uint4(kNone, kNone, kNone, kNone);
-        if (in)
-          u = __ldcs(reinterpret_cast<const uint4 *>(
-              reinterpret_cast<const char *>(p.z) + at * (DT == MOE_F32 ? 4 : 2)));
+        if (in) u = __ldcs(reinterpret_cast<const uint4 *>(at));
         r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
       }
     }
@@ -293,18 +292,16 @@ struct Lay {
     const uint32_t w = r.w[j / 2];
     return __uint_as_float((j & 1) ? (w & 0xFFFF0000u) : (w << 16));
   }
-  static __device__ __forceinline__ void store(const BalParams &p, int t, const float (&d)[NE]) {
+  static __device__ __forceinline__ void store(const BalParams &p, char *row, const float (&d)[NE]) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = first(i);
-      if (e >= p.E) continue;
-      const size_t at = (size_t)t * p.lddz + e;
+      if (first(i) >= p.E) continue;
+      char *at = row + i * (LPR * VEC * ES);
       if constexpr (VEC == 1) {
-        if constexpr (DT == MOE_F32) __stcs(reinterpret_cast<float *>(p.dz) + at, d[i]);
-        else reinterpret_cast<__nv_bfloat16 *>(p.dz)[at] = __float2bfloat16_rn(d[i]);
+        if constexpr (DT == MOE_F32) __stcs(reinterpret_cast<float *>(at), d[i]);
+        else *reinterpret_cast<__nv_bfloat16 *>(at) = __float2bfloat16_rn(d[i]);
       } else if constexpr (DT == MOE_F32) {
-        __stcs(reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.dz) + at),
-               make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]));
+        __stcs(reinterpret_cast<float4 *>(at), make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]));
       } else {
         uint32_t w[4];
 #pragma unroll
@@ -312,8 +309,7 @@ struct Lay {
           const __nv_bfloat162 h = __floats2bfloat162_rn(d[8 * i + 2 * c], d[8 * i + 2 * c + 1]);
           w[c] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        __stcs(reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.dz) + at),
-               make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs(reinterpret_cast<uint4 *>(at), make_uint4(w[0], w[1], w[2], w[3]));
       }
     }
   }
@@ -341,17 +337,19 @@ __device__ __forceinline__ float rcp_fast(float v) {
   return r;
 }
 
+// With u the sigmoid (or exp(z - max)) and inv 1 / sum u: p = u inv, and
+//   dz_i = scale inv u_i (1 - sigmoid_i) (coef_i - dot),  dot = inv sum u_e coef_e
 template <class L, bool kGrad>
-__device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &raw, int t, bool valid,
+__device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &raw, char *dst, bool valid,
                                           bool write, const float *bias, const float *coef, float scale,
                                           float (&acc)[L::NE]) {
-  float v[L::NE], om[L::kSig && kGrad ? L::NE : 1];
+  float u[L::NE], w[L::kSig && kGrad ? L::NE : 1];   // w: u (1 - sigmoid)
   if constexpr (L::LPR == 32) {   // the warp's one token
     if (!valid) {
       if (kGrad && write) {
 #pragma unroll
-        for (int j = 0; j < L::NE; ++j) v[j] = 0.f;
-        L::store(p, t, v);
+        for (int j = 0; j < L::NE; ++j) u[j] = 0.f;
+        L::store(p, dst, u);
       }
       return;
     }
@@ -364,46 +362,44 @@ __device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &r
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
       const float ex = exp_fast(-L::get(raw, j));
-      v[j] = rcp_fast(1.0f + ex);   // 0 from 2^126 on
-      // 1 - sigmoid keeps its digits as exp(-z) sigmoid where the sigmoid is
-      // near 1.
-      if constexpr (kGrad) om[j] = ex < 1.0f ? ex * v[j] : 1.0f - v[j];
-      tot += v[j];
+      u[j] = rcp_fast(1.0f + ex);   // 0 from 2^126 on
+      // 1 - sigmoid as exp(-z) sigmoid: its digits stay where the sigmoid is
+      // near 1.  The bound keeps infinity times 0 out; a NaN is in u.
+      if constexpr (kGrad) w[j] = u[j] * (fminf(ex, 8.5e37f) * u[j]);
+      tot += u[j];
     }
   } else {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      v[j] = L::get(raw, j);
-      if (bias) v[j] += bias[L::first(j / L::VEC) + j % L::VEC];
-      m = fmaxf(m, v[j]);
+      u[j] = L::get(raw, j);
+      if (bias) u[j] += bias[L::first(j / L::VEC) + j % L::VEC];
+      m = fmaxf(m, u[j]);
     }
     m = L::max(m);
     if (m == -INFINITY) m = 0.f;   // a row with nothing left: p = 0
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      v[j] = exp_fast(v[j] - m);
-      tot += v[j];
+      u[j] = exp_fast(u[j] - m);
+      tot += u[j];
     }
   }
   tot = L::sum(tot);
-  const float inv = tot == 0.f ? 0.f : 1.0f / tot;
-  float dot = 0.f;
+  const float inv = tot == 0.f ? 0.f : rcp_fast(tot);   // tot >= 2^-126 otherwise
 #pragma unroll
-  for (int j = 0; j < L::NE; ++j) {
-    v[j] = __fmul_rn(v[j], inv);   // not fused into the sum: the same bits with and without dz
-    acc[j] += v[j];
-    if constexpr (kGrad) dot = fmaf(v[j], coef[L::first(j / L::VEC) + j % L::VEC], dot);
-  }
+  for (int j = 0; j < L::NE; ++j) acc[j] = fmaf(u[j], inv, acc[j]);
   if constexpr (kGrad) {
-    dot = L::sum(dot);
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < L::NE; ++j) dot = fmaf(u[j], coef[L::first(j / L::VEC) + j % L::VEC], dot);
+    dot = L::sum(dot) * inv;
+    const float k = scale * inv;
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
-      float d = scale * v[j] * (coef[L::first(j / L::VEC) + j % L::VEC] - dot);
-      if constexpr (L::kSig) d *= om[j];
-      v[j] = d;
+      const float c = (coef[L::first(j / L::VEC) + j % L::VEC] - dot) * k;
+      u[j] = c * (L::kSig ? w[j] : u[j]);
     }
-    if (write) L::store(p, t, v);
+    if (write) L::store(p, dst, u);
   }
 }
 
@@ -416,32 +412,36 @@ struct Rows {
   static constexpr int kAhead = L::NE <= 8 ? 3 : L::NE <= 16 ? 2 : 1;
   typename L::Raw raw[kAhead];
   bool valid[kAhead];
-  static __device__ __forceinline__ int token(int row) {
-    return row + (int)(threadIdx.x & 31) / L::LPR;
-  }
+  int t;              // the next token to fetch, its logits, and its mask
+  const char *z;
   // The logits' load does not wait for the mask's.
-  __device__ __forceinline__ void fetch(const BalParams &p, int i, int row, int b) {
-    const int t = token(row);
+  __device__ __forceinline__ void fetch(const BalParams &p, int i, int step, int b) {
     valid[i] = t < b && (!p.mask || p.mask[t]);
-    L::load(p, t, t < b, raw[i]);
+    L::load(p, z, t < b, raw[i]);
+    t += step;
+    z += (size_t)step * p.ldz * L::ES;
   }
   __device__ __forceinline__ void start(const BalParams &p, int first, int step, int b) {
+    t = first + (int)(threadIdx.x & 31) / L::LPR;
+    z = reinterpret_cast<const char *>(p.z) + ((size_t)t * p.ldz + L::first(0)) * L::ES;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(p, i, first + i * step, b);
+    for (int i = 0; i < kAhead; ++i) fetch(p, i, step, b);
   }
   template <bool kGrad>
   __device__ __forceinline__ void run(const BalParams &p, int first, int step, int b, const float *bias,
                                       const float *coef, float scale, float (&acc)[L::NE]) {
+    int now = first + (int)(threadIdx.x & 31) / L::LPR;
+    char *dst = reinterpret_cast<char *>(p.dz) + ((size_t)now * p.lddz + L::first(0)) * L::ES;
     for (int row0 = first; row0 < b; row0 += kAhead * step) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int row = row0 + i * step;
-        if (row < b) {
-          typename L::Raw now = raw[i];
+        if (row0 + i * step < b) {   // the same for the whole warp
+          typename L::Raw mine = raw[i];
           const bool ok = valid[i];
-          fetch(p, i, row + kAhead * step, b);
-          const int t = token(row);
-          one_token<L, kGrad>(p, now, t, ok, t < b, bias, coef, scale, acc);
+          fetch(p, i, step, b);
+          one_token<L, kGrad>(p, mine, dst, ok, now < b, bias, coef, scale, acc);
+          now += step;
+          if constexpr (kGrad) dst += (size_t)step * p.lddz * L::ES;
         }
       }
     }
