@@ -67,7 +67,8 @@ struct TcLinear {
   CUtensorMap map_w;       // [rows][K], box 128 x 128 bytes; SwiGLU: [N/16][2][16][K]
   CUtensorMap map_x;       // [T][K], box of a CTA's tokens x 128 bytes
   LinearParams p;
-  int unit, units;         // tokens come in `units` units of 16 (pairs: 32)
+  int unit, units_tb;      // tokens come in units of 16 (pairs: 32), units_tb to a tile
+  int n_wide;              // and one more to the first n_wide
   int bn;                  // most tokens of a tile
   int x_rows;              // tokens a CTA loads per tile (bn, in pairs bn / 2)
   int n_fb, n_tb;          // tiles along the outputs (in pairs: of 256 rows) and the tokens
@@ -183,22 +184,26 @@ __device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// Tile t of the raster: output tile fb, tokens c0 .. c0 + w - 1.  Token tiles
-// run fastest within groups of group_tb, so the CTAs of a wave share few w and
-// x tiles and both stay in L2.
+// Tile t of the raster: output tile fb, tokens c0 .. c0 + w - 1.  The first
+// n_wide token tiles have a unit more than the others, and all of theirs come
+// first: dealt out in turn, the wide tiles then spread over the CTAs.  Token
+// tiles run fastest within groups of group_tb, so the CTAs of a wave share few
+// w and x tiles and both stay in L2.
 struct Tile {
   int fb, c0, w;
 };
 __device__ __forceinline__ Tile tile_at(const TcLinear &q, int t) {
+  const int wide = q.n_fb * q.n_wide;
+  const int first = t < wide ? 0 : q.n_wide, n_tb = t < wide ? q.n_wide : q.n_tb - q.n_wide;
+  if (t >= wide) t -= wide;
   const int per = q.group_tb * q.n_fb;
   const int g = t / per, r = t - g * per;
-  const int width = min(q.group_tb, q.n_tb - g * q.group_tb);
+  const int width = min(q.group_tb, n_tb - g * q.group_tb);
   Tile tl;
   tl.fb = r / width;
-  const int tb = g * q.group_tb + (r - tl.fb * width);
-  const int u0 = (int)((long long)q.units * tb / q.n_tb);
-  tl.c0 = u0 * q.unit;
-  tl.w = (int)((long long)q.units * (tb + 1) / q.n_tb) * q.unit - tl.c0;
+  const int tb = first + g * q.group_tb + (r - tl.fb * width);
+  tl.c0 = (tb * q.units_tb + min(tb, q.n_wide)) * q.unit;
+  tl.w = (q.units_tb + (tb < q.n_wide ? 1 : 0)) * q.unit;
   return tl;
 }
 
@@ -640,16 +645,20 @@ Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
     if (w > max_bn) return;
     const long long tiles = (long long)up(rows, mode == kPair ? 2 * BM : BM) * n_tb;
     if (mode == kSplit && tiles > (long long)kClusters[split] * sms / 152) return;
-    const int slots = mode == kPair ? sms / 2 : sms;
-    const double waves = mode == kSplit ? 1.0 : (double)((tiles + slots - 1) / slots);
-    // Tiles of two widths: between their mean and the larger.
-    const double we = 0.5 * (w + (double)units * unit / n_tb);
-    const double mma = 4.0 * std::max((we + 24.0) / 2.0, 59.0);
-    const double mem = 1.74 * (BM + (mode == kPair ? w / 2 : w));
+    // The CTA with most work takes every slots-th tile from the first: as many
+    // columns as blocks of MMAs, each block with its own floor and 12 clocks.
+    const long long slots = mode == kSplit ? tiles : mode == kPair ? sms / 2 : sms;
+    const long long waves = (tiles + slots - 1) / slots, wide = (long long)(tiles / n_tb) * (units % n_tb);
+    const long long wide_waves = std::min(waves, (wide + slots - 1) / slots);
+    auto block = [&](int w1) {
+      return std::max(4.0 * std::max((w1 + 24.0) / 2.0, 59.0),
+                      1.74 * (BM + (mode == kPair ? w1 / 2 : w1)));
+    };
+    const int narrow = units / n_tb * unit;
+    const double clocks = wide_waves * block(narrow + unit) + (waves - wide_waves) * block(narrow);
     const double bytes = ((double)rows + T) * nkb * kRowBytes / 3500.0;
     const double start = mode == kSolo ? 8500.0 : mode == kPair ? 10500.0 : 11500.0;
-    const double cost =
-        std::max(waves * std::max(1.0, (double)nkb / split) * std::max(mma, mem), bytes) + start + 12.0 * w;
+    const double cost = std::max(clocks * std::max(1.0, (double)nkb / split), bytes) + start + 12.0 * w;
     if (cost < best_cost) {
       best_cost = cost;
       best = Plan{mode, n_tb, split};
@@ -724,9 +733,11 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   const Plan plan = plan_of(p.T, rows, q.nkb, sms, p.out_dtype == MOE_F32 ? kSegMaxBN : kMaxBN);
   const bool pair = plan.mode == kPair;
   q.unit = pair ? 32 : 16;
-  q.units = up(p.T, q.unit);
+  const int units = up(p.T, q.unit);
   q.n_tb = plan.n_tb;
-  q.bn = up(q.units, q.n_tb) * q.unit;
+  q.units_tb = units / q.n_tb;
+  q.n_wide = units % q.n_tb;
+  q.bn = up(units, q.n_tb) * q.unit;
   q.x_rows = pair ? q.bn / 2 : q.bn;
   q.n_fb = up(rows, pair ? 2 * BM : BM);
   q.group_tb = std::min(q.n_tb, 16);
