@@ -58,9 +58,12 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t *row, int off, int byt
 }
 
 // NB: row blocks of 8 per warp -- 1, or 2 (SwiGLU: the gate rows, then the up
-// rows).  HI: more than 8 tokens.  W: warps.  Each lane has four 16-byte
-// pieces of w in flight whatever NB.
-template <int DT, int NB, bool HI, int W>
+// rows).  HI: more than 8 tokens.  W: warps.  kFold (bf16 operands, f32
+// output): the MMAs truncate as they add, 1.8e-8 of the result each, so every
+// four steps their sums are added in f32 to nearest (K = 14336: error 4.5e-7 in
+// place of 1.8e-6, 19.7 us in place of 19.5); a bf16 output does not see it.
+// Each lane has four 16-byte pieces of w in flight whatever NB.
+template <int DT, int NB, bool HI, int W, bool kFold>
 __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const LinearParams p) {
   constexpr int TT = HI ? 16 : 8;
   __shared__ float red[W][TT][8 * NB];
@@ -97,6 +100,19 @@ __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const Linear
       hi[s][i] = HI ? load_piece<false>(xh, off, hi_kb) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
+  float sum[kFold ? NB : 1][4] = {};
+  int steps = 0;
+  auto fold = [&] {
+    if constexpr (kFold) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[b][i] += c[b][i];
+          c[b][i] = 0.f;
+        }
+    }
+  };
   auto work = [&](int s) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
@@ -105,6 +121,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const Linear
         mma_m16n8<DT>(c[b], lo[s][i].x, hi[s][i].x, lo[s][i].y, hi[s][i].y, wv[s][b][i].x, wv[s][b][i].y);
         mma_m16n8<DT>(c[b], lo[s][i].z, hi[s][i].z, lo[s][i].w, hi[s][i].w, wv[s][b][i].z, wv[s][b][i].w);
       }
+    if (kFold && (++steps & 3) == 0) fold();
   };
   // The warp's units: U of every W U.
   constexpr int kStep = W * U;
@@ -120,6 +137,13 @@ __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const Linear
       work(1);
       u += kStep;
     }
+  }
+  if constexpr (kFold) {
+    fold();
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[b][i] = sum[b][i];
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -152,18 +176,18 @@ __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const Linear
 // Warps per block: 8 where there are two blocks for every SM, 16 where there
 // are fewer (more bytes in flight).  bf16, one token: N = 4096, K = 4096 6.7 us
 // with 8, 7.4 with 16; N = 256, K = 6144 3.8 us with 8, 3.1 with 16.
-template <int DT, int NB, bool HI>
+template <int DT, int NB, bool HI, bool kFold>
 cudaError_t launch_few_w(const LinearParams &p, cudaStream_t st) {
   const int blocks = (p.N + 7) / 8;
-  return blocks > 304 ? launch_k(false, linear_few_kernel<DT, NB, HI, 8>, dim3(blocks), dim3(256), 0, st, p)
-                       : launch_k(false, linear_few_kernel<DT, NB, HI, 16>, dim3(blocks), dim3(512), 0, st, p);
+  return blocks > 304 ? launch_k(false, linear_few_kernel<DT, NB, HI, 8, kFold>, dim3(blocks), dim3(256), 0, st, p)
+                      : launch_k(false, linear_few_kernel<DT, NB, HI, 16, kFold>, dim3(blocks), dim3(512), 0, st, p);
 }
 
-template <int DT>
+template <int DT, bool kFold>
 cudaError_t launch_few(const LinearParams &p, cudaStream_t st) {
   if (p.act == MOE_ACT_SWIGLU)
-    return p.T > 8 ? launch_few_w<DT, 2, true>(p, st) : launch_few_w<DT, 2, false>(p, st);
-  return p.T > 8 ? launch_few_w<DT, 1, true>(p, st) : launch_few_w<DT, 1, false>(p, st);
+    return p.T > 8 ? launch_few_w<DT, 2, true, kFold>(p, st) : launch_few_w<DT, 2, false, kFold>(p, st);
+  return p.T > 8 ? launch_few_w<DT, 1, true, kFold>(p, st) : launch_few_w<DT, 1, false, kFold>(p, st);
 }
 
 }  // namespace
@@ -215,8 +239,9 @@ extern "C" __attribute__((visibility("default"))) int moe_linear(
   LinearParams p{x, w, x_scale, w_scale, bias, resid, out, T, N, K, act, out_dtype,
                  ldx, ldw, ldr, ldo, status};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = T > kFewTokens      ? launch_linear_tc(p, dtype, st)
-                          : dtype == MOE_BF16 ? launch_few<MOE_BF16>(p, st)
-                                              : launch_few<MOE_E4M3>(p, st);
+  const cudaError_t err = T > kFewTokens            ? launch_linear_tc(p, dtype, st)
+                          : dtype == MOE_E4M3       ? launch_few<MOE_E4M3, false>(p, st)
+                          : out_dtype == MOE_F32    ? launch_few<MOE_BF16, true>(p, st)
+                                                    : launch_few<MOE_BF16, false>(p, st);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
