@@ -24,7 +24,7 @@ namespace {
 // TB/s).  A ring of cp.async pieces in shared memory in place of the registers
 // was slower at every size (K = 14336, N = 4096: 23.1 against 19.4 us), and so
 // were 16 outputs a block.
-//
+
 template <int DT>
 __device__ __forceinline__ void mma_m16n8(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {

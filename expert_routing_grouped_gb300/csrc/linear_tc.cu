@@ -2,7 +2,7 @@
 //
 // D[128 rows of w][BN tokens] = w_tile . x_tile^T: the weights are the MMA's M
 // side, so a short batch wastes no tensor rows on absent tokens (BN follows T
-// in steps of 32) and an epilogue lane owns one output feature, whose bias and
+// in steps of 16) and an epilogue lane owns one output feature, whose bias and
 // scale it loads once.  Both operands come by TMA, 128 bytes of K a row and
 // stage (64 bf16 or 128 e4m3 values), 128-byte swizzled.
 //
@@ -17,7 +17,7 @@
 // accumulator is handed over every kSegBlocks K blocks and the epilogue adds
 // the segments in f32 to nearest, in registers: under 1e-6 whatever K.  Reading
 // an accumulator takes TMEM from the MMAs, about 300 clocks: 2048 x 14336 x
-// 4096 onto an f32 stream takes 147 us in one segment, 163 in segments of 16.
+// 4096 onto an f32 stream takes 147 us in one segment, 167 in segments of 12.
 //
 // Three forms (kMode):
 //   pair   large products: two CTAs on neighbouring SMs form one 256-row tile
@@ -34,6 +34,11 @@
 //          call.
 // The tokens are cut into n_tb nearly equal tiles (a difference of one unit of
 // 16, in pairs 32), so that the tiles fill whole waves of the SMs.
+//
+// Measured: 8192^3 bf16 566 us (1.94 PFLOP/s, 1.02 of a library product's burst
+// rate; 647 us in the solo form), 4096 x 6144 x 6144 164 us, 4096 x 4096 x 14336
+// e4m3 SwiGLU 270 us (3.56 PFLOP/s); 64 x 6144 x 1024, split in 8, 8.7 us, of
+// which about 6 are start, exchange and end.
 //
 // Every mbarrier wait is bounded: one that gives up sets the status word, and
 // the roles stop, drain their copies and MMAs, and return.
