@@ -44,7 +44,7 @@ constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalBlocks = 456;          // most chunks of a call: 3 blocks on each of 152 SMs
 constexpr int kCountThreads = 1024;
-constexpr int kCluster = 8;
+constexpr int kCluster = 8;              // PeerWords reads as many
 constexpr long long kSmallElems = 1 << 16, kSmallTotal = 1 << 22;   // see is_small
 
 struct BalParams {
@@ -102,6 +102,28 @@ __device__ __forceinline__ uint32_t ld_peer(const void *p, uint32_t rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+
+// The words at p of all CTAs (r < ranks, at most kCluster), all asked for before
+// the first is used.
+struct PeerWords {
+  uint32_t w[8];
+  __device__ __forceinline__ PeerWords(const void *p, int ranks) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) w[r] = r < ranks ? ld_peer(p, r) : 0u;
+  }
+  __device__ __forceinline__ int sum() const {
+    int c = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) c += (int)w[r];
+    return c;
+  }
+  __device__ __forceinline__ float fsum() const {   // in rank order
+    float c = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) c += __uint_as_float(w[r]);
+    return c;
+  }
+};
 
 // First and past-the-last token of segment s, inside [0, T] whatever seq_off holds.
 __device__ __forceinline__ int seg_begin(const BalParams &p, int s) {
@@ -669,16 +691,14 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small
   count_rows(p, a, b, rank * blockDim.x + threadIdx.x, ranks * blockDim.x, hist);
   cluster_sync();
   // Every CTA adds up the whole segment's counts for itself (coef: as floats).
-  int sum = 0, n = 0;
+  int sum = 0;
+  const int n = PeerWords(&hist[p.E], ranks).sum();
   for (int e = threadIdx.x; e < EP; e += blockDim.x) {
-    int c = 0;
-    if (e < p.E)
-      for (int r = 0; r < ranks; ++r) c += (int)ld_peer(&hist[e], r);
+    const int c = e < p.E ? PeerWords(&hist[e], ranks).sum() : 0;
     coef[e] = (float)c;
     sum += c;
     if (rank == 0 && e < p.E) p.counts[(size_t)s * p.E + e] = c;
   }
-  for (int r = 0; r < ranks; ++r) n += (int)ld_peer(&hist[p.E], r);
   if (rank == 0 && threadIdx.x == 0) p.tokens[s] = n;
   sum = __reduce_add_sync(0xffffffffu, sum);
   if ((threadIdx.x & 31) == 0) atomicAdd(&total, sum);
@@ -704,9 +724,7 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small
   cluster_sync();
   float dot = 0.f;
   for (int e = rank + ranks * (int)threadIdx.x; e < p.E; e += ranks * blockDim.x) {
-    float tot = 0.f;
-    for (int r = 0; r < ranks; ++r) tot += __uint_as_float(ld_peer(&mine[e], r));
-    tot *= inv;
+    const float tot = PeerWords(&mine[e], ranks).fsum() * inv;
     p.prob[(size_t)s * p.E + e] = tot;
     sums[EP + e] = (coef[e] + mean) * tot;   // past `mine`, which the peers read
   }

@@ -585,14 +585,20 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
       const int cols = min(share, tl.w - rank * share);
       for (int c = turn * 4; c < cols; c += 4 * G) {
         const int n_cols = min(4, cols - c), col = rank * share + c;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
         Resid<kSwiglu, kBf16, 4> res;
         res.load(p, row, tl.c0 + col, n_cols);
+        // All ranks' partials are asked for before the first is added.
         const uint32_t src = smem_u32(smem) + ((uint32_t)col * BM + quad * 32 + lane) * 4;
-        for (int r = 0; r < ranks; ++r)
+        float part[8][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < n_cols) v[j] += ld_peer(src + j * BM * 4, r);
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) part[r][j] = r < ranks && j < n_cols ? ld_peer(src + j * BM * 4, r) : 0.f;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] += part[r][j];
         finish_columns<kSwiglu, kBf16>(p, row, v, res, tl.c0 + col, n_cols);
       }
     }

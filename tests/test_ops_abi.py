@@ -117,8 +117,8 @@ def test_balance_workspace_sizes():
     ws = moe.balance_workspace
     assert ws(0, 8, 1) == 0 and ws(4, 0, 1) == 0 and ws(4, 1025, 1) == 0 and ws(4, 8, 0) == 0
     assert 0 < ws(1, 8, 1) <= ws(64, 8, 1) <= ws(1 << 20, 8, 1)
-    # bounded whatever T: at most 3072 runs of tokens, and one for each segment
-    assert ws(1 << 25, 1024, 64) <= (3 * 1024 + 64) * (2 * 1024 + 4) * 4 + 4096
+    # bounded whatever T: at most 456 runs of tokens, and one for each segment
+    assert ws(1 << 25, 1024, 64) <= (456 + 64) * (2 * 1024 + 4) * 4
     assert balance(nb=ws(64, 16, 3) - 1) == moe.MOE_ERR_NOMEM
 
 
