@@ -56,7 +56,10 @@ constexpr int BM = 128;             // rows of w per tile
 constexpr int kRowBytes = 128;      // K bytes per row and stage
 constexpr int kMaxStages = 8;
 constexpr int kEpiWarp0 = 4;
-constexpr int kSegBlocks = 12;      // K blocks per accumulator segment (f32 output)
+// K blocks per accumulator segment (f32 output); SwiGLU multiplies two sums, and
+// their errors add.
+template <bool kSwiglu>
+constexpr int kSegBlocks = kSwiglu ? 7 : 12;
 constexpr int kMaxBN = 256;
 constexpr int kSegMaxBN = 192;      // with segment sums in registers
 // Epilogue warps per lane quadrant: they take turns at blocks of 16 columns.
@@ -396,7 +399,8 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
   const int t_first = blockIdx.x / ranks, t_step = gridDim.x / ranks;
   const int kb0 = kMode == kSplit ? (int)((long long)q.nkb * rank / ranks) : 0;
   const int kb1 = kMode == kSplit ? (int)((long long)q.nkb * (rank + 1) / ranks) : q.nkb;
-  const int n_seg = kSegs ? (kb1 - kb0 + kSegBlocks - 1) / kSegBlocks : 1;
+  constexpr int kSeg = kSegBlocks<kSwiglu>;
+  const int n_seg = kSegs ? (kb1 - kb0 + kSeg - 1) / kSeg : 1;
   auto seg_at = [&](int s) { return kb0 + (int)((long long)(kb1 - kb0) * s / n_seg); };
   // The 128-row block of w and the tokens that this CTA loads of a tile.
   auto block_of = [&](const Tile &tl) { return kMode == kPair ? 2 * tl.fb + rank : tl.fb; };
