@@ -14,10 +14,11 @@
 // Sums: the tensor cores truncate when they add to an accumulator, measured
 // 1.8e-8 of the result per addition (16 bf16 products): 1.6e-5 at K = 14336.
 // That is nothing beside a bf16 output's 2^-9, but for f32 output the
-// accumulator is handed over every kSegBlocks K blocks and the epilogue adds
-// the segments in f32 to nearest, in registers: under 1e-6 whatever K.  Reading
-// an accumulator takes TMEM from the MMAs, about 300 clocks: 2048 x 14336 x
-// 4096 onto an f32 stream takes 147 us in one segment, 167 in segments of 12.
+// accumulator is handed over every kSegBlocks K blocks (kSegs) and the epilogue
+// adds the segments in f32 to nearest, in registers: under 1e-6 whatever K.
+// Reading an accumulator takes TMEM from the MMAs, about 300 clocks: 2048 x
+// 14336 x 4096 onto an f32 stream takes 147 us in one segment, 167 in segments
+// of 12.
 //
 // Three forms (kMode):
 //   pair   large products: two CTAs on neighbouring SMs form one 256-row tile
@@ -56,19 +57,23 @@ constexpr int BM = 128;             // rows of w per tile
 constexpr int kRowBytes = 128;      // K bytes per row and stage
 constexpr int kMaxStages = 8;
 constexpr int kEpiWarp0 = 4;
-// K blocks per accumulator segment (f32 output); SwiGLU multiplies two sums, and
-// their errors add.
-template <bool kSwiglu>
-constexpr int kSegBlocks = kSwiglu ? 7 : 12;
+// K blocks per accumulator segment; SwiGLU multiplies two sums, and their errors
+// add.  e4m3 products have 8 significant bits, so their sums lose little (4e-7
+// of the result at K = 6144, 1e-6 at 14336 in one segment): they go without up
+// to kPlainBlocks K blocks.
+template <int DT, bool kSwiglu>
+constexpr int kSegBlocks = DT == MOE_BF16 ? (kSwiglu ? 7 : 12) : (kSwiglu ? 24 : 48);
+constexpr int kPlainBlocks = 48;
 constexpr int kMaxBN = 256;
 constexpr int kSegMaxBN = 192;      // with segment sums in registers
 // Epilogue warps per lane quadrant: they take turns at blocks of 16 columns.
-// f32 output has three, so that a thread's segment sums (64 at BN = 192) fit
-// its registers: spilled, they share the path that feeds the MMAs operands.
-template <bool kBf16>
-constexpr int kEpiGroups = kBf16 ? 2 : 3;
-template <bool kBf16>
-constexpr int kThreads = (kEpiWarp0 + 4 * kEpiGroups<kBf16>) * 32;
+// With segments there are three, so that a thread's segment sums (64 at BN =
+// 192) fit its registers: spilled, they share the path that feeds the MMAs.
+template <bool kSegs>
+constexpr int kEpiGroups = kSegs ? 3 : 2;
+template <bool kSegs>
+constexpr int kThreads = (kEpiWarp0 + 4 * kEpiGroups<kSegs>) * 32;
+
 constexpr size_t kSmemMax = 227 * 1024;
 
 enum Mode { kSolo, kPair, kSplit };
@@ -337,9 +342,9 @@ __device__ __forceinline__ bool wait_inline(uint64_t *bar, uint32_t parity, int 
 }
 
 // A persistent CTA (pair) walks the tiles; kSplit: one tile per cluster.
-// kBf16: the output type; f32 output sums K in segments.
-template <int DT, bool kSwiglu, int kMode, bool kBf16>
-__global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __grid_constant__ TcLinear q) {
+// kBf16: the output type.  kSegs: K in segments.
+template <int DT, bool kSwiglu, int kMode, bool kBf16, bool kSegs>
+__global__ void __launch_bounds__(kThreads<kSegs>, 1) linear_tc_kernel(const __grid_constant__ TcLinear q) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars sm;
   // Pairs: the buffers lie at the same place in both CTAs (the same launch).
@@ -348,8 +353,7 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const LinearParams &p = q.p;
   int32_t *status = p.status ? p.status : &sm.status;
-  constexpr bool kSegs = !kBf16;
-  constexpr int G = kEpiGroups<kBf16>;
+  constexpr int G = kEpiGroups<kSegs>;
   constexpr int kBlockElems = kRowBytes / (DT == MOE_BF16 ? 2 : 1);
   const uint32_t stage_bytes = (BM + q.x_rows) * kRowBytes;
   const uint32_t acc_cols = q.bn <= 32 ? 32 : q.bn <= 64 ? 64 : q.bn <= 128 ? 128 : 256;
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kThreads<kBf16>, 1) linear_tc_kernel(const __g
   const int t_first = blockIdx.x / ranks, t_step = gridDim.x / ranks;
   const int kb0 = kMode == kSplit ? (int)((long long)q.nkb * rank / ranks) : 0;
   const int kb1 = kMode == kSplit ? (int)((long long)q.nkb * (rank + 1) / ranks) : q.nkb;
-  constexpr int kSeg = kSegBlocks<kSwiglu>;
+  constexpr int kSeg = kSegBlocks<DT, kSwiglu>;
   const int n_seg = kSegs ? (kb1 - kb0 + kSeg - 1) / kSeg : 1;
   auto seg_at = [&](int s) { return kb0 + (int)((long long)(kb1 - kb0) * s / n_seg); };
   // The 128-row block of w and the tokens that this CTA loads of a tile.
@@ -691,9 +695,9 @@ Plan plan_of(int T, int rows, int nkb, int sms, int max_bn) {
   return best;
 }
 
-template <int DT, bool kSwiglu, int kMode, bool kBf16>
+template <int DT, bool kSwiglu, int kMode, bool kBf16, bool kSegs>
 cudaError_t launch(const TcLinear &q, int grid, int cluster, cudaStream_t st) {
-  auto kernel = linear_tc_kernel<DT, kSwiglu, kMode, kBf16>;
+  auto kernel = linear_tc_kernel<DT, kSwiglu, kMode, kBf16, kSegs>;
   static DeviceOnce once;
   const cudaError_t err = once.run([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -707,7 +711,7 @@ cudaError_t launch(const TcLinear &q, int grid, int cluster, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads<kBf16>);
+  cfg.blockDim = dim3(kThreads<kSegs>);
   cfg.dynamicSmemBytes = (size_t)q.stages * (BM + q.x_rows) * kRowBytes + 1024;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -715,24 +719,28 @@ cudaError_t launch(const TcLinear &q, int grid, int cluster, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, q);
 }
 
-template <int DT, bool kSwiglu, bool kBf16>
+template <int DT, bool kSwiglu, bool kBf16, bool kSegs>
 cudaError_t launch_mode(const TcLinear &q, const Plan &plan, int sms, cudaStream_t st) {
   const int tiles = q.n_fb * q.n_tb;
   if (plan.mode == kPair)
-    return launch<DT, kSwiglu, kPair, kBf16>(q, 2 * std::min(tiles, sms / 2), 2, st);
+    return launch<DT, kSwiglu, kPair, kBf16, kSegs>(q, 2 * std::min(tiles, sms / 2), 2, st);
   if (plan.mode == kSplit)
-    return launch<DT, kSwiglu, kSplit, kBf16>(q, tiles * plan.split, plan.split, st);
-  return launch<DT, kSwiglu, kSolo, kBf16>(q, std::min(tiles, sms), 1, st);
+    return launch<DT, kSwiglu, kSplit, kBf16, kSegs>(q, tiles * plan.split, plan.split, st);
+  return launch<DT, kSwiglu, kSolo, kBf16, kSegs>(q, std::min(tiles, sms), 1, st);
+}
+
+template <int DT, bool kSwiglu>
+cudaError_t launch_out(const TcLinear &q, const Plan &plan, bool segs, int sms, cudaStream_t st) {
+  if (q.p.out_dtype == MOE_BF16) return launch_mode<DT, kSwiglu, true, false>(q, plan, sms, st);
+  if constexpr (DT == MOE_E4M3)
+    if (!segs) return launch_mode<DT, kSwiglu, false, false>(q, plan, sms, st);
+  return launch_mode<DT, kSwiglu, false, true>(q, plan, sms, st);
 }
 
 template <int DT>
-cudaError_t launch_type(const TcLinear &q, const Plan &plan, int sms, cudaStream_t st) {
-  const bool bf = q.p.out_dtype == MOE_BF16;
-  if (q.p.act == MOE_ACT_SWIGLU)
-    return bf ? launch_mode<DT, true, true>(q, plan, sms, st)
-              : launch_mode<DT, true, false>(q, plan, sms, st);
-  return bf ? launch_mode<DT, false, true>(q, plan, sms, st)
-            : launch_mode<DT, false, false>(q, plan, sms, st);
+cudaError_t launch_type(const TcLinear &q, const Plan &plan, bool segs, int sms, cudaStream_t st) {
+  return q.p.act == MOE_ACT_SWIGLU ? launch_out<DT, true>(q, plan, segs, sms, st)
+                                   : launch_out<DT, false>(q, plan, segs, sms, st);
 }
 
 }  // namespace
@@ -747,7 +755,8 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   TcLinear q;
   q.p = p;
   q.nkb = up(p.K * es, kRowBytes);
-  const Plan plan = plan_of(p.T, rows, q.nkb, sms, p.out_dtype == MOE_F32 ? kSegMaxBN : kMaxBN);
+  const bool segs = p.out_dtype == MOE_F32 && (dtype == MOE_BF16 || q.nkb > kPlainBlocks);
+  const Plan plan = plan_of(p.T, rows, q.nkb, sms, segs ? kSegMaxBN : kMaxBN);
   const bool pair = plan.mode == kPair;
   q.unit = pair ? 32 : 16;
   const int units = up(p.T, q.unit);
@@ -769,8 +778,8 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   }
   if (!make_map(&q.map_x, p.x, dt, es, p.K, p.T, p.ldx, kRowBytes / es, q.x_rows))
     return cudaErrorInvalidValue;
-  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, plan, sms, st)
-                           : launch_type<MOE_E4M3>(q, plan, sms, st);
+  return dtype == MOE_BF16 ? launch_type<MOE_BF16>(q, plan, segs, sms, st)
+                           : launch_type<MOE_E4M3>(q, plan, segs, sms, st);
 }
 
 }  // namespace moe
