@@ -44,6 +44,7 @@
 // Every mbarrier wait is bounded: one that gives up sets the status word, and
 // the roles stop, drain their copies and MMAs, and return.
 #include <algorithm>
+#include <cstdlib>
 #include <cuda.h>
 
 #include "linear.cuh"
@@ -90,6 +91,7 @@ struct TcLinear {
   int group_tb;            // token tiles per raster group
   int nkb;                 // K blocks of the whole product
   int stages;
+  unsigned long long wait_ns;   // limit of each role wait
 };
 
 struct Bars {
@@ -326,19 +328,39 @@ __device__ __forceinline__ void prefetch_resid(const LinearParams &p, int t, int
   asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
 }
 
-// wait_bar without the call: the epilogue holds sums in registers across it.
-__device__ __forceinline__ bool wait_inline(uint64_t *bar, uint32_t parity, int *abort, int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return true;
+// A role's wait: false if the CTA is stopping or the wait ran past its limit,
+// and then *status and *abort are set.
+__device__ __forceinline__ bool wait_loop(uint64_t *bar, uint32_t parity, int *abort, int32_t *status,
+                                          unsigned long long limit_ns) {
   const unsigned long long t0 = globaltimer();
   for (;;) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (limit_ns && mbar_try_wait_sleep(bar, parity)) return true;
     if (*reinterpret_cast<volatile int *>(abort)) return false;
-    if (globaltimer() - t0 > kWaitNs) {
+    if (globaltimer() - t0 >= limit_ns) {
       atomicExch(abort, 1);
       atomicExch(status, kStatusTimeout);
       return false;
     }
   }
+}
+__device__ __noinline__ bool wait_call(uint64_t *bar, uint32_t parity, int *abort, int32_t *status,
+                                       unsigned long long limit_ns) {
+  return wait_loop(bar, parity, abort, status, limit_ns);
+}
+// The producer's and the MMA issuer's, one thread each.  A limit of 0 gives up
+// wherever the phase is not complete when first tested (test_wait does not
+// hold the thread, and costs these loops nothing).
+__device__ __forceinline__ bool wait_role(uint64_t *bar, uint32_t parity, int *abort, int32_t *status,
+                                          unsigned long long limit_ns) {
+  return mbar_test_wait(bar, parity) || wait_call(bar, parity, abort, status, limit_ns);
+}
+// The epilogue's, by whole warps, without a call, because it holds sums in
+// registers across it; it waits long and ends with the other roles.  The lanes
+// vote: one may see the phase complete where another sees the CTA stop, and the
+// tensor-memory loads that follow are warp-collective.
+__device__ __forceinline__ bool wait_inline(uint64_t *bar, uint32_t parity, int *abort, int32_t *status) {
+  const bool ok = mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort, status, kWaitNs);
+  return __all_sync(0xffffffffu, ok);
 }
 
 // A persistent CTA (pair) walks the tiles; kSplit: one tile per cluster.
@@ -412,15 +434,15 @@ __global__ void __launch_bounds__(kThreads<kSegs>, 1) linear_tc_kernel(const __g
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    int s = 0;
-    uint32_t ph = 0, armed = 0, par = 0;
-    bool ok = true;
-    for (int t = t_first; ok && t < n_tiles; t += t_step) {
-      const Tile tl = tile_at(q, t);
-      const int fb = block_of(tl), x_row = x_row_of(tl);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = wait_bar(&sm.empty[s], ph ^ 1, &sm.abort, status))) break;
-        if (elect_one()) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t ph = 0, armed = 0, par = 0;
+      bool ok = true;
+      for (int t = t_first; ok && t < n_tiles; t += t_step) {
+        const Tile tl = tile_at(q, t);
+        const int fb = block_of(tl), x_row = x_row_of(tl);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = wait_role(&sm.empty[s], ph ^ 1, &sm.abort, status, q.wait_ns))) break;
           uint8_t *a = smem + s * stage_bytes;
           uint32_t bar = smem_u32(&sm.full[s]);
           if constexpr (kMode == kPair) bar = peer_addr(&sm.full[s], 0);
@@ -430,71 +452,69 @@ __global__ void __launch_bounds__(kThreads<kSegs>, 1) linear_tc_kernel(const __g
           if constexpr (kSwiglu) load_4d<kMode>(a, &q.map_w, kb * kBlockElems, fb * 4, bar);
           else load_2d<kMode>(a, &q.map_w, kb * kBlockElems, fb * BM, bar);
           load_2d<kMode>(a + BM * kRowBytes, &q.map_x, kb * kBlockElems, x_row, bar);
+          armed |= 1u << s;
+          par = (par & ~(1u << s)) | (ph << s);
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
         }
-        __syncwarp();
-        armed |= 1u << s;
-        par = (par & ~(1u << s)) | (ph << s);
-        if (++s == S) {
-          s = 0;
-          ph ^= 1;
+      }
+      // Every copy that was issued has landed before the CTA goes on.  A pair's
+      // second CTA cannot watch the leader's barriers: its copies are done when
+      // the leader's MMAs have read them; if it stopped early it gives them a
+      // millisecond.
+      const unsigned long long t0 = globaltimer();
+      if (kMode != kPair || rank == 0) {
+        for (int i = 0; i < S; ++i)
+          if ((armed >> i) & 1) drain_bar(&sm.full[i], (par >> i) & 1, t0);
+      } else if (!ok) {
+        while (globaltimer() - t0 < 1000000ull) {
         }
       }
     }
-    // Every copy that was issued has landed before the CTA goes on.  A pair's
-    // second CTA cannot watch the leader's barriers: its copies are done when
-    // the leader's MMAs have read them; if it stopped early it gives them a
-    // millisecond.
-    const unsigned long long t0 = globaltimer();
-    if (kMode != kPair || rank == 0) {
-      for (int i = 0; i < S; ++i)
-        if ((armed >> i) & 1) drain_bar(&sm.full[i], (par >> i) & 1, t0);
-    } else if (!ok) {
-      while (globaltimer() - t0 < 1000000ull) {
-      }
-    }
+    __syncwarp();
   } else if (warp == 1 && (kMode != kPair || rank == 0)) {
     // ---------------------------------------------------------- MMA issuer
-    int s = 0;
-    uint32_t ph = 0, it = 0;
-    const uint64_t da0 = sw128_desc(smem_u32(smem));
-    const uint32_t stage_desc = stage_bytes >> 4;
-    bool ok = true;
-    for (int t = t_first; ok && t < n_tiles; t += t_step) {
-      const Tile tl = tile_at(q, t);
-      const uint32_t idesc = linear_idesc<DT>(kMode == kPair ? 2 * BM : BM, tl.w);
-      for (int sg = 0; ok && sg < n_seg; ++sg, ++it) {
-        const int buf = it & 1;
-        if (!(ok = wait_bar(&sm.acc_empty[buf], ((it >> 1) & 1) ^ 1, &sm.abort, status))) break;
-        tc_fence_after();
-        const uint32_t d = tmem + buf * acc_cols;
-        const int ka = seg_at(sg), ke = seg_at(sg + 1);
-        for (int kb = ka; kb < ke; ++kb) {
-          if (!(ok = wait_bar(&sm.full[s], ph, &sm.abort, status))) break;
+    if (elect_one()) {
+      int s = 0;
+      uint32_t ph = 0, it = 0;
+      const uint64_t da0 = sw128_desc(smem_u32(smem));
+      const uint32_t stage_desc = stage_bytes >> 4;
+      bool ok = true;
+      for (int t = t_first; ok && t < n_tiles; t += t_step) {
+        const Tile tl = tile_at(q, t);
+        const uint32_t idesc = linear_idesc<DT>(kMode == kPair ? 2 * BM : BM, tl.w);
+        for (int sg = 0; ok && sg < n_seg; ++sg, ++it) {
+          const int buf = it & 1;
+          if (!(ok = wait_role(&sm.acc_empty[buf], ((it >> 1) & 1) ^ 1, &sm.abort, status, q.wait_ns))) break;
           tc_fence_after();
-          if (elect_one()) {
+          const uint32_t d = tmem + buf * acc_cols;
+          const int ka = seg_at(sg), ke = seg_at(sg + 1);
+          for (int kb = ka; kb < ke; ++kb) {
+            if (!(ok = wait_role(&sm.full[s], ph, &sm.abort, status, q.wait_ns))) break;
+            tc_fence_after();
             const uint64_t da = da0 + (uint64_t)(s * stage_desc);
             const uint64_t db = da + ((BM * kRowBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               linear_mma<DT, kMode>(d, da + 2 * kk, db + 2 * kk, idesc, kb > ka || kk > 0);
             linear_commit<kMode>(&sm.empty[s]);
+            if (++s == S) {
+              s = 0;
+              ph ^= 1;
+            }
           }
-          __syncwarp();
-          if (++s == S) {
-            s = 0;
-            ph ^= 1;
-          }
+          if (!ok) break;
+          linear_commit<kMode>(&sm.acc_full[buf]);
         }
-        if (!ok) break;
-        if (elect_one()) linear_commit<kMode>(&sm.acc_full[buf]);
-        __syncwarp();
       }
+      // One more commit covers every MMA issued, also those of a tile that was
+      // left in the middle; TMEM is freed only after it has arrived.
+      linear_commit<kMode>(&sm.drain);
+      drain_bar(&sm.drain, 0, globaltimer());
     }
-    // One more commit covers every MMA issued, also those of a tile that was
-    // left in the middle; TMEM is freed only after it has arrived.
-    if (elect_one()) linear_commit<kMode>(&sm.drain);
     __syncwarp();
-    drain_bar(&sm.drain, 0, globaltimer());
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3, turn = (warp - kEpiWarp0) >> 2;
@@ -767,6 +787,10 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   q.x_rows = pair ? q.bn / 2 : q.bn;
   q.n_fb = up(rows, pair ? 2 * BM : BM);
   q.group_tb = std::min(q.n_tb, 16);
+  // Test hook: MOE_LINEAR_NO_WAIT=1 makes every wait that is not complete when
+  // first tested give up, to exercise the way out without a fault or a hang.
+  const char *no_wait = getenv("MOE_LINEAR_NO_WAIT");
+  q.wait_ns = no_wait && no_wait[0] == '1' ? 0 : kWaitNs;
   const size_t stage = (size_t)(BM + q.x_rows) * kRowBytes;
   q.stages = (int)std::min<size_t>(kMaxStages, (kSmemMax - sizeof(Bars) - 64 - 1024) / stage);
   if (sw) {

@@ -800,3 +800,21 @@ def test_ops_on_columns_of_one_tensor(moe):
     check_norm(x, resid, None, n, None, rout, 1, 0)
     for a, b in ((H + N, 512), (768, 1024), (1280, 2048), (2304, 4096)):
         assert bool((wide[:, a:b].float() == SENT).all())
+
+
+@pytest.mark.parametrize("T,K,N", [(40, 8192, 256), (1000, 2048, 320), (1500, 1024, 777), (4096, 1024, 4096)])
+@pytest.mark.parametrize("out_dtype", [0, 1])
+def test_linear_waits_give_up(moe, monkeypatch, T, K, N, out_dtype):
+    """With a limit of 0 every wait that is not complete when first tested gives
+    up (split, one CTA per tile, CTA pairs): the call returns, the status word
+    says 2, and the next call is right.  No fault and no hang: the roles stop,
+    drain their copies and MMAs, free their tensor memory and return."""
+    g = gen(T)
+    x, w, sx, sw, b, r = make_linear(g, T, K, N, 1, 0, out_dtype, False, False)
+    monkeypatch.setenv("MOE_LINEAR_NO_WAIT", "1")
+    out, status = run_linear(moe, x, w, sx, sw, b, r, N, 1, out_dtype, 0)
+    torch.cuda.synchronize()
+    assert int(status) == 2
+    monkeypatch.delenv("MOE_LINEAR_NO_WAIT")
+    out, status = run_linear(moe, x, w, sx, sw, b, r, N, 1, out_dtype, 0)
+    check_linear(out, status, x, w, sx, sw, b, r, N, 0)
