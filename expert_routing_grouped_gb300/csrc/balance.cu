@@ -29,7 +29,7 @@
 // For short segments one kernel does all three steps, a cluster per segment
 // with cluster barriers between them: there the launches are the time.
 //
-// Memory bound when large: T = 65536, E = 256, f32 logits take 33.5 us with the
+// Memory bound when large: T = 65536, E = 256, f32 logits take 32.8 us with the
 // gradient (134 MB: 20 us at a copy's rate; the count and finish kernels and
 // their hand-over are about 8), 20.4 us without (10).  64 x 64: 6.1 us.
 #include <algorithm>
@@ -431,12 +431,12 @@ __device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &r
 }
 
 // A warp's rows first, first + step, .. below b, with the loads of kAhead steps
-// under way: enough bytes in flight to cover the memory's latency where a
-// lane's share is short.
+// under way where a lane's share is short (65536 x 256 step: 32.8 us with 2,
+// 33.6 with 3, 35.6 with 4, whose registers cost more than they hide).
 template <class L>
 struct Rows {
   static constexpr int RPW = 32 / L::LPR;   // rows per warp and step
-  static constexpr int kAhead = L::NE <= 8 ? 3 : L::NE <= 16 ? 2 : 1;
+  static constexpr int kAhead = L::NE <= 16 ? 2 : 1;
   typename L::Raw raw[kAhead];
   bool valid[kAhead];
   int t;              // the next token to fetch, its logits, and its mask
