@@ -475,8 +475,7 @@ struct Rows {
   }
 };
 
-// Shared memory of a block of the pass: the warps' sums, the coefficients and
-// the bias, each over the padded experts of the layout.
+// The bias over the layout's EP experts, 0 past E, into shared memory.
 template <int EP>
 __device__ __forceinline__ void stage_bias(const BalParams &p, float *bias) {
   if (p.bias)
