@@ -45,7 +45,7 @@ constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalBlocks = 456;          // most chunks of a call: 3 blocks on each of 152 SMs
 constexpr int kCountThreads = 1024;
 constexpr int kCluster = 8;              // PeerWords reads as many
-constexpr long long kSmallElems = 1 << 16, kSmallTotal = 1 << 22;   // see is_small
+constexpr long long kSmallElems = 1 << 16;   // logits of a mean segment, see is_small
 
 struct BalParams {
   const void *z;
@@ -766,15 +766,15 @@ int balance_count_chunk(int T, bool grad) {
   return grad ? std::max(256, (T + 63) / 64) : balance_chunk(T);
 }
 
-// One kernel where a mean segment has at most 2^16 logits and all have 2^22
-// (bounds what one segment that holds nearly every token costs).  With a
-// gradient, us in one kernel and in three: T = 512, E = 64, one segment 6.7 and
-// 7.8; 1024 x 256, one segment 14.8 and 10.5; 4096 x 256, 24 segments 12.7 and
-// 21.1, 8 segments 17.7 and 15.9; 16389 x 256, 64 segments 20.0 and 27.5, 24
-// segments 28.7 and 20.7.
-bool is_small(int T, int E, int S) {
-  return (long long)T * E <= kSmallElems * S && (long long)T * E <= kSmallTotal;
-}
+// One kernel where a mean segment has at most 2^16 logits: a block of the three
+// takes its segments one after the other, about 4 us each.  With a gradient, us
+// in one kernel and in three: T = 512, E = 64, one segment 6.1 and 7.9; 1024 x
+// 256, one segment 14.5 and 9.7; 4096 x 256, 24 segments 11.4 and 19.6, 8
+// segments 15.4 and 14.8; 16389 x 256, 64 segments 18.7 and 25.6, 24 segments
+// 23.6 and 19.1; 65536 x 256, 256 segments 56 and 71, 1024 segments 146 and 191;
+// 32768 x 256, 4096 segments of 8 tokens 110 and 607.  One segment with nearly
+// all the tokens costs both: 65536 x 256 in 256 segments then 511 and 769.
+bool is_small(int T, int E, int S) { return (long long)T * E <= kSmallElems * S; }
 
 template <class L>
 cudaError_t launch_layout(const BalParams &p, cudaStream_t st) {

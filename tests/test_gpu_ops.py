@@ -741,11 +741,11 @@ def test_ops_first_call_inside_a_capture():
     assert r.returncode == 0, r.stderr[-2000:]
 
 
-@pytest.mark.parametrize("S", [7, 300, 3000])
-def test_balance_many_segments(moe, S):
+@pytest.mark.parametrize("S,E", [(7, 64), (34, 256), (300, 64), (3000, 64)])
+def test_balance_many_segments(moe, S, E):
     """More segments than a warp looks at once, many of them empty or of one
     token, in each of the kernels' forms."""
-    T, E, k = 9000, 64, 4
+    T, k = 9000, 4
     g = gen(S)
     z, idx, _, m = make_balance(g, T, E, k, 0, 1, True)
     rs = np.random.RandomState(S)
