@@ -667,6 +667,12 @@ __global__ void __launch_bounds__(kFinishWarps * 32) balance_finish_kernel(const
 
 // ---------------------------------------------------------- small batches --
 
+// A segment this many times the mean one has its array's order checked first:
+// in an order that seq_off must not have, every segment could be all T tokens
+// long and the call n_seq * T rows of work.  Such a segment is taken as empty;
+// so no call works on more than kLongSeg * T rows.
+constexpr int kLongSeg = 64;
+
 template <class L>
 __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small_kernel(const BalParams p) {
   constexpr int EP = L::NE * L::LPR;
@@ -678,7 +684,14 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small
   __shared__ int total;
   const int ranks = cluster_size(), rank = cluster_rank(), s = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5;
-  const int a = seg_begin(p, s), b = seg_end(p, s);
+  const int a = seg_begin(p, s);
+  int b = seg_end(p, s);
+  // The same for all CTAs of the cluster; never with one segment (no seq_off).
+  if ((b - a) / kLongSeg > (p.T - 1) / p.S + 1) {
+    int bad = 0;
+    for (int i = threadIdx.x; i < p.S; i += blockDim.x) bad |= p.seq_off[i + 1] < p.seq_off[i];
+    if (__syncthreads_or(bad)) b = a;
+  }
   constexpr int kStep = kBalWarps * Rows<L>::RPW;
   const int first = a + (rank * kBalWarps + warp) * Rows<L>::RPW;
   Rows<L> rows;

@@ -417,7 +417,9 @@ int moe_linear(const void *x, const float *x_scale, const void *w, const float *
  *            counted, its z not used, its dz 0
  *   seq_off  [n_seq + 1] int32, non-decreasing: segment s is the tokens
  *            seq_off[s] .. seq_off[s+1] - 1; NULL (n_seq 1): all T.  Tokens in
- *            no segment are not read and their dz is left as it was
+ *            no segment are not read and their dz is left as it was.  (Values
+ *            in another order or outside [0, T] leave the results open, but
+ *            nothing else is touched and the work stays bounded.)
  *   grad     [n_seq] f32 or NULL (1): the gradient of each segment's loss
  *   loss     [n_seq], prob [n_seq][E] f32; counts [n_seq][E], tokens [n_seq]
  *            (T_s) int32

@@ -784,6 +784,24 @@ def test_balance_disordered_segments_stay_in_bounds(moe):
                 assert int(o[0]) == 72 and int(o[-1]) == 72
 
 
+@pytest.mark.parametrize("mode", [0, 1])
+def test_balance_long_segment_among_short_ones(moe, mode):
+    """One segment with nearly all the tokens is summed like any other; in an
+    array whose order would make every other segment that long, none is."""
+    T, E, k, S = 6000, 64, 2, 600
+    z, idx, _, _ = make_balance(gen(mode), T, E, k, 0)
+    bias = None if mode else randn(gen(7), E)
+    for at in (0, 300, S - 1):
+        off = torch.full((S + 1,), 5900, dtype=torch.int32, device="cuda")
+        off[:at + 1] = 7
+        off[S] = T if at < S - 1 else 5900
+        got = run_balance(moe, z, idx, bias, None, off, k, mode)
+        check_balance(got, z, idx, bias, None, off, k, mode)
+    off = torch.tensor([0, T] * S, dtype=torch.int32, device="cuda")[:S + 1]
+    loss, counts, tokens, prob, dz = run_balance(moe, z, idx, bias, None, off, k, mode)
+    assert int(tokens.sum()) == 0 and int(counts.sum()) == 0 and bool((dz == SENT).all())
+
+
 def test_ops_on_columns_of_one_tensor(moe):
     """Operands and results side by side in the rows of one tensor."""
     g = gen(12)
