@@ -13,7 +13,7 @@
 // values (16 bytes of bf16, 32 of f32) per thread and step.
 //
 // Memory bound: 4096 rows of 6144, f32 onto an f32 stream with bf16 out, take
-// 53.3 us (6.6 TB/s, 0.97 of a copy's rate); bf16 onto f32 with e4m3 out 47.7
+// 53.3 us (6.6 TB/s, 0.97 of a copy's rate); bf16 onto f32 with e4m3 out 48.1
 // us (5.8 TB/s).  One row takes 2.7 us: launch and one memory round trip.
 #include <algorithm>
 
@@ -165,37 +165,46 @@ __global__ void __launch_bounds__(NV == 8 ? 512 : 1024) add_rmsnorm_kernel(const
     }
   } else {
     uint8_t *o = reinterpret_cast<uint8_t *>(p.out) + t * p.ldo;
-    uint32_t row_max = 0u;
-    if (by_row)
-      for (int w = 0; w < nw; ++w) row_max = max(row_max, part_max[w]);
+    float sc, f, back;
+    auto scale_of = [&](uint32_t m) {
+      // NaN fails the comparison and stays.
+      const float amax = __uint_as_float(m) * rstd / 448.0f;
+      sc = amax < 1.17549435e-38f ? 1.17549435e-38f : amax;
+      f = 1.0f / sc;
+      back = f == 0.0f ? 0.0f : -sc;   // sc infinite: 0 or NaN
+    };
+    if (by_row) {
+      uint32_t m = 0u;
+      for (int w = 0; w < nw; ++w) m = max(m, part_max[w]);
+      scale_of(m);
+      if (threadIdx.x == 0) p.scale[t] = sc;
+    }
     const int lanes = p.group / 8;   // threads of one group (4, 8 or 16 of a warp)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = threadIdx.x + j * blockDim.x;
       uint32_t m = mx[j];
-      if (by_row) {
-        m = row_max;
-      } else {   // pieces of a group sit in neighbouring lanes (H is a multiple of the group)
+      if (!by_row)   // pieces of a group sit in neighbouring lanes (H is a multiple of the group)
         for (int d = 1; d < lanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      }
       if (i >= n8) continue;
-      // NaN fails the comparison and stays.
-      const float amax = __uint_as_float(m) * rstd / 448.0f;
-      const float sc = amax < 1.17549435e-38f ? 1.17549435e-38f : amax;
-      // Two products: rstd / sc alone could pass f32's range (a row of zeros).
-      const float f = 1.0f / sc;
+      if (!by_row) scale_of(m);
+      // n / sc as a product with 1 / sc and one correction by the remainder,
+      // which makes the f32 quotient the nearest one (Markstein 1990): bf16 rows
+      // meet ties between codes often, r / max being a ratio of 8-bit numbers,
+      // and a product's rounding would decide them (1037 x 4096 in groups of
+      // 128: 2 codes of 10^4).  rstd / sc alone could pass f32's range (a row
+      // of zeros).
       float n[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) n[c] = r[j][c] * rstd * f;
+      for (int c = 0; c < 8; ++c) {
+        const float v = r[j][c] * rstd, q0 = v * f;
+        n[c] = fmaf(fmaf(q0, back, v), f, q0);
+      }
       uint2 q;
       q.x = pack_e4m3(n[0], n[1], n[2], n[3]);
       q.y = pack_e4m3(n[4], n[5], n[6], n[7]);
       *reinterpret_cast<uint2 *>(o + (size_t)i * 8) = q;
-      if (by_row) {
-        if (i == 0) p.scale[t] = sc;
-      } else if (i % lanes == 0) {
-        p.scale[t * (size_t)(H / p.group) + i / lanes] = sc;
-      }
+      if (!by_row && i % lanes == 0) p.scale[t * (size_t)(H / p.group) + i / lanes] = sc;
     }
   }
 }

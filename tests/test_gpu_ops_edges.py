@@ -1,0 +1,71 @@
+"""Edges of the dense operators on the GPU, against their 64-bit forms
+(ops_ref.py): values at the ends of f32's range, masks beside gradients that
+are not finite, sizes whose launches differ from the small ones', the accuracy
+of f32 outputs, and products that give up.
+
+Tolerances come from the arithmetic, as in test_gpu_ops.py, whose checks are
+used here."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_ops import (DT, E4M3, gen, randn, run_norm)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import expert_routing_grouped_gb300 as m
+    return m
+
+
+# ------------------------------------------------------------ add_rmsnorm --
+
+def four_squares(d):
+    """Four whole numbers up to 256 whose squares add up to d."""
+    for a in range(min(256, int(d ** 0.5)), -1, -1):
+        for b in range(min(a, int((d - a * a) ** 0.5)), -1, -1):
+            rest = d - a * a - b * b
+            c = int(rest ** 0.5)
+            while c >= 0 and 2 * c * c >= rest:
+                e = int(round((rest - c * c) ** 0.5))
+                if c <= 256 and e <= 256 and e * e == rest - c * c:
+                    return a, b, c, e
+                c -= 1
+    raise AssertionError(d)
+
+
+def whole_rows(T, H, seed):
+    """Rows of whole numbers below 257 whose mean square is 64^2 exactly."""
+    rs = np.random.RandomState(seed)
+    rows = np.zeros((T, H))
+    for t in range(T):
+        while True:
+            v = rs.randint(-109, 110, H - 4)
+            d = H * 4096 - int((v * v).sum())
+            if 0 <= d <= 200000:
+                break
+        rows[t] = np.concatenate([v, four_squares(d)])
+    return torch.tensor(rows, dtype=torch.float32, device="cuda")
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("with_gain", [False, True])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_add_rmsnorm_codes_are_the_rounded_quotients(moe, group, with_gain, dtype):
+    """Where nothing before the quotient rounds (whole numbers, a root mean
+    square of 64 and eps 0: 1 / rms is a power of two, and r * gain is rounded
+    once whatever the order), the scale is f32(max |n| / 448) and every code is
+    e4m3(f32(n / scale)) bit for bit -- at exact ties, which whole numbers meet
+    often, too."""
+    T, H = 400, 512
+    x = whole_rows(T, H, 7 + group)
+    gain = 1 + 0.2 * randn(gen(3), H) if with_gain else None
+    out, scale, _ = run_norm(moe, x.to(DT[dtype]), None, gain, 2, group, eps=0.0)
+    n = (x if gain is None else x * gain) / 64
+    want = n.cpu().view(T, -1, group or H)
+    sc = want.abs().amax(2) / 448.0
+    assert torch.equal(scale.cpu().view(T, -1), sc)
+    codes = (want / sc[:, :, None]).clamp(-448, 448).to(E4M3).view(T, H)
+    assert torch.equal(out.cpu().view(torch.uint8), codes.view(torch.uint8))
