@@ -462,13 +462,16 @@ __global__ void __launch_bounds__(kThreads<kSegs>, 1) linear_tc_kernel(const __g
       }
       // Every copy that was issued has landed before the CTA goes on.  A pair's
       // second CTA cannot watch the leader's barriers: its copies are done when
-      // the leader's MMAs have read them; if it stopped early it gives them a
-      // millisecond.
+      // the leader's MMAs have read them and their commits have arrived here; if
+      // it stopped early it gives them a millisecond.
       const unsigned long long t0 = globaltimer();
       if (kMode != kPair || rank == 0) {
         for (int i = 0; i < S; ++i)
           if ((armed >> i) & 1) drain_bar(&sm.full[i], (par >> i) & 1, t0);
-      } else if (!ok) {
+      } else if (ok) {
+        for (int i = 0; i < S; ++i)
+          if ((armed >> i) & 1) drain_bar(&sm.empty[i], (par >> i) & 1, t0);
+      } else {
         while (globaltimer() - t0 < 1000000ull) {
         }
       }
@@ -633,6 +636,13 @@ __global__ void __launch_bounds__(kThreads<kSegs>, 1) linear_tc_kernel(const __g
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kMode == kPair) {
+    // The leader's last commit arrives on the second CTA's drain barrier too, as
+    // an access of its own that the cluster barrier below does not order: that
+    // CTA's shared memory may be another block's once it has left.
+    if (rank != 0 && threadIdx.x == 0) drain_bar(&sm.drain, 0, globaltimer());
+    __syncwarp();
+  }
   // No CTA leaves while a peer may read its shared memory or tensor memory.
   if constexpr (kMode != kSolo) cluster_sync();
   if (warp == 1) {

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_ops import (DT, E4M3, gen, randn, run_norm)
+from test_gpu_ops import (DT, E4M3, check_linear, gen, make_linear, randn, run_linear, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,28 @@ def test_add_rmsnorm_codes_are_the_rounded_quotients(moe, group, with_gain, dtyp
     assert torch.equal(scale.cpu().view(T, -1), sc)
     codes = (want / sc[:, :, None]).clamp(-448, 448).to(E4M3).view(T, H)
     assert torch.equal(out.cpu().view(torch.uint8), codes.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ linear --
+
+def test_linear_pairs_back_to_back(moe):
+    """Products in the CTA-pair form one after another, between them kernels
+    that take the same SMs: the same bits each time."""
+    g = gen(31)
+    T, K, N = 4096, 256, 2048
+    x, w, _, _, _, _ = make_linear(g, T, K, N, 1, 0, 0, False, False)
+    out, st = run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)
+    check_linear(out, st, x, w, None, None, None, None, N, 0)
+    few, _ = run_linear(moe, x[:40], w, None, None, None, None, N, 1, 0, 0)
+    outs = [torch.empty_like(out) for _ in range(3)]
+    small = torch.empty_like(few)
+    norm = torch.empty(T, K, dtype=torch.bfloat16, device="cuda")
+    for i in range(200):
+        moe.linear(x, w, T, N, K, outs[i % 3])
+        if i % 2:
+            moe.linear(x[:40], w, 40, N, K, small)
+        else:
+            moe.add_rmsnorm(x, T, K, 1e-6, norm)
+    for o in outs:
+        assert torch.equal(o, out)
+    assert torch.equal(small, few)
