@@ -412,6 +412,16 @@ __device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &r
     }
   }
   tot = L::sum(tot);
+  if constexpr (L::kSig && kGrad) {
+    // A row of sigmoids that are all tiny is scaled up by 2^64: 1 / tot, its
+    // product with a large gradient, and tiny times small counts all stay in
+    // f32's range, and p = u / tot is the same to the bit.
+    if (tot < 0x1p-32f) {
+#pragma unroll
+      for (int j = 0; j < L::NE; ++j) u[j] *= 0x1p64f, w[j] *= 0x1p64f;
+      tot *= 0x1p64f;
+    }
+  }
   const float inv = tot == 0.f ? 0.f : rcp_fast(tot);   // tot >= 2^-126 otherwise
 #pragma unroll
   for (int j = 0; j < L::NE; ++j) acc[j] = fmaf(u[j], inv, acc[j]);

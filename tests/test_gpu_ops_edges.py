@@ -9,7 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_ops import (DT, E4M3, check_linear, gen, make_linear, randn, run_linear, run_norm)
+from test_gpu_ops import (DT, E4M3, check_balance, check_linear, gen, make_linear, randn,
+                          run_balance, run_linear, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +95,23 @@ def test_linear_pairs_back_to_back(moe):
     for o in outs:
         assert torch.equal(o, out)
     assert torch.equal(small, few)
+
+
+# ------------------------------------------------------------ balance loss --
+
+@pytest.mark.parametrize("level", [-87.0, -84.0, -60.0, -30.0, 10.0])
+@pytest.mark.parametrize("T,E,dtype,extra", [
+    (1, 8, 0, 0), (40, 8, 0, 0), (6, 64, 1, 0), (9, 7, 0, 0), (12, 128, 0, 1), (30, 256, 1, 0),
+    (700, 128, 0, 0), (700, 160, 1, 0)])
+def test_balance_sigmoid_of_far_logits(moe, T, E, dtype, extra, level):
+    """Sigmoids near the ends of f32's range (all of them at least 2^-126) and a
+    large gradient from above, as a scaled loss has: probabilities and gradient
+    are the formula's."""
+    g = gen(T + E)
+    z = (level + 0.25 * torch.rand(T, E, generator=g, device="cuda")).to(DT[dtype])
+    k = 2
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32, device="cuda")
+    grad = torch.full((1,), 65536.0, device="cuda")
+    got = run_balance(moe, z, idx, None, None, None, k, 1, grad=grad, extra=extra)
+    check_balance(got, z, idx, None, None, None, k, 1, grad=grad)
+    assert bool(got[4].isfinite().all())
