@@ -367,7 +367,7 @@ __device__ __forceinline__ float rcp_fast(float v) {
 // With u the sigmoid (or exp(z - max)) and inv 1 / sum u: p = u inv, and
 //   dz_i = scale inv u_i (1 - sigmoid_i) (coef_i - dot),  dot = inv sum u_e coef_e
 template <class L, bool kGrad>
-__device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &raw, char *dst, bool valid,
+__device__ __forceinline__ void one_token(const BalParams &p, const typename L::Raw &raw, char *dst, bool valid,
                                           bool write, const float *bias, const float *coef, float scale,
                                           float (&acc)[L::NE]) {
   float u[L::NE], w[L::kSig && kGrad ? L::NE : 1];   // w: u (1 - sigmoid)
@@ -380,9 +380,6 @@ __device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &r
       }
       return;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < L::Raw::N; ++j) raw.w[j] = valid ? raw.w[j] : L::kNone;
   }
   float tot = 0.f;
   if constexpr (L::kSig) {
@@ -411,6 +408,18 @@ __device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &r
       tot += u[j];
     }
   }
+  if constexpr (L::LPR < 32) {
+    // Beside other tokens of the warp: nothing of a masked one is used, whatever
+    // its logits, the bias or the gradient from above hold.
+    if (!valid) {
+#pragma unroll
+      for (int j = 0; j < L::NE; ++j) {
+        u[j] = 0.f;
+        if constexpr (L::kSig && kGrad) w[j] = 0.f;
+      }
+      tot = 0.f;
+    }
+  }
   tot = L::sum(tot);
   if constexpr (L::kSig && kGrad) {
     // A row of sigmoids that are all tiny is scaled up by 2^64: 1 / tot, its
@@ -430,7 +439,7 @@ __device__ __forceinline__ void one_token(const BalParams &p, typename L::Raw &r
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) dot = fmaf(u[j], coef[L::first(j / L::VEC) + j % L::VEC], dot);
     dot = L::sum(dot) * inv;
-    const float k = scale * inv;
+    const float k = inv == 0.f ? 0.f : scale * inv;   // no probabilities: no gradient
 #pragma unroll
     for (int j = 0; j < L::NE; ++j) {
       const float c = (coef[L::first(j / L::VEC) + j % L::VEC] - dot) * k;

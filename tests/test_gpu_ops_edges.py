@@ -9,8 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_ops import (DT, E4M3, check_balance, check_linear, gen, make_linear, randn,
-                          run_balance, run_linear, run_norm)
+from test_gpu_ops import (DT, E4M3, check_balance, check_linear, gen, make_balance, make_linear,
+                          randn, run_balance, run_linear, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,29 @@ def test_balance_sigmoid_of_far_logits(moe, T, E, dtype, extra, level):
     got = run_balance(moe, z, idx, None, None, None, k, 1, grad=grad, extra=extra)
     check_balance(got, z, idx, None, None, None, k, 1, grad=grad)
     assert bool(got[4].isfinite().all())
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("T,E,dtype", [(20, 8, 0), (20, 64, 1), (20, 60, 0), (20, 7, 1), (20, 256, 0),
+                                       (2000, 64, 0), (2000, 64, 1), (700, 256, 1)])
+def test_balance_masked_rows_stay_zero_whatever_comes_from_above(moe, T, E, dtype, mode):
+    """grad, bias or a masked row's own logits may be anything: dz of a masked
+    row is 0, and a segment without kept tokens has loss and prob 0."""
+    g = gen(E)
+    z, idx, _, _ = make_balance(g, T, E, 2, dtype)
+    m = (torch.arange(T, device="cuda") % 3 != 1).to(torch.uint8)
+    z[m == 0] = torch.tensor([float("nan"), float("inf"), -float("inf"), 1.0], device="cuda").to(
+        z.dtype).repeat(E)[:E]
+    for up in (float("inf"), float("nan"), 2.0):
+        grad = torch.full((1,), up, device="cuda")
+        dz = run_balance(moe, z, idx, None, m, None, 2, mode, grad=grad)[4]
+        assert bool((dz[m == 0] == 0).all())
+    got = run_balance(moe, z, idx, None, m, None, 2, mode, grad=torch.full((1,), 2.0, device="cuda"))
+    kept = z.clone()
+    kept[m == 0] = 0
+    check_balance(got, kept, idx, None, m, None, 2, mode, grad=torch.full((1,), 2.0))
+    bias = torch.full((E,), float("nan"), device="cuda")
+    none = torch.zeros_like(m)
+    loss, counts, tokens, prob, dz = run_balance(moe, z, idx, bias, none, None, 2, mode)
+    assert float(loss) == 0 and int(tokens) == 0 and int(counts.sum()) == 0
+    assert bool((prob == 0).all()) and bool((dz == 0).all())
