@@ -43,6 +43,8 @@ namespace {
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalBlocks = 456;          // most chunks of a call: 3 blocks on each of 152 SMs
+constexpr int kMaxAssign = 1 << 26;      // T * k of a call
+constexpr int kMaxSeq = 65535;
 constexpr int kCountThreads = 1024;
 constexpr int kCluster = 8;              // PeerWords reads as many
 constexpr long long kSmallElems = 1 << 16;   // logits of a mean segment, see is_small
@@ -857,7 +859,9 @@ cudaError_t launch_balance(const BalParams &p, bool vec, cudaStream_t st) {
 extern "C" __attribute__((visibility("default"))) size_t moe_balance_workspace(int T, int num_experts,
                                                                               int n_seq) {
   using namespace moe;
-  if (T < 1 || num_experts < 1 || num_experts > kMaxExperts || n_seq < 1) return 0;
+  if (T < 1 || T > kMaxAssign || num_experts < 1 || num_experts > kMaxExperts || n_seq < 1 ||
+      n_seq > kMaxSeq)
+    return 0;
   // Partial sums of p, and partial counts in the form that has more of them.
   const int chunk = balance_chunk(T);
   const size_t slots = (size_t)(T + chunk - 1) / chunk + n_seq, E4 = (num_experts + 3) / 4 * 4;
@@ -874,9 +878,9 @@ extern "C" __attribute__((visibility("default"))) int moe_balance_loss(
   if (num_experts < 1 || num_experts > kMaxExperts || top_k < 1 || top_k > num_experts ||
       top_k > kMaxTopK || router_mode < 0 || router_mode > 2)
     return MOE_ERR_ROUTING;
-  if (T < 0 || n_seq < 1 || n_seq > 65535 || (!seq_off && n_seq != 1) ||
+  if (T < 0 || n_seq < 1 || n_seq > kMaxSeq || (!seq_off && n_seq != 1) ||
       (z_dtype != MOE_F32 && z_dtype != MOE_BF16) || !(alpha - alpha == 0.f) ||
-      (long long)T * top_k > (1LL << 26))
+      (long long)T * top_k > kMaxAssign)
     return MOE_ERR_ARG;
   const int E = num_experts;
   const long long ldz = z_stride ? z_stride : E, lddz = dz_stride ? dz_stride : E;

@@ -1,0 +1,14 @@
+"""Sizes at the ends of the dense operators' ranges, without a GPU."""
+import expert_routing_grouped_gb300 as moe
+
+INT_MAX = 2 ** 31 - 1
+
+
+def test_balance_workspace_is_zero_for_refused_sizes():
+    """T * top_k is at most 2^26 whatever top_k, and n_seq at most 65535."""
+    ws = moe.balance_workspace
+    for T in ((1 << 26) + 1, 1 << 27, INT_MAX - 455, INT_MAX - 30, INT_MAX):
+        assert ws(T, 8, 1) == 0
+    assert ws(1 << 26, 8, 1) > 0 and ws(4, 8, 65535) > 0
+    assert ws(4, 8, 65536) == 0 and ws(4, 8, INT_MAX) == 0
+    assert ws(-1, 8, 1) == 0 and ws(4, -1, 1) == 0 and ws(4, 8, -1) == 0
