@@ -688,10 +688,11 @@ __global__ void __launch_bounds__(kFinishWarps * 32) balance_finish_kernel(const
 
 // ---------------------------------------------------------- small batches --
 
-// A segment this many times the mean one has its array's order checked first:
-// in an order that seq_off must not have, every segment could be all T tokens
-// long and the call n_seq * T rows of work.  Such a segment is taken as empty;
-// so no call works on more than kLongSeg * T rows.
+// In an order that seq_off must not have, every segment could be all T tokens
+// long and the call n_seq * T rows of work.  So a segment of more than kLongSeg
+// tokens and more than kLongSeg mean segments has its array's order checked
+// first, and counts as empty where the order is wrong: no call works on more
+// than kLongSeg * (T + n_seq) rows.
 constexpr int kLongSeg = 64;
 
 template <class L>
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(kBalThreads, L::NE <= 8 ? 3 : 1) balance_small
   const int a = seg_begin(p, s);
   int b = seg_end(p, s);
   // The same for all CTAs of the cluster; never with one segment (no seq_off).
-  if ((b - a) / kLongSeg > (p.T - 1) / p.S + 1) {
+  if (b - a > kLongSeg && (long long)(b - a) * p.S > (long long)kLongSeg * p.T) {
     int bad = 0;
     for (int i = threadIdx.x; i < p.S; i += blockDim.x) bad |= p.seq_off[i + 1] < p.seq_off[i];
     if (__syncthreads_or(bad)) b = a;

@@ -9,8 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_ops import (DT, E4M3, check_balance, check_linear, gen, make_balance, make_linear,
-                          randn, run_balance, run_linear, run_norm)
+from test_gpu_ops import (DT, E4M3, SENT, check_balance, check_linear, gen, make_balance,
+                          make_linear, randn, run_balance, run_linear, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +141,19 @@ def test_balance_masked_rows_stay_zero_whatever_comes_from_above(moe, T, E, dtyp
     loss, counts, tokens, prob, dz = run_balance(moe, z, idx, bias, none, None, 2, mode)
     assert float(loss) == 0 and int(tokens) == 0 and int(counts.sum()) == 0
     assert bool((prob == 0).all()) and bool((dz == 0).all())
+
+
+def test_balance_disorder_with_more_segments_than_tokens(moe):
+    """An array whose order would make every other of 65534 segments all 127
+    tokens long is worked on as if they were empty; the same count of segments
+    in order is summed as ever."""
+    T, E, k, S = 127, 64, 2, 65534
+    z, idx, _, _ = make_balance(gen(1), T, E, k, 0)
+    off = torch.tensor([0, T] * S, dtype=torch.int32, device="cuda")[:S + 1]
+    loss, counts, tokens, prob, dz = run_balance(moe, z, idx, None, None, off, k, 0)
+    assert int(tokens.sum()) == 0 and int(counts.sum()) == 0 and bool((dz == SENT).all())
+    S = 600
+    off = torch.full((S + 1,), 120, dtype=torch.int32, device="cuda")
+    off[:300] = 3
+    got = run_balance(moe, z, idx, None, None, off, k, 0)
+    check_balance(got, z, idx, None, None, off, k, 0)
