@@ -29,7 +29,8 @@ EXPORTS = ("moe_init", "moe_route", "moe_forward", "moe_forward_residual",
            "moe_stage_times", "moe_status", "moe_device_bytes", "moe_free", "moe_strerror",
            "moe_route_noalloc", "moe_usage_read", "moe_usage_reset", "moe_engine_id",
            "moe_route_trace_write", "moe_route_trace_read", "moe_set_next_layer",
-           "moe_add_rmsnorm", "moe_linear", "moe_balance_loss", "moe_balance_workspace")
+           "moe_add_rmsnorm", "moe_linear", "moe_linear_wait_limit", "moe_balance_loss",
+           "moe_balance_workspace")
 
 
 class MoeLayout(ctypes.Structure):
@@ -86,6 +87,7 @@ def _load():
         "moe_engine_id": (ctypes.c_uint32, [ctypes.c_char_p]),
         "moe_add_rmsnorm": (i, [P, P, P, P, i, i, f, i, i, i, i, P, P, q, q, q, q, P]),
         "moe_linear": (i, [P, P, P, P, P, P, P, i, i, i, i, i, i, q, q, q, q, P, P]),
+        "moe_linear_wait_limit": (i, [i]),
         "moe_balance_loss": (i, [P, P, P, P, P, i, i, i, i, i, i, f, P, q, P, P, P, P, P, q, P, z,
                                  P]),
         "moe_balance_workspace": (z, [i, i, i]),
@@ -262,15 +264,36 @@ def add_rmsnorm(x, T, H, eps, out, resid=None, resid_out=None, gain=None, scale=
                                       out_stride, _stream(stream)), "moe_add_rmsnorm")
 
 
+def linear_wait_limit(us):
+    """moe_linear_wait_limit: the time limit of the waits inside the products that
+    this thread launches from now on (default 2000000; 0 gives up at once)."""
+    return _check(lib.moe_linear_wait_limit(us), "moe_linear_wait_limit")
+
+
+# MOE_LINEAR_NO_WAIT=1 gives a product of this thread a wait limit of 0, for the
+# recovery path's tests.  It acts only on calls that carry a status word, which
+# then holds 2, and only where the program has set it itself: one that the
+# process inherited is nobody's wish for incomplete products.
+_NO_WAIT = "MOE_LINEAR_NO_WAIT"
+_no_wait_inherited = _NO_WAIT in os.environ
+
+
 def linear(x, w, T, N, K, out, dtype=BF16, out_dtype=F32, act=ACT_NONE, x_scale=None,
            w_scale=None, bias=None, resid=None, x_stride=0, w_stride=0, resid_stride=0,
            out_stride=0, status=None, stream=None):
     """moe_linear: out = act(x . w^T (scaled) + bias) + resid; ACT_SWIGLU takes
     2N rows of w."""
-    return _check(lib.moe_linear(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias),
-                                 _ptr(resid), _ptr(out), T, N, K, dtype, out_dtype, act, x_stride,
-                                 w_stride, resid_stride, out_stride, _ptr(status),
-                                 _stream(stream)), "moe_linear")
+    no_wait = status is not None and not _no_wait_inherited and os.environ.get(_NO_WAIT) == "1"
+    if no_wait:
+        linear_wait_limit(0)
+    try:
+        return _check(lib.moe_linear(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias),
+                                     _ptr(resid), _ptr(out), T, N, K, dtype, out_dtype, act,
+                                     x_stride, w_stride, resid_stride, out_stride, _ptr(status),
+                                     _stream(stream)), "moe_linear")
+    finally:
+        if no_wait:
+            linear_wait_limit(2000000)
 
 
 def balance_workspace(T, num_experts, n_seq=1):

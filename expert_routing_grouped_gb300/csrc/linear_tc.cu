@@ -44,7 +44,6 @@
 // Every mbarrier wait is bounded: one that gives up sets the status word, and
 // the roles stop, drain their copies and MMAs, and return.
 #include <algorithm>
-#include <cstdlib>
 #include <cuda.h>
 
 #include "linear.cuh"
@@ -674,6 +673,9 @@ int device_sms() {
 
 int up(int v, int m) { return (v + m - 1) / m; }
 
+// moe_linear_wait_limit's, for the products that this host thread launches.
+thread_local unsigned long long wait_limit_ns = kWaitNs;
+
 // Clusters of 1 .. 8 CTAs, one CTA to an SM, that run at once on 152 SMs
 // (cudaOccupancyMaxActiveClusters): a split into more takes a second wave,
 // which costs more than it gains (48 clusters of 3 for N = 6144: 28 us; of 2:
@@ -797,10 +799,7 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
   q.x_rows = pair ? q.bn / 2 : q.bn;
   q.n_fb = up(rows, pair ? 2 * BM : BM);
   q.group_tb = std::min(q.n_tb, 16);
-  // Test hook: MOE_LINEAR_NO_WAIT=1 makes every wait that is not complete when
-  // first tested give up, to exercise the way out without a fault or a hang.
-  const char *no_wait = getenv("MOE_LINEAR_NO_WAIT");
-  q.wait_ns = no_wait && no_wait[0] == '1' ? 0 : kWaitNs;
+  q.wait_ns = wait_limit_ns;
   const size_t stage = (size_t)(BM + q.x_rows) * kRowBytes;
   q.stages = (int)std::min<size_t>(kMaxStages, (kSmemMax - sizeof(Bars) - 64 - 1024) / stage);
   if (sw) {
@@ -817,3 +816,9 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
 }
 
 }  // namespace moe
+
+extern "C" __attribute__((visibility("default"))) int moe_linear_wait_limit(int us) {
+  if (us < 0) return MOE_ERR_ARG;
+  moe::wait_limit_ns = (unsigned long long)us * 1000ull;
+  return MOE_OK;
+}

@@ -394,6 +394,22 @@ int moe_linear(const void *x, const float *x_scale, const void *w, const float *
                int64_t out_stride, int32_t *status, moe_stream_t stream);
 
 /*
+ * The time limit, in microseconds, of the waits between a product's pipelined
+ * roles, for the products that the calling host thread launches from now on
+ * (default 2000000).  A wait that is not complete when its limit has passed
+ * gives up: the kernel stops its roles, waits (with the full 2 s limit) for
+ * its own copies and MMAs in flight, frees its tensor memory and returns, so
+ * the next product runs normally; the status word holds 2, and moe_linear
+ * returns MOE_OK (the launch succeeded).  0 makes every wait that is not
+ * complete when first tested give up at once: a way to exercise that recovery
+ * path without a fault or a hang, as MOE_OPT_WAIT_LIMIT_US is for the layer.
+ * Products of at most 16 tokens have no such waits.  A captured product keeps
+ * the limit that it was captured with.  Returns MOE_OK, or MOE_ERR_ARG for a
+ * negative limit.
+ */
+int moe_linear_wait_limit(int us);
+
+/*
  * The router's balance loss, per-expert counts and the gradient of its logits.
  * With p[t] the router's probabilities over all experts -- softmax(z[t] + bias)
  * for router_mode 0 and 2, sigmoid(z[t]) / sum sigmoid(z[t]) for mode 1, where

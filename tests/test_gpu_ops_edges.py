@@ -97,6 +97,56 @@ def test_linear_pairs_back_to_back(moe):
     assert torch.equal(small, few)
 
 
+@pytest.mark.parametrize("T,K,N", [(40, 8192, 256), (1000, 2048, 320), (4096, 1024, 4096)])
+def test_linear_wait_limit(moe, T, K, N):
+    """The limit set through the call (split, one CTA per tile, CTA pairs): the
+    product returns and its status word says 2; with the default back the next
+    one is right, and a product of another thread never saw the limit."""
+    import threading
+    g = gen(T)
+    x, w, _, _, _, _ = make_linear(g, T, K, N, 1, 0, 0, False, False)
+    others = []
+    moe.linear_wait_limit(0)
+    try:
+        out, status = run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)
+        torch.cuda.synchronize()
+        t = threading.Thread(target=lambda: others.append(
+            run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)))
+        t.start()
+        t.join()
+    finally:
+        moe.linear_wait_limit(2000000)
+    assert int(status) == 2
+    for out, status in others + [run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)]:
+        check_linear(out, status, x, w, None, None, None, None, N, 0)
+
+
+def test_linear_environment_does_not_reach_the_kernels(moe, monkeypatch):
+    """MOE_LINEAR_NO_WAIT: not without a status word, and not where the process
+    inherited it."""
+    import os
+    import subprocess
+    import sys
+    g = gen(3)
+    T, K, N = 40, 4096, 256
+    x, w, _, _, _, _ = make_linear(g, T, K, N, 1, 0, 0, False, False)
+    want, status = run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)
+    check_linear(want, status, x, w, None, None, None, None, N, 0)
+    out = torch.zeros_like(want)
+    monkeypatch.setenv("MOE_LINEAR_NO_WAIT", "1")
+    moe.linear(x, w, T, N, K, out)
+    assert torch.equal(out, want)
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import test_gpu_ops as t, expert_routing_grouped_gb300 as moe\n"
+            "x, w = t.make_linear(t.gen(3), 40, 4096, 256, 1, 0, 0, False, False)[:2]\n"
+            "out, status = t.run_linear(moe, x, w, None, None, None, None, 256, 1, 0, 0)\n"
+            "t.check_linear(out, status, x, w, None, None, None, None, 256, 0)\n"
+            % (os.path.dirname(here), here))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 # ------------------------------------------------------------ balance loss --
 
 @pytest.mark.parametrize("level", [-87.0, -84.0, -60.0, -30.0, 10.0])

@@ -12,3 +12,8 @@ def test_balance_workspace_is_zero_for_refused_sizes():
     assert ws(1 << 26, 8, 1) > 0 and ws(4, 8, 65535) > 0
     assert ws(4, 8, 65536) == 0 and ws(4, 8, INT_MAX) == 0
     assert ws(-1, 8, 1) == 0 and ws(4, -1, 1) == 0 and ws(4, 8, -1) == 0
+
+
+def test_linear_wait_limit_refuses():
+    assert moe.lib.moe_linear_wait_limit(-1) == moe.MOE_ERR_ARG
+    assert moe.lib.moe_linear_wait_limit(2000000) == moe.MOE_OK
