@@ -437,6 +437,14 @@ __global__ void __launch_bounds__(kThreads<kSegs>, 1) linear_tc_kernel(const __g
       int s = 0;
       uint32_t ph = 0, armed = 0, par = 0;
       bool ok = true;
+      // A limit of 0 is there to show the way out: operands that happen to be at
+      // hand when first tested (40 x 8192 x 256 out of L2, two calls of three)
+      // would not, so they come late.
+      if (q.wait_ns == 0) {
+        const unsigned long long start = globaltimer();
+        while (globaltimer() - start < 20000ull) {
+        }
+      }
       for (int t = t_first; ok && t < n_tiles; t += t_step) {
         const Tile tl = tile_at(q, t);
         const int fb = block_of(tl), x_row = x_row_of(tl);

@@ -401,11 +401,11 @@ int moe_linear(const void *x, const float *x_scale, const void *w, const float *
  * its own copies and MMAs in flight, frees its tensor memory and returns, so
  * the next product runs normally; the status word holds 2, and moe_linear
  * returns MOE_OK (the launch succeeded).  0 makes every wait that is not
- * complete when first tested give up at once: a way to exercise that recovery
- * path without a fault or a hang, as MOE_OPT_WAIT_LIMIT_US is for the layer.
- * Products of at most 16 tokens have no such waits.  A captured product keeps
- * the limit that it was captured with.  Returns MOE_OK, or MOE_ERR_ARG for a
- * negative limit.
+ * complete when first tested give up at once, and the first operands come late
+ * enough for one to do so: a way to exercise that recovery path without a fault
+ * or a hang, as MOE_OPT_WAIT_LIMIT_US is for the layer.  Products of at most
+ * 16 tokens have no such waits.  A captured product keeps the limit that it
+ * was captured with.  Returns MOE_OK, or MOE_ERR_ARG for a negative limit.
  */
 int moe_linear_wait_limit(int us);
 

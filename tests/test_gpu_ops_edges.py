@@ -108,15 +108,15 @@ def test_linear_wait_limit(moe, T, K, N):
     others = []
     moe.linear_wait_limit(0)
     try:
-        out, status = run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)
-        torch.cuda.synchronize()
+        for _ in range(20):   # also where the operands lie in L2
+            out, status = run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)
+            assert int(status) == 2
         t = threading.Thread(target=lambda: others.append(
             run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)))
         t.start()
         t.join()
     finally:
         moe.linear_wait_limit(2000000)
-    assert int(status) == 2
     for out, status in others + [run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)]:
         check_linear(out, status, x, w, None, None, None, None, N, 0)
 
