@@ -29,8 +29,8 @@ EXPORTS = ("moe_init", "moe_route", "moe_forward", "moe_forward_residual",
            "moe_stage_times", "moe_status", "moe_device_bytes", "moe_free", "moe_strerror",
            "moe_route_noalloc", "moe_usage_read", "moe_usage_reset", "moe_engine_id",
            "moe_route_trace_write", "moe_route_trace_read", "moe_set_next_layer",
-           "moe_add_rmsnorm", "moe_linear", "moe_linear_wait_limit", "moe_balance_loss",
-           "moe_balance_workspace")
+           "moe_add_rmsnorm", "moe_linear", "moe_linear_status", "moe_linear_wait_limit",
+           "moe_balance_loss", "moe_balance_workspace")
 
 
 class MoeLayout(ctypes.Structure):
@@ -87,6 +87,7 @@ def _load():
         "moe_engine_id": (ctypes.c_uint32, [ctypes.c_char_p]),
         "moe_add_rmsnorm": (i, [P, P, P, P, i, i, f, i, i, i, i, P, P, q, q, q, q, P]),
         "moe_linear": (i, [P, P, P, P, P, P, P, i, i, i, i, i, i, q, q, q, q, P, P]),
+        "moe_linear_status": (i, [P]),
         "moe_linear_wait_limit": (i, [i]),
         "moe_balance_loss": (i, [P, P, P, P, P, i, i, i, i, i, i, f, P, q, P, P, P, P, P, q, P, z,
                                  P]),
@@ -264,6 +265,15 @@ def add_rmsnorm(x, T, H, eps, out, resid=None, resid_out=None, gain=None, scale=
                                       out_stride, _stream(stream)), "moe_add_rmsnorm")
 
 
+def linear_status():
+    """moe_linear_status: 2 if a product without a status word of its own gave up
+    on the current device since the last call that said so, else 0.  Waits for
+    all work on the device."""
+    s = ctypes.c_int32()
+    _check(lib.moe_linear_status(ctypes.byref(s)), "moe_linear_status")
+    return s.value
+
+
 def linear_wait_limit(us):
     """moe_linear_wait_limit: the time limit of the waits inside the products that
     this thread launches from now on (default 2000000; 0 gives up at once)."""
@@ -282,7 +292,8 @@ def linear(x, w, T, N, K, out, dtype=BF16, out_dtype=F32, act=ACT_NONE, x_scale=
            w_scale=None, bias=None, resid=None, x_stride=0, w_stride=0, resid_stride=0,
            out_stride=0, status=None, stream=None):
     """moe_linear: out = act(x . w^T (scaled) + bias) + resid; ACT_SWIGLU takes
-    2N rows of w."""
+    2N rows of w.  A product whose bounded waits gave up is not complete and says
+    so in status, an int32 tensor, or without one to linear_status()."""
     no_wait = status is not None and not _no_wait_inherited and os.environ.get(_NO_WAIT) == "1"
     if no_wait:
         linear_wait_limit(0)

@@ -41,7 +41,8 @@
 // e4m3 SwiGLU 270 us (3.56 PFLOP/s); 64 x 6144 x 1024, split in 8, 8.7 us, of
 // which about 6 are start, exchange and end.
 //
-// Every mbarrier wait is bounded: one that gives up sets the status word, and
+// Every mbarrier wait is bounded: one that gives up sets the status word (the
+// caller's, or the device's where there is none), and
 // the roles stop, drain their copies and MMAs, and return.
 #include <algorithm>
 #include <cuda.h>
@@ -99,8 +100,11 @@ struct Bars {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int32_t status;          // used when the caller gave no status word
 };
+
+// Set by the products on this device that gave up and had no status word of
+// their caller's; moe_linear_status reads it.
+__device__ int32_t gave_up;
 
 template <int DT>
 __device__ __forceinline__ uint32_t linear_idesc(int m, int n) {
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(kThreads<kSegs>, 1) linear_tc_kernel(const __g
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const LinearParams &p = q.p;
-  int32_t *status = p.status ? p.status : &sm.status;
+  int32_t *status = p.status ? p.status : &gave_up;
   constexpr int G = kEpiGroups<kSegs>;
   constexpr int kBlockElems = kRowBytes / (DT == MOE_BF16 ? 2 : 1);
   const uint32_t stage_bytes = (BM + q.x_rows) * kRowBytes;
@@ -828,5 +832,15 @@ cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) 
 extern "C" __attribute__((visibility("default"))) int moe_linear_wait_limit(int us) {
   if (us < 0) return MOE_ERR_ARG;
   moe::wait_limit_ns = (unsigned long long)us * 1000ull;
+  return MOE_OK;
+}
+
+extern "C" __attribute__((visibility("default"))) int moe_linear_status(int32_t *status) {
+  if (!status) return MOE_ERR_ARG;
+  int32_t none = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpyFromSymbol(status, moe::gave_up, 4) != cudaSuccess ||
+      (*status && cudaMemcpyToSymbol(moe::gave_up, &none, 4) != cudaSuccess))
+    return MOE_ERR_DEVICE;
   return MOE_OK;
 }

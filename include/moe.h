@@ -380,8 +380,9 @@ int moe_add_rmsnorm(const void *x, const void *resid, void *resid_out, const flo
  *   bias     [rows of w] f32, or NULL
  *   resid    [T][N] of out's type, or NULL; may be out itself (the same stride)
  *   out      [T][N] MOE_F32 or MOE_BF16 (out_dtype)
- *   status   int32 on the device, or NULL: set to 2 when a bounded wait of the
- *            kernel gave up (out is then not complete); otherwise left alone
+ *   status   int32 on the device: set to 2 when a bounded wait of the kernel
+ *            gave up (out is then not complete); otherwise left alone.  NULL:
+ *            such a product sets the device's own word (moe_linear_status)
  * Sums are f32; out is rounded once.  T, N and K are at most 2^19; K and the
  * strides of x and w are multiples of 16 bytes, x and w 16-byte aligned; N is
  * any number (a multiple of 16 for SwiGLU).  out must not overlap anything
@@ -392,6 +393,14 @@ int moe_linear(const void *x, const float *x_scale, const void *w, const float *
                const float *bias, const void *resid, void *out, int T, int N, int K, int dtype,
                int out_dtype, int act, int64_t x_stride, int64_t w_stride, int64_t resid_stride,
                int64_t out_stride, int32_t *status, moe_stream_t stream);
+
+/*
+ * Waits for all work on the current device and gives in *status 2 if a product
+ * on it without a status word of its own gave up since the last call that said
+ * so (its out is then not complete), 0 otherwise.  Not during a capture.
+ * Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
+ */
+int moe_linear_status(int32_t *status);
 
 /*
  * The time limit, in microseconds, of the waits between a product's pipelined

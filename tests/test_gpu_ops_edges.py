@@ -121,6 +121,27 @@ def test_linear_wait_limit(moe, T, K, N):
         check_linear(out, status, x, w, None, None, None, None, N, 0)
 
 
+@pytest.mark.parametrize("T,K,N", [(40, 8192, 256), (1000, 2048, 320), (4096, 1024, 4096)])
+def test_linear_that_gave_up_without_a_status_word(moe, T, K, N):
+    """The device's word says so, once; a status word of the caller's own keeps
+    it out of there."""
+    g = gen(T)
+    x, w, _, _, _, _ = make_linear(g, T, K, N, 1, 0, 0, False, False)
+    out = torch.empty(T, N, device="cuda")
+    assert moe.linear_status() == 0
+    moe.linear_wait_limit(0)
+    try:
+        moe.linear(x, w, T, N, K, out)
+        assert moe.linear_status() == 2 and moe.linear_status() == 0
+        _, status = run_linear(moe, x, w, None, None, None, None, N, 1, 0, 0)
+        assert moe.linear_status() == 0 and int(status) == 2
+    finally:
+        moe.linear_wait_limit(2000000)
+    moe.linear(x, w, T, N, K, out)
+    assert moe.linear_status() == 0
+    check_linear(out, torch.zeros(1), x, w, None, None, None, None, N, 0)
+
+
 def test_linear_environment_does_not_reach_the_kernels(moe, monkeypatch):
     """MOE_LINEAR_NO_WAIT: not without a status word, and not where the process
     inherited it."""

@@ -17,3 +17,7 @@ def test_balance_workspace_is_zero_for_refused_sizes():
 def test_linear_wait_limit_refuses():
     assert moe.lib.moe_linear_wait_limit(-1) == moe.MOE_ERR_ARG
     assert moe.lib.moe_linear_wait_limit(2000000) == moe.MOE_OK
+
+
+def test_linear_status_refuses():
+    assert moe.lib.moe_linear_status(None) == moe.MOE_ERR_ARG
