@@ -61,7 +61,8 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t *row, int off, int byt
 // rows).  HI: more than 8 tokens.  W: warps.  kFold (bf16 operands, f32
 // output): the MMAs truncate as they add, 1.8e-8 of the result each, so every
 // four steps their sums are added in f32 to nearest (K = 14336: error 4.5e-7 in
-// place of 1.8e-6, 19.7 us in place of 19.5); a bf16 output does not see it.
+// place of 1.8e-6, 19.7 us in place of 19.5); a bf16 output does not see it, and
+// e4m3 operands lose too little to need it (4.5e-7 at K = 2^19).
 // Each lane has four 16-byte pieces of w in flight whatever NB.
 template <int DT, int NB, bool HI, int W, bool kFold>
 __global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const LinearParams p) {

@@ -15,7 +15,9 @@
 // 1.8e-8 of the result per addition (16 bf16 products): 1.6e-5 at K = 14336.
 // That is nothing beside a bf16 output's 2^-9, but for f32 output the
 // accumulator is handed over every kSegBlocks K blocks (kSegs) and the epilogue
-// adds the segments in f32 to nearest, in registers: under 1e-6 whatever K.
+// adds the segments in f32 to nearest, in registers: under 1e-6 of the result
+// whatever K, for operands of both signs.  (All of one sign, every loss adds up:
+// up to 1.5e-6 for bf16; e4m3 1.1e-6 at K = 14336, 5e-6 for SwiGLU at 6144.)
 // Reading an accumulator takes TMEM from the MMAs, about 300 clocks: 2048 x
 // 14336 x 4096 onto an f32 stream takes 147 us in one segment, 167 in segments
 // of 12.
@@ -60,8 +62,8 @@ constexpr int kMaxStages = 8;
 constexpr int kEpiWarp0 = 4;
 // K blocks per accumulator segment; SwiGLU multiplies two sums, and their errors
 // add.  e4m3 products have 8 significant bits, so their sums lose little (4e-7
-// of the result at K = 6144, 1e-6 at 14336 in one segment): they go without up
-// to kPlainBlocks K blocks.
+// of the result at K = 6144, 7e-7 for SwiGLU, 1e-6 at 14336 in one segment):
+// they go without up to kPlainBlocks K blocks.
 template <int DT, bool kSwiglu>
 constexpr int kSegBlocks = DT == MOE_BF16 ? (kSwiglu ? 7 : 12) : (kSwiglu ? 24 : 48);
 constexpr int kPlainBlocks = 48;
@@ -70,6 +72,8 @@ constexpr int kSegMaxBN = 192;      // with segment sums in registers
 // Epilogue warps per lane quadrant: they take turns at blocks of 16 columns.
 // With segments there are three, so that a thread's segment sums (64 at BN =
 // 192) fit its registers: spilled, they share the path that feeds the MMAs.
+// (Seven or eight scalars of a tile do spill in the solo and pair forms without
+// SwiGLU, at the 128 registers that 512 threads leave.)
 template <bool kSegs>
 constexpr int kEpiGroups = kSegs ? 3 : 2;
 template <bool kSegs>

@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 import torch
 
+import ops_ref as ref
 from test_gpu_ops import (DT, E4M3, SENT, check_balance, check_linear, gen, make_balance,
                           make_linear, randn, run_balance, run_linear, run_norm)
 
@@ -73,6 +74,45 @@ def test_add_rmsnorm_codes_are_the_rounded_quotients(moe, group, with_gain, dtyp
 
 
 # ------------------------------------------------------------------ linear --
+
+# Relative error of a whole f32 result, |out - y| / |y| over all its elements.
+# A truncating addition to an accumulator loses between nothing and one unit in
+# the last place (2^-23) of the running sum, half of it on average.  A segment
+# of K is at most 48 additions (of 16 bf16 products), in each factor of a SwiGLU
+# 28; the additions of the segments, to nearest, are far below.  With operands of
+# both signs a running sum averages 2/3 of its end: 48 * 2^-24 * 2/3 = 1.9e-6,
+# SwiGLU 2 * 28 * 2^-24 * 2/3 = 2.2e-6 times the activation's slope of at most
+# 1.13.  e4m3 products hold 8 significant bits and lose far less, so their longer
+# segments meet the same bound.  One accumulator for all of K = 14336 would lose
+# 896 * 2^-24 * 2/3 = 3.6e-5.
+PLAIN_REL, SWIGLU_REL = 2e-6, 3e-6
+
+
+def one_sign_rel(dtype, act):
+    """Operands of one sign: every loss adds up, whole units at most, and a
+    running sum averages half of its end.  e4m3 segments: 192 additions of 32
+    products, which then hold more bits than the accumulator has left."""
+    adds = 192 if dtype == 2 else 28 if act == 3 else 48
+    return adds * 2.0 ** -23 / 2 * (2 * 1.13 if act == 3 else 1)
+
+
+@pytest.mark.parametrize("one_sign", [False, True])
+@pytest.mark.parametrize("dtype", [1, 2])
+@pytest.mark.parametrize("T,K,N,act", [
+    (1, 4096, 256, 0), (4, 14336, 512, 0), (9, 14336, 256, 3), (16, 131072, 64, 0), (3, 524288 - 256, 40, 0),
+    (16, 262144, 16, 3), (24, 4096, 512, 0), (40, 14336, 256, 3), (130, 14336, 512, 0), (200, 131072, 64, 0),
+    (64, 131072, 32, 3), (200, 524288, 64, 0), (700, 14336, 1024, 0), (1200, 6144, 1536, 3)])
+def test_linear_f32_outputs_are_f32_sums(moe, T, K, N, act, dtype, one_sign):
+    g = gen(T + N)
+    x, w, sx, sw, b, r = make_linear(g, T, K, N, dtype, act, 0, False, False)
+    if one_sign:
+        x, w = x.float().abs().to(x.dtype), w.float().abs().to(w.dtype)
+    out, st = run_linear(moe, x, w, sx, sw, None, None, N, dtype, 0, act)
+    y, _ = ref.linear(x, w, N, act, sx, sw)
+    rel = float((out.double() - y).norm() / y.norm())
+    bound = one_sign_rel(dtype, act) if one_sign else SWIGLU_REL if act == 3 else PLAIN_REL
+    assert int(st) == 0 and rel <= bound, rel
+
 
 def test_linear_pairs_back_to_back(moe):
     """Products in the CTA-pair form one after another, between them kernels
