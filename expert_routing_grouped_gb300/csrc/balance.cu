@@ -886,7 +886,20 @@ extern "C" __attribute__((visibility("default"))) int moe_balance_loss(
   const int E = num_experts;
   const long long ldz = z_stride ? z_stride : E, lddz = dz_stride ? dz_stride : E;
   if (ldz < E || lddz < E || ldz > (1LL << 32) || lddz > (1LL << 32)) return MOE_ERR_ARG;
-  if (T == 0) return MOE_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {   // every segment is empty
+    if (!loss || !counts || !tokens || !prob) return MOE_OK;
+    const size_t S4 = (size_t)n_seq * 4, SE4 = S4 * E;
+    const Area wr[] = {area(loss, S4), area(counts, SE4), area(tokens, S4), area(prob, SE4)};
+    for (int i = 0; i < 4; ++i) {
+      if (reinterpret_cast<uintptr_t>(wr[i].p) & 3) return MOE_ERR_ARG;
+      for (int j = 0; j < i; ++j)
+        if (meet(wr[i], wr[j])) return MOE_ERR_ARG;
+    }
+    for (const Area &a : wr)
+      if (cudaMemsetAsync(const_cast<void *>(a.p), 0, a.bytes, st) != cudaSuccess) return MOE_ERR_DEVICE;
+    return MOE_OK;
+  }
   if (!loss || !counts || !tokens || !prob || !z || !idx) return MOE_ERR_ARG;
   if (workspace_bytes < moe_balance_workspace(T, E, n_seq)) return MOE_ERR_NOMEM;
   if (!workspace) return MOE_ERR_ARG;
@@ -922,7 +935,6 @@ extern "C" __attribute__((visibility("default"))) int moe_balance_loss(
         if (meet(wr[i], wr[j])) return MOE_ERR_ARG;
     }
   }
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   BalParams p{z, router_mode == 1 ? nullptr : bias, idx, mask, seq_off, grad, loss, counts, tokens,
               prob, dz, static_cast<float *>(workspace), nullptr, ldz, lddz, T, E, top_k, n_seq,
               (E + 3) / 4 * 4, balance_chunk(T), balance_count_chunk(T, dz != nullptr), top_k % 4 == 0 && !(reinterpret_cast<uintptr_t>(idx) & 15), alpha};

@@ -456,9 +456,11 @@ int moe_linear_wait_limit(int us);
  * A row whose logits are all -infinity (in mode 1: whose sigmoids are all
  * below 2^-126) has p = 0.  num_experts <= 1024, top_k
  * <= 32, T * top_k <= 2^26, n_seq <= 65535.  Loss and gradient together read z
- * once.  Outputs and workspace must not overlap anything else.  T == 0 checks
- * what it can, launches nothing and writes nothing.  Returns MOE_OK,
- * MOE_ERR_NOMEM (workspace too small), MOE_ERR_ROUTING, MOE_ERR_ARG or
+ * once.  Outputs and workspace must not overlap anything else.  T == 0: every
+ * segment is empty, and loss, counts, tokens and prob, where all four are
+ * given, are set to 0; z, idx, dz and the workspace are not touched (with one
+ * of the four NULL the call checks what it can and writes nothing).  Returns
+ * MOE_OK, MOE_ERR_NOMEM (workspace too small), MOE_ERR_ROUTING, MOE_ERR_ARG or
  * MOE_ERR_DEVICE.
  */
 int moe_balance_loss(const void *z, const float *bias, const int32_t *idx, const uint8_t *mask,

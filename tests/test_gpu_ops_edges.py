@@ -268,3 +268,33 @@ def test_balance_disorder_with_more_segments_than_tokens(moe):
     off[:300] = 3
     got = run_balance(moe, z, idx, None, None, off, k, 0)
     check_balance(got, z, idx, None, None, off, k, 0)
+
+
+def test_balance_of_no_tokens_is_zero(moe):
+    """T = 0: every segment is empty, and its results are an empty segment's,
+    in a captured call too."""
+    E, S = 16, 5
+    f = dict(device="cuda")
+    loss, prob = torch.full((S + 1,), SENT, **f), torch.full((S + 1, E), SENT, **f)
+    counts = torch.full((S + 1, E), 77, dtype=torch.int32, **f)
+    tokens = torch.full((S + 1,), 77, dtype=torch.int32, **f)
+    off = torch.zeros(S + 1, dtype=torch.int32, **f)
+    z, idx = torch.empty(0, E, **f), torch.empty(0, 2, dtype=torch.int32, **f)
+    ws = torch.empty(0, dtype=torch.uint8, **f)
+
+    def call():
+        moe.balance_loss(z, idx, 0, E, 2, loss, counts, tokens, prob, ws, seq_off=off, n_seq=S)
+
+    def check():
+        for t, fill in ((loss, SENT), (prob, SENT), (counts, 77), (tokens, 77)):
+            assert bool((t[:S] == 0).all()) and bool((t[S:] == fill).all())
+
+    call()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for t, fill in ((loss, SENT), (prob, SENT), (counts, 77), (tokens, 77)):
+        t.fill_(fill)
+    graph.replay()
+    check()

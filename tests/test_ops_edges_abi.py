@@ -21,3 +21,16 @@ def test_linear_wait_limit_refuses():
 
 def test_linear_status_refuses():
     assert moe.lib.moe_linear_status(None) == moe.MOE_ERR_ARG
+
+
+def test_balance_of_no_tokens_refuses():
+    """The outputs that T = 0 sets to zero are checked like any call's."""
+    a = [(i + 1) << 26 for i in range(4)]   # loss, counts, tokens, prob
+
+    def call(loss, counts, tokens, prob):
+        return moe.lib.moe_balance_loss(None, None, None, None, a[0] << 4, 0, 16, 2, 3, 0, 0, 0.01, None,
+                                        0, loss, counts, tokens, prob, None, 0, None, 0, None)
+
+    assert call(a[0] + 2, a[1], a[2], a[3]) == moe.MOE_ERR_ARG
+    assert call(a[0], a[1], a[1] + 64, a[3]) == moe.MOE_ERR_ARG
+    assert call(a[0], a[1], a[2], None) == moe.MOE_OK
