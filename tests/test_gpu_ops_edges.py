@@ -10,8 +10,8 @@ import pytest
 import torch
 
 import ops_ref as ref
-from test_gpu_ops import (DT, E4M3, SENT, check_balance, check_linear, gen, make_balance,
-                          make_linear, randn, run_balance, run_linear, run_norm)
+from test_gpu_ops import (DT, E4M3, SENT, check_balance, check_linear, check_norm, gen,
+                          make_balance, make_linear, randn, run_balance, run_linear, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -71,6 +71,59 @@ def test_add_rmsnorm_codes_are_the_rounded_quotients(moe, group, with_gain, dtyp
     assert torch.equal(scale.cpu().view(T, -1), sc)
     codes = (want / sc[:, :, None]).clamp(-448, 448).to(E4M3).view(T, H)
     assert torch.equal(out.cpu().view(torch.uint8), codes.view(torch.uint8))
+
+
+# Rows of more than 4096 values in batches of 304 rows and more: at most 512
+# threads a row, each with two, four or eight pieces.
+@pytest.mark.parametrize("T,H", [(304, 4096 + 16), (310, 12288), (305, 20000), (304, 32768)])
+@pytest.mark.parametrize("out_dtype,group", [(1, 0), (2, 0), (2, 32)])
+def test_add_rmsnorm_many_long_rows(moe, T, H, out_dtype, group):
+    if group:
+        H = H // group * group
+    g = gen(T + H)
+    x = (3 * randn(g, T, H)).bfloat16()
+    resid = 5 * randn(g, T, H)
+    gain = 1 + 0.3 * randn(g, H)
+    out, scale, rout = run_norm(moe, x, resid, gain, out_dtype, group)
+    check_norm(x, resid, gain, out, scale, rout, out_dtype, group)
+
+
+def wide(T, n, extra, dtype):
+    """A whole buffer of T rows of n + extra values, all SENT, and its first n columns."""
+    full = torch.full((T, n + extra), SENT, device="cuda").to(dtype)
+    return full, full[:, :n]
+
+
+@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("H", [192, 4096 + 32])
+def test_padding_of_every_row_is_left_alone(moe, T, H):
+    """Also behind the last row's end."""
+    g = gen(T)
+    for out_dtype, group in ((1, 0), (2, 0), (2, 32)):
+        x, resid = randn(g, T, H).bfloat16(), randn(g, T, H)
+        full, out = wide(T, H, 32, DT[out_dtype])
+        rfull, rout = wide(T, H, 32, torch.float32)
+        scale = torch.full((T * (H // (group or H)) + 8,), SENT, device="cuda")
+        moe.add_rmsnorm(x, T, H, 1e-6, out, resid=resid, resid_out=rout,
+                        scale=scale if out_dtype == 2 else None, group=group, out_dtype=out_dtype,
+                        out_stride=H + 32, resid_out_stride=H + 32)
+        assert bool((full[:, H:].float() == SENT).all()) and bool((rfull[:, H:] == SENT).all())
+        assert bool((scale[T * (H // (group or H)):] == SENT).all())
+    for rows in (T, 20 * T):   # few tokens, and the tensor-core form
+        for out_dtype in (0, 1):
+            x, w, sx, sw, b, r = make_linear(g, rows, 64, 37, 1, 0, out_dtype, False, False)
+            full, out = wide(rows, 37, 3, DT[out_dtype])
+            moe.linear(x, w, rows, 37, 64, out, out_dtype=out_dtype, out_stride=40)
+            assert bool((full[:, 37:].float() == SENT).all())
+    for E in (7, 64):
+        z, idx, _, _ = make_balance(g, T, E, 2, 0)
+        full, dz = wide(T, E, 4, torch.float32)
+        f = dict(device="cuda")
+        ws = torch.empty(moe.balance_workspace(T, E), dtype=torch.uint8, **f)
+        moe.balance_loss(z, idx, T, E, 2, torch.empty(1, **f), torch.empty(1, E, dtype=torch.int32, **f),
+                         torch.empty(1, dtype=torch.int32, **f), torch.empty(1, E, **f), ws, dz=dz,
+                         dz_stride=E + 4)
+        assert bool((full[:, E:] == SENT).all()) and bool((full[:, :E] != SENT).all())
 
 
 # ------------------------------------------------------------------ linear --
@@ -252,6 +305,25 @@ def test_balance_masked_rows_stay_zero_whatever_comes_from_above(moe, T, E, dtyp
     loss, counts, tokens, prob, dz = run_balance(moe, z, idx, bias, none, None, 2, mode)
     assert float(loss) == 0 and int(tokens) == 0 and int(counts.sum()) == 0
     assert bool((prob == 0).all()) and bool((dz == 0).all())
+
+
+# Chunks of the pass above 32 tokens (T > 14592) and of the histograms above
+# 256 (T > 16384), and several rows of one warp in a segment.
+@pytest.mark.parametrize("T,E,k,S,dtype,mode", [
+    (16389, 256, 8, 24, 1, 1), (16389, 64, 4, 5, 0, 0), (40001, 64, 2, 7, 1, 0), (40001, 130, 4, 3, 0, 1),
+    (40001, 8, 2, 1, 0, 0), (70000, 32, 2, 11, 0, 1)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_balance_long_batches(moe, T, E, k, S, dtype, mode, mask):
+    g = gen(T + E)
+    z, idx, off, m = make_balance(g, T, E, k, dtype, S, mask)
+    bias = 0.3 * randn(g, E)
+    grad = 1 + 0.1 * randn(g, S)
+    got = run_balance(moe, z, idx, bias, m, off, k, mode, grad=grad)
+    check_balance(got, z, idx, bias, m, off, k, mode, grad=grad)
+    plain = run_balance(moe, z, idx, bias, m, off, k, mode, want_dz=False)
+    check_balance(plain, z, idx, bias, m, off, k, mode)
+    for a, b in zip(got[:4], plain[:4]):   # with and without a gradient, the same bits
+        assert torch.equal(a, b)
 
 
 def test_balance_disorder_with_more_segments_than_tokens(moe):
