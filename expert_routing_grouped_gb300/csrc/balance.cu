@@ -29,7 +29,7 @@
 // For short segments one kernel does all three steps, a cluster per segment
 // with cluster barriers between them: there the launches are the time.
 //
-// Memory bound when large: T = 65536, E = 256, f32 logits take 32.8 us with the
+// Memory bound when large: T = 65536, E = 256, f32 logits take 32.9 us with the
 // gradient (134 MB: 20 us at a copy's rate; the count and finish kernels and
 // their hand-over are about 8), 20.4 us without (10).  64 x 64: 6.1 us.
 #include <algorithm>

@@ -19,7 +19,7 @@
 // whatever K, for operands of both signs.  (All of one sign, every loss adds up:
 // up to 1.5e-6 for bf16; e4m3 1.1e-6 at K = 14336, 5e-6 for SwiGLU at 6144.)
 // Reading an accumulator takes TMEM from the MMAs, about 300 clocks: 2048 x
-// 14336 x 4096 onto an f32 stream takes 147 us in one segment, 167 in segments
+// 14336 x 4096 onto an f32 stream takes 147 us in one segment, 164 in segments
 // of 12.
 //
 // Three forms (kMode):
@@ -38,10 +38,11 @@
 // The tokens are cut into n_tb nearly equal tiles (a difference of one unit of
 // 16, in pairs 32), so that the tiles fill whole waves of the SMs.
 //
-// Measured: 8192^3 bf16 566 us (1.94 PFLOP/s, 1.02 of a library product's burst
-// rate; 647 us in the solo form), 4096 x 6144 x 6144 164 us, 4096 x 4096 x 14336
-// e4m3 SwiGLU 270 us (3.56 PFLOP/s); 64 x 6144 x 1024, split in 8, 8.7 us, of
-// which about 6 are start, exchange and end.
+// Measured on the device, in graphs of calls: 8192^3 bf16 566 to 580 us (1.94 to
+// 1.89 PFLOP/s, a library product's burst rate; 647 us in the solo form), 4096 x
+// 6144 x 6144 165 us, 4096 x 4096 x 14336 e4m3 SwiGLU 270 us (3.56 PFLOP/s; 315
+// in a long loop of calls, at the card's power limit); 64 x 6144 x 1024, split
+// in 8, 8.7 us, of which about 6 are start, exchange and end.
 //
 // Every mbarrier wait is bounded: one that gives up sets the status word (the
 // caller's, or the device's where there is none), and

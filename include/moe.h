@@ -346,12 +346,12 @@ int moe_route_noalloc(const void *x, int T, int hidden, int num_experts, int top
  *              of H; 0 with bf16 output
  *   scale      [T][H / group] f32, contiguous ([T] with group 0); unused
  *              (may be NULL) with bf16 output
- * H a multiple of 8 (16 for e4m3), at most 32768; x, resid, resid_out, gain
- * and out 16-byte aligned with row strides of a multiple of 16 bytes.  out and
- * scale must not overlap anything else, resid_out nothing but resid.  A NaN or
- * an infinity makes its whole row of out NaN or 0 as the formula does (e4m3: a
- * group with a NaN has a NaN scale).  T == 0 checks what it can and launches
- * nothing.  Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
+ * H a multiple of 8 (16 for e4m3), at most 32768, strides at most 2^32; x,
+ * resid, resid_out, gain and out 16-byte aligned with row strides of a multiple
+ * of 16 bytes.  out and scale must not overlap anything else, resid_out nothing
+ * but resid.  A NaN or an infinity makes its whole row of out NaN or 0 as the
+ * formula does (e4m3: a group with a NaN has a NaN scale).  T == 0 checks what
+ * it can and launches nothing.  Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
  */
 int moe_add_rmsnorm(const void *x, const void *resid, void *resid_out, const float *gain, int T,
                     int H, float eps, int x_dtype, int resid_dtype, int out_dtype, int group,
@@ -383,10 +383,10 @@ int moe_add_rmsnorm(const void *x, const void *resid, void *resid_out, const flo
  *   status   int32 on the device: set to 2 when a bounded wait of the kernel
  *            gave up (out is then not complete); otherwise left alone.  NULL:
  *            such a product sets the device's own word (moe_linear_status)
- * Sums are f32; out is rounded once.  T, N and K are at most 2^19; K and the
- * strides of x and w are multiples of 16 bytes, x and w 16-byte aligned; N is
- * any number (a multiple of 16 for SwiGLU).  out must not overlap anything
- * else.  T == 0 checks what it can and launches nothing.
+ * Sums are f32; out is rounded once.  T, N and K are at most 2^19, strides
+ * 2^31; K and the strides of x and w are multiples of 16 bytes, x and w 16-byte
+ * aligned; N is any number (a multiple of 16 for SwiGLU).  out must not overlap
+ * anything else.  T == 0 checks what it can and launches nothing.
  * Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
  */
 int moe_linear(const void *x, const float *x_scale, const void *w, const float *w_scale,
@@ -454,8 +454,8 @@ int moe_linear_wait_limit(int us);
  *            16-byte aligned, not shared with a call that may overlap this one;
  *            nothing in it needs clearing
  * A row whose logits are all -infinity (in mode 1: whose sigmoids are all
- * below 2^-126) has p = 0.  num_experts <= 1024, top_k
- * <= 32, T * top_k <= 2^26, n_seq <= 65535.  Loss and gradient together read z
+ * below 2^-126) has p = 0.  num_experts <= 1024, top_k <= 32, T * top_k <=
+ * 2^26, n_seq <= 65535, strides <= 2^32.  Loss and gradient together read z
  * once.  Outputs and workspace must not overlap anything else.  T == 0: every
  * segment is empty, and loss, counts, tokens and prob, where all four are
  * given, are set to 0; z, idx, dz and the workspace are not touched (with one
