@@ -20,6 +20,7 @@ ROUTER_SOFTMAX, ROUTER_SIGMOID, ROUTER_SOFTMAX_RAW = 0, 1, 2
 X_F32, X_BF16 = 0, 1
 F32, BF16, E4M3 = 0, 1, 2
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU = 0, 1, 2, 3
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = 0, 1, 2, 3
 
 MOE_DBG_IDX, MOE_DBG_W, MOE_DBG_COUNTS, MOE_DBG_OFFSETS, MOE_DBG_PERM, MOE_DBG_INV = range(6)
 
@@ -30,7 +31,8 @@ EXPORTS = ("moe_init", "moe_route", "moe_forward", "moe_forward_residual",
            "moe_route_noalloc", "moe_usage_read", "moe_usage_reset", "moe_engine_id",
            "moe_route_trace_write", "moe_route_trace_read", "moe_set_next_layer",
            "moe_add_rmsnorm", "moe_linear", "moe_linear_status", "moe_linear_wait_limit",
-           "moe_balance_loss", "moe_balance_workspace")
+           "moe_balance_loss", "moe_balance_workspace", "moe_rope", "moe_rope_freqs",
+           "moe_kv4_page_bytes", "moe_kv4_append", "moe_kv4_attention", "moe_kv4_workspace")
 
 
 class MoeLayout(ctypes.Structure):
@@ -62,7 +64,7 @@ def _load():
         raise ImportError("libmoe.so is not built (run __graft_entry__.build()); "
                           "the MoE layer has no other implementation")
     lib = ctypes.CDLL(LIB_PATH)
-    P, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    P, i, f, d = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double
     q, z = ctypes.c_int64, ctypes.c_size_t
     sig = {
         "moe_init": (i, [P, P, P]),
@@ -92,6 +94,13 @@ def _load():
         "moe_balance_loss": (i, [P, P, P, P, P, i, i, i, i, i, i, f, P, q, P, P, P, P, P, q, P, z,
                                  P]),
         "moe_balance_workspace": (z, [i, i, i]),
+        "moe_rope": (i, [P, P, P, i, i, i, i, i, i, f, i, P, q, q, q, q, P]),
+        "moe_rope_freqs": (i, [i, d, i, d, d, d, d, P, P]),
+        "moe_kv4_page_bytes": (z, [i, i, i]),
+        "moe_kv4_append": (i, [P, P, P, P, P, P, i, i, i, i, i, i, i, i, q, q, P]),
+        "moe_kv4_attention": (i, [P, P, P, P, P, i, i, i, i, i, i, i, i, i, f, f, i, i, P, q, q, P, z,
+                                  P, P]),
+        "moe_kv4_workspace": (z, [i, i, i, i, i, i, i, i]),
         "moe_route_trace_write": (i, [ctypes.c_char_p, i, i, ctypes.c_uint32, P]),
         "moe_route_trace_read": (i, [ctypes.c_char_p, i, i, ctypes.c_uint32, P, P]),
     }
@@ -324,6 +333,66 @@ def balance_loss(z, idx, T, num_experts, top_k, loss, counts, tokens, prob, work
                                        _ptr(tokens), _ptr(prob), _ptr(dz), dz_stride,
                                        _ptr(workspace), workspace.nbytes, _stream(stream)),
                   "moe_balance_loss")
+
+
+def rope(x, pos, freqs, T, n_heads, head_dim, out, rot_dim=0, interleaved=False, inverse=False,
+         mscale=1.0, dtype=BF16, x_stride=0, x_head_stride=0, out_stride=0, out_head_stride=0,
+         stream=None):
+    """moe_rope: rotary positions of the first rot_dim (0: all) elements of each
+    head; inverse turns back, which is also the gradient."""
+    return _check(lib.moe_rope(_ptr(x), _ptr(pos), _ptr(freqs), T, n_heads, head_dim,
+                               rot_dim or head_dim, int(interleaved), int(inverse), mscale, dtype,
+                               _ptr(out), x_stride, x_head_stride, out_stride, out_head_stride,
+                               _stream(stream)), "moe_rope")
+
+
+def rope_freqs(rot_dim, theta=10000.0, scaling=ROPE_PLAIN, factor=1.0, context=0.0, beta_fast=32.0,
+               beta_slow=1.0):
+    """moe_rope_freqs: (numpy float64 [rot_dim / 2] radians per position, mscale)."""
+    import numpy as np
+    f = np.zeros(max(rot_dim // 2, 1), np.float64)
+    m = ctypes.c_float()
+    _check(lib.moe_rope_freqs(rot_dim, theta, scaling, factor, context, beta_fast, beta_slow,
+                              f.ctypes.data, ctypes.byref(m)), "moe_rope_freqs")
+    return f, m.value
+
+
+def kv4_page_bytes(page_size, n_kv_heads, head_dim):
+    """Bytes of one page of a 4-bit cache (0 for sizes that are refused)."""
+    return lib.moe_kv4_page_bytes(page_size, n_kv_heads, head_dim)
+
+
+def kv4_append(k, v, cache, pages, kv_len, T, n_kv_heads, head_dim, page_size, n_pages, max_pages,
+               q_off=None, n_seq=None, dtype=BF16, k_stride=0, v_stride=0, stream=None):
+    """moe_kv4_append: the T rows of K and V into the 4-bit cache; without q_off
+    one row for each of T sequences."""
+    return _check(lib.moe_kv4_append(_ptr(k), _ptr(v), _ptr(cache), _ptr(pages), _ptr(q_off),
+                                     _ptr(kv_len), T, T if n_seq is None else n_seq, n_kv_heads,
+                                     head_dim, page_size, n_pages, max_pages, dtype, k_stride,
+                                     v_stride, _stream(stream)), "moe_kv4_append")
+
+
+def kv4_workspace(T, n_seq, n_heads, n_kv_heads, head_dim, page_size, max_pages, max_q=0):
+    """Bytes of scratch that kv4_attention needs."""
+    return lib.moe_kv4_workspace(T, n_seq, max_q, n_heads, n_kv_heads, head_dim, page_size, max_pages)
+
+
+def kv4_attention(q, cache, pages, kv_len, T, n_heads, n_kv_heads, head_dim, page_size, n_pages,
+                  max_pages, out, workspace, q_off=None, n_seq=None, max_q=0, scale=None,
+                  softcap=0.0, window=0, causal=True, q_stride=0, out_stride=0, status=None,
+                  stream=None):
+    """moe_kv4_attention: attention of the batch's rows over the 4-bit cache.
+    scale defaults to head_dim ** -0.5; workspace is a tensor or array of at
+    least kv4_workspace(...) bytes, or None where that is 0."""
+    if scale is None:
+        scale = head_dim ** -0.5
+    return _check(lib.moe_kv4_attention(_ptr(q), _ptr(cache), _ptr(pages), _ptr(q_off),
+                                        _ptr(kv_len), T, T if n_seq is None else n_seq, max_q,
+                                        n_heads, n_kv_heads, head_dim, page_size, n_pages,
+                                        max_pages, scale, softcap, window, int(causal), _ptr(out),
+                                        q_stride, out_stride, _ptr(workspace),
+                                        0 if workspace is None else workspace.nbytes,
+                                        _ptr(status), _stream(stream)), "moe_kv4_attention")
 
 
 def layout_for(wl, max_tokens):

@@ -1,0 +1,108 @@
+// kv4.cuh -- the 4-bit cache's geometry and a batch's, shared by the kernels that
+// fill the cache and attend over it (layout: include/moe.h).
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+constexpr int kKvGroup = 64;   // values per (step, lo)
+
+// A batch over the cache: which rows are whose, and where tokens live.
+struct KvBatch {
+  const int32_t *pages, *q_off, *kv_len;
+  int T, n_seq;
+  int log_page;              // page_size = 1 << log_page
+  int n_pages, max_pages;
+  int Hkv;
+};
+
+// One sequence: rows t0 .. t0 + nq - 1 are the last nq of its len tokens.
+struct KvSeq {
+  int t0, nq, len;
+};
+
+static __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return min(max(v, lo), hi); }
+
+static __device__ __forceinline__ int kv_len_at(const KvBatch &b, int s) {
+  return clamp_int(__ldg(b.kv_len + s), 0, b.max_pages << b.log_page);
+}
+
+static __device__ __forceinline__ KvSeq kv_seq_at(const KvBatch &b, int s) {
+  KvSeq q;
+  if (b.q_off) {
+    q.t0 = clamp_int(__ldg(b.q_off + s), 0, b.T);
+    q.nq = clamp_int(__ldg(b.q_off + s + 1), q.t0, b.T) - q.t0;
+  } else {
+    q.t0 = s;
+    q.nq = 1;
+  }
+  q.len = kv_len_at(b, s);
+  return q;
+}
+
+// The page of a sequence's token, -1 for a hole.
+static __device__ __forceinline__ int kv_page_at(const KvBatch &b, int s, int token) {
+  const int id = __ldg(b.pages + (size_t)s * b.max_pages + (token >> b.log_page));
+  return (unsigned)id < (unsigned)b.n_pages ? id : -1;
+}
+
+// The sequence of row t (n_seq: none), found by a whole warp, 32 offsets at a time.
+static __device__ __forceinline__ int kv_seq_of(const KvBatch &b, int t, int lane) {
+  if (!b.q_off) return t;
+  int base = 0, n = b.n_seq + 1;   // how many offsets are at most t: base .. base + n
+  while (n > 32) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const int k = __popc(__ballot_sync(0xffffffffu, i < n && __ldg(b.q_off + base + i) <= t));
+    if (k == 0) return b.n_seq;
+    const int skip = (k - 1) * step;
+    base += skip;
+    n = min(step, n - skip);
+  }
+  const int s = base - 1 + __popc(__ballot_sync(0xffffffffu, lane < n && __ldg(b.q_off + base + lane) <= t));
+  return s < 0 ? b.n_seq : s;
+}
+
+// Byte offsets inside one block (a page's tokens of one KV head).
+template <int D>
+struct KvBlock {
+  static constexpr int kCodes = D / 2;                  // bytes of a token's codes
+  static constexpr int kScales = D / kKvGroup * 4;      // bytes of its (step, lo)
+  static __device__ __forceinline__ size_t bytes(int log_page) {
+    return (size_t)(2 * (kCodes + kScales)) << log_page;
+  }
+  // which: 0 K, 1 V
+  static __device__ __forceinline__ uint32_t codes(int log_page, int which, int slot) {
+    return ((which << log_page) + slot) * kCodes;
+  }
+  static __device__ __forceinline__ uint32_t scales(int log_page, int which, int slot) {
+    return ((2 * kCodes) << log_page) + ((which << log_page) + slot) * kScales;
+  }
+};
+
+// ------------------------------------------------- argument checks (host) --
+
+static inline bool kv4_good_page(int page_size) {
+  return page_size >= 16 && page_size <= 256 && (page_size & (page_size - 1)) == 0;
+}
+
+static inline int kv4_log2(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+// The sizes of a batch over a cache.
+static inline bool kv4_good_batch(int T, int max_T, int n_seq, bool rows_given, int n_kv_heads,
+                                  int head_dim, int page_size, int n_pages, int max_pages) {
+  return T >= 0 && T <= max_T && n_seq >= 1 && n_seq <= 65535 && (rows_given || T == n_seq || T == 0) &&
+         n_kv_heads >= 1 && n_kv_heads <= 1024 && (head_dim == 64 || head_dim == 128) &&
+         kv4_good_page(page_size) && n_pages >= 1 && max_pages >= 1 &&
+         (long long)max_pages * page_size <= (1 << 30);
+}
+
+static inline bool kv4_off_by(const void *p, uintptr_t mask) {
+  return (reinterpret_cast<uintptr_t>(p) & mask) != 0;
+}
+
+}  // namespace moe

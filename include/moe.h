@@ -472,6 +472,152 @@ int moe_balance_loss(const void *z, const float *bias, const int32_t *idx, const
 /* Bytes of scratch that moe_balance_loss needs (0 for sizes it refuses or T < 1). */
 size_t moe_balance_workspace(int T, int num_experts, int n_seq);
 
+/* Scalings of moe_rope_freqs. */
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1   /* every pair slowed by factor (position interpolation) */
+#define MOE_ROPE_BASE 2     /* theta raised to theta factor^(R / (R - 2)): the slowest pair is
+                               slowed by factor, the fastest not at all ("NTK-aware") */
+#define MOE_ROPE_PARTS 3    /* by parts (Peng et al. 2023, "YaRN"): see below */
+
+/*
+ * Rotary positions of query and key heads, in place or not, before the rows go
+ * into a cache or an attention:
+ *
+ *   a = pos[t] freqs[i]                          for each pair i < R / 2, R = rot_dim
+ *   out_u = mscale (u cos a - v sin a),  out_v = mscale (u sin a + v cos a)
+ *
+ * with (u, v) the elements (i, i + R / 2) of a head, or (2 i, 2 i + 1) when
+ * interleaved is not 0; elements from R on are copied.  inverse not 0 turns by
+ * -a: the transposed operator, and so the gradient of x from the gradient of
+ * out (with the same mscale).
+ *
+ *   x, out   [T][n_heads][head_dim] MOE_F32 or MOE_BF16 (dtype): a token's heads
+ *            lie x_head_stride elements apart (0: head_dim), its row x_stride
+ *            (0: n_heads times the head stride).  Query and key heads of one
+ *            fused row turn in one call.  out may be x itself (the same
+ *            strides); otherwise the two must not overlap.
+ *   pos      [T] int32, any values
+ *   freqs    [R / 2] doubles on the device: radians per position, e.g. from
+ *            moe_rope_freqs
+ * Angles are taken modulo a turn in 64-bit fixed point, so a position as far as
+ * 2^31 turns as exactly as a near one; the rotation is f32, rounded once.
+ * n_heads * head_dim <= 2^20, head_dim <= 1024, R even and <= head_dim, T <=
+ * 2^24, strides <= 2^32; elements aligned to their own size (16-byte aligned
+ * rows are faster).  T == 0 checks what it can and launches nothing.
+ * Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
+ */
+int moe_rope(const void *x, const int32_t *pos, const double *freqs, int T, int n_heads,
+             int head_dim, int rot_dim, int interleaved, int inverse, float mscale, int dtype,
+             void *out, int64_t x_stride, int64_t x_head_stride, int64_t out_stride,
+             int64_t out_head_stride, moe_stream_t stream);
+/*
+ * The frequencies of moe_rope, on the host: freqs[i] = theta^(-2 i / rot_dim),
+ * i < rot_dim / 2, scaled for contexts `factor` times as long as the model's own
+ * `context`.  By parts: a pair that makes r = context freqs[i] / (2 pi) turns
+ * keeps its frequency for r >= beta_fast, is divided by factor for r <= beta_slow
+ * and mixed in between by (r - beta_slow) / (beta_fast - beta_slow); *mscale is
+ * then 0.1 ln(factor) + 1 (1 for the other scalings; mscale may be NULL).
+ * context, beta_fast and beta_slow are read by parts only.  Returns MOE_OK or
+ * MOE_ERR_ARG (rot_dim not even or outside 2 .. 1024, theta or factor not finite
+ * or below 1, by base with rot_dim 2, by parts with context < 1 or not
+ * 0 <= beta_slow < beta_fast).
+ */
+int moe_rope_freqs(int rot_dim, double theta, int scaling, double factor, double context,
+                   double beta_fast, double beta_slow, double *freqs, float *mscale);
+
+/*
+ * A cache of keys and values in 4 bits.  Tokens live in pages of page_size (16,
+ * 32, 64, 128 or 256); a cache is n_pages pages one after another, a page one
+ * block per KV head, and a block of moe_kv4_page_bytes(page_size, 1, head_dim)
+ * = page_size head_dim 9 / 8 bytes holds, for the page's tokens in order,
+ *
+ *   K codes [page_size][head_dim / 2]   two values a byte, the even one low
+ *   V codes [page_size][head_dim / 2]
+ *   K scales [page_size][head_dim / 64][2] float16: (step, lo) of 64 values
+ *   V scales [page_size][head_dim / 64][2]
+ *
+ * A code c in 0 .. 15 stands for lo + step c.  Of 64 values x, clamped to
+ * +-60000: lo = f16(min x), step = f16(max(max x - lo, 0) / 15), c = the nearest
+ * of 0 .. 15 to (x - lo) / step (ties to even; 0 where step is 0), all in f32.
+ * 64 values with a NaN among them have NaN for step and lo.  head_dim is 64 or
+ * 128.
+ *
+ * Both calls below describe a batch alike: n_seq sequences, sequence s with the
+ * rows q_off[s] .. q_off[s + 1] - 1 of the call's T rows (its new tokens), the
+ * last of its kv_len[s] tokens: row i of n stands at position kv_len - n + i.
+ *   q_off   [n_seq + 1] int32, non-decreasing; NULL: one row a sequence (T =
+ *           n_seq).  Rows in no sequence are not read, their results left as
+ *           they were.
+ *   kv_len  [n_seq] int32: tokens of the sequence, the call's own among them
+ *   pages   [n_seq][max_pages] int32: the pages of a sequence in order; entries
+ *           past its length are not read.  An id outside 0 .. n_pages - 1 is a
+ *           hole: nothing is put there and nothing there is seen.
+ * Values are taken as they are at run time (a graph's replays may change them).
+ * Offsets and lengths out of range are clamped (offsets to T and to their
+ * predecessor, lengths to max_pages page_size): memory outside the operands is
+ * never touched.
+ */
+size_t moe_kv4_page_bytes(int page_size, int n_kv_heads, int head_dim);
+
+/*
+ * Puts the rows of K and V into the cache at their positions; rows at negative
+ * positions (more rows than kv_len) and in holes are dropped.  Two sequences that
+ * share a page must not both have new rows in it.
+ *   k, v   [T][n_kv_heads][head_dim] MOE_F32 or MOE_BF16 (dtype), row strides
+ *          k_stride, v_stride (0: n_kv_heads head_dim)
+ * k, v and cache 16-byte aligned, strides a multiple of 16 bytes and at most
+ * 2^32; n_kv_heads <= 1024, T <= 2^24, T n_kv_heads <= 2^28, n_seq <= 65535,
+ * max_pages page_size <= 2^30.  The cache must not overlap anything else.  T == 0 checks what it can
+ * and launches nothing.  Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
+ */
+int moe_kv4_append(const void *k, const void *v, void *cache, const int32_t *pages,
+                   const int32_t *q_off, const int32_t *kv_len, int T, int n_seq, int n_kv_heads,
+                   int head_dim, int page_size, int n_pages, int max_pages, int dtype,
+                   int64_t k_stride, int64_t v_stride, moe_stream_t stream);
+
+/*
+ * Attention of the batch's rows over that cache, for single tokens, a few
+ * drafted tokens or prompts, in any mixture.  Query head h reads KV head
+ * h / (n_heads / n_kv_heads); per row at position p and query head,
+ *
+ *   s[j]   = scale q . K[j]                      (softcap > 0: softcap tanh(s / softcap))
+ *   out    = sum_j w[j] V[j],  w = softmax of s over the tokens j that the row sees:
+ *            j < kv_len, with causal j <= p, with window W > 0 also j > p - W
+ *
+ * A row that sees no token is 0.  A NaN in a token's K or V reaches the rows
+ * that see the token, whose results are NaN, and no others.
+ *
+ *   q, out   [T][n_heads][head_dim] bf16, row strides q_stride, out_stride (0:
+ *            n_heads head_dim)
+ *   max_q    the most rows that any one sequence has, where the caller knows it;
+ *            0: not known.  Rows of a sequence past the first max_q are left as
+ *            they were.
+ *   workspace  at least moe_kv4_workspace(...) bytes, 16-byte aligned, not shared
+ *            with a call that may overlap this one; nothing in it needs clearing
+ *   status   int32 on the device: set to 2 when a bounded wait of the kernel
+ *            gave up (out is then not complete); otherwise left alone.  NULL:
+ *            such a call sets the device's own word (moe_linear_status, which
+ *            reports products and attention alike, as moe_linear_wait_limit
+ *            limits the waits of both)
+ * Sums and softmax statistics are f32; keys, values and weights enter the
+ * products as float16 (queries scaled by powers of two), out is rounded once.
+ * q, out and cache 16-byte aligned, strides a multiple of 8 and at most 2^31;
+ * n_heads a multiple of n_kv_heads, n_heads <= 1024, T <= 2^19, n_seq <= 65535,
+ * max_pages page_size <= 2^30, scale finite, softcap finite and >= 0.  out and
+ * workspace must not overlap anything else.  The same call gives the same bits
+ * each time.  T == 0 checks what it can and launches nothing.  Returns MOE_OK,
+ * MOE_ERR_NOMEM (workspace too small), MOE_ERR_ARG or MOE_ERR_DEVICE.
+ */
+int moe_kv4_attention(const void *q, const void *cache, const int32_t *pages,
+                      const int32_t *q_off, const int32_t *kv_len, int T, int n_seq, int max_q,
+                      int n_heads, int n_kv_heads, int head_dim, int page_size, int n_pages,
+                      int max_pages, float scale, float softcap, int window, int causal, void *out,
+                      int64_t q_stride, int64_t out_stride, void *workspace,
+                      size_t workspace_bytes, int32_t *status, moe_stream_t stream);
+/* Bytes of scratch that moe_kv4_attention needs (0 for sizes it refuses or T < 1). */
+size_t moe_kv4_workspace(int T, int n_seq, int max_q, int n_heads, int n_kv_heads, int head_dim,
+                         int page_size, int max_pages);
+
 /* Fields of moe_debug_read. */
 #define MOE_DBG_IDX 0      /* int32 [T][k]  */
 #define MOE_DBG_W 1        /* f32   [T][k]  */
