@@ -2,6 +2,7 @@
 // fill the cache and attend over it (layout: include/moe.h).
 #pragma once
 
+#include "linear.cuh"
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -79,6 +80,66 @@ struct KvBlock {
     return ((2 * kCodes) << log_page) + ((which << log_page) + slot) * kScales;
   }
 };
+
+// What attention's kernels share.
+struct AttendParams {
+  const __nv_bfloat16 *q;
+  const uint8_t *cache;
+  __nv_bfloat16 *out;
+  KvBatch b;
+  long long ldq, ldo;        // row strides in elements
+  int H, G;                  // query heads, and those of one KV head
+  int max_q;                 // 0: not known
+  int window, causal;
+  float scale, softcap;
+  float *part_o;             // [slot][column][D] partial outputs
+  float2 *part_ml;           // [slot][column] (maximum, sum)
+  int target;                // parts that a batch is cut into, at least
+  int32_t *status;
+  unsigned long long wait_ns;
+};
+
+// A sequence as attention takes it: `rows` of its nq rows are worked out.
+struct AttendSeq : KvSeq {
+  int rows;
+};
+static __device__ __forceinline__ AttendSeq attend_seq_at(const AttendParams &p, int s) {
+  AttendSeq q;
+  static_cast<KvSeq &>(q) = kv_seq_at(p.b, s);
+  q.rows = p.max_q ? min(q.nq, p.max_q) : q.nq;
+  return q;
+}
+
+// Sequences of at most this many columns (rows times query heads of a KV head)
+// take kv4_few.cu's kernels, the others kv4_many.cu's.
+constexpr int kFewColumns = 16;
+int few_target(int sms);
+size_t few_slots(const AttendParams &p);
+cudaError_t launch_few(const AttendParams &p, int D, cudaStream_t st);
+
+static __device__ __forceinline__ uint2 pack_out(float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoScore = -1e30f;   // a maximum before any score
+
+static __device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+static __device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// cap tanh(x / cap) in units of log2 e, from x 2 log2(e) / cap: an absolute error
+// of a few units of cap, which is what a score's error counts as.
+static __device__ __forceinline__ float capped(float x2, float cap_log2) {
+  return cap_log2 - 2.f * cap_log2 * rcp_approx(1.f + ex2(x2));
+}
 
 // ------------------------------------------------- argument checks (host) --
 

@@ -14,16 +14,6 @@
 namespace moe {
 namespace {
 
-struct AttendParams {
-  const __nv_bfloat16 *q;
-  const uint8_t *cache;
-  __nv_bfloat16 *out;
-  KvBatch b;
-  long long ldq, ldo;
-  int H, max_q, window, causal;
-  float scale, softcap;
-};
-
 template <int D>
 __global__ void __launch_bounds__(128) kv4_attend_kernel(const AttendParams p) {
   constexpr int N = D / 32, NG = D / kKvGroup;
@@ -32,9 +22,9 @@ __global__ void __launch_bounds__(128) kv4_attend_kernel(const AttendParams p) {
   const int t = blockIdx.x, h = blockIdx.y, hk = h / (p.H / p.b.Hkv);
   const int s = kv_seq_of(p.b, t, lane);
   if (s >= p.b.n_seq) return;
-  const KvSeq sq = kv_seq_at(p.b, s);
+  const AttendSeq sq = attend_seq_at(p, s);
   const int i = t - sq.t0;
-  if (i >= sq.nq || (p.max_q && i >= p.max_q)) return;
+  if (i >= sq.rows || sq.rows * p.G <= kFewColumns) return;
   const int pos = sq.len - sq.nq + i;
   const int end = p.causal ? min(sq.len, pos + 1) : sq.len;
   const int first = p.window ? max(0, pos - p.window + 1) : 0;
@@ -98,6 +88,22 @@ bool good_sizes(int T, int n_seq, bool rows_given, int max_q, int n_heads, int n
          max_q >= 0 && n_heads >= 1 && n_heads <= 1024 && n_heads % n_kv_heads == 0;
 }
 
+// Where the partial results of a call lie in its workspace.
+struct Scratch {
+  size_t o, ml, bytes;
+};
+// On 152 SMs, whatever the device: the size is the same on every machine.
+constexpr int kPlanSms = 152;
+Scratch workspace_of(AttendParams &p, int D) {
+  p.target = few_target(kPlanSms);
+  const size_t columns = (p.G <= kFewColumns ? few_slots(p) : 0) * kFewColumns;
+  Scratch w;
+  w.o = 0;
+  w.ml = columns * D * sizeof(float);
+  w.bytes = w.ml + columns * sizeof(float2);
+  return w;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -106,7 +112,10 @@ extern "C" __attribute__((visibility("default"))) size_t moe_kv4_workspace(
     int max_pages) {
   if (T < 1 || !moe::good_sizes(T, n_seq, true, max_q, n_heads, n_kv_heads, head_dim, page_size, 1, max_pages))
     return 0;
-  return 0;
+  moe::AttendParams p{};
+  p.b.n_seq = n_seq, p.b.Hkv = n_kv_heads, p.b.max_pages = max_pages, p.b.log_page = moe::kv4_log2(page_size);
+  p.b.T = T, p.H = n_heads, p.G = n_heads / n_kv_heads, p.max_q = max_q;
+  return moe::workspace_of(p, head_dim).bytes;
 }
 
 extern "C" __attribute__((visibility("default"))) int moe_kv4_attention(
@@ -143,12 +152,24 @@ extern "C" __attribute__((visibility("default"))) int moe_kv4_attention(
   for (const Area &a : ins)
     if (meet(ao, a) || meet(aw, a)) return MOE_ERR_ARG;
   if (meet(ao, aw)) return MOE_ERR_ARG;
-  AttendParams p{static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(cache),
-                 static_cast<__nv_bfloat16 *>(out),
-                 KvBatch{pages, q_off, kv_len, T, n_seq, kv4_log2(page_size), n_pages, max_pages, n_kv_heads},
-                 ldq, ldo, n_heads, max_q, window, causal, scale, softcap};
+  AttendParams p{};
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.cache = static_cast<const uint8_t *>(cache);
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.b = KvBatch{pages, q_off, kv_len, T, n_seq, kv4_log2(page_size), n_pages, max_pages, n_kv_heads};
+  p.ldq = ldq, p.ldo = ldo, p.H = n_heads, p.G = n_heads / n_kv_heads, p.max_q = max_q;
+  p.window = window, p.causal = causal != 0, p.scale = scale, p.softcap = softcap, p.status = status;
+  const Scratch w = workspace_of(p, head_dim);
+  if (w.bytes) {
+    p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.o);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + w.ml);
+  }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = launch_k(false, head_dim == 64 ? kv4_attend_kernel<64> : kv4_attend_kernel<128>,
-                                   dim3(T, n_heads), dim3(128), 0, st, p);
+  cudaError_t err = cudaSuccess;
+  const long long rows = q_off ? (max_q ? std::min(max_q, T) : T) : 1;   // of one sequence, at most
+  if (p.G <= kFewColumns) err = launch_few(p, head_dim, st);
+  if (err == cudaSuccess && rows * p.G > kFewColumns)
+    err = launch_k(false, head_dim == 64 ? kv4_attend_kernel<64> : kv4_attend_kernel<128>, dim3(T, n_heads),
+                   dim3(128), 0, st, p);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
