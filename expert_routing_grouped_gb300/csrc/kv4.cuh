@@ -94,7 +94,7 @@ struct AttendParams {
   float scale, softcap;
   float *part_o;             // [slot][column][D] partial outputs
   float2 *part_ml;           // [slot][column] (maximum, sum)
-  int target;                // parts that a batch is cut into, at least
+  int target;                // blocks that a batch is spread over
   int32_t *status;
   unsigned long long wait_ns;
 };
@@ -113,7 +113,6 @@ static __device__ __forceinline__ AttendSeq attend_seq_at(const AttendParams &p,
 // Sequences of at most this many columns (rows times query heads of a KV head)
 // take kv4_few.cu's kernels, the others kv4_many.cu's.
 constexpr int kFewColumns = 16;
-int few_target(int sms);
 size_t few_slots(const AttendParams &p);
 cudaError_t launch_few(const AttendParams &p, int D, cudaStream_t st);
 

@@ -92,10 +92,7 @@ bool good_sizes(int T, int n_seq, bool rows_given, int max_q, int n_heads, int n
 struct Scratch {
   size_t o, ml, bytes;
 };
-// On 152 SMs, whatever the device: the size is the same on every machine.
-constexpr int kPlanSms = 152;
-Scratch workspace_of(AttendParams &p, int D) {
-  p.target = few_target(kPlanSms);
+Scratch workspace_of(const AttendParams &p, int D) {
   const size_t columns = (p.G <= kFewColumns ? few_slots(p) : 0) * kFewColumns;
   Scratch w;
   w.o = 0;

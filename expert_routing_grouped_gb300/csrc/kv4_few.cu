@@ -33,21 +33,27 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kTile = 32;                   // tokens of a ring slot
-constexpr int kMinTiles = kWarps;           // tiles of a part, at least
-constexpr int kPlanSeqs = 1024;             // sequences of a batch that is cut into parts
+constexpr int kMinTiles = 8;                // tiles of a span, at least: one for each warp
+constexpr int kPlanSeqs = 1024;             // sequences of a batch that is cut into spans
 constexpr int kColumns = kFewColumns;
+constexpr int kFewSms = 152;                // blocks are sized for the GB300's SMs
 
 template <int D>
 struct Slot {
   static constexpr int kK = 0, kV = kTile * D / 2, kKs = kTile * D, kVs = kKs + kTile * D / 16;
   static constexpr int kBytes = kVs + kTile * D / 16;
 };
-template <int D>
-constexpr int kRing = D == 128 ? 3 : 5;     // slots of a warp
-template <int D>
-constexpr int kSmem = kWarps * kRing<D> * Slot<D>::kBytes;
+// Up to 8 columns: two blocks of 8 warps on an SM; up to 16, whose outputs take
+// twice the registers: one of 12.
+template <int NT>
+constexpr int kWarps = NT == 1 ? 8 : 12;
+template <int NT>
+constexpr int kBlocks = NT == 1 ? 2 : 1;
+template <int D, int NT>
+constexpr int kRing = D == 64 ? 6 : NT == 1 ? 3 : 4;     // slots of a warp
+template <int D, int NT>
+constexpr int kSmem = kWarps<NT> * kRing<D, NT> * Slot<D>::kBytes;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -102,6 +108,35 @@ __device__ __forceinline__ void four_pairs(uint32_t w, uint32_t lo_bias, uint32_
   o[2] = sub2(codes_lo(w8), lo_bias);
   o[3] = sub2(codes_hi(w8), hi_bias);
 }
+// Two f32 operations in one instruction.
+__device__ __forceinline__ float2 fma_2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul_2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add_2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -112,128 +147,116 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t v) {
 }
 
 // ------------------------------------------------------------------ plan --
+//
+// The tiles of all sequences and KV heads in one line, each (sequence, head) with
+// its own, are cut into equal spans, one for each block, whatever the lengths: a
+// block works through the segments of its span.  A segment that is a whole
+// (sequence, head) is finished by its block; the others leave partial results, at
+// most two for each block: slot 2 b for the one at the start of its span, 2 b + 1
+// for one that starts later and goes on in the next.
 
-// A part of the batch: tiles first .. first + n - 1 of sequence s.
-struct Part {
-  int s, hk, part, parts, first, n, slot;   // slot: of the sequence's first part and KV head 0
-};
+// What a segment costs beside its tiles, in tiles: start and end take about as
+// long as ten tiles of a block.
+constexpr int kSegmentCost = 8;
 
 struct SeqTiles {
-  int first, n;   // tiles that any row of the sequence sees; n = 0 with first < 0: none of this kernel's
+  int first, n;   // the tiles that any row sees (one at least); n = 0: none of this kernel's sequences
 };
 
 __device__ __forceinline__ SeqTiles tiles_of(const AttendParams &p, const AttendSeq &q) {
-  if (q.rows < 1 || q.rows * p.G > kColumns) return SeqTiles{-1, 0};
+  if (q.rows < 1 || q.rows * p.G > kColumns) return SeqTiles{0, 0};
   int lo = 0;
   if (p.window) lo = max(0, q.len - q.nq - p.window + 1) / kTile;
-  return SeqTiles{lo, (q.len + kTile - 1) / kTile - lo};
+  return SeqTiles{lo, max(1, (q.len + kTile - 1) / kTile - lo)};
 }
 
+// Tiles of a sequence's line, for one head.
+__device__ __forceinline__ int span_of(const SeqTiles &t) { return t.n ? t.n + kSegmentCost : 0; }
+
 // Exclusive prefix of v over the block's threads, and the total.
-__device__ __forceinline__ int2 block_scan(int2 v, int2 *warp_sums, int2 &total) {
+__device__ __forceinline__ long long block_scan(long long v, long long *warp_sums, long long &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int2 x = v;
+  long long x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
-    if (lane >= o) x.x += a, x.y += b;
+    const long long a = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += a;
   }
-  __syncthreads();
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int2 before = make_int2(x.x - v.x, x.y - v.y);
-  total = make_int2(0, 0);
+  long long before = x - v;
+  total = 0;
   for (int w = 0; w < nw; ++w) {
-    const int2 s = warp_sums[w];
-    if (w < warp) before.x += s.x, before.y += s.y;
-    total.x += s.x, total.y += s.y;
+    const long long s = warp_sums[w];
+    if (w < warp) before += s;
+    total += s;
   }
   return before;
 }
 
-// Which part `item` is (seq < 0), or the parts of sequence `seq`: false if there
-// is none.  Every block works it out from the lengths: cutting all sequences into
-// parts of at most `cut` tiles, which makes at least about `target` parts of a
-// large batch.  Only sequences of several parts have slots, twice `target` at
-// most (n / cut > 1 rounds up to less than twice itself).
-__device__ bool find_part(const AttendParams &p, int item, int seq, Part &out) {
-  __shared__ int2 sums[32];
-  __shared__ Part found;
-  const int Hkv = p.b.Hkv;
-  if (p.b.n_seq > kPlanSeqs) {   // whole sequences
-    const int s = seq >= 0 ? seq : item / Hkv;
-    if (s >= p.b.n_seq) return false;
-    const SeqTiles t = tiles_of(p, attend_seq_at(p, s));
-    if (t.first < 0) return false;
-    out = Part{s, item - s * Hkv, 0, 1, t.first, t.n, 0};
-    return true;
-  }
-  constexpr int kMost = kPlanSeqs / 128;   // sequences of a thread, 128 threads at least
-  const int per = (p.b.n_seq + blockDim.x - 1) / blockDim.x;
-  SeqTiles t[kMost];
+// The line: its length per block, and of a sequence where it starts.
+struct Line {
+  long long total, cut, start;
+  int s;
+};
+
+// With seq < 0 the sequence in which block `block`'s span starts, else that of
+// sequence seq.  line.s < 0: none.
+__device__ __forceinline__ Line find_line(const AttendParams &p, int block, int seq) {
+  __shared__ long long sums[32];
+  __shared__ long long start;
+  __shared__ int where;
+  const int per = (p.b.n_seq + blockDim.x - 1) / blockDim.x, s0 = threadIdx.x * per;
   long long mine = 0;
-#pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    const int s = threadIdx.x * per + i;
-    t[i] = SeqTiles{-1, 0};
-    if (i < per && s < p.b.n_seq) t[i] = tiles_of(p, attend_seq_at(p, s));
-    mine += t[i].n;
-  }
-  // 1024 sequences of 2^30 / 32 tiles and 1024 KV heads need 45 bits: counted in
-  // units that leave 31, rounded up.
-  const int unit = (int)(mine >> 20), rest = (int)(mine & 0xFFFFF);
-  int2 total;
-  block_scan(make_int2(unit, rest), sums, total);
-  const long long tiles = ((long long)total.x << 20) + total.y;
-  const long long want = (tiles * Hkv + p.target - 1) / p.target;
-  const int cut = (int)max(want, (long long)kMinTiles);
-  int2 n = make_int2(0, 0);
-#pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    if (t[i].first < 0) continue;
-    const int parts = max(1, (t[i].n + cut - 1) / cut);
-    n.x += parts, n.y += parts > 1 ? parts : 0;
-  }
-  int2 all;
-  int2 at = block_scan(n, sums, all);
-  if (threadIdx.x == 0) found.s = -1;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    if (t[i].first < 0) continue;
-    const int s = threadIdx.x * per + i;
-    const int parts = max(1, (t[i].n + cut - 1) / cut);
-    if (seq >= 0 ? s == seq : item / Hkv >= at.x && item / Hkv < at.x + parts) {
-      // Parts of a sequence are nearly equal: the first n % parts have a tile more.
-      const int part = seq >= 0 ? 0 : item / Hkv - at.x, each = t[i].n / parts, more = t[i].n % parts;
-      found = Part{s, item % Hkv, part, parts, t[i].first + part * each + min(part, more),
-                   each + (part < more), at.y * Hkv};
+  for (int s = s0; s < min(s0 + per, p.b.n_seq); ++s)
+    mine += (long long)span_of(tiles_of(p, attend_seq_at(p, s))) * p.b.Hkv;
+  if (threadIdx.x == 0) where = -1;
+  Line line;
+  long long at = block_scan(mine, sums, line.total);
+  line.cut = max((line.total + p.target - 1) / p.target, (long long)kMinTiles);
+  const long long u = line.cut * block;
+  if (seq >= 0 ? seq >= s0 && seq < s0 + per : u >= at && u < at + mine) {
+    for (int s = s0;; ++s) {
+      const long long span = (long long)span_of(tiles_of(p, attend_seq_at(p, s))) * p.b.Hkv;
+      if (seq >= 0 ? s == seq : u < at + span) {
+        where = s;
+        start = at;
+        break;
+      }
+      at += span;
     }
-    at.x += parts, at.y += parts > 1 ? parts : 0;
   }
   __syncthreads();
-  out = found;
-  return out.s >= 0;
+  line.s = where;
+  line.start = start;
+  return line;
 }
+
+// A segment: tiles first .. first + n - 1 of a sequence and KV head; whole: all of them.
+struct Segment {
+  int s, hk, first, n, slot;
+  bool whole;
+};
 
 // ---------------------------------------------------------------- kernel --
 
+template <int NT>
+struct Joined {
+  float m[kWarps<NT>][8 * NT], l[kWarps<NT>][8 * NT];
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendParams p) {
-  constexpr int NG = D / kKvGroup, MT = D / 16, SB = Slot<D>::kBytes, NS = kRing<D>;
+__device__ __forceinline__ void do_segment(const AttendParams &p, const Segment part, uint8_t *smem,
+                                           Joined<NT> &jn) {
+  constexpr int NG = D / kKvGroup, MT = D / 16, SB = Slot<D>::kBytes, NS = kRing<D, NT>, W = kWarps<NT>;
   constexpr int kPieces = D / 32;            // 16-byte pieces of a token's codes
   constexpr int VW = D / 64;                 // words of V codes a lane holds of a token
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float warp_m[kWarps][8 * NT], warp_l[kWarps][8 * NT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining blocks may wait beside these
-  Part part;
-  if (!find_part(p, blockIdx.x, -1, part)) return;
   const AttendSeq sq = attend_seq_at(p, part.s);
   const int cols = sq.rows * p.G, lp = p.b.log_page;
 
-  // ---- the ring: this warp's tiles are first + warp, + kWarps, ...
-  const int n_mine = part.n > warp ? (part.n - warp + kWarps - 1) / kWarps : 0;
+  // ---- the ring: this warp's tiles are first + warp, + W, ...
+  const int n_mine = part.n > warp ? (part.n - warp + W - 1) / W : 0;
   uint8_t *ring = smem + warp * (NS * SB);
   const uint32_t ring_s = smem_addr(ring);
   const int32_t *pages = p.b.pages + (size_t)part.s * p.b.max_pages;
@@ -243,7 +266,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
   auto page_pair = [&](int i) {
     int2 r = make_int2(-1, -1);
     if (i >= n_mine) return r;
-    const int tok = (part.first + warp + i * kWarps) * kTile;
+    const int tok = (part.first + warp + i * W) * kTile;
     auto get = [&](int token) {
       if (token >= sq.len) return -1;
       const int id = __ldg(pages + (token >> lp));
@@ -253,45 +276,40 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
     r.y = lp > 4 ? (tok + 16 < sq.len ? r.x : -1) : get(tok + 16);
     return r;
   };
+  // A lane's share of a tile's copies.  Codes: rows of D / 2 bytes, K's in the order
+  // of the S rows; of 64-byte rows every other pair has its halves exchanged, so
+  // that no loads below meet in a bank.  Whole rows wherever there is a page: a
+  // row past the length holds some codes or other, and every code is a finite
+  // number.  Scales: zeros past the length, whatever lies there.
+  constexpr int kRows = 32 / kPieces;        // tokens of a round of copies: 8 or 16
+  constexpr int kTok = 16 / (NG * 4);        // tokens of a 16-byte piece of scales
+  constexpr int kSp = kTile / kTok;          // pieces of K's, and of V's: 16 or 8
+  const int c_tk = lane / kPieces, c_pc = lane % kPieces;
+  const uint32_t c_kr = (c_tk & 8) + 2 * (c_tk & 3) + ((c_tk >> 2) & 1);
+  const uint32_t dst_k = ring_s + Slot<D>::kK + c_kr * (D / 2) + (D == 128 ? c_pc ^ (c_kr & 2) : c_pc) * 16;
+  const uint32_t dst_v = ring_s + Slot<D>::kV + c_tk * (D / 2) + (D == 128 ? c_pc ^ (c_tk & 2) : c_pc) * 16;
+  const int s_which = lane >= kSp, s_tk = (lane - s_which * kSp) * kTok, s_half = s_tk >= 16;
+  const uint32_t dst_s = ring_s + (s_which ? Slot<D>::kVs : Slot<D>::kKs) + (lane - s_which * kSp) * 16;
+  const uint32_t src_c = c_tk * (D / 2) + c_pc * 16, src_v = (uint32_t)(D / 2) << lp;
+  const uint32_t src_s = ((uint32_t)D << lp) + ((uint32_t)(s_which * (D / 16)) << lp) + (s_tk & 15) * (D / 16);
   auto issue = [&](int i, int2 pg) {
     if (i < n_mine) {
-      const int tok = (part.first + warp + i * kWarps) * kTile, mask = (1 << lp) - 1;
-      const uint32_t dst = ring_s + (i % NS) * SB;
-      const uint8_t *blk[2];
-      int slot[2];
+      const int tok = (part.first + warp + i * W) * kTile, mask = (1 << lp) - 1;
+      const uint32_t to = (i % NS) * SB;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int id = h ? pg.y : pg.x;
-        blk[h] = head + (size_t)max(id, 0) * page_bytes;
-        slot[h] = (tok + 16 * h) & mask;
-      }
-      // Codes: whole rows where there is a page (rows past the length hold some
-      // codes or other, and every code is a finite number); K rows in the order
-      // of the S rows, and 16-byte pieces 2 and 3 in place of 0 and 1 in every
-      // other pair of rows, for loads without bank conflicts.
-      constexpr int kRows = 32 / kPieces;      // tokens of one round of copies
+        const int id = h ? pg.y : pg.x, ok = id >= 0 ? 16 : 0;
+        const uint32_t slot = (tok + 16 * h) & mask;
+        const uint8_t *blk = head + (size_t)max(id, 0) * page_bytes;
+        const uint8_t *src = blk + slot * (D / 2) + src_c;
 #pragma unroll
-      for (int c = 0; c < kTile / kRows; ++c) {
-        const int h = c * kRows / 16;
-        const int tk = c * kRows % 16 + lane / kPieces, pc = lane % kPieces;   // token in the half, piece
-        const int ok = (h ? pg.y : pg.x) >= 0 ? 16 : 0;
-        const uint32_t kr = 16 * h + (tk & 8) + 2 * (tk & 3) + ((tk >> 2) & 1);   // S row of the token
-        const uint32_t vr = 16 * h + tk;
-        const uint32_t kp = D == 128 ? pc ^ (kr & 2) : pc, vp = D == 128 ? pc ^ (vr & 2) : pc;
-        copy16(dst + Slot<D>::kK + kr * (D / 2) + kp * 16,
-               blk[h] + KvBlock<D>::codes(lp, 0, slot[h] + tk) + pc * 16, ok);
-        copy16(dst + Slot<D>::kV + vr * (D / 2) + vp * 16,
-               blk[h] + KvBlock<D>::codes(lp, 1, slot[h] + tk) + pc * 16, ok);
-      }
-      // Scales: zeros past the length, whatever lies there.
-      constexpr int kTok = 16 / (NG * 4);      // tokens of a piece
-      constexpr int kSp = kTile / kTok;        // pieces of K's, and of V's: 16 or 8
-      if (lane < 2 * kSp) {
-        const int which = lane >= kSp, pc = lane - which * kSp, tk = pc * kTok, h = tk / 16;
-        const int left = (sq.len - tok - tk) * (NG * 4);
-        copy16(dst + (which ? Slot<D>::kVs : Slot<D>::kKs) + pc * 16,
-               (h ? blk[1] : blk[0]) + KvBlock<D>::scales(lp, which, (h ? slot[1] : slot[0]) + (tk & 15)),
-               (h ? pg.y : pg.x) >= 0 ? min(16, max(0, left)) : 0);
+        for (int c = 0; c < 16 / kRows; ++c) {
+          copy16(dst_k + to + (16 * h + c * kRows) * (D / 2), src + c * kRows * (D / 2), ok);
+          copy16(dst_v + to + (16 * h + c * kRows) * (D / 2), src + src_v + c * kRows * (D / 2), ok);
+        }
+        if (lane < 2 * kSp && s_half == h)
+          copy16(dst_s + to, blk + slot * (D / 16) + src_s,
+                 ok ? min(16, max(0, (sq.len - tok - s_tk) * (NG * 4))) : 0);
       }
     }
     copy_commit();
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
   // ---- q as B operands: lane (g, t4) holds column 8 nt + g, dimensions 16 t4 ..
   // + 15 of each group
   uint32_t qb[NT][NG][8];
-  float qsum[NT][NG][2], cs[NT][2];   // of the columns 8 nt + 2 t4, + 1 of the accumulators
+  float2 qsum[NT][NG], cs[NT];   // of the columns 8 nt + 2 t4, + 1 of the accumulators
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int c = 8 * nt + g;
@@ -362,13 +380,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
     }
+    // from column g's lanes to those of the accumulators' columns 2 t4, 2 t4 + 1
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int src = (2 * t4 + j) * 4;
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) qsum[nt][gr][j] = __shfl_sync(0xffffffffu, sum[gr], src);
-      cs[nt][j] = __shfl_sync(0xffffffffu, back, src);
-    }
+    for (int gr = 0; gr < NG; ++gr)
+      qsum[nt][gr] = make_float2(__shfl_sync(0xffffffffu, sum[gr], 8 * t4), __shfl_sync(0xffffffffu, sum[gr], 8 * t4 + 4));
+    cs[nt] = make_float2(__shfl_sync(0xffffffffu, back, 8 * t4), __shfl_sync(0xffffffffu, back, 8 * t4 + 4));
   }
   // Position of each accumulator column's row; the tokens that every column sees.
   int pos[NT][2];
@@ -380,11 +396,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
   if (p.causal) all_hi = max(0, sq.len - sq.nq + 1);
   if (p.window) all_lo = max(0, sq.len - p.window);
 
-  float m[NT][2], l[NT][2], o[MT][NT][4];
+  float2 nm[NT], l[NT];   // less the running maxima, and the sums
+  float o[MT][NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) m[nt][j] = kNoScore, l[nt][j] = 0.f;
+    nm[nt] = both(-kNoScore), l[nt] = both(0.f);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -398,7 +414,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
     copy_wait<NS - 1>();
     __syncwarp();
     uint8_t *sl = ring + (it % NS) * SB;
-    const int tok = (part.first + warp + it * kWarps) * kTile;
+    const int tok = (part.first + warp + it * W) * kTile;
     const uint32_t hole = holes >> ((it % NS) * 2) & 3u;
     {
       // A token whose V holds a NaN: its K becomes NaN, its V zeros, so that only
@@ -416,7 +432,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
         __syncwarp();
       }
     }
-    float s[2][NT][4];
+    float2 s[2][NT][2];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       float acc[NG][NT][4];
@@ -454,22 +470,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
           const float2 k = unpack_f16(ks[gr]);
           const float mid = fmaf(8.f, k.x, k.y);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float x = fmaf(k.x, acc[gr][nt][2 * r + j], mid * qsum[nt][gr][j]);
-              s[mt][nt][2 * r + j] = gr ? s[mt][nt][2 * r + j] + x : x;
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 a = make_float2(acc[gr][nt][2 * r], acc[gr][nt][2 * r + 1]);
+            const float2 x = gr ? fma_2(both(mid), qsum[nt][gr], s[mt][nt][r]) : mul_2(both(mid), qsum[nt][gr]);
+            s[mt][nt][r] = fma_2(both(k.x), a, x);
+          }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) s[mt][nt][2 * r + j] *= cs[nt][j];
+        for (int nt = 0; nt < NT; ++nt) s[mt][nt][r] = mul_2(s[mt][nt][r], cs[nt]);
       }
     }
     if (p.softcap > 0.f) {
 #pragma unroll
-      for (int i = 0; i < 2 * NT * 4; ++i) (&s[0][0][0])[i] = capped((&s[0][0][0])[i], cap_log2);
+      for (int i = 0; i < 4 * NT; ++i) {
+        float2 &x = s[i / (2 * NT)][i / 2 % NT][i & 1];
+        x = make_float2(capped(x.x, cap_log2), capped(x.y, cap_log2));
+      }
     }
     if (tok < all_lo || tok + kTile > all_hi || hole) {
 #pragma unroll
@@ -483,7 +499,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const bool see = in && (!p.causal || j0 <= pos[nt][j]) && (!p.window || j0 > pos[nt][j] - p.window);
-              if (!see) s[mt][nt][2 * r + j] = -INFINITY;
+              if (!see) (j ? s[mt][nt][r].y : s[mt][nt][r].x) = -INFINITY;
             }
         }
     }
@@ -492,11 +508,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
     float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        top[nt][j] = fmaxf(fmaxf(s[0][nt][j], s[0][nt][2 + j]), fmaxf(s[1][nt][j], s[1][nt][2 + j]));
-        over |= top[nt][j] > m[nt][j] + 8.f;
-      }
+{
+      top[nt][0] = fmaxf(fmaxf(s[0][nt][0].x, s[0][nt][1].x), fmaxf(s[1][nt][0].x, s[1][nt][1].x));
+      top[nt][1] = fmaxf(fmaxf(s[0][nt][0].y, s[0][nt][1].y), fmaxf(s[1][nt][0].y, s[1][nt][1].y));
+      over |= top[nt][0] > 8.f - nm[nt].x || top[nt][1] > 8.f - nm[nt].y;
+    }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -505,10 +521,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
           float x = top[nt][j];
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          x = fmaxf(x, m[nt][j]);
-          const float f = ex2(m[nt][j] - x);
-          m[nt][j] = x;
-          l[nt][j] *= f;
+          float &nmj = j ? nm[nt].y : nm[nt].x;
+          x = fmaxf(x, -nmj);
+          const float f = ex2(-nmj - x);
+          nmj = -x;
+          (j ? l[nt].y : l[nt].x) *= f;
 #pragma unroll
           for (int i = 0; i < MT; ++i) o[i][nt][j] *= f, o[i][nt][2 + j] *= f;
         }
@@ -521,9 +538,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float a = ex2(s[mt][nt][2 * r] - m[nt][0]), b = ex2(s[mt][nt][2 * r + 1] - m[nt][1]);
-          l[nt][0] += a, l[nt][1] += b;
-          pb[mt][nt][r] = transpose8x8(pack_f16(a, b));
+          const float2 x = add_2(s[mt][nt][r], nm[nt]), w = make_float2(ex2(x.x), ex2(x.y));
+          l[nt] = add_2(l[nt], w);
+          pb[mt][nt][r] = transpose8x8(pack_f16(w.x, w.y));
         }
     // V: tokens t4, t4 + 4 (k-pair of rows 2 t4, 2 t4 + 1), + 8 and + 12 of each block;
     // dimensions VW * 8 g .. of each.
@@ -577,29 +594,28 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
 
   // ---- join the warps: column sums, a common maximum, then the outputs
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], d);
-      if (g == 0) {
-        warp_m[warp][8 * nt + 2 * t4 + j] = m[nt][j];
-        warp_l[warp][8 * nt + 2 * t4 + j] = l[nt][j];
-      }
+    for (int d = 4; d < 32; d <<= 1)
+      l[nt] = add_2(l[nt], make_float2(__shfl_xor_sync(0xffffffffu, l[nt].x, d), __shfl_xor_sync(0xffffffffu, l[nt].y, d)));
+    if (g == 0) {
+      jn.m[warp][8 * nt + 2 * t4] = -nm[nt].x, jn.m[warp][8 * nt + 2 * t4 + 1] = -nm[nt].y;
+      jn.l[warp][8 * nt + 2 * t4] = l[nt].x, jn.l[warp][8 * nt + 2 * t4 + 1] = l[nt].y;
     }
+  }
   __syncthreads();   // also: the rings are free
   constexpr int kRow = D + 4;
   float *joined = reinterpret_cast<float *>(smem);   // [warp][column][kRow]
-  static_assert(kWarps * 8 * NT * kRow * 4 <= kSmem<D>, "the joined outputs fit the rings");
+  static_assert(W * 8 * NT * kRow * 4 <= kSmem<D, NT>, "the joined outputs fit the rings");
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int c = 8 * nt + 2 * t4 + j;
-      float top = warp_m[0][c];
+      float top = jn.m[0][c];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_m[w][c]);
-      const float f = ex2(m[nt][j] - top);
+      for (int w = 1; w < W; ++w) top = fmaxf(top, jn.m[w][c]);
+      const float f = ex2(-(j ? nm[nt].y : nm[nt].x) - top);
       float *dst = joined + (warp * 8 * NT + c) * kRow + g * (D / 8);
 #pragma unroll
       for (int i = 0; i < MT; i += 2)
@@ -607,28 +623,64 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_few_kernel(const AttendPar
             make_float4(o[i][nt][j] * f, o[i][nt][2 + j] * f, o[i + 1][nt][j] * f, o[i + 1][nt][2 + j] * f);
     }
   __syncthreads();
-  for (int u = threadIdx.x; u < cols * (D / 4); u += kWarps * 32) {
+  for (int u = threadIdx.x; u < cols * (D / 4); u += W * 32) {
     const int c = u / (D / 4), d = u % (D / 4) * 4;
-    float top = warp_m[0][c];
+    float top = jn.m[0][c];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_m[w][c]);
+    for (int w = 1; w < W; ++w) top = fmaxf(top, jn.m[w][c]);
     float sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      sum += warp_l[w][c] * ex2(warp_m[w][c] - top);
+    for (int w = 0; w < W; ++w) {
+      sum += jn.l[w][c] * ex2(jn.m[w][c] - top);
       const float4 v = *reinterpret_cast<const float4 *>(joined + (w * 8 * NT + c) * kRow + d);
       y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
     }
-    if (part.parts == 1) {
+    if (part.whole) {
       const float f = sum != 0.f ? 1.f / sum : 0.f;
       const int i = c / p.G, h = part.hk * p.G + c - i * p.G;
       *reinterpret_cast<uint2 *>(p.out + (size_t)(sq.t0 + i) * p.ldo + (size_t)h * D + d) =
           pack_out(make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
     } else {
-      const size_t at = (size_t)(part.slot + part.part * p.b.Hkv + part.hk) * kColumns + c;
+      const size_t at = (size_t)part.slot * kColumns + c;
       *reinterpret_cast<float4 *>(p.part_o + at * D + d) = y;
       if (d == 0) p.part_ml[at] = make_float2(top, sum);
+    }
+  }
+}
+
+// kCut: blocks take equal spans of the line; otherwise block u is (sequence, head) u.
+template <int D, int NT, bool kCut>
+__global__ void __launch_bounds__(kWarps<NT> * 32, kBlocks<NT>) kv4_few_kernel(const AttendParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Joined<NT> jn;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining blocks may wait beside these
+  if constexpr (!kCut) {
+    Segment g;
+    g.s = blockIdx.x / p.b.Hkv, g.hk = blockIdx.x - g.s * p.b.Hkv;
+    const SeqTiles t = tiles_of(p, attend_seq_at(p, g.s));
+    if (t.n == 0) return;
+    g.first = t.first, g.n = t.n, g.slot = 0, g.whole = true;
+    do_segment<D, NT>(p, g, smem, jn);
+  } else {
+    const Line line = find_line(p, blockIdx.x, -1);
+    if (line.s < 0) return;
+    const long long begin = line.cut * blockIdx.x, end = min(begin + line.cut, line.total);
+    long long u = begin, start = line.start;   // start: of sequence s in the line
+    for (int s = line.s; s < p.b.n_seq && u < end; ++s) {
+      const SeqTiles t = tiles_of(p, attend_seq_at(p, s));
+      const int span = span_of(t);
+      for (int hk = span ? (int)((u - start) / span) : p.b.Hkv; hk < p.b.Hkv && u < end; ++hk) {
+        const long long first = start + (long long)hk * span;   // this head's tiles: first .. first + t.n
+        const int a = (int)(u - first), b = (int)min((long long)t.n, end - first);
+        if (a < b) {
+          const Segment g{s, hk, t.first + a, b - a, 2 * (int)blockIdx.x + (first > begin), a == 0 && b == t.n};
+          do_segment<D, NT>(p, g, smem, jn);
+          __syncthreads();   // the joined outputs are read before the next tiles come
+        }
+        u = first + span;
+      }
+      start += (long long)span * p.b.Hkv;
     }
   }
 }
@@ -644,26 +696,30 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttendParams p, int
   const AttendSeq sq = attend_seq_at(p, s);
   const int cols = sq.rows * p.G, hk = u / max_cols, c = u - hk * max_cols;
   if (cols > kColumns || c >= cols) return;
-  Part part;
-  if (!find_part(p, 0, s, part) || part.parts == 1) return;
+  const SeqTiles t = tiles_of(p, sq);
+  const Line line = find_line(p, 0, s);
+  const long long head = line.start + (long long)hk * span_of(t);
+  const int b0 = (int)(head / line.cut), b1 = (int)((head + t.n - 1) / line.cut);
+  if (b0 == b1) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float *po = after_wait(p.part_o);
   const float2 *pml = after_wait(p.part_ml);
-  const size_t first = (size_t)(part.slot + hk) * kColumns + c, step = (size_t)p.b.Hkv * kColumns;
+  // Slot of block b's part: its span's first segment, or one that starts inside it.
+  auto slot = [&](int b) { return (size_t)(2 * b + (head > line.cut * b)) * kColumns + c; };
   float top = kNoScore;
-  for (int i = lane; i < part.parts; i += 32) top = fmaxf(top, __ldcg(pml + first + i * step).x);
+  for (int b = b0 + lane; b <= b1; b += 32) top = fmaxf(top, __ldcg(pml + slot(b)).x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   float sum = 0.f;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = warp; i < part.parts; i += 4) {
-    const float2 ml = __ldcg(pml + first + i * step);
+  for (int b = b0 + warp; b <= b1; b += 4) {
+    const float2 ml = __ldcg(pml + slot(b));
     const float f = ex2(ml.x - top);
     sum += ml.y * f;
     if (lane < D / 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + (first + i * step) * D) + lane);
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + slot(b) * D) + lane);
       y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
     }
   }
@@ -683,41 +739,46 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttendParams p, int
       pack_out(make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kCut>
 cudaError_t launch(const AttendParams &p, int grid, cudaStream_t st) {
-  auto kernel = kv4_few_kernel<D, NT>;
+  auto kernel = kv4_few_kernel<D, NT, kCut>;
   static DeviceOnce once;
   const cudaError_t err = once.run([&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, NT>);
   });
   if (err != cudaSuccess) return err;
-  return launch_k(false, kernel, dim3(grid), dim3(kWarps * 32), kSmem<D>, st, p);
+  return launch_k(false, kernel, dim3(grid), dim3(kWarps<NT> * 32), kSmem<D, NT>, st, p);
+}
+
+template <int D, int NT>
+cudaError_t launch(AttendParams p, bool cut, int max_cols, cudaStream_t st) {
+  if (!cut) return launch<D, NT, false>(p, p.b.n_seq * p.b.Hkv, st);
+  p.target = kFewSms * kBlocks<NT>;
+  const cudaError_t err = launch<D, NT, true>(p, p.target, st);
+  if (err != cudaSuccess) return err;
+  return launch_k(true, kv4_join_kernel<D>, dim3((unsigned)(p.b.n_seq * p.b.Hkv * max_cols)), dim3(128), 0, st, p,
+                  max_cols);
+}
+
+// Whether the line of tiles is cut: not for more sequences than a block can look
+// over at its start, nor where no sequence is longer than a span's least.
+bool is_cut(const AttendParams &p) {
+  return p.b.n_seq <= kPlanSeqs && ((long long)p.b.max_pages << p.b.log_page) > kMinTiles * kTile;
 }
 
 }  // namespace
 
-int few_target(int sms) { return sms * 4; }
-
-// Slots of partial results: none where no sequence can have two parts.
-size_t few_slots(const AttendParams &p) {
-  if (p.b.n_seq > kPlanSeqs || ((long long)p.b.max_pages << p.b.log_page) <= kMinTiles * kTile) return 0;
-  return 2 * (size_t)p.target + 2 * p.b.Hkv;
-}
+// Slots of partial results: two for each block.
+size_t few_slots(const AttendParams &p) { return is_cut(p) ? 2 * kFewSms * 2 : 0; }
 
 cudaError_t launch_few(const AttendParams &p, int D, cudaStream_t st) {
   // Columns that some sequence may have.
   const long long rows = p.b.q_off ? (p.max_q ? std::min(p.max_q, p.b.T) : p.b.T) : 1;
   const int max_cols = (int)std::min<long long>(kColumns / p.G * p.G, rows * p.G);
-  const bool two = max_cols > 8;
-  const size_t slots = few_slots(p);
-  const long long pairs = (long long)p.b.n_seq * p.b.Hkv;
-  const int grid = (int)(pairs + (slots ? p.target : 0));
-  cudaError_t err;
-  if (D == 128) err = two ? launch<128, 2>(p, grid, st) : launch<128, 1>(p, grid, st);
-  else err = two ? launch<64, 2>(p, grid, st) : launch<64, 1>(p, grid, st);
-  if (err != cudaSuccess || !slots) return err;
-  return launch_k(true, D == 128 ? kv4_join_kernel<128> : kv4_join_kernel<64>,
-                  dim3((unsigned)(p.b.n_seq * p.b.Hkv * max_cols)), dim3(128), 0, st, p, max_cols);
+  const bool cut = is_cut(p);
+  if (D == 128)
+    return max_cols > 8 ? launch<128, 2>(p, cut, max_cols, st) : launch<128, 1>(p, cut, max_cols, st);
+  return max_cols > 8 ? launch<64, 2>(p, cut, max_cols, st) : launch<64, 1>(p, cut, max_cols, st);
 }
 
 }  // namespace moe
