@@ -9,20 +9,25 @@
 // reading the cache, 9/16 bytes an element: the design keeps instructions per
 // code low and loads in flight many.
 //
+//   Codes: a code in the lowest bits of a float16 is the subnormal number c 2^-24,
+//      four bits further up c 2^-20: one AND makes a pair of exact operands, with
+//      nothing to add or take away.  The factors 2^24 and 16 go into q, the scales
+//      and the output.
 //   K: a lane's 16 codes of a token and group are 4 k-steps of the MMA as they lie
-//      (which dimension is which k is free as long as q agrees).  They enter as
-//      exact integers c - 8, one accumulator for each group, and
-//      s = sum_g step_g acc_g + (lo_g + 8 step_g) sum(q of g): no rounding of K.
+//      (which dimension is which k is free as long as q agrees), one accumulator
+//      for each group: s = sum_g step_g acc_g + lo_g sum(q of g), no rounding of K.
 //   q: float16 after a power of two per column that brings its largest just under
-//      2^15: exact to 2^-29 of that.
-//   P: the accumulator's layout, transposed by movmatrix, is the B operand.
-//   V: lo + step c in float16 (pairs of tokens of one dimension, so step and lo are
-//      pairs as they come), rounded once: 2^-12 of the value.
+//      2^15: exact to 2^-25 of that.
+//   P: for each group w step, rounded to float16 (2^-12 of the weight), in the
+//      accumulator's layout, transposed by movmatrix: the B operand.  V's codes are
+//      exact, and sum w lo is kept beside in f32.
 //
 // Each warp streams its own tiles of 32 tokens through a private ring in shared
 // memory by cp.async (no barrier, no waiting but its own), with a running
-// maximum that moves only when a score passes it by 2^8 (weights up to 256 are
-// float16 as well as those up to 1), so most tiles exchange nothing.  The block's
+// maximum that moves only when a score passes it by 8 (weights up to 2^8 are
+// float16 as well as those up to 1), so most tiles exchange nothing.  The maximum
+// also holds a power of two that keeps w step in float16's range whatever the size
+// of V: it moves when a step passes it by 8.  The block's
 // warps join at the end.  A batch is cut into parts of about equal length over
 // the tokens of all its sequences; a second kernel joins the parts of sequences
 // that have several.
@@ -74,39 +79,27 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// (w & mask) | magic: 1024 + c from bits 0-3 of each half, 64 + c from bits 4-7.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(d) : "r"(w));
-  return d;
-}
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, 0x00F000F0, 0x54005400, 0xEA;" : "=r"(d) : "r"(w));
-  return d;
-}
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-// Four pairs of codes of w (nibbles i and i + 4 of it: a pair's halves), less `less`.
-__device__ __forceinline__ void four_pairs(uint32_t w, uint32_t lo_bias, uint32_t hi_bias, uint32_t (&o)[4]) {
+// Four pairs of codes of w (nibbles i and i + 4 of it: a pair's halves) as float16
+// operands: c 2^-24, c 2^-20 in turn.
+__device__ __forceinline__ void four_pairs(uint32_t w, uint32_t (&o)[4]) {
   const uint32_t w8 = w >> 8;
-  o[0] = sub2(codes_lo(w), lo_bias);
-  o[1] = sub2(codes_hi(w), hi_bias);
-  o[2] = sub2(codes_lo(w8), lo_bias);
-  o[3] = sub2(codes_hi(w8), hi_bias);
+  o[0] = w & 0x000F000Fu;
+  o[1] = w & 0x00F000F0u;
+  o[2] = w8 & 0x000F000Fu;
+  o[3] = w8 & 0x00F000F0u;
 }
 // Two f32 operations in one instruction.
 __device__ __forceinline__ float2 fma_2(float2 a, float2 b, float2 c) {
@@ -136,7 +129,15 @@ __device__ __forceinline__ float2 add_2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ float2 xor_2(float2 v, int d) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d));
+}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ uint32_t max2_f16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -243,6 +244,7 @@ struct Segment {
 template <int NT>
 struct Joined {
   float m[kWarps<NT>][8 * NT], l[kWarps<NT>][8 * NT];
+  uint4 q[NT][2][2][32];   // two column tiles: q's B operands
 };
 
 template <int D, int NT>
@@ -250,7 +252,6 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
                                            Joined<NT> &jn) {
   constexpr int NG = D / kKvGroup, MT = D / 16, SB = Slot<D>::kBytes, NS = kRing<D, NT>, W = kWarps<NT>;
   constexpr int kPieces = D / 32;            // 16-byte pieces of a token's codes
-  constexpr int VW = D / 64;                 // words of V codes a lane holds of a token
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   const AttendSeq sq = attend_seq_at(p, part.s);
   const int cols = sq.rows * p.G, lp = p.b.log_page;
@@ -330,7 +331,8 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 
   // ---- q as B operands: lane (g, t4) holds column 8 nt + g, dimensions 16 t4 ..
   // + 15 of each group
-  uint32_t qb[NT][NG][8];
+  // (two column tiles: kept in shared memory, where registers are short)
+  uint32_t qb[1][NG][8];
   float2 qsum[NT][NG], cs[NT];   // of the columns 8 nt + 2 t4, + 1 of the accumulators
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -361,8 +363,8 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
     // 2^up times the largest is under 2^15; rows with an infinity or NaN as they are
     const int eb = (int)(top >> 23);
     const int up = eb == 255 ? 0 : min(15 + 126 - max(eb, 1), 127);
-    const float f = __int_as_float((up + 127) << 23);
-    float back = p.scale * kLog2e * (p.softcap > 0.f ? 2.f / p.softcap : 1.f);
+    const float f = __int_as_float((up + 127) << 23), f16th = f * 0.0625f;
+    float back = p.scale * kLog2e * (p.softcap > 0.f ? 2.f / p.softcap : 1.f) * 16777216.f;   // 2^24
     back = up > 100 ? back * 7.888609052210118e-31f * __int_as_float((227 - up) << 23)   // 2^-100
                     : back * __int_as_float((127 - up) << 23);
     float sum[NG];
@@ -372,13 +374,24 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         const int d = 8 * (ks / 2) + 2 * (ks & 1);
-        qb[nt][gr][2 * ks] = pack_f16(v[gr][d] * f, v[gr][d + 4] * f);
-        qb[nt][gr][2 * ks + 1] = pack_f16(v[gr][d + 1] * f, v[gr][d + 5] * f);
-        const float2 a = unpack_f16(qb[nt][gr][2 * ks]), b = unpack_f16(qb[nt][gr][2 * ks + 1]);
-        sum[gr] += (a.x + a.y) + (b.x + b.y);
+        // the second pair meets codes 16 times as large
+        qb[0][gr][2 * ks] = pack_f16(v[gr][d] * f, v[gr][d + 4] * f);
+        qb[0][gr][2 * ks + 1] = pack_f16(v[gr][d + 1] * f16th, v[gr][d + 5] * f16th);
+        const float2 a = unpack_f16(qb[0][gr][2 * ks]), b = unpack_f16(qb[0][gr][2 * ks + 1]);
+        sum[gr] += (a.x + a.y) + 16.f * (b.x + b.y);
       }
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
+      sum[gr] *= 5.9604644775390625e-08f;   // 2^-24, as the products of codes
+    }
+    if constexpr (NT > 1) {
+      if (warp == 0) {
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            jn.q[nt][gr][i][lane] = make_uint4(qb[0][gr][4 * i], qb[0][gr][4 * i + 1], qb[0][gr][4 * i + 2], qb[0][gr][4 * i + 3]);
+      }
     }
     // from column g's lanes to those of the accumulators' columns 2 t4, 2 t4 + 1
 #pragma unroll
@@ -386,29 +399,26 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
       qsum[nt][gr] = make_float2(__shfl_sync(0xffffffffu, sum[gr], 8 * t4), __shfl_sync(0xffffffffu, sum[gr], 8 * t4 + 4));
     cs[nt] = make_float2(__shfl_sync(0xffffffffu, back, 8 * t4), __shfl_sync(0xffffffffu, back, 8 * t4 + 4));
   }
-  // Position of each accumulator column's row; the tokens that every column sees.
-  int pos[NT][2];
-  int all_lo = 0, all_hi = sq.len;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) pos[nt][j] = sq.len - sq.nq + min(8 * nt + 2 * t4 + j, cols - 1) / p.G;
+  if constexpr (NT > 1) __syncthreads();
+  int all_lo = 0, all_hi = sq.len;   // the tokens that every column sees
   if (p.causal) all_hi = max(0, sq.len - sq.nq + 1);
   if (p.window) all_lo = max(0, sq.len - p.window);
 
-  float2 nm[NT], l[NT];   // less the running maxima, and the sums
+  float2 nm[NT], l[NT];   // less the running maxima and the exponent below; the sums
+  float2 low[NG][NT];     // sums of w lo
   float o[MT][NT][4];
+  int step_e = -150;      // no step so far is more than 8 times 2^step_e
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     nm[nt] = both(-kNoScore), l[nt] = both(0.f);
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) low[gr][nt] = both(0.f);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
   }
   const float cap_log2 = p.softcap * kLog2e;
-  const uint32_t c1032 = 0x64086408u, c72 = 0x54805480u;   // less 1024 + 8 and 64 + 8
-  const uint32_t c1024 = 0x64006400u, c64 = 0x54005400u;
 
   for (int it = 0; it < n_mine; ++it) {
     copy_wait<NS - 1>();
@@ -434,14 +444,23 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
     }
     float2 s[2][NT][2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      float acc[NG][NT][4];
+    for (int gr = 0; gr < NG; ++gr) {
+      uint32_t bq[NT][8];
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (NT == 1) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int i = 0; i < 8; ++i) bq[nt][i] = qb[0][gr][i];
+        } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[gr][nt][c] = 0.f;
+          for (int i = 0; i < 2; ++i) {
+            const uint4 u = jn.q[nt][gr][i][lane];
+            bq[nt][4 * i] = u.x, bq[nt][4 * i + 1] = u.y, bq[nt][4 * i + 2] = u.z, bq[nt][4 * i + 3] = u.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
         // rows g and g + 8 of the S tile: 8 bytes of the group each
         uint32_t pr[2][2][4];
 #pragma unroll
@@ -449,37 +468,40 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
           const uint32_t row = 16 * mt + 8 * r + g;
           const uint32_t pc = D == 128 ? (2 * gr + (t4 >> 1)) ^ (row & 2) : (t4 >> 1);
           const uint2 w = *reinterpret_cast<const uint2 *>(sl + Slot<D>::kK + row * (D / 2) + pc * 16 + (t4 & 1) * 8);
-          four_pairs(w.x, c1032, c72, pr[r][0]);
-          four_pairs(w.y, c1032, c72, pr[r][1]);
+          four_pairs(w.x, pr[r][0]);
+          four_pairs(w.y, pr[r][1]);
         }
+        float acc[NT][4];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           const uint32_t a[4] = {pr[0][ks / 2][2 * (ks & 1)], pr[1][ks / 2][2 * (ks & 1)],
                                  pr[0][ks / 2][2 * (ks & 1) + 1], pr[1][ks / 2][2 * (ks & 1) + 1]};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(acc[gr][nt], a, qb[nt][gr][2 * ks], qb[nt][gr][2 * ks + 1]);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        // the token of S row 8 r + g
-        const int tk = 16 * mt + 8 * r + (g >> 1) + 4 * (g & 1);
-        const uint32_t *ks = reinterpret_cast<const uint32_t *>(sl + Slot<D>::kKs) + tk * NG;
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          const float2 k = unpack_f16(ks[gr]);
-          const float mid = fmaf(8.f, k.x, k.y);
-#pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float2 a = make_float2(acc[gr][nt][2 * r], acc[gr][nt][2 * r + 1]);
-            const float2 x = gr ? fma_2(both(mid), qsum[nt][gr], s[mt][nt][r]) : mul_2(both(mid), qsum[nt][gr]);
-            s[mt][nt][r] = fma_2(both(k.x), a, x);
+            if (ks == 0) mma_f16_first(acc[nt], a, bq[nt][0], bq[nt][1]);
+            else mma_f16(acc[nt], a, bq[nt][2 * ks], bq[nt][2 * ks + 1]);
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[mt][nt][r] = mul_2(s[mt][nt][r], cs[nt]);
+        for (int r = 0; r < 2; ++r) {
+          // the token of S row 8 r + g
+          const int tk = 16 * mt + 8 * r + (g >> 1) + 4 * (g & 1);
+          const float2 k = unpack_f16(reinterpret_cast<const uint32_t *>(sl + Slot<D>::kKs)[tk * NG + gr]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 a = make_float2(acc[nt][2 * r], acc[nt][2 * r + 1]);
+            const float2 x = gr ? fma_2(both(k.y), qsum[nt][gr], s[mt][nt][r]) : mul_2(both(k.y), qsum[nt][gr]);
+            s[mt][nt][r] = fma_2(both(k.x), a, x);
+          }
+        }
       }
     }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) s[mt][nt][r] = mul_2(s[mt][nt][r], cs[nt]);
     if (p.softcap > 0.f) {
 #pragma unroll
       for (int i = 0; i < 4 * NT; ++i) {
@@ -498,22 +520,44 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const bool see = in && (!p.causal || j0 <= pos[nt][j]) && (!p.window || j0 > pos[nt][j] - p.window);
+              const int pos = sq.len - sq.nq + min(8 * nt + 2 * t4 + j, cols - 1) / p.G;
+              const bool see = in && (!p.causal || j0 <= pos) && (!p.window || j0 > pos - p.window);
               if (!see) (j ? s[mt][nt][r].y : s[mt][nt][r].x) = -INFINITY;
             }
         }
     }
-    // The running maximum, when some score passes it by 8.
-    bool over = false;
+    // V's scales of the S rows' tokens.
+    uint32_t vsc[2][2][NG];
+    uint32_t steps = 0;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t *vs = reinterpret_cast<const uint32_t *>(sl + Slot<D>::kVs) +
+                             (16 * mt + 8 * r + (g >> 1) + 4 * (g & 1)) * NG;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          vsc[mt][r][gr] = vs[gr];
+          steps = max2_f16(steps, vs[gr]);
+        }
+      }
+    // The running maxima, when some score or step passes theirs by 8.
+    const float step = __low2float(*reinterpret_cast<const __half2 *>(&steps));
+    bool over = __float_as_int(step) > (step_e + 130) << 23;
+    const float room = 8.f - (float)step_e;
     float top[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-{
+    for (int nt = 0; nt < NT; ++nt) {
       top[nt][0] = fmaxf(fmaxf(s[0][nt][0].x, s[0][nt][1].x), fmaxf(s[1][nt][0].x, s[1][nt][1].x));
       top[nt][1] = fmaxf(fmaxf(s[0][nt][0].y, s[0][nt][1].y), fmaxf(s[1][nt][0].y, s[1][nt][1].y));
-      over |= top[nt][0] > 8.f - nm[nt].x || top[nt][1] > 8.f - nm[nt].y;
+      const float2 x = add_2(make_float2(top[nt][0], top[nt][1]), nm[nt]);
+      over |= x.x > room || x.y > room;
     }
     if (__any_sync(0xffffffffu, over)) {
+      // The power of two at or above the largest step.
+      const int sb = (int)__reduce_max_sync(0xffffffffu, __float_as_uint(step));
+      const int was = step_e;
+      step_e = max(max(was, -24), ((sb + 0x7FFFFF) >> 23) - 127);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -522,68 +566,61 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
           float &nmj = j ? nm[nt].y : nm[nt].x;
-          x = fmaxf(x, -nmj);
-          const float f = ex2(-nmj - x);
-          nmj = -x;
+          const float now = -fmaxf(x, -nmj - (float)was) - (float)step_e;
+          const float f = ex2(now - nmj);   // first time: ex2(-1e30) = 0
+          nmj = now;
           (j ? l[nt].y : l[nt].x) *= f;
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) (j ? low[gr][nt].y : low[gr][nt].x) *= f;
 #pragma unroll
           for (int i = 0; i < MT; ++i) o[i][nt][j] *= f, o[i][nt][2 + j] *= f;
         }
     }
-    // Weights, and their B operands for the two blocks of 16 tokens.
-    uint32_t pb[2][NT][2];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float2 x = add_2(s[mt][nt][r], nm[nt]), w = make_float2(ex2(x.x), ex2(x.y));
-          l[nt] = add_2(l[nt], w);
-          pb[mt][nt][r] = transpose8x8(pack_f16(w.x, w.y));
-        }
-    // V: tokens t4, t4 + 4 (k-pair of rows 2 t4, 2 t4 + 1), + 8 and + 12 of each block;
-    // dimensions VW * 8 g .. of each.
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      uint32_t st[2], lo[2], w[2][2][VW];
+      // Weights, and for each group their B operands.
+      uint32_t pb[NG][NT][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t sc[2];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t row = 16 * mt + 8 * r + t4 + 4 * e;
-          sc[e] = *(reinterpret_cast<const uint32_t *>(sl + Slot<D>::kVs) + row * NG + (NG == 2 ? g >> 2 : 0));
-          if constexpr (D == 128) {
-            const uint32_t pc = (g >> 1) ^ (row & 2);
-            const uint2 u = *reinterpret_cast<const uint2 *>(sl + Slot<D>::kV + row * 64 + pc * 16 + (g & 1) * 8);
-            w[r][e][0] = u.x, w[r][e][VW - 1] = u.y;
-          } else {
-            w[r][e][0] = *reinterpret_cast<const uint32_t *>(sl + Slot<D>::kV + row * 32 + g * 4);
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 x = add_2(s[mt][nt][r], nm[nt]), w = make_float2(ex2(x.x), ex2(x.y));
+          l[nt] = add_2(l[nt], w);
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            const float2 sc = unpack_f16(vsc[mt][r][gr]);
+            low[gr][nt] = fma_2(w, both(sc.y), low[gr][nt]);
+            const float2 ws = mul_2(w, both(sc.x));
+            pb[gr][nt][r] = transpose8x8(pack_f16(ws.x, ws.y));
           }
         }
-        st[r] = __byte_perm(sc[0], sc[1], 0x5410);
-        lo[r] = __byte_perm(sc[0], sc[1], 0x7632);
-      }
+      // V: the k-pairs are tokens t4, t4 + 4 (rows 2 t4, 2 t4 + 1) and 8 further; a lane
+      // holds dimensions 8 g .. 8 g + 7 of each group.
 #pragma unroll
-      for (int v = 0; v < VW; ++v)
+      for (int gr = 0; gr < NG; ++gr) {
+        uint32_t w[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t row = 16 * mt + 8 * r + t4 + 4 * e;
+            const uint32_t pc = D == 128 ? (2 * gr + (g >> 2)) ^ (row & 2) : g >> 2;
+            w[r][e] = *reinterpret_cast<const uint32_t *>(sl + Slot<D>::kV + row * (D / 2) + pc * 16 + (g & 3) * 4);
+          }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           // four dimensions: two row pairs of the MMA's A
           uint32_t c[2][4];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            four_pairs(__byte_perm(w[r][0][v], w[r][1][v], half ? 0x7632 : 0x5410), c1024, c64, c[r]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[r][e] = fma2(c[r][e], st[r], lo[r]);
-          }
+          for (int r = 0; r < 2; ++r) four_pairs(__byte_perm(w[r][0], w[r][1], half ? 0x7632 : 0x5410), c[r]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t a[4] = {c[0][2 * i], c[0][2 * i + 1], c[1][2 * i], c[1][2 * i + 1]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(o[v * 4 + half * 2 + i][nt], a, pb[mt][nt][0], pb[mt][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[gr * 4 + half * 2 + i][nt], a, pb[gr][nt][0], pb[gr][nt][1]);
           }
         }
+      }
     }
     __syncwarp();
     issue(it + NS, next);
@@ -597,7 +634,11 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1)
-      l[nt] = add_2(l[nt], make_float2(__shfl_xor_sync(0xffffffffu, l[nt].x, d), __shfl_xor_sync(0xffffffffu, l[nt].y, d)));
+      l[nt] = add_2(l[nt], xor_2(l[nt], d));
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) low[gr][nt] = add_2(low[gr][nt], xor_2(low[gr][nt], d));
     if (g == 0) {
       jn.m[warp][8 * nt + 2 * t4] = -nm[nt].x, jn.m[warp][8 * nt + 2 * t4 + 1] = -nm[nt].y;
       jn.l[warp][8 * nt + 2 * t4] = l[nt].x, jn.l[warp][8 * nt + 2 * t4 + 1] = l[nt].y;
@@ -616,11 +657,18 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 #pragma unroll
       for (int w = 1; w < W; ++w) top = fmaxf(top, jn.m[w][c]);
       const float f = ex2(-(j ? nm[nt].y : nm[nt].x) - top);
-      float *dst = joined + (warp * 8 * NT + c) * kRow + g * (D / 8);
+      const float f24 = f * 16777216.f, f20 = f * 1048576.f;   // the codes' 2^-24 and 2^-20
+      float *dst = joined + (warp * 8 * NT + c) * kRow + g * 8;
 #pragma unroll
-      for (int i = 0; i < MT; i += 2)
-        *reinterpret_cast<float4 *>(dst + 2 * i) =
-            make_float4(o[i][nt][j] * f, o[i][nt][2 + j] * f, o[i + 1][nt][j] * f, o[i + 1][nt][2 + j] * f);
+      for (int gr = 0; gr < NG; ++gr) {
+        const float lo = (j ? low[gr][nt].y : low[gr][nt].x) * f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float(&a)[4] = o[gr * 4 + 2 * h][nt], (&b)[4] = o[gr * 4 + 2 * h + 1][nt];
+          *reinterpret_cast<float4 *>(dst + gr * 64 + h * 4) =
+              make_float4(fmaf(a[j], f24, lo), fmaf(a[2 + j], f20, lo), fmaf(b[j], f24, lo), fmaf(b[2 + j], f20, lo));
+        }
+      }
     }
   __syncthreads();
   for (int u = threadIdx.x; u < cols * (D / 4); u += W * 32) {
