@@ -15,7 +15,8 @@ SO = os.path.join(HERE, "libmoe.so")
 ROOT = os.path.dirname(HERE)
 SOURCES = ["router.cu", "dispatch.cu", "gemv.cu", "ggemm_tc.cu", "misc.cu", "moe_api.cu",
            "route_trace.cu", "decode_tc.cu", "norm.cu", "linear.cu", "linear_tc.cu",
-           "balance.cu", "rope.cu", "kv4.cu", "kv4_attend.cu", "kv4_few.cu"]
+           "balance.cu", "rope.cu", "kv4.cu", "kv4_attend.cu", "kv4_few.cu",
+           "kv4_many.cu"]
 HEADERS = ["moe_internal.cuh", "ptx.cuh", "tc.cuh", "linear.cuh", "area.cuh", "kv4.cuh"]
 
 NVCC_FLAGS = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -116,6 +116,9 @@ constexpr int kFewColumns = 16;
 size_t few_slots(const AttendParams &p);
 cudaError_t launch_few(const AttendParams &p, int D, cudaStream_t st);
 
+size_t many_rows(const AttendParams &p);
+cudaError_t launch_many(const AttendParams &p, int D, cudaStream_t st);
+
 static __device__ __forceinline__ uint2 pack_out(float4 v) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
   return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));

@@ -1,10 +1,8 @@
-// kv4_attend.cu -- attention over the 4-bit paged cache (moe_kv4_attention in
-// include/moe.h).
-//
-// One block per row and query head: its warps take the row's tokens in turn, a
-// lane holds D / 32 neighbouring dimensions, and each warp keeps the running
-// maximum, sum and output of an online softmax; the warps' parts are joined at
-// the end.
+// kv4_attend.cu -- moe_kv4_attention's argument checks, workspace and choice of
+// kernels (include/moe.h): sequences of up to 16 columns (rows times query heads
+// of a KV head) in kv4_few.cu, which reads the cache at most once and is bound by
+// that, larger ones in kv4_many.cu on the tensor cores.  Each kernel leaves the
+// other's sequences alone, so a batch may mix them.
 #include <algorithm>
 #include <cmath>
 
@@ -14,73 +12,6 @@
 namespace moe {
 namespace {
 
-template <int D>
-__global__ void __launch_bounds__(128) kv4_attend_kernel(const AttendParams p) {
-  constexpr int N = D / 32, NG = D / kKvGroup;
-  __shared__ float part[4][D], pm[4], pl[4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x, h = blockIdx.y, hk = h / (p.H / p.b.Hkv);
-  const int s = kv_seq_of(p.b, t, lane);
-  if (s >= p.b.n_seq) return;
-  const AttendSeq sq = attend_seq_at(p, s);
-  const int i = t - sq.t0;
-  if (i >= sq.rows || sq.rows * p.G <= kFewColumns) return;
-  const int pos = sq.len - sq.nq + i;
-  const int end = p.causal ? min(sq.len, pos + 1) : sq.len;
-  const int first = p.window ? max(0, pos - p.window + 1) : 0;
-  float q[N], o[N];
-#pragma unroll
-  for (int c = 0; c < N; ++c) {
-    q[c] = __bfloat162float(p.q[(size_t)t * p.ldq + h * D + lane * N + c]);
-    o[c] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const int g = lane * N / kKvGroup, lp = p.b.log_page;
-  for (int j = first + warp; j < end; j += 4) {
-    const int page = kv_page_at(p.b, s, j);
-    if (page < 0) continue;
-    const int slot = j & ((1 << lp) - 1);
-    const uint8_t *block = p.cache + ((size_t)page * p.b.Hkv + hk) * KvBlock<D>::bytes(lp);
-    float kv[2][N];
-    bool nan = false;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint8_t *c = block + KvBlock<D>::codes(lp, w, slot) + lane * N / 2;
-      const __half2 sl = *reinterpret_cast<const __half2 *>(block + KvBlock<D>::scales(lp, w, slot) + g * 4);
-      const float st = __low2float(sl), lo = __high2float(sl);
-      nan |= st != st;
-#pragma unroll
-      for (int e = 0; e < N; ++e) kv[w][e] = fmaf(st, (float)(c[e / 2] >> (4 * (e & 1)) & 15), lo);
-    }
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) x = fmaf(q[e], kv[0][e], x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= p.scale;
-    if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
-    if (__any_sync(0xffffffffu, nan)) x = NAN;
-    const float top = fmaxf(m, x), keep = m > -INFINITY ? expf(m - top) : 0.f, w = expf(x - top);
-    l = l * keep + w;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = o[e] * keep + w * kv[1][e];
-    m = top;
-  }
-#pragma unroll
-  for (int e = 0; e < N; ++e) part[warp][lane * N + e] = o[e];
-  if (lane == 0) pm[warp] = m, pl[warp] = l;
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  const float top = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-  float sum = 0.f, y = 0.f;
-  for (int w = 0; w < 4; ++w) {
-    const float f = pl[w] != 0.f ? expf(pm[w] - top) : 0.f;
-    sum += pl[w] * f;
-    y += part[w][threadIdx.x] * f;
-  }
-  p.out[(size_t)t * p.ldo + h * D + threadIdx.x] = __float2bfloat16_rn(sum != 0.f ? y / sum : 0.f);
-}
-
 // Sizes that the call and its workspace are refused for.
 bool good_sizes(int T, int n_seq, bool rows_given, int max_q, int n_heads, int n_kv_heads, int head_dim,
                 int page_size, int n_pages, int max_pages) {
@@ -88,16 +19,24 @@ bool good_sizes(int T, int n_seq, bool rows_given, int max_q, int n_heads, int n
          max_q >= 0 && n_heads >= 1 && n_heads <= 1024 && n_heads % n_kv_heads == 0;
 }
 
+// Whether some sequence may have more than kFewColumns columns.
+bool may_have_many(const AttendParams &p) {
+  const long long rows = p.b.q_off ? (p.max_q ? std::min(p.max_q, p.b.T) : p.b.T) : 1;
+  return rows * p.G > kFewColumns;
+}
+
 // Where the partial results of a call lie in its workspace.
 struct Scratch {
   size_t o, ml, bytes;
 };
 Scratch workspace_of(const AttendParams &p, int D) {
-  const size_t columns = (p.G <= kFewColumns ? few_slots(p) : 0) * kFewColumns;
+  // The kernels run one after the other: one area serves both.
+  size_t rows = p.G <= kFewColumns ? few_slots(p) * kFewColumns : 0;
+  if (may_have_many(p)) rows = std::max(rows, many_rows(p));
   Scratch w;
   w.o = 0;
-  w.ml = columns * D * sizeof(float);
-  w.bytes = w.ml + columns * sizeof(float2);
+  w.ml = rows * D * sizeof(float);
+  w.bytes = w.ml + rows * sizeof(float2);
   return w;
 }
 
@@ -112,7 +51,11 @@ extern "C" __attribute__((visibility("default"))) size_t moe_kv4_workspace(
   moe::AttendParams p{};
   p.b.n_seq = n_seq, p.b.Hkv = n_kv_heads, p.b.max_pages = max_pages, p.b.log_page = moe::kv4_log2(page_size);
   p.b.T = T, p.H = n_heads, p.G = n_heads / n_kv_heads, p.max_q = max_q;
-  return moe::workspace_of(p, head_dim).bytes;
+  // Enough with q_off and without.
+  p.b.q_off = nullptr;
+  const size_t without = T == n_seq ? moe::workspace_of(p, head_dim).bytes : 0;
+  p.b.q_off = reinterpret_cast<const int32_t *>(uintptr_t(4));
+  return std::max(without, moe::workspace_of(p, head_dim).bytes);
 }
 
 extern "C" __attribute__((visibility("default"))) int moe_kv4_attention(
@@ -163,10 +106,9 @@ extern "C" __attribute__((visibility("default"))) int moe_kv4_attention(
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err = cudaSuccess;
-  const long long rows = q_off ? (max_q ? std::min(max_q, T) : T) : 1;   // of one sequence, at most
-  if (p.G <= kFewColumns) err = launch_few(p, head_dim, st);
-  if (err == cudaSuccess && rows * p.G > kFewColumns)
-    err = launch_k(false, head_dim == 64 ? kv4_attend_kernel<64> : kv4_attend_kernel<128>, dim3(T, n_heads),
-                   dim3(128), 0, st, p);
+  p.wait_ns = linear_wait_ns();
+  if (!p.status) err = linear_gave_up(&p.status);
+  if (err == cudaSuccess && p.G <= kFewColumns) err = launch_few(p, head_dim, st);
+  if (err == cudaSuccess && may_have_many(p)) err = launch_many(p, head_dim, st);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }

@@ -743,13 +743,20 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttendParams p, int
   const int s = blockIdx.x / per_seq, u = blockIdx.x - s * per_seq;
   const AttendSeq sq = attend_seq_at(p, s);
   const int cols = sq.rows * p.G, hk = u / max_cols, c = u - hk * max_cols;
-  if (cols > kColumns || c >= cols) return;
   const SeqTiles t = tiles_of(p, sq);
-  const Line line = find_line(p, 0, s);
-  const long long head = line.start + (long long)hk * span_of(t);
-  const int b0 = (int)(head / line.cut), b1 = (int)((head + t.n - 1) / line.cut);
-  if (b0 == b1) return;
+  bool any = t.n > 0 && c < cols;
+  Line line{};
+  long long head = 0;
+  int b0 = 0, b1 = 0;
+  if (any) {
+    line = find_line(p, 0, s);
+    head = line.start + (long long)hk * span_of(t);
+    b0 = (int)(head / line.cut), b1 = (int)((head + t.n - 1) / line.cut);
+    any = b0 < b1;
+  }
+  // Every block waits: this grid must not be over before the one it joins.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!any) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float *po = after_wait(p.part_o);
   const float2 *pml = after_wait(p.part_ml);

@@ -1,0 +1,644 @@
+// kv4_many.cu -- attention of many rows a sequence over the 4-bit cache: prompts,
+// drafted tokens of many heads, on the 5th-gen tensor cores.
+//
+// A block takes 256 rows (tokens times query heads of one KV head, which read the
+// same keys) in two tiles of 128, and walks the keys that they see in tiles of 128:
+//
+//   S_i = Q_i . K^T (tcgen05, both operands in shared memory), softmax, and
+//   O_i += P_i . V  (P_i float16 in tensor memory over S_i's columns)
+//
+//   warps 0-3, 4-7   the softmax of tile 0 and 1: a thread owns a row, so maxima
+//                    and sums need no exchange
+//   warps 8-11       turn codes into lo + step c in float16, 128-byte swizzled: a
+//                    thread owns a token of the tile; its next codes are on the way
+//                    while it writes.  Done once for 256 rows.
+//   warp 12          issues the MMAs: the S of one tile runs under the softmax of
+//                    the other
+//
+// The running maximum moves only when a score passes it by 8: weights up to 2^8 are
+// float16 as well as those up to 1, and the outputs in tensor memory need scaling
+// rarely.  Rounded to float16: keys and values (2^-12 of each), weights; queries
+// enter after a power of two per row that brings the largest just under 2^15.
+//
+// The 8 dimensions of a word of codes lie in the order 0 4 1 5 2 6 3 7 (pairs of
+// nibbles i and i + 4 decode together), in Q as in K; the output puts V's back.
+//
+// Where a call has fewer blocks than SMs the keys are cut into parts, whose results
+// a second kernel joins.
+#include <algorithm>
+
+#include "kv4.cuh"
+#include "tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRows = 128;      // rows of a tile
+constexpr int kKeys = 128;      // keys of a tile
+constexpr int kBlockRows = 2 * kRows;
+constexpr int kThreads = 512;
+constexpr int kMinPart = 4;     // key tiles of a part, at least
+constexpr int kSms = 152;
+
+// Registers a thread: 512 x 128 at launch, then by warpgroup; the shares add up to
+// what the block was launched with.
+constexpr int kSoftmaxRegs = 176, kDecodeRegs = 112, kIssueRegs = 48;
+static_assert(2 * kSoftmaxRegs + kDecodeRegs + kIssueRegs == 4 * 128, "the block's registers");
+
+template <int D>
+struct Smem {
+  static constexpr int kQ = kRows * D * 2, kK = kKeys * D * 2;   // one tile of Q; of K or V
+  static constexpr int kBytes = 2 * kQ + 4 * kK + 1024;          // two stages of K and V
+};
+
+struct Bars {
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  uint32_t tmem_base;
+  int abort;
+  uint8_t holes[4][4];   // [tile % 4][decoding warp]: two bits, 16 tokens each without a page
+};
+
+__device__ __forceinline__ bool wait_loop(uint64_t *bar, uint32_t parity, int *abort, int32_t *status,
+                                          unsigned long long limit_ns) {
+  const unsigned long long t0 = globaltimer();
+  for (;;) {
+    if (limit_ns && mbar_try_wait_sleep(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int *>(abort)) return false;
+    if (globaltimer() - t0 >= limit_ns) {
+      atomicExch(abort, 1);
+      atomicExch(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+// One thread's wait (the issuer): a limit of 0 gives up where the phase is not
+// complete when first tested.
+__device__ __forceinline__ bool wait_one(uint64_t *bar, uint32_t parity, int *abort, int32_t *status,
+                                         unsigned long long limit_ns) {
+  return mbar_test_wait(bar, parity) || wait_loop(bar, parity, abort, status, limit_ns);
+}
+// A whole warp's: the lanes vote, for what follows is warp-collective.
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, int *abort, int32_t *status) {
+  const bool ok = mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort, status, kWaitNs);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// K-major operand of 128 rows: as sw128_desc.  MN-major (V: dimensions run along
+// the rows of 128 bytes, tokens are K): 64 dimensions by 8 tokens in 1024 bytes,
+// the next 8 tokens 1024 bytes on (stride), the next 64 dimensions a block of 128
+// tokens on (leading).
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
+  d |= (uint64_t)((kKeys * 128) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ float2 fma_2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add_2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma2_f16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// 64 + c of the codes in bits 4-7 and 20-23.
+__device__ __forceinline__ uint32_t code_pair_hi(uint32_t w) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, 0x00F000F0, 0x54005400, 0xEA;" : "=r"(d) : "r"(w));
+  return d;
+}
+// lo + step c of the 8 codes of w, in the order 0 4 1 5 2 6 3 7: c is exact, and
+// the sum is rounded once.
+__device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t step, uint32_t lo) {
+  const uint32_t w8 = w >> 8;
+  uint4 r;
+  r.x = fma2_f16(hsub2_f16(lop_nib16_lo(w), 0x64006400u), step, lo);
+  r.y = fma2_f16(hsub2_f16(code_pair_hi(w), 0x54005400u), step, lo);
+  r.z = fma2_f16(hsub2_f16(lop_nib16_lo(w8), 0x64006400u), step, lo);
+  r.w = fma2_f16(hsub2_f16(code_pair_hi(w8), 0x54005400u), step, lo);
+  return r;
+}
+template <int R>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// ------------------------------------------------------------------ plan --
+//
+// Sequence s has its tiles of 256 rows at u = floor(q_off[s] G / 256) + s and on:
+// places enough for them all, found without the other sequences' lengths.
+
+__device__ __forceinline__ long long tile_base(const AttendParams &p, int s) {
+  const long long row = p.b.q_off ? clamp_int(__ldg(p.b.q_off + s), 0, p.b.T) : s;
+  return row * p.G / kBlockRows + s;
+}
+
+struct Job {
+  int s, hk, row0;     // first row (token x head of the KV head) of the block
+  int lo, hi;          // key tiles that any of its rows sees
+  int parts;
+  AttendSeq sq;
+};
+
+// The job of place u, found by a whole warp; false: none.
+__device__ __forceinline__ bool find_job(const AttendParams &p, int u, int nsplit, Job &job) {
+  const int lane = threadIdx.x & 31;
+  int base = 0, n = p.b.n_seq + 1;
+  while (n > 32) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const int k = __popc(__ballot_sync(0xffffffffu, i < n && tile_base(p, base + i) <= u));
+    if (k == 0) return false;
+    const int skip = (k - 1) * step;
+    base += skip;
+    n = min(step, n - skip);
+  }
+  job.s = base - 1 + __popc(__ballot_sync(0xffffffffu, lane < n && tile_base(p, base + lane) <= u));
+  if (job.s < 0 || job.s >= p.b.n_seq) return false;
+  job.sq = attend_seq_at(p, job.s);
+  const int rows = job.sq.rows * p.G;
+  const long long first = (u - tile_base(p, job.s)) * kBlockRows;
+  if (rows <= kFewColumns || first >= rows) return false;
+  job.row0 = (int)first;
+  const int last = min(rows, job.row0 + kBlockRows) - 1;
+  const int pos0 = job.sq.len - job.sq.nq + job.row0 / p.G, pos1 = job.sq.len - job.sq.nq + last / p.G;
+  const int end = p.causal ? min(job.sq.len, max(0, pos1 + 1)) : job.sq.len;
+  job.lo = p.window ? max(0, pos0 - p.window + 1) / kKeys : 0;
+  job.hi = max(job.lo, (end + kKeys - 1) / kKeys);
+  job.parts = min(nsplit, max(1, (job.hi - job.lo) / kMinPart));
+  return true;
+}
+
+// Key tiles of a part.
+__device__ __forceinline__ int part_at(const Job &job, int part) {
+  return job.lo + (int)((long long)(job.hi - job.lo) * part / job.parts);
+}
+
+// ---------------------------------------------------------------- kernel --
+
+template <int D, bool kCap>
+__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int nsplit) {
+  constexpr int NG = D / kKvGroup;   // groups of 64 dimensions: 128 bytes of a row of K, V or Q
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars sm;
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Heads of one place are neighbours, the last places (of a prompt: the rows that
+  // see most keys) come first.
+  const int unit = gridDim.x - 1 - blockIdx.x, u = unit / p.b.Hkv, hk = unit - u * p.b.Hkv;
+  Job job;
+  if (!find_job(p, u, nsplit, job) || (int)blockIdx.y >= job.parts) return;
+  const int part = blockIdx.y, t0 = part_at(job, part), n_tiles = part_at(job, part + 1) - t0;
+  const int rows = min(job.sq.rows * p.G - job.row0, kBlockRows);
+  const int tiles = rows > kRows ? 2 : 1;   // tiles of rows
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 4);
+      mbar_init(&sm.k_full[i], 4);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_full[i], 4);
+      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.o_done[i], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&sm.tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  uint8_t *q_s = smem, *k_s = smem + 2 * Smem<D>::kQ, *v_s = k_s + 2 * Smem<D>::kK;
+  const uint32_t o_col = 2 * kKeys;   // S_0, S_1 in columns 0 and 128; then O_0, O_1
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax
+    more_regs<kSoftmaxRegs>();
+    const int i = warp >> 2, r = (warp & 3) * 32 + lane;   // tile, row of the tile
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int row = job.row0 + i * kRows + r;
+    const bool mine = i * kRows + r < rows;
+    const int tok = min(row, job.sq.rows * p.G - 1) / p.G, h = hk * p.G + row - tok * p.G;
+    if (i < tiles) {
+      // The row of Q: scaled, in the codes' order, into the swizzled tile.
+      float cs = fabsf(p.scale) * kLog2e * (kCap ? 2.f / p.softcap : 1.f);
+      if (p.scale == 0.f) cs = 1.f;
+      {
+        uint4 raw[D / 8];
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)(job.sq.t0 + tok) * p.ldq + (size_t)h * D);
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          raw[c] = mine ? src[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+        }
+        const int eb = (int)(top >> 23);
+        const int up = eb == 255 ? 0 : min(15 + 126 - max(eb, 1), 127);
+        float f = __int_as_float((up + 127) << 23);
+        cs = up > 100 ? cs * 7.888609052210118e-31f * __int_as_float((227 - up) << 23)   // 2^-100
+                      : cs * __int_as_float((127 - up) << 23);
+        cs = fmaxf(cs, 1.17549435e-38f);
+        // s = cs (q f) . k with cs > 0: the scale's sign goes to q
+        if (p.scale < 0.f) f = -f;
+        if (p.scale == 0.f) f = 0.f;
+        uint8_t *dst = q_s + i * Smem<D>::kQ + r * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16) * f;
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * f;
+          }
+          const uint4 o = make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1], v[5]), pack_f16(v[2], v[6]),
+                                     pack_f16(v[3], v[7]));
+          *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + (((c & 7) ^ (r & 7)) * 16)) = o;
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full[i]);
+      }
+      // Keys first .. end - 1 are the row's.
+      const int pos = job.sq.len - job.sq.nq + tok;
+      const int end = p.causal ? min(job.sq.len, pos + 1) : job.sq.len;
+      const int first = p.window ? max(0, pos - p.window + 1) : 0;
+      const float cap_log2 = p.softcap * kLog2e;
+      const uint32_t s_col = tmem + lane_base + i * kKeys, o_at = tmem + lane_base + o_col + i * D;
+      float m = kNoScore;
+      float2 l = make_float2(0.f, 0.f);
+      bool ok = true;
+      for (int j = 0; j < n_tiles; ++j) {
+        if (!(ok = wait_all(&sm.s_full[i], j & 1, &sm.abort, p.status))) break;
+        tc_fence_after();
+        float s[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_col + c, s + c);
+        if constexpr (kCap) {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) s[c] = capped(s[c] * cs, cap_log2);
+        }
+        const int k0 = (t0 + j) * kKeys, a = first - k0, b = end - k0;
+        const uint32_t holes = *reinterpret_cast<const volatile uint32_t *>(sm.holes[j & 3]);
+        if (__any_sync(0xffffffffu, a > 0 || b < kKeys) || holes) {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) {
+            const bool see = c >= a && c < b && !(holes >> (c / 32 * 8 + c / 16 % 2) & 1);
+            s[c] = see ? s[c] : -INFINITY;
+          }
+        }
+        float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < kKeys; c += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[c + e]);
+        const float scale = kCap ? 1.f : cs;
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * scale;
+        const bool over = top > m + 8.f;
+        if (__any_sync(0xffffffffu, over)) {
+          const float now = over ? top : m, f = ex2(m - now);
+          m = now;
+          l.x *= f, l.y *= f;
+          if (j > 0) {
+            // The outputs so far: the last tile's MMAs are done first.
+            if (!(ok = wait_all(&sm.o_done[i], (j - 1) & 1, &sm.abort, p.status))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              uint32_t v[16];
+              tmem_ld16(o_at + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * f);
+              tmem_st16(o_at + c, v);
+            }
+          }
+        }
+        const float2 sc = make_float2(scale, scale), nm = make_float2(-m, -m);
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = fma_2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sc, nm);
+            const float2 w = make_float2(ex2(x.x), ex2(x.y));
+            l = add_2(l, w);
+            v[e] = pack_f16(w.x, w.y);
+          }
+          tmem_st16(s_col + c / 2, v);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[i]);
+      }
+      if (ok && n_tiles > 0) ok = wait_all(&sm.o_done[i], (n_tiles - 1) & 1, &sm.abort, p.status);
+      if (ok) {
+        tc_fence_after();
+        const float sum = l.x + l.y;
+        if (job.parts == 1) {
+          const float f = sum != 0.f ? 1.f / sum : 0.f;
+          __nv_bfloat16 *dst = p.out + (size_t)(job.sq.t0 + tok) * p.ldo + (size_t)h * D;
+#pragma unroll
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            if (n_tiles > 0) {
+              tmem_ld16(o_at + c, o);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+              // columns 0 4 1 5 2 6 3 7
+              const uint2 x = pack_out(make_float4(o[e] * f, o[e + 2] * f, o[e + 4] * f, o[e + 6] * f));
+              const uint2 y = pack_out(make_float4(o[e + 1] * f, o[e + 3] * f, o[e + 5] * f, o[e + 7] * f));
+              if (mine) *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(x.x, x.y, y.x, y.y);
+            }
+          }
+        } else {
+          const size_t at = ((size_t)unit * nsplit + part) * kBlockRows + i * kRows + r;
+          float *dst = p.part_o + at * D;
+#pragma unroll
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tmem_ld16(o_at + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+              if (!mine) continue;
+              *reinterpret_cast<float4 *>(dst + c + e) = make_float4(o[e], o[e + 2], o[e + 4], o[e + 6]);
+              *reinterpret_cast<float4 *>(dst + c + e + 4) = make_float4(o[e + 1], o[e + 3], o[e + 5], o[e + 7]);
+            }
+          }
+          if (mine) p.part_ml[at] = make_float2(m, sum);
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // -------------------------------------------------------------- decode
+    fewer_regs<kDecodeRegs>();
+    const int r = threadIdx.x - 256, lp = p.b.log_page;   // token of the tile
+    const uint8_t *head = p.cache + (size_t)hk * KvBlock<D>::bytes(lp);
+    const size_t page_bytes = KvBlock<D>::bytes(lp) * p.b.Hkv;
+    struct Codes {
+      uint4 c[2][D / 32];
+      uint32_t sc[2][NG];
+    };
+    // A token's codes and scales; zeros where it has no page or is past the end.
+    // Returns whether it is in a hole.
+    auto load = [&](int j, Codes &x) {
+      const int token = (t0 + j) * kKeys + r;
+      const bool in = j < n_tiles && token < job.sq.len;
+      const int page = in ? kv_page_at(p.b, job.s, token) : -1;
+      if (page < 0) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) x.c[w][c] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) x.sc[w][g] = 0;
+        }
+      } else {
+        const int slot = token & ((1 << lp) - 1);
+        const uint8_t *blk = head + (size_t)page * page_bytes;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint4 *c = reinterpret_cast<const uint4 *>(blk + KvBlock<D>::codes(lp, w, slot));
+          const uint32_t *s = reinterpret_cast<const uint32_t *>(blk + KvBlock<D>::scales(lp, w, slot));
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) x.c[w][e] = __ldg(c + e);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) x.sc[w][g] = __ldg(s + g);
+        }
+      }
+      return in && page < 0;
+    };
+    auto write = [&](uint8_t *dst, const uint4 (&c)[D / 32], const uint32_t (&sc)[NG]) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t step = __byte_perm(sc[g], 0, 0x1010), lo = __byte_perm(sc[g], 0, 0x3232);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint4 q = c[g * 2 + e / 4];
+          const uint32_t w = e % 4 == 0 ? q.x : e % 4 == 1 ? q.y : e % 4 == 2 ? q.z : q.w;
+          *reinterpret_cast<uint4 *>(dst + g * (kKeys * 128) + r * 128 + ((e ^ (r & 7)) * 16)) = decode_word(w, step, lo);
+        }
+      }
+    };
+    if (p.wait_ns == 0) {   // a limit of 0 is there to show the way out: the first operands come late
+      const unsigned long long start = globaltimer();
+      while (globaltimer() - start < 20000ull) {
+      }
+    }
+    Codes x;
+    bool hole = load(0, x);
+    for (int j = 0; j < n_tiles; ++j) {
+      const int st = j & 1;
+      // A token whose V holds a NaN: its K becomes NaN, its V zeros, so that only the
+      // rows that see it know.
+      bool bad = false;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) bad |= (x.sc[1][g] & 0x7FFFu) > 0x7C00u;
+      if (bad) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) x.sc[0][g] = 0x7FFF7FFFu, x.sc[1][g] = 0u;
+      }
+      const uint32_t gone = __ballot_sync(0xffffffffu, hole);
+      if (!wait_all(&sm.k_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
+      if (lane == 0) sm.holes[j & 3][warp - 8] = (gone & 0xFFFFu ? 1 : 0) | (gone >> 16 ? 2 : 0);
+      write(k_s + st * Smem<D>::kK, x.c[0], x.sc[0]);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[st]);
+      if (!wait_all(&sm.v_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
+      write(v_s + st * Smem<D>::kK, x.c[1], x.sc[1]);
+      hole = load(j + 1, x);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[st]);
+    }
+  } else {
+    // --------------------------------------------------------------- issue
+    fewer_regs<kIssueRegs>();
+    if (warp == 12 && elect_one()) {
+      const uint32_t id_s = idesc_f16(kRows, kKeys), id_o = idesc_f16(kRows, D) | 1u << 16;   // B transposed
+      const uint64_t dq = sw128_desc(smem_u32(q_s)), dk = sw128_desc(smem_u32(k_s)), dv = v_desc(smem_u32(v_s));
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return ok = ok && wait_one(bar, parity, &sm.abort, p.status, p.wait_ns);
+      };
+      auto scores = [&](int i, int st) {
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * ((kRows * 128) >> 4) + (kk & 3) * 2;
+          mma_ss(tmem + i * kKeys, dq + i * (Smem<D>::kQ >> 4) + off, dk + st * (Smem<D>::kK >> 4) + off, id_s, kk > 0);
+        }
+        mma_commit(&sm.s_full[i]);
+      };
+      if (n_tiles > 0) {
+        wait(&sm.k_full[0], 0);
+        for (int i = 0; ok && i < tiles; ++i)
+          if (wait(&sm.q_full[i], 0)) scores(i, 0);
+        if (ok) mma_commit(&sm.k_empty[0]);
+      }
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        const int st = j & 1, nx = st ^ 1;
+        if (j + 1 < n_tiles) wait(&sm.k_full[nx], ((j + 1) >> 1) & 1);
+        wait(&sm.v_full[st], (j >> 1) & 1);
+        for (int i = 0; ok && i < tiles; ++i) {
+          if (!wait(&sm.p_full[i], j & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ts(tmem + o_col + i * D, tmem + i * kKeys + kk * 8, dv + st * (Smem<D>::kK >> 4) + kk * (2048 >> 4), id_o,
+                   j > 0 || kk > 0);
+          mma_commit(&sm.o_done[i]);
+          if (j + 1 < n_tiles) scores(i, nx);
+        }
+        if (!ok) break;
+        mma_commit(&sm.v_empty[st]);
+        if (j + 1 < n_tiles) mma_commit(&sm.k_empty[nx]);
+      }
+      // One more commit covers every MMA issued; tensor memory is freed after it.
+      mma_commit(&sm.drain);
+      drain_bar(&sm.drain, 0, globaltimer());
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// Joins the parts of four rows of a block, a warp each.
+template <int D>
+__global__ void __launch_bounds__(128) kv4_many_join_kernel(const AttendParams p, int nsplit) {
+  const int unit = blockIdx.x, u = unit / p.b.Hkv, hk = unit - u * p.b.Hkv;
+  Job job;
+  const bool any = find_job(p, u, nsplit, job) && job.parts > 1;
+  // Every block waits: this grid must not be over before the one it joins.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (!any || job.row0 + r >= job.sq.rows * p.G) return;
+  const int row = job.row0 + r;
+  const float *po = after_wait(p.part_o);
+  const float2 *pml = after_wait(p.part_ml);
+  const size_t first = (size_t)unit * nsplit * kBlockRows + r;
+  float top = kNoScore;
+  for (int i = lane; i < job.parts; i += 32) top = fmaxf(top, __ldcg(pml + first + (size_t)i * kBlockRows).x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float sum = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < job.parts; ++i) {
+    const size_t at = first + (size_t)i * kBlockRows;
+    const float2 ml = __ldcg(pml + at);
+    const float f = ex2(ml.x - top);
+    sum += ml.y * f;
+    if (lane < D / 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + at * D) + lane);
+      y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
+    }
+  }
+  if (lane >= D / 4) return;
+  const float f = sum != 0.f ? 1.f / sum : 0.f;
+  const int tok = row / p.G, h = hk * p.G + row - tok * p.G;
+  *reinterpret_cast<uint2 *>(p.out + (size_t)(job.sq.t0 + tok) * p.ldo + (size_t)h * D + lane * 4) =
+      pack_out(make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+}
+
+// Places of all sequences' tiles of rows, and the parts that keys may be cut into.
+long long places(const AttendParams &p) {
+  const long long rows = (p.b.q_off ? (long long)p.b.T : p.b.n_seq) * p.G;
+  return rows / kBlockRows + p.b.n_seq;
+}
+int split_of(const AttendParams &p) {
+  const long long keys = (long long)p.b.max_pages << p.b.log_page;
+  const long long most = std::max<long long>(1, (keys + kKeys - 1) / kKeys / kMinPart);
+  return (int)std::max<long long>(1, std::min<long long>(kSms / (places(p) * p.b.Hkv), most));
+}
+
+template <int D, bool kCap>
+cudaError_t launch(const AttendParams &p, cudaStream_t st) {
+  auto kernel = kv4_many_kernel<D, kCap>;
+  static DeviceOnce once;
+  cudaError_t err = once.run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  });
+  if (err != cudaSuccess) return err;
+  const int nsplit = split_of(p);
+  const unsigned units = (unsigned)(places(p) * p.b.Hkv);
+  err = launch_k(false, kernel, dim3(units, nsplit), dim3(kThreads), Smem<D>::kBytes, st, p, nsplit);
+  if (err != cudaSuccess || nsplit == 1) return err;
+  return launch_k(true, kv4_many_join_kernel<D>, dim3(units, kBlockRows / 4), dim3(128), 0, st, p, nsplit);
+}
+
+}  // namespace
+
+// Partial results of a call, in rows of D and of (maximum, sum).
+size_t many_rows(const AttendParams &p) {
+  const int nsplit = split_of(p);
+  return nsplit == 1 ? 0 : (size_t)places(p) * p.b.Hkv * nsplit * kBlockRows;
+}
+
+cudaError_t launch_many(const AttendParams &p, int D, cudaStream_t st) {
+  if (D == 64) return p.softcap > 0.f ? launch<64, true>(p, st) : launch<64, false>(p, st);
+  return p.softcap > 0.f ? launch<128, true>(p, st) : launch<128, false>(p, st);
+}
+
+}  // namespace moe

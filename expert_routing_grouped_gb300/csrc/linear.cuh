@@ -38,6 +38,10 @@ struct LinearParams {
 
 // linear_tc.cu: more than kFewTokens tokens.
 constexpr int kFewTokens = 16;
+// The wait limit of what this host thread launches (moe_linear_wait_limit), and the
+// current device's word for kernels without a status word (moe_linear_status).
+unsigned long long linear_wait_ns();
+cudaError_t linear_gave_up(int32_t **word);
 cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st);
 
 // sx sw acc + bias, the pre-activation of row n of w.

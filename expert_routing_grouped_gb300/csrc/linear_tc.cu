@@ -794,6 +794,22 @@ cudaError_t launch_type(const TcLinear &q, const Plan &plan, bool segs, int sms,
 
 }  // namespace
 
+unsigned long long linear_wait_ns() { return wait_limit_ns; }
+
+cudaError_t linear_gave_up(int32_t **word) {
+  static std::atomic<int32_t *> known[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 64 && (*word = known[dev].load(std::memory_order_acquire))) return cudaSuccess;
+  void *at = nullptr;
+  err = cudaGetSymbolAddress(&at, gave_up);
+  if (err != cudaSuccess) return err;
+  *word = static_cast<int32_t *>(at);
+  if (dev < 64) known[dev].store(*word, std::memory_order_release);
+  return cudaSuccess;
+}
+
 cudaError_t launch_linear_tc(const LinearParams &p, int dtype, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
