@@ -48,7 +48,7 @@ static_assert(2 * kSoftmaxRegs + kDecodeRegs + kIssueRegs == 4 * 128, "the block
 template <int D>
 struct Smem {
   static constexpr int kQ = kRows * D * 2, kK = kKeys * D * 2;   // one tile of Q; of K or V
-  static constexpr int kBytes = 2 * kQ + 4 * kK + 1024;          // two stages of K and V
+  static constexpr int kBytes = 2 * kQ + 4 * kK + 1024;          // two stages of K and V; room to align
 };
 
 struct Bars {
@@ -97,19 +97,39 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
   d |= (uint64_t)2 << 61;
   return d;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMAs take the descriptors' lower words and constants to add to them: left to
+// itself the compiler keeps the sums of all MMAs in registers, more than there are.
+template <uint32_t A, uint32_t B>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 u, v;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "add.u32 x, %1, %7;\n\tadd.u32 y, %3, %8;\n\tmov.b64 u, {x, %2};\n\tmov.b64 v, {y, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(acc), "n"(A), "n"(B)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+template <uint32_t B>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 v;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "add.u32 y, %2, %6;\n\tmov.b64 v, {y, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], v, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(acc), "n"(B)
       : "memory");
+}
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+// f(Int<0>) .. f(Int<N - 1>).
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    each<N, I + 1>(f);
+  }
 }
 
 __device__ __forceinline__ float2 fma_2(float2 a, float2 b, float2 c) {
@@ -217,10 +237,8 @@ __device__ __forceinline__ int part_at(const Job &job, int part) {
 template <int D, bool kCap>
 __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int nsplit) {
   constexpr int NG = D / kKvGroup;   // groups of 64 dimensions: 128 bytes of a row of K, V or Q
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Bars sm;
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // Heads of one place are neighbours, the last places (of a prompt: the rows that
@@ -256,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  constexpr uint32_t tmem = 0;   // all 512 columns are this block's
   uint8_t *q_s = smem, *k_s = smem + 2 * Smem<D>::kQ, *v_s = k_s + 2 * Smem<D>::kK;
   const uint32_t o_col = 2 * kKeys;   // S_0, S_1 in columns 0 and 128; then O_0, O_1
 
@@ -511,44 +529,65 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
     // --------------------------------------------------------------- issue
     fewer_regs<kIssueRegs>();
     if (warp == 12 && elect_one()) {
+      // Everything that differs between the MMAs of two key tiles is a constant: they
+      // take 64 clocks each, and an issue of many instructions in between, beside three
+      // busy warps of the scheduler, took longer than that.
       const uint32_t id_s = idesc_f16(kRows, kKeys), id_o = idesc_f16(kRows, D) | 1u << 16;   // B transposed
       const uint64_t dq = sw128_desc(smem_u32(q_s)), dk = sw128_desc(smem_u32(k_s)), dv = v_desc(smem_u32(v_s));
+      const uint32_t q0 = (uint32_t)dq, k0 = (uint32_t)dk, v0 = (uint32_t)dv;
+      const uint32_t kmajor = (uint32_t)(dq >> 32), mnmajor = (uint32_t)(dv >> 32);
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         return ok = ok && wait_one(bar, parity, &sm.abort, p.status, p.wait_ns);
       };
-      auto scores = [&](int i, int st) {
+      auto scores = [&](auto i_, auto st_) {
+        constexpr int i = decltype(i_)::value, st = decltype(st_)::value;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * ((kRows * 128) >> 4) + (kk & 3) * 2;
-          mma_ss(tmem + i * kKeys, dq + i * (Smem<D>::kQ >> 4) + off, dk + st * (Smem<D>::kK >> 4) + off, id_s, kk > 0);
-        }
+        each<D / 16>([&](auto k_) {
+          constexpr int kk = decltype(k_)::value;
+          constexpr uint32_t off = (kk / 4) * ((kRows * 128) >> 4) + (kk & 3) * 2;
+          mma_ss<i * (Smem<D>::kQ >> 4) + off, st * (Smem<D>::kK >> 4) + off>(i * kKeys, q0, kmajor, k0, kmajor, id_s,
+                                                                              kk > 0);
+        });
         mma_commit(&sm.s_full[i]);
       };
-      if (n_tiles > 0) {
-        wait(&sm.k_full[0], 0);
-        for (int i = 0; ok && i < tiles; ++i)
-          if (wait(&sm.q_full[i], 0)) scores(i, 0);
+      auto outputs = [&](auto i_, auto st_, int j) {
+        constexpr int i = decltype(i_)::value, st = decltype(st_)::value;
+        tc_fence_after();
+        each<kKeys / 16>([&](auto k_) {
+          constexpr int kk = decltype(k_)::value;
+          mma_ts<st * (Smem<D>::kK >> 4) + kk * (2048 >> 4)>(2 * kKeys + i * D, i * kKeys + kk * 8, v0, mnmajor, id_o,
+                                                             kk > 0 ? 1u : (uint32_t)(j > 0));
+        });
+        mma_commit(&sm.o_done[i]);
+      };
+      constexpr Int<0> c0{};
+      constexpr Int<1> c1{};
+      // Key tile j, in stage st, and the scores of the next.
+      auto key_tile = [&](int j, auto st_, auto nx_) {
+        constexpr int st = decltype(st_)::value, nx = decltype(nx_)::value;
+        const bool more = j + 1 < n_tiles;
+        if (more) wait(&sm.k_full[nx], ((j + 1) >> 1) & 1);
+        wait(&sm.v_full[st], (j >> 1) & 1);
+        if (!wait(&sm.p_full[0], j & 1)) return;
+        outputs(c0, st_, j);
+        if (more) scores(c0, nx_);
+        if (tiles > 1) {
+          if (!wait(&sm.p_full[1], j & 1)) return;
+          outputs(c1, st_, j);
+          if (more) scores(c1, nx_);
+        }
+        mma_commit(&sm.v_empty[st]);
+        if (more) mma_commit(&sm.k_empty[nx]);
+      };
+      if (n_tiles > 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[0], 0)) {
+        scores(c0, c0);
+        if (tiles > 1 && wait(&sm.q_full[1], 0)) scores(c1, c0);
         if (ok) mma_commit(&sm.k_empty[0]);
       }
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        const int st = j & 1, nx = st ^ 1;
-        if (j + 1 < n_tiles) wait(&sm.k_full[nx], ((j + 1) >> 1) & 1);
-        wait(&sm.v_full[st], (j >> 1) & 1);
-        for (int i = 0; ok && i < tiles; ++i) {
-          if (!wait(&sm.p_full[i], j & 1)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tmem + o_col + i * D, tmem + i * kKeys + kk * 8, dv + st * (Smem<D>::kK >> 4) + kk * (2048 >> 4), id_o,
-                   j > 0 || kk > 0);
-          mma_commit(&sm.o_done[i]);
-          if (j + 1 < n_tiles) scores(i, nx);
-        }
-        if (!ok) break;
-        mma_commit(&sm.v_empty[st]);
-        if (j + 1 < n_tiles) mma_commit(&sm.k_empty[nx]);
+      for (int j = 0; ok && j < n_tiles; j += 2) {
+        key_tile(j, c0, c1);
+        if (ok && j + 1 < n_tiles) key_tile(j + 1, c1, c0);
       }
       // One more commit covers every MMA issued; tensor memory is freed after it.
       mma_commit(&sm.drain);
@@ -560,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
   __syncthreads();
   if (warp == 12) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem_base) : "memory");
   }
 }
 
