@@ -236,7 +236,6 @@ __device__ __forceinline__ int part_at(const Job &job, int part) {
 
 template <int D, bool kCap>
 __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int nsplit) {
-  constexpr int NG = D / kKvGroup;   // groups of 64 dimensions: 128 bytes of a row of K, V or Q
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Bars sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -445,52 +444,61 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
   } else if (warp < 12) {
     // -------------------------------------------------------------- decode
     fewer_regs<kDecodeRegs>();
-    const int r = threadIdx.x - 256, lp = p.b.log_page;   // token of the tile
+    // A warp has 32 tokens of the tile, in rounds of 512 neighbouring bytes of codes: a
+    // lane has 16 of them, 32 dimensions of one token.
+    constexpr int kPieces = D / 32, kPer = 32 / kPieces, kRounds = 32 / kPer;   // tokens of a round: 8 (D = 64: 16)
+    const int lp = p.b.log_page, w0 = (warp - 8) * 32, tk = lane / kPieces, pc = lane % kPieces, g = pc / 2;
     const uint8_t *head = p.cache + (size_t)hk * KvBlock<D>::bytes(lp);
     const size_t page_bytes = KvBlock<D>::bytes(lp) * p.b.Hkv;
     struct Codes {
-      uint4 c[2][D / 32];
-      uint32_t sc[2][NG];
+      uint4 c[kRounds];
+      uint32_t sc[kRounds];
     };
-    // A token's codes and scales; zeros where it has no page or is past the end.
-    // Returns whether it is in a hole.
-    auto load = [&](int j, Codes &x) {
-      const int token = (t0 + j) * kKeys + r;
-      const bool in = j < n_tiles && token < job.sq.len;
-      const int page = in ? kv_page_at(p.b, job.s, token) : -1;
-      if (page < 0) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) x.c[w][c] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) x.sc[w][g] = 0;
-        }
-      } else {
-        const int slot = token & ((1 << lp) - 1);
-        const uint8_t *blk = head + (size_t)page * page_bytes;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint4 *c = reinterpret_cast<const uint4 *>(blk + KvBlock<D>::codes(lp, w, slot));
-          const uint32_t *s = reinterpret_cast<const uint32_t *>(blk + KvBlock<D>::scales(lp, w, slot));
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) x.c[w][e] = __ldg(c + e);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) x.sc[w][g] = __ldg(s + g);
+    // Pages of the warp's first and last 16 tokens of tile j; -1: past the end, -2: a hole.
+    auto pages_of = [&](int j) {
+      int2 r = make_int2(-1, -1);
+      const int token = (t0 + j) * kKeys + w0;
+      if (j >= n_tiles || token >= job.sq.len) return r;
+      r.x = kv_page_at(p.b, job.s, token);
+      r.x = r.x < 0 ? -2 : r.x;
+      if (token + 16 < job.sq.len) {
+        r.y = r.x;
+        if (lp == 4) {
+          r.y = kv_page_at(p.b, job.s, token + 16);
+          r.y = r.y < 0 ? -2 : r.y;
         }
       }
-      return in && page < 0;
+      return r;
     };
-    auto write = [&](uint8_t *dst, const uint4 (&c)[D / 32], const uint32_t (&sc)[NG]) {
+    // Codes and scales of K (which 0) or V; zeros where there is no page or no token.
+    auto load = [&](int j, int2 page, int which, Codes &x) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t step = __byte_perm(sc[g], 0, 0x1010), lo = __byte_perm(sc[g], 0, 0x3232);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 q = c[g * 2 + e / 4];
-          const uint32_t w = e % 4 == 0 ? q.x : e % 4 == 1 ? q.y : e % 4 == 2 ? q.z : q.w;
-          *reinterpret_cast<uint4 *>(dst + g * (kKeys * 128) + r * 128 + ((e ^ (r & 7)) * 16)) = decode_word(w, step, lo);
+      for (int c = 0; c < kRounds; ++c) {
+        const int id = c * kPer < 16 ? page.x : page.y, t = c * kPer + tk, token = (t0 + j) * kKeys + w0 + t;
+        x.c[c] = make_uint4(0, 0, 0, 0);
+        x.sc[c] = 0;
+        if (id >= 0 && token < job.sq.len) {
+          const int slot = token & ((1 << lp) - 1);
+          const uint8_t *blk = head + (size_t)id * page_bytes;
+          x.c[c] = __ldg(reinterpret_cast<const uint4 *>(blk + KvBlock<D>::codes(lp, which, slot)) + pc);
+          x.sc[c] = __ldg(reinterpret_cast<const uint32_t *>(blk + KvBlock<D>::scales(lp, which, slot)) + g);
         }
+      }
+    };
+    // 64 bytes of a row of 128, by 16-byte pieces exchanged as the swizzle has it; lanes
+    // of the second 64 dimensions take their words in another order, so that a store
+    // meets itself in no bank.
+    auto write = [&](uint8_t *dst, const Codes &x) {
+#pragma unroll
+      for (int c = 0; c < kRounds; ++c) {
+        const int row = w0 + c * kPer + tk;
+        const uint32_t step = __byte_perm(x.sc[c], 0, 0x1010), lo = __byte_perm(x.sc[c], 0, 0x3232);
+        const uint4 q = g ? make_uint4(x.c[c].z, x.c[c].w, x.c[c].x, x.c[c].y) : x.c[c];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint8_t *to = dst + g * (kKeys * 128) + row * 128;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4 *>(to + ((((pc & 1) * 4 + (e ^ (2 * g))) ^ (row & 7)) * 16)) = decode_word(w[e], step, lo);
       }
     };
     if (p.wait_ns == 0) {   // a limit of 0 is there to show the way out: the first operands come late
@@ -498,29 +506,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       while (globaltimer() - start < 20000ull) {
       }
     }
-    Codes x;
-    bool hole = load(0, x);
+    Codes k, v;
+    int2 page = pages_of(0), next = pages_of(1);
+    load(0, page, 0, k);
+    load(0, page, 1, v);
     for (int j = 0; j < n_tiles; ++j) {
       const int st = j & 1;
       // A token whose V holds a NaN: its K becomes NaN, its V zeros, so that only the
       // rows that see it know.
-      bool bad = false;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) bad |= (x.sc[1][g] & 0x7FFFu) > 0x7C00u;
-      if (bad) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) x.sc[0][g] = 0x7FFF7FFFu, x.sc[1][g] = 0u;
+      for (int c = 0; c < kRounds; ++c) {
+        const uint32_t other = D == 128 ? __shfl_xor_sync(0xffffffffu, v.sc[c], 2) : v.sc[c];
+        if ((v.sc[c] & 0x7FFFu) > 0x7C00u || (other & 0x7FFFu) > 0x7C00u) k.sc[c] = 0x7FFF7FFFu, v.sc[c] = 0u;
       }
-      const uint32_t gone = __ballot_sync(0xffffffffu, hole);
       if (!wait_all(&sm.k_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
-      if (lane == 0) sm.holes[j & 3][warp - 8] = (gone & 0xFFFFu ? 1 : 0) | (gone >> 16 ? 2 : 0);
-      write(k_s + st * Smem<D>::kK, x.c[0], x.sc[0]);
+      if (lane == 0) sm.holes[j & 3][warp - 8] = (page.x == -2 ? 1 : 0) | (page.y == -2 ? 2 : 0);
+      write(k_s + st * Smem<D>::kK, k);
+      load(j + 1, next, 0, k);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[st]);
       if (!wait_all(&sm.v_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
-      write(v_s + st * Smem<D>::kK, x.c[1], x.sc[1]);
-      hole = load(j + 1, x);
+      write(v_s + st * Smem<D>::kK, v);
+      load(j + 1, next, 1, v);
+      page = next;
+      next = pages_of(j + 2);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[st]);
