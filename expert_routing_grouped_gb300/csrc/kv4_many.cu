@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kRows = 128;      // rows of a tile
 constexpr int kKeys = 128;      // keys of a tile
+constexpr int kSub = 64;        // keys of a softmax step
 constexpr int kBlockRows = 2 * kRows;
 constexpr int kThreads = 512;
 constexpr int kMinPart = 4;     // key tiles of a part, at least
@@ -43,7 +44,9 @@ constexpr int kSms = 152;
 // Registers a thread: 512 x 128 at launch, then by warpgroup; the shares add up to
 // what the block was launched with.
 constexpr int kSoftmaxRegs = 176, kDecodeRegs = 112, kIssueRegs = 48;
-static_assert(2 * kSoftmaxRegs + kDecodeRegs + kIssueRegs == 4 * 128, "the block's registers");
+static_assert(2 * kSoftmaxRegs + kDecodeRegs + kIssueRegs == 4 * 128 && kSoftmaxRegs >= 128 && kDecodeRegs <= 128 &&
+                  kIssueRegs <= 128,
+              "the block's registers; inc only up, dec only down");
 
 template <int D>
 struct Smem {
@@ -53,7 +56,8 @@ struct Smem {
 
 struct Bars {
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];   // [tile of rows][step % 2]
+  uint64_t drain;
   uint32_t tmem_base;
   int abort;
   uint8_t holes[4][4];   // [tile % 4][decoding warp]: two bits, 16 tokens each without a page
@@ -177,6 +181,36 @@ __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t step, uint32_t
   r.w = fma2_f16(hsub2_f16(code_pair_hi(w8), 0x54005400u), step, lo);
   return r;
 }
+// 32 lanes x 64 consecutive columns: both loads on the way at once, and their wait, in
+// one statement (as tmem_ld32).
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float *v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,"
+      "%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
+        "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
+        "=r"(r[63])
+      : "r"(taddr), "r"(taddr + 32)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <int R>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -194,7 +228,7 @@ __device__ __forceinline__ long long tile_base(const AttendParams &p, int s) {
 
 struct Job {
   int s, hk, row0;     // first row (token x head of the KV head) of the block
-  int lo, hi;          // key tiles that any of its rows sees
+  int lo, hi, end;     // key tiles that any of its rows sees; the last key's successor
   int parts;
   AttendSeq sq;
 };
@@ -221,6 +255,7 @@ __device__ __forceinline__ bool find_job(const AttendParams &p, int u, int nspli
   const int last = min(rows, job.row0 + kBlockRows) - 1;
   const int pos0 = job.sq.len - job.sq.nq + job.row0 / p.G, pos1 = job.sq.len - job.sq.nq + last / p.G;
   const int end = p.causal ? min(job.sq.len, max(0, pos1 + 1)) : job.sq.len;
+  job.end = end;
   job.lo = p.window ? max(0, pos0 - p.window + 1) / kKeys : 0;
   job.hi = max(job.lo, (end + kKeys - 1) / kKeys);
   job.parts = min(nsplit, max(1, (job.hi - job.lo) / kMinPart));
@@ -246,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
   Job job;
   if (!find_job(p, u, nsplit, job) || (int)blockIdx.y >= job.parts) return;
   const int part = blockIdx.y, t0 = part_at(job, part), n_tiles = part_at(job, part + 1) - t0;
+  const int n_sub = min(n_tiles * 2, max(0, (job.end - t0 * kKeys + kSub - 1) / kSub));   // steps
   const int rows = min(job.sq.rows * p.G - job.row0, kBlockRows);
   const int tiles = rows > kRows ? 2 : 1;   // tiles of rows
 
@@ -256,9 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], 4);
       mbar_init(&sm.v_empty[i], 1);
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
-      mbar_init(&sm.o_done[i], 1);
+      mbar_init(&sm.s_full[i][0], 1);
+      mbar_init(&sm.s_full[i][1], 1);
+      mbar_init(&sm.p_full[i][0], 4);
+      mbar_init(&sm.p_full[i][1], 4);
+      mbar_init(&sm.o_done[i][0], 1);
+      mbar_init(&sm.o_done[i][1], 1);
     }
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -333,33 +372,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       const int first = p.window ? max(0, pos - p.window + 1) : 0;
       const float cap_log2 = p.softcap * kLog2e;
       const uint32_t s_col = tmem + lane_base + i * kKeys, o_at = tmem + lane_base + o_col + i * D;
+      // Steps free_lo .. free_hi - 1 of the part hide nothing from this warp's rows.
+      const int free_lo = (__reduce_max_sync(0xffffffffu, first) + kSub - 1) / kSub - 2 * t0;
+      const int free_hi = __reduce_min_sync(0xffffffffu, end) / kSub - 2 * t0;
       float m = kNoScore;
       float2 l = make_float2(0.f, 0.f);
       bool ok = true;
-      for (int j = 0; j < n_tiles; ++j) {
-        if (!(ok = wait_all(&sm.s_full[i], j & 1, &sm.abort, p.status))) break;
+      for (int t = 0; t < n_sub; ++t) {
+        const int h = t & 1;
+        if (!(ok = wait_all(&sm.s_full[i][h], (t >> 1) & 1, &sm.abort, p.status))) break;
         tc_fence_after();
-        float s[kKeys];
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_col + c, s + c);
+        const uint32_t at = s_col + h * kSub;
+        float s[kSub];
+        tmem_ld64(at, s);
         if constexpr (kCap) {
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) s[c] = capped(s[c] * cs, cap_log2);
+          for (int c = 0; c < kSub; ++c) s[c] = capped(s[c] * cs, cap_log2);
         }
-        const int k0 = (t0 + j) * kKeys, a = first - k0, b = end - k0;
-        const uint32_t holes = *reinterpret_cast<const volatile uint32_t *>(sm.holes[j & 3]);
-        if (__any_sync(0xffffffffu, a > 0 || b < kKeys) || holes) {
+        const uint32_t holes = *reinterpret_cast<const volatile uint16_t *>(&sm.holes[(t >> 1) & 3][2 * h]);
+        if (t < free_lo || t >= free_hi || holes) {
+          const int k0 = t0 * kKeys + t * kSub, a = first - k0, b = end - k0;
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) {
+          for (int c = 0; c < kSub; ++c) {
             const bool see = c >= a && c < b && !(holes >> (c / 32 * 8 + c / 16 % 2) & 1);
             s[c] = see ? s[c] : -INFINITY;
           }
         }
         float t4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int c = 4; c < kKeys; c += 4)
+        for (int c = 4; c + 4 < kSub; c += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[c + e]);
+          for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[c + e], s[c + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kSub - 4 + e]);
         const float scale = kCap ? 1.f : cs;
         const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * scale;
         const bool over = top > m + 8.f;
@@ -367,9 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
           const float now = over ? top : m, f = ex2(m - now);
           m = now;
           l.x *= f, l.y *= f;
-          if (j > 0) {
-            // The outputs so far: the last tile's MMAs are done first.
-            if (!(ok = wait_all(&sm.o_done[i], (j - 1) & 1, &sm.abort, p.status))) break;
+          if (t > 0) {
+            // The outputs so far: the last step's MMAs are done first.  (Step t - 3's are:
+            // these scores came after step t - 2's.)
+            if (!(ok = wait_all(&sm.o_done[i][h ^ 1], ((t - 1) >> 1) & 1, &sm.abort, p.status))) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
@@ -383,23 +429,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
           }
         }
         const float2 sc = make_float2(scale, scale), nm = make_float2(-m, -m);
+        uint32_t v[kSub / 2];
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 32) {
-          uint32_t v[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = fma_2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sc, nm);
-            const float2 w = make_float2(ex2(x.x), ex2(x.y));
-            l = add_2(l, w);
-            v[e] = pack_f16(w.x, w.y);
-          }
-          tmem_st16(s_col + c / 2, v);
+        for (int e = 0; e < kSub / 2; ++e) {
+          const float2 x = fma_2(make_float2(s[2 * e], s[2 * e + 1]), sc, nm);
+          const float2 w = make_float2(ex2(x.x), ex2(x.y));
+          l = add_2(l, w);
+          v[e] = pack_f16(w.x, w.y);
         }
+        tmem_st32(at, v);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[i]);
+        if (lane == 0) mbar_arrive(&sm.p_full[i][h]);
       }
-      if (ok && n_tiles > 0) ok = wait_all(&sm.o_done[i], (n_tiles - 1) & 1, &sm.abort, p.status);
+      if (ok && n_sub > 0) ok = wait_all(&sm.o_done[i][(n_sub - 1) & 1], ((n_sub - 1) >> 1) & 1, &sm.abort, p.status);
       if (ok) {
         tc_fence_after();
         const float sum = l.x + l.y;
@@ -409,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
 #pragma unroll
           for (int c = 0; c < D; c += 16) {
             float o[16];
-            if (n_tiles > 0) {
+            if (n_sub > 0) {
               tmem_ld16(o_at + c, o);
             } else {
 #pragma unroll
@@ -542,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       // Everything that differs between the MMAs of two key tiles is a constant: they
       // take 64 clocks each, and an issue of many instructions in between, beside three
       // busy warps of the scheduler, took longer than that.
-      const uint32_t id_s = idesc_f16(kRows, kKeys), id_o = idesc_f16(kRows, D) | 1u << 16;   // B transposed
+      const uint32_t id_s = idesc_f16(kRows, kSub), id_o = idesc_f16(kRows, D) | 1u << 16;   // B transposed
       const uint64_t dq = sw128_desc(smem_u32(q_s)), dk = sw128_desc(smem_u32(k_s)), dv = v_desc(smem_u32(v_s));
       const uint32_t q0 = (uint32_t)dq, k0 = (uint32_t)dk, v0 = (uint32_t)dv;
       const uint32_t kmajor = (uint32_t)(dq >> 32), mnmajor = (uint32_t)(dv >> 32);
@@ -550,54 +593,70 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         return ok = ok && wait_one(bar, parity, &sm.abort, p.status, p.wait_ns);
       };
-      auto scores = [&](auto i_, auto st_) {
-        constexpr int i = decltype(i_)::value, st = decltype(st_)::value;
-        tc_fence_after();
+      // Scores of tile i against half h of the keys of stage st.
+      auto scores = [&](auto i_, auto st_, auto h_) {
+        constexpr int i = decltype(i_)::value, st = decltype(st_)::value, h = decltype(h_)::value;
         each<D / 16>([&](auto k_) {
           constexpr int kk = decltype(k_)::value;
           constexpr uint32_t off = (kk / 4) * ((kRows * 128) >> 4) + (kk & 3) * 2;
-          mma_ss<i * (Smem<D>::kQ >> 4) + off, st * (Smem<D>::kK >> 4) + off>(i * kKeys, q0, kmajor, k0, kmajor, id_s,
-                                                                              kk > 0);
+          mma_ss<i * (Smem<D>::kQ >> 4) + off, st * (Smem<D>::kK >> 4) + h * ((kSub * 128) >> 4) + off>(
+              i * kKeys + h * kSub, q0, kmajor, k0, kmajor, id_s, kk > 0);
         });
-        mma_commit(&sm.s_full[i]);
+        mma_commit(&sm.s_full[i][h]);
       };
-      auto outputs = [&](auto i_, auto st_, int j) {
-        constexpr int i = decltype(i_)::value, st = decltype(st_)::value;
-        tc_fence_after();
-        each<kKeys / 16>([&](auto k_) {
+      auto outputs = [&](auto i_, auto st_, auto h_, int t) {
+        constexpr int i = decltype(i_)::value, st = decltype(st_)::value, h = decltype(h_)::value;
+        each<kSub / 16>([&](auto k_) {
           constexpr int kk = decltype(k_)::value;
-          mma_ts<st * (Smem<D>::kK >> 4) + kk * (2048 >> 4)>(2 * kKeys + i * D, i * kKeys + kk * 8, v0, mnmajor, id_o,
-                                                             kk > 0 ? 1u : (uint32_t)(j > 0));
+          mma_ts<st * (Smem<D>::kK >> 4) + (h * kSub / 16 + kk) * (2048 >> 4)>(
+              2 * kKeys + i * D, i * kKeys + h * kSub + kk * 8, v0, mnmajor, id_o, kk > 0 ? 1u : (uint32_t)(t > 0));
         });
-        mma_commit(&sm.o_done[i]);
+        mma_commit(&sm.o_done[i][h]);
       };
       constexpr Int<0> c0{};
       constexpr Int<1> c1{};
-      // Key tile j, in stage st, and the scores of the next.
-      auto key_tile = [&](int j, auto st_, auto nx_) {
-        constexpr int st = decltype(st_)::value, nx = decltype(nx_)::value;
-        const bool more = j + 1 < n_tiles;
-        if (more) wait(&sm.k_full[nx], ((j + 1) >> 1) & 1);
-        wait(&sm.v_full[st], (j >> 1) & 1);
-        if (!wait(&sm.p_full[0], j & 1)) return;
-        outputs(c0, st_, j);
-        if (more) scores(c0, nx_);
-        if (tiles > 1) {
-          if (!wait(&sm.p_full[1], j & 1)) return;
-          outputs(c1, st_, j);
-          if (more) scores(c1, nx_);
+      // Step t (half h of stage st): its outputs, and the scores of step t + 2 in its place.
+      auto step = [&](int t, auto st_, auto nx_, auto h_) {
+        constexpr int st = decltype(st_)::value, nx = decltype(nx_)::value, h = decltype(h_)::value;
+        const uint32_t phase = (t >> 1) & 1;
+        const bool more = t + 2 < n_sub;
+        if (h == 0) {
+          wait(&sm.v_full[st], (t >> 2) & 1);
+          if (more) wait(&sm.k_full[nx], ((t + 2) >> 2) & 1);
         }
-        mma_commit(&sm.v_empty[st]);
-        if (more) mma_commit(&sm.k_empty[nx]);
+        if (!wait(&sm.p_full[0][h], phase)) return;
+        tc_fence_after();
+        outputs(c0, st_, h_, t);
+        if (more) scores(c0, nx_, h_);
+        if (tiles > 1) {
+          if (!wait(&sm.p_full[1][h], phase)) return;
+          tc_fence_after();
+          outputs(c1, st_, h_, t);
+          if (more) scores(c1, nx_, h_);
+        }
+        if (h == 1) {
+          mma_commit(&sm.v_empty[st]);
+          mma_commit(&sm.k_empty[nx]);
+        }
       };
-      if (n_tiles > 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[0], 0)) {
-        scores(c0, c0);
-        if (tiles > 1 && wait(&sm.q_full[1], 0)) scores(c1, c0);
+      if (n_sub > 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[0], 0)) {
+        tc_fence_after();
+        scores(c0, c0, c0);
+        if (tiles > 1 && wait(&sm.q_full[1], 0)) {
+          tc_fence_after();
+          scores(c1, c0, c0);
+        }
+        if (ok && n_sub > 1) {
+          scores(c0, c0, c1);
+          if (tiles > 1) scores(c1, c0, c1);
+        }
         if (ok) mma_commit(&sm.k_empty[0]);
       }
-      for (int j = 0; ok && j < n_tiles; j += 2) {
-        key_tile(j, c0, c1);
-        if (ok && j + 1 < n_tiles) key_tile(j + 1, c1, c0);
+      for (int t = 0; ok && t < n_sub; t += 4) {
+        step(t, c0, c1, c0);
+        if (ok && t + 1 < n_sub) step(t + 1, c0, c1, c1);
+        if (ok && t + 2 < n_sub) step(t + 2, c1, c0, c0);
+        if (ok && t + 3 < n_sub) step(t + 3, c1, c0, c1);
       }
       // One more commit covers every MMA issued; tensor memory is freed after it.
       mma_commit(&sm.drain);
