@@ -23,13 +23,75 @@ struct AppendParams {
   uint8_t *cache;
   KvBatch b;
   long long ldk, ldv;   // row strides in elements
-  int warps_row;        // warps of one row: 4 groups each
+  int warps_row;        // warps of one row
 };
 
 // x held in float16 terms: +-60000 leaves room for lo + 15 step.
 __device__ __forceinline__ float kv_clamp(float x) { return fminf(fmaxf(x, -60000.f), 60000.f); }
 
-template <int DT, int D>
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 1 / v of a float16 number v to nearest: the hardware's approximation and one Newton
+// step.
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return fmaf(fmaf(-v, r, 1.f), r, r);
+}
+// a / b to nearest from r = 1 / b: a product, corrected by its remainder (Markstein
+// 1990).
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+// v shifted up by a byte, below it hi and lo limited to 0 .. 15.
+__device__ __forceinline__ uint32_t pack_u4(int hi, int lo, uint32_t v) {
+  uint32_t d;
+  asm("cvt.pack.sat.u4.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(hi), "r"(lo), "r"(v));
+  return d;
+}
+
+// A lane's 8 values of one group, as they came.
+template <int DT>
+struct Raw8 {
+  uint4 v[DT == MOE_BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void *src, size_t at) {
+    if constexpr (DT == MOE_BF16) {
+      v[0] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(src) + at);
+    } else {
+      const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(src) + at);
+      v[0] = p[0], v[1] = p[1];
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (DT == MOE_BF16) {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[4 * i] = __uint_as_float(v[i].x), x[4 * i + 1] = __uint_as_float(v[i].y);
+        x[4 * i + 2] = __uint_as_float(v[i].z), x[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    }
+  }
+};
+
+// A warp takes NU rounds of 4 groups of a row: the row's place is looked up once for
+// them, while all their loads are on the way.
+template <int DT, int D, int NU>
 __global__ void __launch_bounds__(kAppendWarps * 32) kv4_append_kernel(const AppendParams p) {
   constexpr int NG = D / kKvGroup;
   const int lane = threadIdx.x & 31;
@@ -37,29 +99,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv4_append_kernel(const App
   const int t = (int)(w / p.warps_row);
   if (t >= p.b.T) return;
   const int groups = p.b.Hkv * NG;   // of K, then as many of V
-  const int u = (int)(w - (long long)t * p.warps_row) * 4 + (lane >> 3);
-  const bool mine = u < 2 * groups;
-  const int which = u >= groups, r = u - which * groups;
-  float x[8];
+  const int u0 = (int)(w - (long long)t * p.warps_row) * 4 * NU + (lane >> 3);
+  Raw8<DT> raw[NU];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  if (mine) {
-    const size_t at = (size_t)t * (which ? p.ldv : p.ldk) + r * kKvGroup + (lane & 7) * 8;
-    const void *src = which ? p.v : p.k;
-    if constexpr (DT == MOE_BF16) {
-      const uint4 q = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(src) + at);
-      const uint32_t v[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(v[i] << 16);
-        x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-      }
-    } else {
-      const float4 *f = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(src) + at);
-      const float4 a = f[0], c = f[1];
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-      x[4] = c.x, x[5] = c.y, x[6] = c.z, x[7] = c.w;
-    }
+  for (int n = 0; n < NU; ++n) {
+    const int u = u0 + 4 * n, which = u >= groups, r = u - which * groups;
+    if (u < 2 * groups)
+      raw[n].load(which ? p.v : p.k, (size_t)t * (which ? p.ldv : p.ldk) + r * kKvGroup + (lane & 7) * 8);
   }
   const int s = kv_seq_of(p.b, t, lane);
   int page = -1, pos = -1;
@@ -69,45 +115,69 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv4_append_kernel(const App
     pos = q.len - q.nq + i;
     if (i < q.nq && pos >= 0) page = kv_page_at(p.b, s, pos);
   }
-  bool nan = false;
+  if (page < 0) return;   // the whole warp's row
+  const int slot = pos & ((1 << p.b.log_page) - 1);
+  uint8_t *const first = p.cache + (size_t)page * p.b.Hkv * KvBlock<D>::bytes(p.b.log_page);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    nan |= x[i] != x[i];
-    x[i] = kv_clamp(x[i]);
-  }
-  float lo = x[0], hi = x[0];
+  for (int n = 0; n < NU; ++n) {
+    const int u = u0 + 4 * n;
+    const bool mine = u < 2 * groups;
+    float x[8];
+    if (mine) {
+      raw[n].get(x);
+    } else {
 #pragma unroll
-  for (int i = 1; i < 8; ++i) lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    // A NaN stays in the smallest and the largest.
+    float lo = min3(min3(min3(x[0], x[1], x[2]), x[3], x[4]), min3(x[5], x[6], x[7]), x[5]);
+    float hi = max3(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]), x[5]);
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  nan = __ballot_sync(0xffffffffu, nan) >> (lane & 24) & 0xFF;
-  if (!mine || page < 0) return;
-  const __half l16 = __float2half_rn(lo);
-  const float l = __half2float(l16);
-  const __half s16 = __float2half_rn(__fdiv_rn(fmaxf(hi - l, 0.f), 15.f));
-  const float st = __half2float(s16), inv = st > 0.f ? __frcp_rn(st) : 0.f;
-  uint32_t word = 0;
+    for (int o = 1; o < 8; o <<= 1) {
+      const float a = __shfl_xor_sync(0xffffffffu, lo, o), c = __shfl_xor_sync(0xffffffffu, hi, o);
+      lo = min3(lo, a, a), hi = max3(hi, c, c);
+    }
+    if (!mine) continue;
+    bool nan = false;
+    if (!(lo >= -60000.f && hi <= 60000.f)) {   // far values or a NaN
+      nan = lo != lo;
+      lo = kv_clamp(lo), hi = kv_clamp(hi);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // The quotient to nearest: a product with 1 / step, corrected by its
-    // remainder (Markstein 1990).
-    const float d = x[i] - l, q0 = d * inv, q = fmaf(fmaf(-q0, st, d), inv, q0);
-    const uint32_t c = (uint32_t)fminf(fmaxf(rintf(q), 0.f), 15.f);
-    word |= c << (4 * i);
+      for (int i = 0; i < 8; ++i) x[i] = kv_clamp(x[i]);
+    }
+    const __half l16 = __float2half_rn(lo);
+    const float l = __half2float(l16), range = fmaxf(hi - l, 0.f);
+    const __half s16 = __float2half_rn(quotient(range, 15.f, 0.06666667f));
+    const float st = __half2float(s16), inv = st > 0.f ? reciprocal(st) : 0.f;
+    // c = rint((x - lo) / step): 1.5 2^23 more than the quotient is rounded to whole
+    // numbers, which are then its lowest bits.
+    int c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = __float_as_int(quotient(x[i] - l, st, inv) + 12582912.f) - 0x4B400000;
+    uint32_t word = pack_u4(c[1], c[0], pack_u4(c[3], c[2], pack_u4(c[5], c[4], pack_u4(c[7], c[6], 0u))));
+    if (nan) word = 0;
+    const int which = u >= groups, r = u - which * groups, head = r / NG, g = r % NG;
+    uint8_t *block = first + (size_t)head * KvBlock<D>::bytes(p.b.log_page);
+    *reinterpret_cast<uint32_t *>(block + KvBlock<D>::codes(p.b.log_page, which, slot) + g * (kKvGroup / 2) +
+                                  (lane & 7) * 4) = word;
+    if ((lane & 7) == 0) {
+      const uint32_t pair = __half_as_ushort(s16) | (uint32_t)__half_as_ushort(l16) << 16;
+      *reinterpret_cast<uint32_t *>(block + KvBlock<D>::scales(p.b.log_page, which, slot) + g * 4) =
+          nan ? 0x7FFF7FFFu : pair;
+    }
   }
-  if (nan) word = 0;
-  const int slot = pos & ((1 << p.b.log_page) - 1), head = r / NG, g = r % NG;
-  uint8_t *block = p.cache + ((size_t)page * p.b.Hkv + head) * KvBlock<D>::bytes(p.b.log_page);
-  *reinterpret_cast<uint32_t *>(block + KvBlock<D>::codes(p.b.log_page, which, slot) + g * (kKvGroup / 2) +
-                                (lane & 7) * 4) = word;
-  if ((lane & 7) == 0) {
-    const uint32_t pair = __half_as_ushort(s16) | (uint32_t)__half_as_ushort(l16) << 16;
-    *reinterpret_cast<uint32_t *>(block + KvBlock<D>::scales(p.b.log_page, which, slot) + g * 4) =
-        nan ? 0x7FFF7FFFu : pair;
-  }
+}
+
+template <int DT, int D>
+cudaError_t launch_append(AppendParams p, int n_kv_heads, cudaStream_t st) {
+  // Rounds of a warp: one where there are few rows (latency), four where the rows
+  // alone fill the SMs.
+  const int rounds = (2 * n_kv_heads * (D / kKvGroup) + 3) / 4;
+  const bool many = (long long)p.b.T * rounds >= 152 * 64 && rounds > 1;
+  p.warps_row = many ? (rounds + 3) / 4 : rounds;
+  const long long warps = (long long)p.b.T * p.warps_row;   // at most 2^29
+  const dim3 grid((unsigned)((warps + kAppendWarps - 1) / kAppendWarps)), block(kAppendWarps * 32);
+  return launch_k(false, many ? kv4_append_kernel<DT, D, 4> : kv4_append_kernel<DT, D, 1>, grid, block, 0, st, p);
 }
 
 }  // namespace
@@ -150,11 +220,12 @@ extern "C" __attribute__((visibility("default"))) int moe_kv4_append(
     return MOE_ERR_ARG;
   AppendParams p{k, v, static_cast<uint8_t *>(cache),
                  KvBatch{pages, q_off, kv_len, T, n_seq, kv4_log2(page_size), n_pages, max_pages, n_kv_heads},
-                 ldk, ldv, (2 * n_kv_heads * (head_dim / kKvGroup) + 3) / 4};
-  const long long warps = (long long)T * p.warps_row;   // at most 2^29
-  const dim3 grid((unsigned)((warps + kAppendWarps - 1) / kAppendWarps)), block(kAppendWarps * 32);
+                 ldk, ldv, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  auto kernel = dtype == MOE_F32 ? (head_dim == 64 ? kv4_append_kernel<MOE_F32, 64> : kv4_append_kernel<MOE_F32, 128>)
-                                 : (head_dim == 64 ? kv4_append_kernel<MOE_BF16, 64> : kv4_append_kernel<MOE_BF16, 128>);
-  return launch_k(false, kernel, grid, block, 0, st, p) == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
+  cudaError_t err;
+  if (dtype == MOE_F32)
+    err = head_dim == 64 ? launch_append<MOE_F32, 64>(p, n_kv_heads, st) : launch_append<MOE_F32, 128>(p, n_kv_heads, st);
+  else
+    err = head_dim == 64 ? launch_append<MOE_BF16, 64>(p, n_kv_heads, st) : launch_append<MOE_BF16, 128>(p, n_kv_heads, st);
+  return err == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
