@@ -92,11 +92,13 @@ def attend(q, K, V, scale, softcap, window, causal, seen=None):
     [len][Hkv][D], in f64; seen [len]: False for tokens in holes.
 
     The bound counts, per row: keys, values and weights rounded to float16 (half
-    a step, 2^-12 of the value, each key and value once more for the offset that
-    a decode folds in), f32 sums that truncate (a unit, 2^-23, for every 16
-    products), a few roundings of the exponent's argument.  A score off by d
+    a step, 2^-11 of the value), f32 sums that truncate (a unit, 2^-23, for every
+    16 products), a few roundings of the exponent's argument.  A score off by d
     moves every weight by at most exp(2 d) - 1 of itself, numerator and sum
-    together; small weights round by 2^-25 of the largest."""
+    together; small weights round by 2^-25 of the largest.  Where the weights
+    carry the scales, w step is what is rounded and meets the code, not the
+    value: step c = V - lo, and lo is the least value of the token's 64 (whose
+    code is 0), so that rounding counts 2^-11 w (V - least)."""
     n, H, D = q.shape
     L, Hkv = K.shape[:2]
     G = H // Hkv
@@ -132,7 +134,9 @@ def attend(q, K, V, scale, softcap, window, causal, seen=None):
         e = torch.nan_to_num(e).amax(1, keepdim=True) if L else torch.zeros_like(l)
         e = e + 2.0 ** -20 * (1 + (softcap if softcap else torch.nan_to_num(top.abs(), posinf=0.0)))
         rel = torch.expm1(2 * e) + 2.0 ** -10 + (L / 8 + 64) * 2.0 ** -23
-        bound[:, h] = rel * (p @ vv.abs()) + 2.0 ** -24 * L * (vv.abs().amax(0) if L else 0)
+        above = vv.unflatten(1, (-1, GROUP))
+        above = (above - above.amin(2, keepdim=True)).flatten(1)
+        bound[:, h] = rel * (p @ vv.abs()) + 2.0 ** -11 * (p @ above) + 2.0 ** -24 * L * (vv.abs().amax(0) if L else 0)
     return o, bound
 
 
