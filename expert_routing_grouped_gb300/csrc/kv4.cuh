@@ -143,6 +143,47 @@ static __device__ __forceinline__ float capped(float x2, float cap_log2) {
   return cap_log2 - 2.f * cap_log2 * rcp_approx(1.f + ex2(x2));
 }
 
+// A running (maximum, sum, output) of one row, four dimensions of it in a lane.
+struct RowPart {
+  float top = kNoScore, sum = 0.f;
+  float4 y = {0.f, 0.f, 0.f, 0.f};
+  // Takes N partial results at(0) .. at(n - 1), n <= N, asked for all at once.
+  template <int N, int D, class At>
+  __device__ __forceinline__ void take(const float *po, const float2 *pml, int n, int lane, At at) {
+    float2 ml[N];
+    float4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      ml[i] = make_float2(kNoScore, 0.f);
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const size_t k = at(i);
+        ml[i] = __ldcg(pml + k);
+        if (lane < D / 4) v[i] = __ldcg(reinterpret_cast<const float4 *>(po + k * D) + lane);
+      }
+    }
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < N; ++i) now = fmaxf(now, ml[i].x);
+    scale(ex2(top - now));
+    top = now;
+#pragma unroll
+    for (int i = 0; i < N; ++i) add(ml[i].y, v[i], ex2(ml[i].x - now));
+  }
+  __device__ __forceinline__ void scale(float f) {
+    sum *= f;
+    y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+  }
+  __device__ __forceinline__ void add(float l, const float4 &v, float f) {
+    sum += l * f;
+    y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
+  }
+  __device__ __forceinline__ uint2 result() const {
+    const float f = sum != 0.f ? 1.f / sum : 0.f;
+    return pack_out(make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+  }
+};
+
 // ------------------------------------------------- argument checks (host) --
 
 static inline bool kv4_good_page(int page_size) {

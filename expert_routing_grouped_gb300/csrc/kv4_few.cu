@@ -39,7 +39,7 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 32;                   // tokens of a ring slot
-constexpr int kMinTiles = 8;                // tiles of a span, at least: one for each warp
+constexpr int kMinTiles = 4;                // tiles of a span, at least: one for each warp
 constexpr int kPlanSeqs = 1024;             // sequences of a batch that is cut into spans
 constexpr int kColumns = kFewColumns;
 constexpr int kFewSms = 152;                // blocks are sized for the GB300's SMs
@@ -49,16 +49,15 @@ struct Slot {
   static constexpr int kK = 0, kV = kTile * D / 2, kKs = kTile * D, kVs = kKs + kTile * D / 16;
   static constexpr int kBytes = kVs + kTile * D / 16;
 };
-// Up to 8 columns: two blocks of 8 warps on an SM; up to 16, whose outputs take
-// twice the registers: one of 12.
+// Four warps to a block: up to 8 columns four blocks on an SM; up to 16, whose
+// outputs take twice the registers, three.
+constexpr int kWarps = 4;
 template <int NT>
-constexpr int kWarps = NT == 1 ? 8 : 12;
-template <int NT>
-constexpr int kBlocks = NT == 1 ? 2 : 1;
-template <int D, int NT>
-constexpr int kRing = D == 64 ? 6 : NT == 1 ? 3 : 4;     // slots of a warp
-template <int D, int NT>
-constexpr int kSmem = kWarps<NT> * kRing<D, NT> * Slot<D>::kBytes;
+constexpr int kBlocks = NT == 1 ? 4 : 3;
+template <int D>
+constexpr int kRing = D == 64 ? 6 : 3;      // slots of a warp
+template <int D>
+constexpr int kSmem = kWarps * kRing<D> * Slot<D>::kBytes;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -73,7 +72,7 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -81,7 +80,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 }
 // The same onto zeros.
 __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -89,7 +88,7 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 // Four pairs of codes of w (nibbles i and i + 4 of it: a pair's halves) as float16
@@ -243,14 +242,14 @@ struct Segment {
 
 template <int NT>
 struct Joined {
-  float m[kWarps<NT>][8 * NT], l[kWarps<NT>][8 * NT];
-  uint4 q[NT][2][2][32];   // two column tiles: q's B operands
+  float m[kWarps][8 * NT], l[kWarps][8 * NT];
+  uint4 q[NT == 1 ? 1 : NT][NT == 1 ? 1 : 2][2][NT == 1 ? 1 : 32];   // two column tiles: q's B operands
 };
 
 template <int D, int NT>
 __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment part, uint8_t *smem,
                                            Joined<NT> &jn) {
-  constexpr int NG = D / kKvGroup, MT = D / 16, SB = Slot<D>::kBytes, NS = kRing<D, NT>, W = kWarps<NT>;
+  constexpr int NG = D / kKvGroup, MT = D / 16, SB = Slot<D>::kBytes, NS = kRing<D>, W = kWarps;
   constexpr int kPieces = D / 32;            // 16-byte pieces of a token's codes
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   const AttendSeq sq = attend_seq_at(p, part.s);
@@ -647,7 +646,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
   __syncthreads();   // also: the rings are free
   constexpr int kRow = D + 4;
   float *joined = reinterpret_cast<float *>(smem);   // [warp][column][kRow]
-  static_assert(W * 8 * NT * kRow * 4 <= kSmem<D, NT>, "the joined outputs fit the rings");
+  static_assert(W * 8 * NT * kRow * 4 <= kSmem<D>, "the joined outputs fit the rings");
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -699,7 +698,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 
 // kCut: blocks take equal spans of the line; otherwise block u is (sequence, head) u.
 template <int D, int NT, bool kCut>
-__global__ void __launch_bounds__(kWarps<NT> * 32, kBlocks<NT>) kv4_few_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocks<NT>) kv4_few_kernel(const AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Joined<NT> jn;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining blocks may wait beside these
@@ -733,65 +732,58 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, kBlocks<NT>) kv4_few_kernel(c
   }
 }
 
-// One block per sequence, row and query head: joins its parts, four at a time in
-// four warps.
-template <int D>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const AttendParams p, int max_cols) {
-  __shared__ float4 ys[4][D / 4];
-  __shared__ float2 mls[4];
-  const int per_seq = p.b.Hkv * max_cols;
-  const int s = blockIdx.x / per_seq, u = blockIdx.x - s * per_seq;
+// Joins the parts of rows and query heads of one sequence, WR warps to each: a warp
+// takes eight parts in one go.
+constexpr int kJoinWarps = 8;
+template <int D, int WR>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const AttendParams p, int max_cols) {
+  __shared__ float4 ys[kJoinWarps][D / 4];
+  __shared__ float2 mls[kJoinWarps];
+  constexpr int kRowsBlock = kJoinWarps / WR;
+  const int per_seq = p.b.Hkv * max_cols, blocks_seq = (per_seq + kRowsBlock - 1) / kRowsBlock;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WR;
+  const int s = blockIdx.x / blocks_seq, u = (blockIdx.x - s * blocks_seq) * kRowsBlock + warp / WR;
   const AttendSeq sq = attend_seq_at(p, s);
   const int cols = sq.rows * p.G, hk = u / max_cols, c = u - hk * max_cols;
   const SeqTiles t = tiles_of(p, sq);
-  bool any = t.n > 0 && c < cols;
+  int b0 = 0, b1 = 0;
   Line line{};
   long long head = 0;
-  int b0 = 0, b1 = 0;
-  if (any) {
+  if (t.n > 0) {   // the whole block
     line = find_line(p, 0, s);
     head = line.start + (long long)hk * span_of(t);
     b0 = (int)(head / line.cut), b1 = (int)((head + t.n - 1) / line.cut);
-    any = b0 < b1;
   }
   // Every block waits: this grid must not be over before the one it joins.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!any) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float *po = after_wait(p.part_o);
-  const float2 *pml = after_wait(p.part_ml);
-  // Slot of block b's part: its span's first segment, or one that starts inside it.
-  auto slot = [&](int b) { return (size_t)(2 * b + (head > line.cut * b)) * kColumns + c; };
-  float top = kNoScore;
-  for (int b = b0 + lane; b <= b1; b += 32) top = fmaxf(top, __ldcg(pml + slot(b)).x);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float sum = 0.f;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int b = b0 + warp; b <= b1; b += 4) {
-    const float2 ml = __ldcg(pml + slot(b));
-    const float f = ex2(ml.x - top);
-    sum += ml.y * f;
-    if (lane < D / 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + slot(b) * D) + lane);
-      y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
-    }
+  if (WR == kJoinWarps && (b0 == b1 || u >= per_seq || c >= cols)) return;   // the whole block
+  const bool mine = b0 < b1 && u < per_seq && c < cols;
+  RowPart row;
+  if (mine) {
+    const float *po = after_wait(p.part_o);
+    const float2 *pml = after_wait(p.part_ml);
+    // Slot of block b's part: its span's first segment, or one that starts inside it.
+    for (int b = b0 + part; b <= b1; b += 8 * WR)
+      row.take<8, D>(po, pml, (b1 - b) / WR + 1, lane, [&](int i) {
+        return (size_t)(2 * (b + i * WR) + (head > line.cut * (b + i * WR))) * kColumns + c;
+      });
   }
-  if (lane < D / 4) ys[warp][lane] = y;
-  if (lane == 0) mls[warp].x = sum;
-  __syncthreads();
-  if (warp || lane >= D / 4) return;
-  sum = (mls[0].x + mls[1].x) + (mls[2].x + mls[3].x);
+  if constexpr (WR > 1) {
+    if (lane < D / 4) ys[warp][lane] = row.y;
+    if (lane == 0) mls[warp] = make_float2(row.top, row.sum);
+    __syncthreads();
+    if (part) return;
+    float now = row.top;
 #pragma unroll
-  for (int w = 1; w < 4; ++w) {
-    const float4 v = ys[w][lane];
-    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+    for (int w = 1; w < WR; ++w) now = fmaxf(now, mls[warp + w].x);
+    row.scale(ex2(row.top - now));
+#pragma unroll
+    for (int w = 1; w < WR; ++w)
+      row.add(mls[warp + w].y, ys[warp + w][lane % (D / 4)], ex2(mls[warp + w].x - now));
   }
-  const float f = sum != 0.f ? 1.f / sum : 0.f;
+  if (!mine || lane >= D / 4) return;
   const int i = c / p.G, h = hk * p.G + c - i * p.G;
-  *reinterpret_cast<uint2 *>(p.out + (size_t)(sq.t0 + i) * p.ldo + (size_t)h * D + lane * 4) =
-      pack_out(make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+  *reinterpret_cast<uint2 *>(p.out + (size_t)(sq.t0 + i) * p.ldo + (size_t)h * D + lane * 4) = row.result();
 }
 
 template <int D, int NT, bool kCut>
@@ -799,10 +791,10 @@ cudaError_t launch(const AttendParams &p, int grid, cudaStream_t st) {
   auto kernel = kv4_few_kernel<D, NT, kCut>;
   static DeviceOnce once;
   const cudaError_t err = once.run([&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, NT>);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>);
   });
   if (err != cudaSuccess) return err;
-  return launch_k(false, kernel, dim3(grid), dim3(kWarps<NT> * 32), kSmem<D, NT>, st, p);
+  return launch_k(false, kernel, dim3(grid), dim3(kWarps * 32), kSmem<D>, st, p);
 }
 
 template <int D, int NT>
@@ -811,8 +803,13 @@ cudaError_t launch(AttendParams p, bool cut, int max_cols, cudaStream_t st) {
   p.target = kFewSms * kBlocks<NT>;
   const cudaError_t err = launch<D, NT, true>(p, p.target, st);
   if (err != cudaSuccess) return err;
-  return launch_k(true, kv4_join_kernel<D>, dim3((unsigned)(p.b.n_seq * p.b.Hkv * max_cols)), dim3(128), 0, st, p,
-                  max_cols);
+  // Eight warps to a row where its parts are many (one or two heads have a good part
+  // of all blocks), else one.
+  const int per_seq = p.b.Hkv * max_cols;
+  const bool wide = p.target >= 4 * p.b.n_seq * p.b.Hkv;
+  const int blocks_seq = wide ? per_seq : (per_seq + kJoinWarps - 1) / kJoinWarps;
+  return launch_k(true, wide ? kv4_join_kernel<D, kJoinWarps> : kv4_join_kernel<D, 1>,
+                  dim3((unsigned)(p.b.n_seq * blocks_seq)), dim3(kJoinWarps * 32), 0, st, p, max_cols);
 }
 
 // Whether the line of tiles is cut: not for more sequences than a block can look
@@ -824,7 +821,7 @@ bool is_cut(const AttendParams &p) {
 }  // namespace
 
 // Slots of partial results: two for each block.
-size_t few_slots(const AttendParams &p) { return is_cut(p) ? 2 * kFewSms * 2 : 0; }
+size_t few_slots(const AttendParams &p) { return is_cut(p) ? 2 * kFewSms * kBlocks<1> : 0; }
 
 cudaError_t launch_few(const AttendParams &p, int D, cudaStream_t st) {
   // Columns that some sequence may have.

@@ -686,28 +686,12 @@ __global__ void __launch_bounds__(128) kv4_many_join_kernel(const AttendParams p
   const float *po = after_wait(p.part_o);
   const float2 *pml = after_wait(p.part_ml);
   const size_t first = (size_t)unit * nsplit * kBlockRows + r;
-  float top = kNoScore;
-  for (int i = lane; i < job.parts; i += 32) top = fmaxf(top, __ldcg(pml + first + (size_t)i * kBlockRows).x);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float sum = 0.f;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < job.parts; ++i) {
-    const size_t at = first + (size_t)i * kBlockRows;
-    const float2 ml = __ldcg(pml + at);
-    const float f = ex2(ml.x - top);
-    sum += ml.y * f;
-    if (lane < D / 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + at * D) + lane);
-      y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
-    }
-  }
+  RowPart rp;
+  for (int i = 0; i < job.parts; i += 8)
+    rp.take<8, D>(po, pml, job.parts - i, lane, [&](int k) { return first + (size_t)(i + k) * kBlockRows; });
   if (lane >= D / 4) return;
-  const float f = sum != 0.f ? 1.f / sum : 0.f;
   const int tok = row / p.G, h = hk * p.G + row - tok * p.G;
-  *reinterpret_cast<uint2 *>(p.out + (size_t)(job.sq.t0 + tok) * p.ldo + (size_t)h * D + lane * 4) =
-      pack_out(make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+  *reinterpret_cast<uint2 *>(p.out + (size_t)(job.sq.t0 + tok) * p.ldo + (size_t)h * D + lane * 4) = rp.result();
 }
 
 // Places of all sequences' tiles of rows, and the parts that keys may be cut into.
