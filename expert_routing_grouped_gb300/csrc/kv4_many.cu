@@ -267,6 +267,112 @@ __device__ __forceinline__ int part_at(const Job &job, int part) {
   return job.lo + (int)((long long)(job.hi - job.lo) * part / job.parts);
 }
 
+// The codes' role, a warpgroup (wd the warp in it): K, V or both of a part's key tiles,
+// decoded into their stages.
+template <int D>
+__device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &job, Bars &sm, uint8_t *k_s, uint8_t *v_s,
+                                             int hk, int t0, int n_tiles, int wd, bool do_k, bool do_v) {
+  const int lane = threadIdx.x & 31;
+  // A warp has 32 tokens of the tile, in rounds of 512 neighbouring bytes of codes: a
+  // lane has 16 of them, 32 dimensions of one token.
+  constexpr int kPieces = D / 32, kPer = 32 / kPieces, kRounds = 32 / kPer;   // tokens of a round: 8 (D = 64: 16)
+  const int lp = p.b.log_page, w0 = wd * 32, tk = lane / kPieces, pc = lane % kPieces, g = pc / 2;
+  const uint8_t *head = p.cache + (size_t)hk * KvBlock<D>::bytes(lp);
+  const size_t page_bytes = KvBlock<D>::bytes(lp) * p.b.Hkv;
+  struct Codes {
+    uint4 c[kRounds];
+    uint32_t sc[kRounds];
+  };
+  // Pages of the warp's first and last 16 tokens of tile j; -1: past the end, -2: a hole.
+  auto pages_of = [&](int j) {
+    int2 r = make_int2(-1, -1);
+    const int token = (t0 + j) * kKeys + w0;
+    if (j >= n_tiles || token >= job.sq.len) return r;
+    r.x = kv_page_at(p.b, job.s, token);
+    r.x = r.x < 0 ? -2 : r.x;
+    if (token + 16 < job.sq.len) {
+      r.y = r.x;
+      if (lp == 4) {
+        r.y = kv_page_at(p.b, job.s, token + 16);
+        r.y = r.y < 0 ? -2 : r.y;
+      }
+    }
+    return r;
+  };
+  // Codes (where asked for) and scales of K (which 0) or V; zeros where there is no
+  // page or no token.
+  auto load = [&](int j, int2 page, int which, bool codes, Codes &x) {
+#pragma unroll
+    for (int c = 0; c < kRounds; ++c) {
+      const int id = c * kPer < 16 ? page.x : page.y, t = c * kPer + tk, token = (t0 + j) * kKeys + w0 + t;
+      x.c[c] = make_uint4(0, 0, 0, 0);
+      x.sc[c] = 0;
+      if (id >= 0 && token < job.sq.len) {
+        const int slot = token & ((1 << lp) - 1);
+        const uint8_t *blk = head + (size_t)id * page_bytes;
+        if (codes) x.c[c] = __ldg(reinterpret_cast<const uint4 *>(blk + KvBlock<D>::codes(lp, which, slot)) + pc);
+        x.sc[c] = __ldg(reinterpret_cast<const uint32_t *>(blk + KvBlock<D>::scales(lp, which, slot)) + g);
+      }
+    }
+  };
+  // 64 bytes of a row of 128, by 16-byte pieces exchanged as the swizzle has it; lanes
+  // of the second 64 dimensions take their words in another order, so that a store
+  // meets itself in no bank.
+  auto write = [&](uint8_t *dst, const Codes &x) {
+#pragma unroll
+    for (int c = 0; c < kRounds; ++c) {
+      const int row = w0 + c * kPer + tk;
+      const uint32_t step = __byte_perm(x.sc[c], 0, 0x1010), lo = __byte_perm(x.sc[c], 0, 0x3232);
+      const uint4 q = g ? make_uint4(x.c[c].z, x.c[c].w, x.c[c].x, x.c[c].y) : x.c[c];
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      uint8_t *to = dst + g * (kKeys * 128) + row * 128;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4 *>(to + ((((pc & 1) * 4 + (e ^ (2 * g))) ^ (row & 7)) * 16)) = decode_word(w[e], step, lo);
+    }
+  };
+  if (p.wait_ns == 0) {   // a limit of 0 is there to show the way out: the first operands come late
+    const unsigned long long start = globaltimer();
+    while (globaltimer() - start < 20000ull) {
+    }
+  }
+  Codes k, v;
+  int2 page = pages_of(0), next = pages_of(1);
+  if (do_k) load(0, page, 0, true, k);
+  load(0, page, 1, do_v, v);   // its scales also say whose K is to be a NaN
+  for (int j = 0; j < n_tiles; ++j) {
+    const int st = j & 1;
+    // A token whose V holds a NaN: its K becomes NaN, its V zeros, so that only the
+    // rows that see it know.
+#pragma unroll
+    for (int c = 0; c < kRounds; ++c) {
+      const uint32_t other = D == 128 ? __shfl_xor_sync(0xffffffffu, v.sc[c], 2) : v.sc[c];
+      if ((v.sc[c] & 0x7FFFu) > 0x7C00u || (other & 0x7FFFu) > 0x7C00u) k.sc[c] = 0x7FFF7FFFu, v.sc[c] = 0u;
+    }
+    if (do_k) {
+      if (!wait_all(&sm.k_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
+      if (lane == 0) sm.holes[j & 3][wd] = (page.x == -2 ? 1 : 0) | (page.y == -2 ? 2 : 0);
+      write(k_s + st * Smem<D>::kK, k);
+      load(j + 1, next, 0, true, k);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[st]);
+    }
+    if (do_v) {
+      if (!wait_all(&sm.v_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
+      write(v_s + st * Smem<D>::kK, v);
+    }
+    load(j + 1, next, 1, do_v, v);
+    page = next;
+    next = pages_of(j + 2);
+    if (do_v) {
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[st]);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- kernel --
 
 template <int D, bool kCap>
@@ -483,101 +589,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
           if (mine) p.part_ml[at] = make_float2(m, sum);
         }
       }
+    } else {
+      decode_tiles<D>(p, job, sm, k_s, v_s, hk, t0, n_tiles, warp - 4, false, true);
     }
   } else if (warp < 12) {
     // -------------------------------------------------------------- decode
     fewer_regs<kDecodeRegs>();
-    // A warp has 32 tokens of the tile, in rounds of 512 neighbouring bytes of codes: a
-    // lane has 16 of them, 32 dimensions of one token.
-    constexpr int kPieces = D / 32, kPer = 32 / kPieces, kRounds = 32 / kPer;   // tokens of a round: 8 (D = 64: 16)
-    const int lp = p.b.log_page, w0 = (warp - 8) * 32, tk = lane / kPieces, pc = lane % kPieces, g = pc / 2;
-    const uint8_t *head = p.cache + (size_t)hk * KvBlock<D>::bytes(lp);
-    const size_t page_bytes = KvBlock<D>::bytes(lp) * p.b.Hkv;
-    struct Codes {
-      uint4 c[kRounds];
-      uint32_t sc[kRounds];
-    };
-    // Pages of the warp's first and last 16 tokens of tile j; -1: past the end, -2: a hole.
-    auto pages_of = [&](int j) {
-      int2 r = make_int2(-1, -1);
-      const int token = (t0 + j) * kKeys + w0;
-      if (j >= n_tiles || token >= job.sq.len) return r;
-      r.x = kv_page_at(p.b, job.s, token);
-      r.x = r.x < 0 ? -2 : r.x;
-      if (token + 16 < job.sq.len) {
-        r.y = r.x;
-        if (lp == 4) {
-          r.y = kv_page_at(p.b, job.s, token + 16);
-          r.y = r.y < 0 ? -2 : r.y;
-        }
-      }
-      return r;
-    };
-    // Codes and scales of K (which 0) or V; zeros where there is no page or no token.
-    auto load = [&](int j, int2 page, int which, Codes &x) {
-#pragma unroll
-      for (int c = 0; c < kRounds; ++c) {
-        const int id = c * kPer < 16 ? page.x : page.y, t = c * kPer + tk, token = (t0 + j) * kKeys + w0 + t;
-        x.c[c] = make_uint4(0, 0, 0, 0);
-        x.sc[c] = 0;
-        if (id >= 0 && token < job.sq.len) {
-          const int slot = token & ((1 << lp) - 1);
-          const uint8_t *blk = head + (size_t)id * page_bytes;
-          x.c[c] = __ldg(reinterpret_cast<const uint4 *>(blk + KvBlock<D>::codes(lp, which, slot)) + pc);
-          x.sc[c] = __ldg(reinterpret_cast<const uint32_t *>(blk + KvBlock<D>::scales(lp, which, slot)) + g);
-        }
-      }
-    };
-    // 64 bytes of a row of 128, by 16-byte pieces exchanged as the swizzle has it; lanes
-    // of the second 64 dimensions take their words in another order, so that a store
-    // meets itself in no bank.
-    auto write = [&](uint8_t *dst, const Codes &x) {
-#pragma unroll
-      for (int c = 0; c < kRounds; ++c) {
-        const int row = w0 + c * kPer + tk;
-        const uint32_t step = __byte_perm(x.sc[c], 0, 0x1010), lo = __byte_perm(x.sc[c], 0, 0x3232);
-        const uint4 q = g ? make_uint4(x.c[c].z, x.c[c].w, x.c[c].x, x.c[c].y) : x.c[c];
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        uint8_t *to = dst + g * (kKeys * 128) + row * 128;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4 *>(to + ((((pc & 1) * 4 + (e ^ (2 * g))) ^ (row & 7)) * 16)) = decode_word(w[e], step, lo);
-      }
-    };
-    if (p.wait_ns == 0) {   // a limit of 0 is there to show the way out: the first operands come late
-      const unsigned long long start = globaltimer();
-      while (globaltimer() - start < 20000ull) {
-      }
-    }
-    Codes k, v;
-    int2 page = pages_of(0), next = pages_of(1);
-    load(0, page, 0, k);
-    load(0, page, 1, v);
-    for (int j = 0; j < n_tiles; ++j) {
-      const int st = j & 1;
-      // A token whose V holds a NaN: its K becomes NaN, its V zeros, so that only the
-      // rows that see it know.
-#pragma unroll
-      for (int c = 0; c < kRounds; ++c) {
-        const uint32_t other = D == 128 ? __shfl_xor_sync(0xffffffffu, v.sc[c], 2) : v.sc[c];
-        if ((v.sc[c] & 0x7FFFu) > 0x7C00u || (other & 0x7FFFu) > 0x7C00u) k.sc[c] = 0x7FFF7FFFu, v.sc[c] = 0u;
-      }
-      if (!wait_all(&sm.k_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
-      if (lane == 0) sm.holes[j & 3][warp - 8] = (page.x == -2 ? 1 : 0) | (page.y == -2 ? 2 : 0);
-      write(k_s + st * Smem<D>::kK, k);
-      load(j + 1, next, 0, k);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[st]);
-      if (!wait_all(&sm.v_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
-      write(v_s + st * Smem<D>::kK, v);
-      load(j + 1, next, 1, v);
-      page = next;
-      next = pages_of(j + 2);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[st]);
-    }
+    // With one tile of rows the other softmax group takes V.
+    decode_tiles<D>(p, job, sm, k_s, v_s, hk, t0, n_tiles, warp - 8, true, tiles > 1);
   } else {
     // --------------------------------------------------------------- issue
     fewer_regs<kIssueRegs>();
