@@ -1,7 +1,7 @@
 // kv4_attend.cu -- moe_kv4_attention's argument checks, workspace and choice of
 // kernels (include/moe.h): sequences of up to 16 columns (rows times query heads
-// of a KV head) in kv4_few.cu, which reads the cache at most once and is bound by
-// that, larger ones in kv4_many.cu on the tensor cores.  Each kernel leaves the
+// of a KV head) in kv4_few.cu, which reads the cache once, larger ones in kv4_many.cu
+// on the 5th-gen tensor cores, which decodes it once for 256 columns.  Each kernel leaves the
 // other's sequences alone, so a batch may mix them.
 #include <algorithm>
 #include <cmath>

@@ -1,13 +1,10 @@
 // kv4_few.cu -- attention of a few rows a sequence over the 4-bit cache: decoded
-// tokens, and drafted ones, up to 16 columns (rows times query heads of a KV
-// head).
+// tokens, and drafted ones, up to 16 columns (rows times query heads of a KV head).
 //
 //   S^T[token][column] = K . q^T,  O^T[dim][column] = V^T . P^T
 //
 // on warp-level MMAs (m16n8k16, float16): 16 tokens, then 16 dimensions, are the
-// rows, columns the 8-wide side, so 8 query heads waste nothing.  Bound by
-// reading the cache, 9/16 bytes an element: the design keeps instructions per
-// code low and loads in flight many.
+// rows, columns the 8-wide side, so 8 query heads waste nothing.
 //
 //   Codes: a code in the lowest bits of a float16 is the subnormal number c 2^-24,
 //      four bits further up c 2^-20: one AND makes a pair of exact operands, with
@@ -18,7 +15,7 @@
 //      for each group: s = sum_g step_g acc_g + lo_g sum(q of g), no rounding of K.
 //   q: float16 after a power of two per column that brings its largest just under
 //      2^15: exact to 2^-25 of that.
-//   P: for each group w step, rounded to float16 (2^-12 of the weight), in the
+//   P: for each group w step, rounded to float16 (2^-11 at most), in the
 //      accumulator's layout, transposed by movmatrix: the B operand.  V's codes are
 //      exact, and sum w lo is kept beside in f32.
 //
@@ -27,10 +24,19 @@
 // maximum that moves only when a score passes it by 8 (weights up to 2^8 are
 // float16 as well as those up to 1), so most tiles exchange nothing.  The maximum
 // also holds a power of two that keeps w step in float16's range whatever the size
-// of V: it moves when a step passes it by 8.  The block's
-// warps join at the end.  A batch is cut into parts of about equal length over
-// the tokens of all its sequences; a second kernel joins the parts of sequences
-// that have several.
+// of V: it moves when a step passes it by 8.  The block's warps join at the end.
+//
+// The tiles of all sequences and KV heads lie in one line that is cut into equal
+// spans, one for each block, whatever the lengths; a second kernel joins what was cut.
+//
+// The floor is the cache, 9/16 bytes an element; what bounds it is instructions: 818
+// for 32 tokens of 16 columns, issued at 2.0 a clock and SM.  One token of 96 query
+// and 8 KV heads over 131072 tokens: 47.5 us (3.2 TB/s); 64 tokens of 32 and 8 heads
+// over up to 8192 each: 49.5 us (3.8 TB/s); one over 4096: 10.6 us, mostly launches,
+// the plan and the joining.  An earlier form (52.5 us over 131072) took 34.6 us with
+// the copies alone.  Tried: codes in 16 mantissa bits and V's scales on the values
+// (57.9 us against 52.8), the codes as the A side of tcgen05 MMAs (69 against 53),
+// four blocks an SM with shorter rings for 16 columns (67.2 against 52.7).
 #include <algorithm>
 
 #include "kv4.cuh"

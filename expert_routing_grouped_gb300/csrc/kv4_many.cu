@@ -2,23 +2,32 @@
 // drafted tokens of many heads, on the 5th-gen tensor cores.
 //
 // A block takes 256 rows (tokens times query heads of one KV head, which read the
-// same keys) in two tiles of 128, and walks the keys that they see in tiles of 128:
+// same keys) in two tiles of 128, and walks the keys that they see, decoded 128 at a
+// time, in steps of 64:
 //
 //   S_i = Q_i . K^T (tcgen05, both operands in shared memory), softmax, and
 //   O_i += P_i . V  (P_i float16 in tensor memory over S_i's columns)
 //
 //   warps 0-3, 4-7   the softmax of tile 0 and 1: a thread owns a row, so maxima
 //                    and sums need no exchange
-//   warps 8-11       turn codes into lo + step c in float16, 128-byte swizzled: a
-//                    thread owns a token of the tile; its next codes are on the way
-//                    while it writes.  Done once for 256 rows.
-//   warp 12          issues the MMAs: the S of one tile runs under the softmax of
-//                    the other
+//   warps 8-11       turn codes into lo + step c in float16, 128-byte swizzled, once
+//                    for 256 rows; the next tile's codes are on the way meanwhile
+//   warps 12, 13     issue the MMAs of tile 0 and 1: scores run two steps ahead of
+//                    the softmax, in two buffers of tensor memory
+//
+// 8192 tokens of 32 query and 8 KV heads, causal: 434 us, 1268 TFLOP/s of what
+// counts (0.66 of a large matrix product's rate); the tensor pipe is busy 55 % of the
+// clocks, the schedulers 53 %.  Clocks read inside an earlier form (441 us) showed the
+// codes' role at work for 3760 of the 3836 that a tile of 128 keys takes: it sets the
+// pace, and shares its schedulers with the softmax.  So neither more warps for it
+// (481 us against 450) nor more for the softmax (516 against 441) helped, nor codes
+// shared by two blocks of a cluster (824 against 441: remote stores), nor two tiles
+// of codes in flight in registers (625 against 450: spills).
 //
 // The running maximum moves only when a score passes it by 8: weights up to 2^8 are
 // float16 as well as those up to 1, and the outputs in tensor memory need scaling
-// rarely.  Rounded to float16: keys and values (2^-12 of each), weights; queries
-// enter after a power of two per row that brings the largest just under 2^15.
+// rarely.  Rounded to float16 (2^-11 at most): keys, values and weights; queries enter
+// after a power of two per row that brings the largest just under 2^15.
 //
 // The 8 dimensions of a word of codes lie in the order 0 4 1 5 2 6 3 7 (pairs of
 // nibbles i and i + 4 decode together), in Q as in K; the output puts V's back.
@@ -57,7 +66,7 @@ struct Smem {
 struct Bars {
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2][2], p_full[2][2], o_done[2][2];   // [tile of rows][step % 2]
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
   uint8_t holes[4][4];   // [tile % 4][decoding warp]: two bits, 16 tokens each without a page
@@ -267,68 +276,79 @@ __device__ __forceinline__ int part_at(const Job &job, int part) {
   return job.lo + (int)((long long)(job.hi - job.lo) * part / job.parts);
 }
 
-// The codes' role, a warpgroup (wd the warp in it): K, V or both of a part's key tiles,
-// decoded into their stages.
+// The codes' role, a warpgroup (wd the warp in it): a part's key tiles, decoded into
+// their stages.  It sets the pace of a prompt: what it need not wait for is asked for a
+// tile ahead.
 template <int D>
 __device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &job, Bars &sm, uint8_t *k_s, uint8_t *v_s,
-                                             int hk, int t0, int n_tiles, int wd, bool do_k, bool do_v) {
-  const int lane = threadIdx.x & 31;
+                                             int hk, int t0, int n_tiles, int wd) {
   // A warp has 32 tokens of the tile, in rounds of 512 neighbouring bytes of codes: a
   // lane has 16 of them, 32 dimensions of one token.
   constexpr int kPieces = D / 32, kPer = 32 / kPieces, kRounds = 32 / kPer;   // tokens of a round: 8 (D = 64: 16)
+  const int lane = threadIdx.x & 31;
   const int lp = p.b.log_page, w0 = wd * 32, tk = lane / kPieces, pc = lane % kPieces, g = pc / 2;
+  const int32_t *pages = p.b.pages + (size_t)job.s * p.b.max_pages;
   const uint8_t *head = p.cache + (size_t)hk * KvBlock<D>::bytes(lp);
   const size_t page_bytes = KvBlock<D>::bytes(lp) * p.b.Hkv;
+  // The page numbers of the warp's first and last 16 tokens of tile j as they stand in
+  // the table (looked at a tile later, when they have come).
+  auto pages_of = [&](int j) {
+    const int token = (t0 + j) * kKeys + w0;
+    int2 r = make_int2(-1, -1);
+    if (j < n_tiles && token < job.sq.len) r.x = __ldg(pages + (token >> lp));
+    if (lp == 4 && j < n_tiles && token + 16 < job.sq.len) r.y = __ldg(pages + (token >> lp) + 1);
+    return r;
+  };
   struct Codes {
     uint4 c[kRounds];
     uint32_t sc[kRounds];
   };
-  // Pages of the warp's first and last 16 tokens of tile j; -1: past the end, -2: a hole.
-  auto pages_of = [&](int j) {
-    int2 r = make_int2(-1, -1);
-    const int token = (t0 + j) * kKeys + w0;
-    if (j >= n_tiles || token >= job.sq.len) return r;
-    r.x = kv_page_at(p.b, job.s, token);
-    r.x = r.x < 0 ? -2 : r.x;
-    if (token + 16 < job.sq.len) {
-      r.y = r.x;
-      if (lp == 4) {
-        r.y = kv_page_at(p.b, job.s, token + 16);
-        r.y = r.y < 0 ? -2 : r.y;
-      }
-    }
-    return r;
-  };
-  // Codes (where asked for) and scales of K (which 0) or V; zeros where there is no
-  // page or no token.
-  auto load = [&](int j, int2 page, int which, bool codes, Codes &x) {
+  const uint32_t codes_at = KvBlock<D>::codes(lp, 0, tk) + pc * 16, codes_v = KvBlock<D>::codes(lp, 1, 0);
+  const uint32_t scales_at = KvBlock<D>::scales(lp, 0, tk) + g * 4;
+  const uint32_t scales_v = KvBlock<D>::scales(lp, 1, 0) - KvBlock<D>::scales(lp, 0, 0);
+  // Codes and scales of K (which 0) or V; zeros where there is no page or no token.
+  auto load = [&](int j, int2 page, int which, Codes &x) {
+    const int token0 = (t0 + j) * kKeys + w0, left = j < n_tiles ? job.sq.len - token0 - tk : 0;
+    if (lp > 4) page.y = page.x;
 #pragma unroll
-    for (int c = 0; c < kRounds; ++c) {
-      const int id = c * kPer < 16 ? page.x : page.y, t = c * kPer + tk, token = (t0 + j) * kKeys + w0 + t;
-      x.c[c] = make_uint4(0, 0, 0, 0);
-      x.sc[c] = 0;
-      if (id >= 0 && token < job.sq.len) {
-        const int slot = token & ((1 << lp) - 1);
-        const uint8_t *blk = head + (size_t)id * page_bytes;
-        if (codes) x.c[c] = __ldg(reinterpret_cast<const uint4 *>(blk + KvBlock<D>::codes(lp, which, slot)) + pc);
-        x.sc[c] = __ldg(reinterpret_cast<const uint32_t *>(blk + KvBlock<D>::scales(lp, which, slot)) + g);
+    for (int h = 0; h < 2; ++h) {
+      const int id = h ? page.y : page.x;
+      const bool ok = (unsigned)id < (unsigned)p.b.n_pages;
+      const int slot = (token0 + 16 * h) & ((1 << lp) - 1);
+      const uint8_t *blk = head + (size_t)(ok ? id : 0) * page_bytes;
+      const uint8_t *codes = blk + slot * (D / 2) + codes_at + (which ? codes_v : 0);
+      const uint8_t *scales = blk + slot * (D / 16) + scales_at + (which ? scales_v : 0);
+#pragma unroll
+      for (int c = h * kRounds / 2; c < (h + 1) * kRounds / 2; ++c) {
+        const int t = c * kPer - 16 * h;   // of the half's tokens
+        x.c[c] = make_uint4(0, 0, 0, 0);
+        x.sc[c] = 0;
+        if (ok && 16 * h + t < left) {
+          x.c[c] = __ldg(reinterpret_cast<const uint4 *>(codes + t * (D / 2)));
+          x.sc[c] = __ldg(reinterpret_cast<const uint32_t *>(scales + t * (D / 16)));
+        }
       }
     }
   };
   // 64 bytes of a row of 128, by 16-byte pieces exchanged as the swizzle has it; lanes
   // of the second 64 dimensions take their words in another order, so that a store
   // meets itself in no bank.
+  const int row = w0 + tk;
+  uint32_t at[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) at[e] = g * (kKeys * 128) + row * 128 + ((((pc & 1) * 4 + (e ^ (2 * g))) ^ (row & 7)) * 16);
   auto write = [&](uint8_t *dst, const Codes &x) {
 #pragma unroll
     for (int c = 0; c < kRounds; ++c) {
-      const int row = w0 + c * kPer + tk;
       const uint32_t step = __byte_perm(x.sc[c], 0, 0x1010), lo = __byte_perm(x.sc[c], 0, 0x3232);
       const uint4 q = g ? make_uint4(x.c[c].z, x.c[c].w, x.c[c].x, x.c[c].y) : x.c[c];
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-      uint8_t *to = dst + g * (kKeys * 128) + row * 128;
+      uint4 d[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<uint4 *>(to + ((((pc & 1) * 4 + (e ^ (2 * g))) ^ (row & 7)) * 16)) = decode_word(w[e], step, lo);
+      for (int e = 0; e < 4; ++e) d[e] = decode_word(w[e], step, lo);
+      // Rounds are a multiple of 8 rows apart: the swizzle is the same.
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + at[e] + c * kPer * 128) = d[e];
     }
   };
   if (p.wait_ns == 0) {   // a limit of 0 is there to show the way out: the first operands come late
@@ -338,42 +358,115 @@ __device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &j
   }
   Codes k, v;
   int2 page = pages_of(0), next = pages_of(1);
-  if (do_k) load(0, page, 0, true, k);
-  load(0, page, 1, do_v, v);   // its scales also say whose K is to be a NaN
+  load(0, page, 0, k);
+  load(0, page, 1, v);
   for (int j = 0; j < n_tiles; ++j) {
     const int st = j & 1;
     // A token whose V holds a NaN: its K becomes NaN, its V zeros, so that only the
     // rows that see it know.
+    bool nan = false;
 #pragma unroll
-    for (int c = 0; c < kRounds; ++c) {
-      const uint32_t other = D == 128 ? __shfl_xor_sync(0xffffffffu, v.sc[c], 2) : v.sc[c];
-      if ((v.sc[c] & 0x7FFFu) > 0x7C00u || (other & 0x7FFFu) > 0x7C00u) k.sc[c] = 0x7FFF7FFFu, v.sc[c] = 0u;
+    for (int c = 0; c < kRounds; ++c) nan |= (v.sc[c] & 0x7FFFu) > 0x7C00u;
+    if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll
+      for (int c = 0; c < kRounds; ++c) {
+        const uint32_t other = D == 128 ? __shfl_xor_sync(0xffffffffu, v.sc[c], 2) : v.sc[c];
+        if ((v.sc[c] & 0x7FFFu) > 0x7C00u || (other & 0x7FFFu) > 0x7C00u) k.sc[c] = 0x7FFF7FFFu, v.sc[c] = 0u;
+      }
     }
-    if (do_k) {
-      if (!wait_all(&sm.k_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
-      if (lane == 0) sm.holes[j & 3][wd] = (page.x == -2 ? 1 : 0) | (page.y == -2 ? 2 : 0);
-      write(k_s + st * Smem<D>::kK, k);
-      load(j + 1, next, 0, true, k);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[st]);
+    // (The issuers order what is written here before the MMAs.)
+    if (!wait_all(&sm.k_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
+    if (lane == 0) {
+      const int left = job.sq.len - (t0 + j) * kKeys - w0, y = lp > 4 ? page.x : page.y;
+      sm.holes[j & 3][wd] = (left > 0 && (unsigned)page.x >= (unsigned)p.b.n_pages ? 1 : 0) |
+                            (left > 16 && (unsigned)y >= (unsigned)p.b.n_pages ? 2 : 0);
     }
-    if (do_v) {
-      if (!wait_all(&sm.v_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
-      write(v_s + st * Smem<D>::kK, v);
-    }
-    load(j + 1, next, 1, do_v, v);
+    write(k_s + st * Smem<D>::kK, k);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.k_full[st]);
+    load(j + 1, next, 0, k);
+    if (!wait_all(&sm.v_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
+    write(v_s + st * Smem<D>::kK, v);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.v_full[st]);
+    load(j + 1, next, 1, v);
     page = next;
     next = pages_of(j + 2);
-    if (do_v) {
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[st]);
-    }
   }
 }
 
-// ---------------------------------------------------------------- kernel --
+// The MMAs of tile i of rows, issued by one thread.
+template <int D, int i>
+__device__ __forceinline__ void issue_tile(const AttendParams &p, Bars &sm, uint8_t *q_s, uint8_t *k_s, uint8_t *v_s,
+                                           int n_sub) {
+  // Everything that differs between the MMAs of two steps is a constant: they take 32
+  // to 64 clocks each, and the issue of one, beside three busy warps of the scheduler,
+  // takes about as long.
+  const uint32_t id_s = idesc_f16(kRows, kSub), id_o = idesc_f16(kRows, D) | 1u << 16;   // B transposed
+  const uint64_t dq = sw128_desc(smem_u32(q_s)), dk = sw128_desc(smem_u32(k_s)), dv = v_desc(smem_u32(v_s));
+  const uint32_t q0 = (uint32_t)dq, k0 = (uint32_t)dk, v0 = (uint32_t)dv;
+  const uint32_t kmajor = (uint32_t)(dq >> 32), mnmajor = (uint32_t)(dv >> 32);
+  bool ok = true;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    return ok = ok && wait_one(bar, parity, &sm.abort, p.status, p.wait_ns);
+  };
+  // Scores against half h of the keys of stage st.
+  auto scores = [&](auto st_, auto h_) {
+    constexpr int st = decltype(st_)::value, h = decltype(h_)::value;
+    each<D / 16>([&](auto k_) {
+      constexpr int kk = decltype(k_)::value;
+      constexpr uint32_t off = (kk / 4) * ((kRows * 128) >> 4) + (kk & 3) * 2;
+      mma_ss<i * (Smem<D>::kQ >> 4) + off, st * (Smem<D>::kK >> 4) + h * ((kSub * 128) >> 4) + off>(
+          i * kKeys + h * kSub, q0, kmajor, k0, kmajor, id_s, kk > 0);
+    });
+    mma_commit(&sm.s_full[i][h]);
+  };
+  auto outputs = [&](auto st_, auto h_, int t) {
+    constexpr int st = decltype(st_)::value, h = decltype(h_)::value;
+    each<kSub / 16>([&](auto k_) {
+      constexpr int kk = decltype(k_)::value;
+      mma_ts<st * (Smem<D>::kK >> 4) + (h * kSub / 16 + kk) * (2048 >> 4)>(
+          2 * kKeys + i * D, i * kKeys + h * kSub + kk * 8, v0, mnmajor, id_o, kk > 0 ? 1u : (uint32_t)(t > 0));
+    });
+    mma_commit(&sm.o_done[i][h]);
+  };
+  constexpr Int<0> c0{};
+  constexpr Int<1> c1{};
+  // Step t (half h of stage st): its outputs, and the scores of step t + 2 in its place.
+  auto step = [&](int t, auto st_, auto nx_, auto h_) {
+    constexpr int st = decltype(st_)::value, nx = decltype(nx_)::value, h = decltype(h_)::value;
+    const bool more = t + 2 < n_sub;
+    if (h == 0) {
+      wait(&sm.v_full[st], (t >> 2) & 1);
+      if (more) wait(&sm.k_full[nx], ((t + 2) >> 2) & 1);
+      fence_proxy_async();
+    }
+    if (!wait(&sm.p_full[i][h], (t >> 1) & 1)) return;
+    tc_fence_after();
+    outputs(st_, h_, t);
+    if (more) scores(nx_, h_);
+    if (h == 1) {
+      mma_commit(&sm.v_empty[st]);
+      mma_commit(&sm.k_empty[nx]);
+    }
+  };
+  if (n_sub > 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[i], 0)) {
+    fence_proxy_async();
+    tc_fence_after();
+    scores(c0, c0);
+    if (n_sub > 1) scores(c0, c1);
+    mma_commit(&sm.k_empty[0]);
+  }
+  for (int t = 0; ok && t < n_sub; t += 4) {
+    step(t, c0, c1, c0);
+    if (ok && t + 1 < n_sub) step(t + 1, c0, c1, c1);
+    if (ok && t + 2 < n_sub) step(t + 2, c1, c0, c0);
+    if (ok && t + 3 < n_sub) step(t + 3, c1, c0, c1);
+  }
+  // One more commit covers every MMA issued; tensor memory is freed after it.
+  mma_commit(&sm.drain[i]);
+  drain_bar(&sm.drain[i], 0, globaltimer());
+}
 
 template <int D, bool kCap>
 __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int nsplit) {
@@ -395,9 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.k_full[i], 4);
-      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.k_empty[i], tiles);
       mbar_init(&sm.v_full[i], 4);
-      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.v_empty[i], tiles);
       mbar_init(&sm.s_full[i][0], 1);
       mbar_init(&sm.s_full[i][1], 1);
       mbar_init(&sm.p_full[i][0], 4);
@@ -405,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       mbar_init(&sm.o_done[i][0], 1);
       mbar_init(&sm.o_done[i][1], 1);
     }
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -504,15 +598,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
             s[c] = see ? s[c] : -INFINITY;
           }
         }
-        float t4[4] = {s[0], s[1], s[2], s[3]};
+        float t8[8];
 #pragma unroll
-        for (int c = 4; c + 4 < kSub; c += 8)
+        for (int e = 0; e < 8; ++e) t8[e] = max3(s[e], s[e + 8], s[e + 16]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[c + e], s[c + 4 + e]);
+        for (int e = 0; e < 8; ++e) t8[e] = max3(t8[e], s[e + 24], s[e + 32]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kSub - 4 + e]);
+        for (int e = 0; e < 8; ++e) t8[e] = max3(t8[e], s[e + 40], s[e + 48]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t8[e] = fmaxf(t8[e], s[e + 56]);
         const float scale = kCap ? 1.f : cs;
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * scale;
+        const float top = max3(max3(t8[0], t8[1], t8[2]), max3(t8[3], t8[4], t8[5]), fmaxf(t8[6], t8[7])) * scale;
         const bool over = top > m + 8.f;
         if (__any_sync(0xffffffffu, over)) {
           const float now = over ? top : m, f = ex2(m - now);
@@ -589,98 +685,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
           if (mine) p.part_ml[at] = make_float2(m, sum);
         }
       }
-    } else {
-      decode_tiles<D>(p, job, sm, k_s, v_s, hk, t0, n_tiles, warp - 4, false, true);
     }
   } else if (warp < 12) {
     // -------------------------------------------------------------- decode
     fewer_regs<kDecodeRegs>();
-    // With one tile of rows the other softmax group takes V.
-    decode_tiles<D>(p, job, sm, k_s, v_s, hk, t0, n_tiles, warp - 8, true, tiles > 1);
+    decode_tiles<D>(p, job, sm, k_s, v_s, hk, t0, n_tiles, warp - 8);
   } else {
     // --------------------------------------------------------------- issue
     fewer_regs<kIssueRegs>();
-    if (warp == 12 && elect_one()) {
-      // Everything that differs between the MMAs of two key tiles is a constant: they
-      // take 64 clocks each, and an issue of many instructions in between, beside three
-      // busy warps of the scheduler, took longer than that.
-      const uint32_t id_s = idesc_f16(kRows, kSub), id_o = idesc_f16(kRows, D) | 1u << 16;   // B transposed
-      const uint64_t dq = sw128_desc(smem_u32(q_s)), dk = sw128_desc(smem_u32(k_s)), dv = v_desc(smem_u32(v_s));
-      const uint32_t q0 = (uint32_t)dq, k0 = (uint32_t)dk, v0 = (uint32_t)dv;
-      const uint32_t kmajor = (uint32_t)(dq >> 32), mnmajor = (uint32_t)(dv >> 32);
-      bool ok = true;
-      auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return ok = ok && wait_one(bar, parity, &sm.abort, p.status, p.wait_ns);
-      };
-      // Scores of tile i against half h of the keys of stage st.
-      auto scores = [&](auto i_, auto st_, auto h_) {
-        constexpr int i = decltype(i_)::value, st = decltype(st_)::value, h = decltype(h_)::value;
-        each<D / 16>([&](auto k_) {
-          constexpr int kk = decltype(k_)::value;
-          constexpr uint32_t off = (kk / 4) * ((kRows * 128) >> 4) + (kk & 3) * 2;
-          mma_ss<i * (Smem<D>::kQ >> 4) + off, st * (Smem<D>::kK >> 4) + h * ((kSub * 128) >> 4) + off>(
-              i * kKeys + h * kSub, q0, kmajor, k0, kmajor, id_s, kk > 0);
-        });
-        mma_commit(&sm.s_full[i][h]);
-      };
-      auto outputs = [&](auto i_, auto st_, auto h_, int t) {
-        constexpr int i = decltype(i_)::value, st = decltype(st_)::value, h = decltype(h_)::value;
-        each<kSub / 16>([&](auto k_) {
-          constexpr int kk = decltype(k_)::value;
-          mma_ts<st * (Smem<D>::kK >> 4) + (h * kSub / 16 + kk) * (2048 >> 4)>(
-              2 * kKeys + i * D, i * kKeys + h * kSub + kk * 8, v0, mnmajor, id_o, kk > 0 ? 1u : (uint32_t)(t > 0));
-        });
-        mma_commit(&sm.o_done[i][h]);
-      };
-      constexpr Int<0> c0{};
-      constexpr Int<1> c1{};
-      // Step t (half h of stage st): its outputs, and the scores of step t + 2 in its place.
-      auto step = [&](int t, auto st_, auto nx_, auto h_) {
-        constexpr int st = decltype(st_)::value, nx = decltype(nx_)::value, h = decltype(h_)::value;
-        const uint32_t phase = (t >> 1) & 1;
-        const bool more = t + 2 < n_sub;
-        if (h == 0) {
-          wait(&sm.v_full[st], (t >> 2) & 1);
-          if (more) wait(&sm.k_full[nx], ((t + 2) >> 2) & 1);
-        }
-        if (!wait(&sm.p_full[0][h], phase)) return;
-        tc_fence_after();
-        outputs(c0, st_, h_, t);
-        if (more) scores(c0, nx_, h_);
-        if (tiles > 1) {
-          if (!wait(&sm.p_full[1][h], phase)) return;
-          tc_fence_after();
-          outputs(c1, st_, h_, t);
-          if (more) scores(c1, nx_, h_);
-        }
-        if (h == 1) {
-          mma_commit(&sm.v_empty[st]);
-          mma_commit(&sm.k_empty[nx]);
-        }
-      };
-      if (n_sub > 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[0], 0)) {
-        tc_fence_after();
-        scores(c0, c0, c0);
-        if (tiles > 1 && wait(&sm.q_full[1], 0)) {
-          tc_fence_after();
-          scores(c1, c0, c0);
-        }
-        if (ok && n_sub > 1) {
-          scores(c0, c0, c1);
-          if (tiles > 1) scores(c1, c0, c1);
-        }
-        if (ok) mma_commit(&sm.k_empty[0]);
-      }
-      for (int t = 0; ok && t < n_sub; t += 4) {
-        step(t, c0, c1, c0);
-        if (ok && t + 1 < n_sub) step(t + 1, c0, c1, c1);
-        if (ok && t + 2 < n_sub) step(t + 2, c1, c0, c0);
-        if (ok && t + 3 < n_sub) step(t + 3, c1, c0, c1);
-      }
-      // One more commit covers every MMA issued; tensor memory is freed after it.
-      mma_commit(&sm.drain);
-      drain_bar(&sm.drain, 0, globaltimer());
-    }
+    // A warp for each tile of rows: they wait for their own softmax only.
+    if (warp == 12 && elect_one()) issue_tile<D, 0>(p, sm, q_s, k_s, v_s, n_sub);
+    if (warp == 13 && tiles > 1 && elect_one()) issue_tile<D, 1>(p, sm, q_s, k_s, v_s, n_sub);
     __syncwarp();
   }
   tc_fence_before();

@@ -396,16 +396,16 @@ int moe_linear(const void *x, const float *x_scale, const void *w, const float *
 
 /*
  * Waits for all work on the current device and gives in *status 2 if a product
- * on it without a status word of its own gave up since the last call that said
- * so (its out is then not complete), 0 otherwise.  Not during a capture.
- * Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
+ * or an attention on it without a status word of its own gave up since the last
+ * call that said so (its out is then not complete), 0 otherwise.  Not during a
+ * capture.  Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
  */
 int moe_linear_status(int32_t *status);
 
 /*
- * The time limit, in microseconds, of the waits between a product's pipelined
- * roles, for the products that the calling host thread launches from now on
- * (default 2000000).  A wait that is not complete when its limit has passed
+ * The time limit, in microseconds, of the waits between the pipelined roles of
+ * a product, and of attention with more than 16 columns, for the calls that the
+ * calling host thread makes from now on (default 2000000).  A wait that is not complete when its limit has passed
  * gives up: the kernel stops its roles, waits (with the full 2 s limit) for
  * its own copies and MMAs in flight, frees its tensor memory and returns, so
  * the next product runs normally; the status word holds 2, and moe_linear
@@ -413,8 +413,8 @@ int moe_linear_status(int32_t *status);
  * complete when first tested give up at once, and the first operands come late
  * enough for one to do so: a way to exercise that recovery path without a fault
  * or a hang, as MOE_OPT_WAIT_LIMIT_US is for the layer.  Products of at most
- * 16 tokens have no such waits.  A captured product keeps the limit that it
- * was captured with.  Returns MOE_OK, or MOE_ERR_ARG for a negative limit.
+ * 16 tokens have no such waits.  A captured call keeps the limit that it was
+ * captured with.  Returns MOE_OK, or MOE_ERR_ARG for a negative limit.
  */
 int moe_linear_wait_limit(int us);
 

@@ -540,3 +540,118 @@ def test_attention_block_together(moe):
         want = before.double() + att.view(T, -1).double() @ w_o.double().t()
         size = att.view(T, -1).double().abs() @ w_o.double().abs().t()
         assert bool(((stream.double() - want).abs() <= (H * D / 8 + 32) * 2.0 ** -23 * size + 2.0 ** -23 * want.abs()).all())
+
+
+# ------------------------------------------------- waits, captures, far addresses --
+
+def test_attention_waits_give_up(moe):
+    """A wait limit of 0 gives up: the status word says so, with none moe_linear_status
+    does; nothing hangs, and the next call is right."""
+    g = gen(16)
+    for H, Hkv, D, new, have in ((8, 2, 128, [300, 20], [700, 500]), (40, 1, 64, [1, 1], [900, 2000])):
+        c = ref.Cache(g, have, Hkv, D, 32)
+        off, o = batch(new, c)
+        T = o[-1]
+        q = randn(g, T, H, D).bfloat16()
+        out = torch.zeros_like(q)
+        n = moe.kv4_workspace(T, len(new), H, Hkv, D, 32, c.max_pages)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+        def call(st):
+            moe.kv4_attention(q, c.bytes, c.pages, c.kv_len, T, H, Hkv, D, 32, c.n_pages, c.max_pages, out, ws,
+                              q_off=off, n_seq=len(new), status=st)
+            torch.cuda.synchronize()
+
+        assert moe.linear_status() == 0
+        moe.linear_wait_limit(0)
+        try:
+            call(status)
+            assert int(status) == 2 and moe.linear_status() == 0
+            call(None)
+            assert moe.linear_status() == 2 and moe.linear_status() == 0
+        finally:
+            moe.linear_wait_limit(2000000)
+        status.zero_()
+        call(status)
+        assert int(status) == 0
+        check(out, q, c, o)
+
+
+def test_two_streams_at_once(moe):
+    """Different calls on two streams, each with its own workspace, many times over."""
+    g = gen(17)
+    jobs = []
+    for H, Hkv, D, new, have in ((12, 1, 128, [1, 1], [3000, 50]), (8, 2, 64, [150], [400])):
+        c = ref.Cache(g, have, Hkv, D, 64)
+        off, o = batch(new, c)
+        q = randn(g, o[-1], H, D).bfloat16()
+        n = moe.kv4_workspace(o[-1], len(new), H, Hkv, D, 64, c.max_pages)
+        jobs.append((c, off, o, q, torch.empty_like(q), torch.empty(max(n, 16), dtype=torch.uint8, device="cuda"),
+                     torch.cuda.Stream(), len(new)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, off, o, q, out, ws, st, n in jobs:
+            moe.kv4_attention(q, c.bytes, c.pages, c.kv_len, o[-1], q.shape[1], c.Hkv, q.shape[2], 64, c.n_pages,
+                              c.max_pages, out, ws, q_off=off, n_seq=n, stream=st)
+    torch.cuda.synchronize()
+    for c, off, o, q, out, ws, st, n in jobs:
+        check(out, q, c, o)
+
+
+@pytest.mark.parametrize("new", [[1], [40]])
+def test_far_pages_and_rows(moe, new):
+    """Pages past 4 GB of a cache, rows of q past 4 GB: appended to and attended."""
+    g = gen(18)
+    H, Hkv, D, page, have = 8, 8, 128, 256, [700]
+    c = ref.Cache(g, have, Hkv, D, page, spare=0)
+    n_pages = (5 << 30) // moe.kv4_page_bytes(page, Hkv, D)
+    far = torch.empty(n_pages, *c.bytes.shape[1:], dtype=torch.uint8, device="cuda")
+    last = torch.arange(n_pages - c.n_pages, n_pages, device="cuda")
+    far[last] = c.bytes
+    c.bytes, c.pages, c.n_pages = far, (c.pages + (n_pages - c.n_pages)).to(torch.int32), n_pages
+    n = new[0]
+    x = randn(g, 2, n, Hkv, D).bfloat16()
+    off, o = batch(new, c)
+    moe.kv4_append(x[0], x[1], c.bytes, c.pages, c.kv_len, n, Hkv, D, page, c.n_pages, c.max_pages, q_off=off,
+                   n_seq=1)
+    for kept, rows in ((c.K, x[0]), (c.V, x[1])):
+        kept[0][have[0] - n:] = ref.values(*ref.quantise(rows.float()))
+    if n == 1:
+        q = randn(g, 1, H, D).bfloat16()
+    else:
+        stride = (1 << 27) + 64   # 40 rows: 10 GB apart
+        wide = torch.empty(stride * (n - 1) + H * D, dtype=torch.bfloat16, device="cuda")
+        q = wide.as_strided((n, H, D), (stride, D, 1))
+        q.copy_(randn(g, n, H, D))
+    check(run(moe, q, c, new, off), q, c, o)
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first calls are captured: attributes and lookups work there."""
+    import subprocess
+    import sys
+    code = """
+import torch, expert_routing_grouped_gb300 as moe
+torch.cuda.init()
+D, H, Hkv, P = 64, 4, 2, 16
+k = torch.randn(40, Hkv, D, device='cuda').bfloat16()
+q = torch.randn(40, H, D, device='cuda').bfloat16()
+cache = torch.zeros(4, moe.kv4_page_bytes(P, Hkv, D), dtype=torch.uint8, device='cuda')
+pages = torch.tensor([[2, 0, 3, 1]], dtype=torch.int32, device='cuda')
+n = torch.tensor([40], dtype=torch.int32, device='cuda')
+off = torch.tensor([0, 40], dtype=torch.int32, device='cuda')
+out = torch.zeros_like(q)
+ws = torch.empty(max(16, moe.kv4_workspace(40, 1, H, Hkv, D, P, 4)), dtype=torch.uint8, device='cuda')
+f = torch.ones(D // 2, dtype=torch.float64, device='cuda')
+pos = torch.arange(40, dtype=torch.int32, device='cuda')
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    moe.rope(q, pos, f, 40, H, D, q)
+    moe.kv4_append(k, k, cache, pages, n, 40, Hkv, D, P, 4, 4, q_off=off, n_seq=1)
+    moe.kv4_attention(q, cache, pages, n, 40, H, Hkv, D, P, 4, 4, out, ws, q_off=off, n_seq=1)
+g.replay()
+torch.cuda.synchronize()
+assert bool(out.isfinite().all()) and float(out.abs().max()) > 0
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
