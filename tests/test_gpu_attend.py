@@ -655,3 +655,17 @@ torch.cuda.synchronize()
 assert bool(out.isfinite().all()) and float(out.abs().max()) > 0
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 30) + 5, 1 << 30])
+@pytest.mark.parametrize("H,new,have", [(2, [5, 3, 1], [3, 40, 1]), (4, [70, 40], [50, 60])])
+def test_widest_windows(moe, H, new, have, window):
+    """Windows as wide as int32 goes, with rows at negative positions: no window at all."""
+    g = gen(19)
+    c = ref.Cache(g, have, 2, 128, 16)
+    off, o = batch(new, c)
+    q = randn(g, o[-1], H, 128).bfloat16()
+    for causal in (True, False):
+        out = run(moe, q, c, new, off, window=window, causal=causal)
+        assert torch.equal(out, run(moe, q, c, new, off, causal=causal))
+        check(out, q, c, o, causal=causal)
