@@ -125,13 +125,15 @@ static __device__ __forceinline__ uint2 pack_out(float4 v) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNoScore = -1e30f;   // a maximum before any score
+constexpr float kNoScore = -3e38f;   // a maximum before any score
 
 static __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A score's factor held finite (an infinite one would make NaN of scores of 0).
+static __device__ __forceinline__ float finite(float x) { return fminf(fmaxf(x, -3.4028235e38f), 3.4028235e38f); }
 static __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -372,6 +372,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
     float back = p.scale * kLog2e * (p.softcap > 0.f ? 2.f / p.softcap : 1.f) * 16777216.f;   // 2^24
     back = up > 100 ? back * 7.888609052210118e-31f * __int_as_float((227 - up) << 23)   // 2^-100
                     : back * __int_as_float((127 - up) << 23);
+    back = finite(back);
     float sum[NG];
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
@@ -572,7 +573,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
           float &nmj = j ? nm[nt].y : nm[nt].x;
           const float now = -fmaxf(x, -nmj - (float)was) - (float)step_e;
-          const float f = ex2(now - nmj);   // first time: ex2(-1e30) = 0
+          const float f = ex2(now - nmj);   // first time: ex2(-3e38) = 0
           nmj = now;
           (j ? l[nt].y : l[nt].x) *= f;
 #pragma unroll

@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
         float f = __int_as_float((up + 127) << 23);
         cs = up > 100 ? cs * 7.888609052210118e-31f * __int_as_float((227 - up) << 23)   // 2^-100
                       : cs * __int_as_float((127 - up) << 23);
-        cs = fmaxf(cs, 1.17549435e-38f);
+        cs = fmaxf(finite(cs), 1.17549435e-38f);
         // s = cs (q f) . k with cs > 0: the scale's sign goes to q
         if (p.scale < 0.f) f = -f;
         if (p.scale == 0.f) f = 0.f;

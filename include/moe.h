@@ -405,11 +405,11 @@ int moe_linear_status(int32_t *status);
 /*
  * The time limit, in microseconds, of the waits between the pipelined roles of
  * a product, and of attention with more than 16 columns, for the calls that the
- * calling host thread makes from now on (default 2000000).  A wait that is not complete when its limit has passed
- * gives up: the kernel stops its roles, waits (with the full 2 s limit) for
- * its own copies and MMAs in flight, frees its tensor memory and returns, so
- * the next product runs normally; the status word holds 2, and moe_linear
- * returns MOE_OK (the launch succeeded).  0 makes every wait that is not
+ * calling host thread makes from now on (default 2000000).  A wait that is not
+ * complete when its limit has passed gives up: the kernel stops its roles, waits
+ * (with the full 2 s limit) for its own copies and MMAs in flight, frees its
+ * tensor memory and returns, so the next call runs normally; the status word
+ * holds 2, and the call returned MOE_OK (the launch succeeded).  0 makes every wait that is not
  * complete when first tested give up at once, and the first operands come late
  * enough for one to do so: a way to exercise that recovery path without a fault
  * or a hang, as MOE_OPT_WAIT_LIMIT_US is for the layer.  Products of at most
@@ -567,8 +567,8 @@ size_t moe_kv4_page_bytes(int page_size, int n_kv_heads, int head_dim);
  *          k_stride, v_stride (0: n_kv_heads head_dim)
  * k, v and cache 16-byte aligned, strides a multiple of 16 bytes and at most
  * 2^32; n_kv_heads <= 1024, T <= 2^24, T n_kv_heads <= 2^28, n_seq <= 65535,
- * max_pages page_size <= 2^30.  The cache must not overlap anything else.  T == 0 checks what it can
- * and launches nothing.  Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
+ * max_pages page_size <= 2^30.  The cache must not overlap anything else.  T == 0
+ * checks what it can and launches nothing.  Returns MOE_OK, MOE_ERR_ARG or MOE_ERR_DEVICE.
  */
 int moe_kv4_append(const void *k, const void *v, void *cache, const int32_t *pages,
                    const int32_t *q_off, const int32_t *kv_len, int T, int n_seq, int n_kv_heads,
@@ -601,6 +601,8 @@ int moe_kv4_append(const void *k, const void *v, void *cache, const int32_t *pag
  *            limits the waits of both)
  * Sums and softmax statistics are f32; keys, values and weights enter the
  * products as float16 (queries scaled by powers of two), out is rounded once.
+ * Scores past 2^24 leave their differences, and so the weights, no precision in
+ * f32, and results there may be infinite.
  * q, out and cache 16-byte aligned, strides a multiple of 8 and at most 2^31;
  * n_heads a multiple of n_kv_heads, n_heads <= 1024, T <= 2^19, n_seq <= 65535,
  * max_pages page_size <= 2^30, scale finite, softcap finite and >= 0.  out and

@@ -669,3 +669,29 @@ def test_widest_windows(moe, H, new, have, window):
         out = run(moe, q, c, new, off, window=window, causal=causal)
         assert torch.equal(out, run(moe, q, c, new, off, causal=causal))
         check(out, q, c, o, causal=causal)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_extreme_scales(moe, n, D):
+    """Factors beyond f32: scores of 0 stay 0, a cap of nearly nothing levels all
+    weights, and a row whose scores are all far below 0 still sees its tokens."""
+    g = gen(20)
+    c = ref.Cache(g, [90], 1, D, 16)
+    off, o = batch([n], c)
+    q = randn(g, n, 1, D).bfloat16()
+    zero = torch.zeros_like(q)
+    for x, kw in ((zero, dict(scale=3e38)), (zero, dict(scale=-2e38, softcap=1e-30)), (q, dict(scale=0.0)),
+                  (q, dict(scale=0.0, softcap=1e-40)), (q, dict(scale=1.0, softcap=1e-40)),
+                  (q, dict(scale=2.0 ** -140))):
+        check(run(moe, x, c, [n], off, **kw), x, c, o, **kw)
+    # Keys 1, 2, 3, ... times -2^100: the first token alone has weight.
+    rows = (1 + torch.arange(90.0, device="cuda"))[:, None, None].expand(90, 1, D)
+    assert torch.equal(c.put(0, 0, 0, rows), rows.double())
+    q = torch.full_like(q, -2.0 ** 100)
+    out = run(moe, q, c, [n], off).double()
+    want = c.V[0][0].double()
+    least = want.unflatten(1, (-1, 64)).amin(2, keepdim=True).expand(1, D // 64, 64).flatten(1)
+    # weight 1 (or 1 step, whose rounding meets the code), V and out rounded
+    tol = (2.0 ** -10 + 2.0 ** -8) * want.abs() * 1.01 + 2.0 ** -11 * (want - least)
+    assert bool(((out - want).abs() <= tol).all())
