@@ -146,3 +146,30 @@ def test_page_bytes():
     assert moe.kv4_page_bytes(16, 1, 64) == 16 * 72 and moe.kv4_page_bytes(64, 8, 128) == 64 * 8 * 144
     for bad in ((8, 1, 64), (16, 0, 64), (16, 1025, 64), (16, 1, 96), (0, 1, 64), (24, 1, 64)):
         assert moe.kv4_page_bytes(*bad) == 0
+
+
+def test_workspace():
+    """0 for sizes that the call refuses; a smaller one, none, or one that meets an
+    operand is refused."""
+    good = dict(T=6, n_seq=3, n_heads=8, n_kv_heads=2, head_dim=128, page_size=16, max_pages=4)
+    assert moe.kv4_workspace(**good) == 0   # 64 tokens at most: nothing to cut
+    good["max_pages"] = mp = 1024
+    need = moe.kv4_workspace(**good)
+    assert need > 0
+    for bad in (dict(T=0), dict(T=-1), dict(T=(1 << 19) + 1), dict(n_seq=0), dict(n_heads=9), dict(n_heads=1026),
+                dict(head_dim=96), dict(page_size=8), dict(max_pages=0), dict(max_pages=(1 << 26) + 1),
+                dict(max_q=-1)):
+        assert moe.kv4_workspace(**{**good, **bad}) == 0
+    assert attention(mp=mp, nb=need - 1) == moe.MOE_ERR_NOMEM and attention(mp=mp, nb=0) == moe.MOE_ERR_NOMEM
+    assert attention(mp=mp, ws=None, nb=0) == moe.MOE_ERR_ARG and attention(mp=mp, ws=None) == moe.MOE_ERR_ARG
+    for i in (0, 1, 2, 3, 4, 5, 8):   # q, out, cache, pages, q_off, kv_len, status
+        assert attention(mp=mp, ws=addr(i) - 16) == moe.MOE_ERR_ARG
+
+
+@pytest.mark.parametrize("H,Hkv", [(8, 8), (96, 8), (40, 1)])
+def test_workspace_is_enough_for_fewer(H, Hkv):
+    """What T rows need is enough for a known max_q, and for as many single rows."""
+    for T, S in ((1, 1), (64, 64), (300, 5), (4096, 1)):
+        all_ = moe.kv4_workspace(T, S, H, Hkv, 128, 64, 2048)
+        for mq in (1, 3, 16, 4096):
+            assert moe.kv4_workspace(T, S, H, Hkv, 128, 64, 2048, max_q=mq) <= all_
