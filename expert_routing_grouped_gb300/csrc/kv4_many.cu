@@ -163,6 +163,15 @@ __device__ __forceinline__ float2 add_2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ float2 mul_2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -218,6 +227,11 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float *v) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 template <int R>
@@ -585,9 +599,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
         const uint32_t at = s_col + h * kSub;
         float s[kSub];
         tmem_ld64(at, s);
+        // Capped: cap tanh(x / cap) = cap - 2 cap r, r = 1 / (1 + e^(2 x / cap)), so r stands
+        // for the score, and the least r for the largest.
+        constexpr float kUnseen = kCap ? INFINITY : -INFINITY;
         if constexpr (kCap) {
 #pragma unroll
-          for (int c = 0; c < kSub; ++c) s[c] = capped(s[c] * cs, cap_log2);
+          for (int c = 0; c < kSub; c += 2) {
+            const float2 x = mul_2(make_float2(s[c], s[c + 1]), make_float2(cs, cs));
+            const float2 e = add_2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
+            s[c] = rcp_approx(e.x), s[c + 1] = rcp_approx(e.y);
+          }
         }
         const uint32_t holes = *reinterpret_cast<const volatile uint16_t *>(&sm.holes[(t >> 1) & 3][2 * h]);
         if (t < free_lo || t >= free_hi || holes) {
@@ -595,20 +616,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
 #pragma unroll
           for (int c = 0; c < kSub; ++c) {
             const bool see = c >= a && c < b && !(holes >> (c / 32 * 8 + c / 16 % 2) & 1);
-            s[c] = see ? s[c] : -INFINITY;
+            s[c] = see ? s[c] : kUnseen;
           }
         }
+        auto most = [](float a, float b, float c) { return kCap ? min3(a, b, c) : max3(a, b, c); };
         float t8[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t8[e] = max3(s[e], s[e + 8], s[e + 16]);
+        for (int e = 0; e < 8; ++e) t8[e] = most(s[e], s[e + 8], s[e + 16]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t8[e] = max3(t8[e], s[e + 24], s[e + 32]);
+        for (int e = 0; e < 8; ++e) t8[e] = most(t8[e], s[e + 24], s[e + 32]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t8[e] = max3(t8[e], s[e + 40], s[e + 48]);
+        for (int e = 0; e < 8; ++e) t8[e] = most(t8[e], s[e + 40], s[e + 48]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t8[e] = fmaxf(t8[e], s[e + 56]);
-        const float scale = kCap ? 1.f : cs;
-        const float top = max3(max3(t8[0], t8[1], t8[2]), max3(t8[3], t8[4], t8[5]), fmaxf(t8[6], t8[7])) * scale;
+        for (int e = 0; e < 8; ++e) t8[e] = most(t8[e], t8[e], s[e + 56]);
+        const float far = most(most(t8[0], t8[1], t8[2]), most(t8[3], t8[4], t8[5]), most(t8[6], t8[7], t8[7]));
+        // A score is scale s + base.
+        const float scale = kCap ? -2.f * cap_log2 : cs, base = kCap ? cap_log2 : 0.f;
+        const float top = fmaf(far, scale, base);
         const bool over = top > m + 8.f;
         if (__any_sync(0xffffffffu, over)) {
           const float now = over ? top : m, f = ex2(m - now);
@@ -630,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
             }
           }
         }
-        const float2 sc = make_float2(scale, scale), nm = make_float2(-m, -m);
+        const float2 sc = make_float2(scale, scale), nm = make_float2(base - m, base - m);
         uint32_t v[kSub / 2];
 #pragma unroll
         for (int e = 0; e < kSub / 2; ++e) {
