@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv4_append_kernel(const App
     const KvSeq q = kv_seq_at(p.b, s);
     const int i = t - q.t0;
     pos = q.len - q.nq + i;
-    if (i < q.nq && pos >= 0) page = kv_page_at(p.b, s, pos);
+    if (i >= 0 && i < q.nq && pos >= 0) page = kv_page_at(p.b, s, pos);
   }
   if (page < 0) return;   // the whole warp's row
   const int slot = pos & ((1 << p.b.log_page) - 1);

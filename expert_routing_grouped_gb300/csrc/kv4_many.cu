@@ -273,7 +273,8 @@ __device__ __forceinline__ bool find_job(const AttendParams &p, int u, int nspli
   job.sq = attend_seq_at(p, job.s);
   const int rows = job.sq.rows * p.G;
   const long long first = (u - tile_base(p, job.s)) * kBlockRows;
-  if (rows <= kFewColumns || first >= rows) return false;
+  // (Offsets out of order can name a sequence that starts later.)
+  if (rows <= kFewColumns || first < 0 || first >= rows) return false;
   job.row0 = (int)first;
   const int last = min(rows, job.row0 + kBlockRows) - 1;
   const int pos0 = job.sq.len - job.sq.nq + job.row0 / p.G, pos1 = job.sq.len - job.sq.nq + last / p.G;

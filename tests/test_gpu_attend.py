@@ -695,3 +695,30 @@ def test_extreme_scales(moe, n, D):
     # weight 1 (or 1 step, whose rounding meets the code), V and out rounded
     tol = (2.0 ** -10 + 2.0 ** -8) * want.abs() * 1.01 + 2.0 ** -11 * (want - least)
     assert bool(((out - want).abs() <= tol).all())
+
+
+def test_offsets_out_of_order(moe):
+    """Offsets in any order: rows outside the call's and pages that are not the
+    sequences' own stay as they were, and the next ordered call is right."""
+    g = gen(21)
+    H, Hkv, D, page, T = 8, 2, 64, 16, 400
+    n = 40
+    c = ref.Cache(g, [60] * n, Hkv, D, page)
+    q = randn(g, T, H, D).bfloat16()
+    x = randn(g, 2, T, Hkv, D).bfloat16()
+    held = c.bytes.clone()
+    own = torch.zeros(c.n_pages, dtype=torch.bool, device="cuda")
+    own[c.pages[:, :4].reshape(-1).long()] = True
+    rng = np.random.default_rng(5)
+    for _ in range(8):
+        off = torch.from_numpy(rng.integers(-100, T + 100, n + 1).astype(np.int32)).cuda()
+        area = torch.full((T + 200, H, D), SENT, device="cuda").bfloat16()
+        run(moe, q, c, [0] * n, off, out=area[100:100 + T])
+        assert bool((area[:100] == SENT).all()) and bool((area[100 + T:] == SENT).all())
+        moe.kv4_append(x[0], x[1], c.bytes, c.pages, c.kv_len, T, Hkv, D, page, c.n_pages, c.max_pages,
+                       q_off=off, n_seq=n)
+        assert torch.equal(c.bytes[~own], held[~own])
+        c.bytes.copy_(held)
+    new = [10] * n
+    off, o = batch(new, c)
+    check(run(moe, q, c, new, off), q, c, o)
