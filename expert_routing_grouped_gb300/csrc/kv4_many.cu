@@ -32,8 +32,9 @@
 // The 8 dimensions of a word of codes lie in the order 0 4 1 5 2 6 3 7 (pairs of
 // nibbles i and i + 4 decode together), in Q as in K; the output puts V's back.
 //
-// Where a call has fewer blocks than SMs the keys are cut into parts, whose results
-// a second kernel joins.
+// A call of few tiles of rows has their key tiles in one line that is cut into equal
+// spans, one for each SM; a second kernel joins what was cut.  Larger calls have a
+// block for each tile of rows.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -47,8 +48,14 @@ constexpr int kKeys = 128;      // keys of a tile
 constexpr int kSub = 64;        // keys of a softmax step
 constexpr int kBlockRows = 2 * kRows;
 constexpr int kThreads = 512;
-constexpr int kMinPart = 4;     // key tiles of a part, at least
+constexpr int kMinPart = 4;     // key tiles of a span, at least
 constexpr int kSms = 152;
+// Tiles of rows (times KV heads) up to which the line is cut, one for each SM: 32 of
+// 128 key tiles take 57 us cut and 182 whole, 176 of 4 to 11 57 us cut and 45 whole
+// (joining is 7 to 10 us of a call).
+constexpr int kCutUnits = kSms;
+// What a tile of rows costs beside its key tiles, in those.
+constexpr int kSegmentCost = 2;
 
 // Registers a thread: 512 x 128 at launch, then by warpgroup; the shares add up to
 // what the block was launched with.
@@ -60,7 +67,17 @@ static_assert(2 * kSoftmaxRegs + kDecodeRegs + kIssueRegs == 4 * 128 && kSoftmax
 template <int D>
 struct Smem {
   static constexpr int kQ = kRows * D * 2, kK = kKeys * D * 2;   // one tile of Q; of K or V
-  static constexpr int kBytes = 2 * kQ + 4 * kK + 1024;          // two stages of K and V; room to align
+  static constexpr int kBytes = 2 * kQ + 4 * kK;                 // two stages of K and V
+};
+
+// Some key tiles of a tile of rows.
+struct Segment {
+  int s, hk;          // sequence, KV head
+  int q0, nq, len;    // the sequence's first row of q, its rows, its tokens
+  int row0, rows;     // the first row (token x head of the KV head), how many
+  int t0, n, end;     // key tiles t0 .. t0 + n - 1; the last key's successor, of all
+  int slot;           // of the partial result; -1: whole, and so final
+  __device__ __forceinline__ int steps() const { return min(n * 2, max(0, (end - t0 * kKeys + kSub - 1) / kSub)); }
 };
 
 struct Bars {
@@ -69,6 +86,7 @@ struct Bars {
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
+  int n_segments;
   uint8_t holes[4][4];   // [tile % 4][decoding warp]: two bits, 16 tokens each without a page
 };
 
@@ -249,69 +267,127 @@ __device__ __forceinline__ long long tile_base(const AttendParams &p, int s) {
   return row * p.G / kBlockRows + s;
 }
 
-struct Job {
-  int s, hk, row0;     // first row (token x head of the KV head) of the block
-  int lo, hi, end;     // key tiles that any of its rows sees; the last key's successor
-  int parts;
-  AttendSeq sq;
-};
+// The tile of rows at place u, of sequence s (the last that starts at or before it),
+// with all its key tiles; rows 0: none.
+__device__ __forceinline__ Segment tile_at(const AttendParams &p, int s, int u) {
+  Segment g{};
+  if (s < 0 || s >= p.b.n_seq) return g;
+  const AttendSeq sq = attend_seq_at(p, s);
+  const int rows = sq.rows * p.G;
+  const long long first = (u - tile_base(p, s)) * kBlockRows;
+  // (Offsets out of order can name a sequence that starts later.)
+  if (rows <= kFewColumns || first < 0 || first >= rows) return g;
+  g.s = s, g.q0 = sq.t0, g.nq = sq.nq, g.len = sq.len;
+  g.row0 = (int)first, g.rows = min(rows - g.row0, kBlockRows);
+  const int pos0 = sq.len - sq.nq + g.row0 / p.G, pos1 = sq.len - sq.nq + (g.row0 + g.rows - 1) / p.G;
+  g.end = p.causal ? min(sq.len, max(0, pos1 + 1)) : sq.len;
+  g.t0 = p.window ? max(0, pos0 - p.window + 1) / kKeys : 0;
+  g.n = max(0, (g.end + kKeys - 1) / kKeys - g.t0);
+  g.slot = -1;
+  return g;
+}
 
-// The job of place u, found by a whole warp; false: none.
-__device__ __forceinline__ bool find_job(const AttendParams &p, int u, int nsplit, Job &job) {
+// The sequence of place u, found by a whole warp.
+__device__ __forceinline__ int seq_of_place(const AttendParams &p, int u) {
   const int lane = threadIdx.x & 31;
   int base = 0, n = p.b.n_seq + 1;
   while (n > 32) {
     const int step = (n + 31) / 32, i = lane * step;
     const int k = __popc(__ballot_sync(0xffffffffu, i < n && tile_base(p, base + i) <= u));
-    if (k == 0) return false;
+    if (k == 0) return -1;
     const int skip = (k - 1) * step;
     base += skip;
     n = min(step, n - skip);
   }
-  job.s = base - 1 + __popc(__ballot_sync(0xffffffffu, lane < n && tile_base(p, base + lane) <= u));
-  if (job.s < 0 || job.s >= p.b.n_seq) return false;
-  job.sq = attend_seq_at(p, job.s);
-  const int rows = job.sq.rows * p.G;
-  const long long first = (u - tile_base(p, job.s)) * kBlockRows;
-  // (Offsets out of order can name a sequence that starts later.)
-  if (rows <= kFewColumns || first < 0 || first >= rows) return false;
-  job.row0 = (int)first;
-  const int last = min(rows, job.row0 + kBlockRows) - 1;
-  const int pos0 = job.sq.len - job.sq.nq + job.row0 / p.G, pos1 = job.sq.len - job.sq.nq + last / p.G;
-  const int end = p.causal ? min(job.sq.len, max(0, pos1 + 1)) : job.sq.len;
-  job.end = end;
-  job.lo = p.window ? max(0, pos0 - p.window + 1) / kKeys : 0;
-  job.hi = max(job.lo, (end + kKeys - 1) / kKeys);
-  job.parts = min(nsplit, max(1, (job.hi - job.lo) / kMinPart));
-  return true;
+  return base - 1 + __popc(__ballot_sync(0xffffffffu, lane < n && tile_base(p, base + lane) <= u));
 }
 
-// Key tiles of a part.
-__device__ __forceinline__ int part_at(const Job &job, int part) {
-  return job.lo + (int)((long long)(job.hi - job.lo) * part / job.parts);
+// What a block joins: the parts of one tile of rows, of the blocks first .. last.
+struct Joint {
+  int q0, hk, row0, rows;
+  int first, last, slot, pad;   // last <= first: nothing; the first one's slot
+};
+
+// The segments of this block's span into the list, in any order; scratch: shared
+// memory for a number for each place and one more.  At most two of them are partial:
+// slot 2 b for one that goes on from an earlier span, 2 b + 1 for one that starts in
+// this one and goes on in the next.
+__device__ __forceinline__ void cut_line(const AttendParams &p, int n_places, Bars &sm, Segment *list,
+                                         long long *scratch) {
+  __shared__ long long sums[kThreads / 32];
+  const int u = threadIdx.x, lane = u & 31, warp = u >> 5, b = blockIdx.x;
+  for (int s = u; s <= p.b.n_seq; s += kThreads) scratch[s] = tile_base(p, s);
+  if (u == 0) sm.n_segments = 0;
+  Joint *joint = reinterpret_cast<Joint *>(p.plan) + b;
+  if (u == 0) joint->first = 0, joint->last = 0;
+  __syncthreads();
+  Segment g{};
+  if (u < n_places) {
+    int lo = 0, hi = p.b.n_seq + 1;   // the last base at or before u is in lo .. hi - 1, if any is
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (scratch[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    g = tile_at(p, scratch[lo] <= u ? lo : -1, u);
+  }
+  const int tiles = max(g.n, 1), span = g.rows ? tiles + kSegmentCost : 0;
+  long long x = (long long)span * p.b.Hkv;
+  const long long mine = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += a;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  long long start = x - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) start += sums[w];
+    total += sums[w];
+  }
+  const long long len = max((total + kSms - 1) / kSms, (long long)kMinPart), begin = len * b, end = begin + len;
+  if (span && start < end && start + mine > begin) {
+    for (int hk = begin > start ? (int)((begin - start) / span) : 0; hk < p.b.Hkv; ++hk) {
+      const long long at = start + (long long)hk * span;   // this head's tiles: at .. at + tiles
+      if (at >= end) break;
+      const int a = (int)max(begin - at, 0ll), z = (int)min(end - at, (long long)tiles);
+      if (a >= z) continue;
+      Segment h = g;
+      h.hk = hk;
+      h.t0 += a, h.n = min(z, g.n) - a;
+      if (a > 0 || z < tiles) h.slot = 2 * b + (at > begin);
+      if (a == 0 && z < tiles)
+        *joint = Joint{g.q0, hk, g.row0, g.rows, b, (int)((at + tiles - 1) / len), h.slot, 0};
+      list[atomicAdd(&sm.n_segments, 1)] = h;
+    }
+  }
+  __syncthreads();
 }
 
-// The codes' role, a warpgroup (wd the warp in it): a part's key tiles, decoded into
-// their stages.  It sets the pace of a prompt: what it need not wait for is asked for a
-// tile ahead.
+// The codes' role, a warpgroup (wd the warp in it): a segment's key tiles, decoded into
+// their stages (done: tiles before them).  It sets the pace of a prompt: what it need
+// not wait for is asked for a tile ahead.  false: gave up.
 template <int D>
-__device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &job, Bars &sm, uint8_t *k_s, uint8_t *v_s,
-                                             int hk, int t0, int n_tiles, int wd) {
+__device__ __forceinline__ bool decode_tiles(const AttendParams &p, const Segment &job, Bars &sm, uint8_t *k_s,
+                                             uint8_t *v_s, int done, int wd) {
+  const int t0 = job.t0, n_tiles = job.n;
   // A warp has 32 tokens of the tile, in rounds of 512 neighbouring bytes of codes: a
   // lane has 16 of them, 32 dimensions of one token.
   constexpr int kPieces = D / 32, kPer = 32 / kPieces, kRounds = 32 / kPer;   // tokens of a round: 8 (D = 64: 16)
   const int lane = threadIdx.x & 31;
   const int lp = p.b.log_page, w0 = wd * 32, tk = lane / kPieces, pc = lane % kPieces, g = pc / 2;
   const int32_t *pages = p.b.pages + (size_t)job.s * p.b.max_pages;
-  const uint8_t *head = p.cache + (size_t)hk * KvBlock<D>::bytes(lp);
+  const uint8_t *head = p.cache + (size_t)job.hk * KvBlock<D>::bytes(lp);
   const size_t page_bytes = KvBlock<D>::bytes(lp) * p.b.Hkv;
   // The page numbers of the warp's first and last 16 tokens of tile j as they stand in
   // the table (looked at a tile later, when they have come).
   auto pages_of = [&](int j) {
     const int token = (t0 + j) * kKeys + w0;
     int2 r = make_int2(-1, -1);
-    if (j < n_tiles && token < job.sq.len) r.x = __ldg(pages + (token >> lp));
-    if (lp == 4 && j < n_tiles && token + 16 < job.sq.len) r.y = __ldg(pages + (token >> lp) + 1);
+    if (j < n_tiles && token < job.len) r.x = __ldg(pages + (token >> lp));
+    if (lp == 4 && j < n_tiles && token + 16 < job.len) r.y = __ldg(pages + (token >> lp) + 1);
     return r;
   };
   struct Codes {
@@ -323,7 +399,7 @@ __device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &j
   const uint32_t scales_v = KvBlock<D>::scales(lp, 1, 0) - KvBlock<D>::scales(lp, 0, 0);
   // Codes and scales of K (which 0) or V; zeros where there is no page or no token.
   auto load = [&](int j, int2 page, int which, Codes &x) {
-    const int token0 = (t0 + j) * kKeys + w0, left = j < n_tiles ? job.sq.len - token0 - tk : 0;
+    const int token0 = (t0 + j) * kKeys + w0, left = j < n_tiles ? job.len - token0 - tk : 0;
     if (lp > 4) page.y = page.x;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -366,17 +442,12 @@ __device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &j
       for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + at[e] + c * kPer * 128) = d[e];
     }
   };
-  if (p.wait_ns == 0) {   // a limit of 0 is there to show the way out: the first operands come late
-    const unsigned long long start = globaltimer();
-    while (globaltimer() - start < 20000ull) {
-    }
-  }
   Codes k, v;
   int2 page = pages_of(0), next = pages_of(1);
   load(0, page, 0, k);
   load(0, page, 1, v);
   for (int j = 0; j < n_tiles; ++j) {
-    const int st = j & 1;
+    const int all = done + j, st = all & 1, parity = ((all >> 1) & 1) ^ 1;
     // A token whose V holds a NaN: its K becomes NaN, its V zeros, so that only the
     // rows that see it know.
     bool nan = false;
@@ -390,17 +461,17 @@ __device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &j
       }
     }
     // (The issuers order what is written here before the MMAs.)
-    if (!wait_all(&sm.k_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
+    if (!wait_all(&sm.k_empty[st], parity, &sm.abort, p.status)) return false;
     if (lane == 0) {
-      const int left = job.sq.len - (t0 + j) * kKeys - w0, y = lp > 4 ? page.x : page.y;
-      sm.holes[j & 3][wd] = (left > 0 && (unsigned)page.x >= (unsigned)p.b.n_pages ? 1 : 0) |
+      const int left = job.len - (t0 + j) * kKeys - w0, y = lp > 4 ? page.x : page.y;
+      sm.holes[all & 3][wd] = (left > 0 && (unsigned)page.x >= (unsigned)p.b.n_pages ? 1 : 0) |
                             (left > 16 && (unsigned)y >= (unsigned)p.b.n_pages ? 2 : 0);
     }
     write(k_s + st * Smem<D>::kK, k);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.k_full[st]);
     load(j + 1, next, 0, k);
-    if (!wait_all(&sm.v_empty[st], ((j >> 1) & 1) ^ 1, &sm.abort, p.status)) break;
+    if (!wait_all(&sm.v_empty[st], parity, &sm.abort, p.status)) return false;
     write(v_s + st * Smem<D>::kK, v);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.v_full[st]);
@@ -408,12 +479,13 @@ __device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &j
     page = next;
     next = pages_of(j + 2);
   }
+  return true;
 }
 
 // The MMAs of tile i of rows, issued by one thread.
-template <int D, int i>
+template <int D, int i, bool kCut>
 __device__ __forceinline__ void issue_tile(const AttendParams &p, Bars &sm, uint8_t *q_s, uint8_t *k_s, uint8_t *v_s,
-                                           int n_sub) {
+                                           const Segment *list) {
   // Everything that differs between the MMAs of two steps is a constant: they take 32
   // to 64 clocks each, and the issue of one, beside three busy warps of the scheduler,
   // takes about as long.
@@ -447,65 +519,93 @@ __device__ __forceinline__ void issue_tile(const AttendParams &p, Bars &sm, uint
   };
   constexpr Int<0> c0{};
   constexpr Int<1> c1{};
-  // Step t (half h of stage st): its outputs, and the scores of step t + 2 in its place.
-  auto step = [&](int t, auto st_, auto nx_, auto h_) {
-    constexpr int st = decltype(st_)::value, nx = decltype(nx_)::value, h = decltype(h_)::value;
-    const bool more = t + 2 < n_sub;
-    if (h == 0) {
-      wait(&sm.v_full[st], (t >> 2) & 1);
-      if (more) wait(&sm.k_full[nx], ((t + 2) >> 2) & 1);
-      fence_proxy_async();
-    }
-    if (!wait(&sm.p_full[i][h], (t >> 1) & 1)) return;
-    tc_fence_after();
-    outputs(st_, h_, t);
-    if (more) scores(nx_, h_);
-    if (h == 1) {
-      mma_commit(&sm.v_empty[st]);
-      mma_commit(&sm.k_empty[nx]);
-    }
+  // What a barrier has been through, over all segments: key tiles, each half's steps, Q.
+  int all = 0, halves[2] = {0, 0}, queries = 0;
+  // Key tile j of a segment, in stage st: its outputs, and the scores of the next one
+  // (stage nx) in its place.
+  auto tile = [&](int j, int n_tiles, int n_sub, auto st_, auto nx_) {
+    constexpr int st = decltype(st_)::value, nx = decltype(nx_)::value;
+    wait(&sm.v_full[st], (all >> 1) & 1);
+    if (j + 1 < n_tiles) wait(&sm.k_full[nx], ((all + 1) >> 1) & 1);
+    fence_proxy_async();
+    auto half = [&](auto h_) {
+      constexpr int h = decltype(h_)::value;
+      const int t = 2 * j + h;
+      if (t >= n_sub || !wait(&sm.p_full[i][h], halves[h] & 1)) return;
+      ++halves[h];
+      tc_fence_after();
+      outputs(st_, h_, t);
+      if (t + 2 < n_sub) scores(nx_, h_);
+    };
+    half(c0);
+    half(c1);
+    mma_commit(&sm.v_empty[st]);
+    if (j + 1 < n_tiles) mma_commit(&sm.k_empty[nx]);
+    ++all;
   };
-  if (n_sub > 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[i], 0)) {
+  auto first = [&](int n_sub, auto st_) {
+    constexpr int st = decltype(st_)::value;
+    if (!wait(&sm.k_full[st], (all >> 1) & 1) || !wait(&sm.q_full[i], queries & 1)) return;
+    ++queries;
     fence_proxy_async();
     tc_fence_after();
-    scores(c0, c0);
-    if (n_sub > 1) scores(c0, c1);
-    mma_commit(&sm.k_empty[0]);
-  }
-  for (int t = 0; ok && t < n_sub; t += 4) {
-    step(t, c0, c1, c0);
-    if (ok && t + 1 < n_sub) step(t + 1, c0, c1, c1);
-    if (ok && t + 2 < n_sub) step(t + 2, c1, c0, c0);
-    if (ok && t + 3 < n_sub) step(t + 3, c1, c0, c1);
+    scores(st_, c0);
+    if (n_sub > 1) scores(st_, c1);
+    mma_commit(&sm.k_empty[st]);
+  };
+  for (int g = 0; ok && g < (kCut ? sm.n_segments : 1); ++g) {
+    const Segment &job = list[g];
+    const int n = job.n;
+    if (i == 1 && job.rows <= kRows) {   // no second tile of rows: its stages are let go
+      for (int j = 0; ok && j < n; ++j, ++all) {
+        const int st = all & 1, parity = (all >> 1) & 1;
+        if (wait(&sm.k_full[st], parity)) mbar_arrive(&sm.k_empty[st]);
+        if (wait(&sm.v_full[st], parity)) mbar_arrive(&sm.v_empty[st]);
+      }
+      continue;
+    }
+    if (n == 0) continue;
+    const int n_sub = job.steps();
+    if (all & 1) first(n_sub, c1);
+    else first(n_sub, c0);
+    for (int j = 0; ok && j < n; ++j) {
+      if (all & 1) tile(j, n, n_sub, c1, c0);
+      else tile(j, n, n_sub, c0, c1);
+    }
   }
   // One more commit covers every MMA issued; tensor memory is freed after it.
   mma_commit(&sm.drain[i]);
   drain_bar(&sm.drain[i], 0, globaltimer());
 }
 
-template <int D, bool kCap>
-__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int nsplit) {
+// kCut: a block takes a span of the line; otherwise one tile of rows.
+template <int D, bool kCap, bool kCut>
+__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int n_places) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Bars sm;
+  __shared__ Segment list[kCut ? kCutUnits : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // Heads of one place are neighbours, the last places (of a prompt: the rows that
-  // see most keys) come first.
-  const int unit = gridDim.x - 1 - blockIdx.x, u = unit / p.b.Hkv, hk = unit - u * p.b.Hkv;
-  Job job;
-  if (!find_job(p, u, nsplit, job) || (int)blockIdx.y >= job.parts) return;
-  const int part = blockIdx.y, t0 = part_at(job, part), n_tiles = part_at(job, part + 1) - t0;
-  const int n_sub = min(n_tiles * 2, max(0, (job.end - t0 * kKeys + kSub - 1) / kSub));   // steps
-  const int rows = min(job.sq.rows * p.G - job.row0, kBlockRows);
-  const int tiles = rows > kRows ? 2 : 1;   // tiles of rows
+  if constexpr (kCut) {
+    cut_line(p, n_places, sm, list, reinterpret_cast<long long *>(smem));
+    if (sm.n_segments == 0) return;
+  } else {
+    // Heads of one place are neighbours, the last places (of a prompt: the rows that
+    // see most keys) come first.
+    const int unit = gridDim.x - 1 - blockIdx.x, u = unit / p.b.Hkv;
+    Segment g = tile_at(p, seq_of_place(p, u), u);
+    g.hk = unit - u * p.b.Hkv;
+    if (g.rows == 0) return;
+    if (threadIdx.x == 0) list[0] = g;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.k_full[i], 4);
-      mbar_init(&sm.k_empty[i], tiles);
+      mbar_init(&sm.k_empty[i], 2);
       mbar_init(&sm.v_full[i], 4);
-      mbar_init(&sm.v_empty[i], tiles);
+      mbar_init(&sm.v_empty[i], 2);
       mbar_init(&sm.s_full[i][0], 1);
       mbar_init(&sm.s_full[i][1], 1);
       mbar_init(&sm.p_full[i][0], 4);
@@ -536,16 +636,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
     more_regs<kSoftmaxRegs>();
     const int i = warp >> 2, r = (warp & 3) * 32 + lane;   // tile, row of the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const int row = job.row0 + i * kRows + r;
-    const bool mine = i * kRows + r < rows;
-    const int tok = min(row, job.sq.rows * p.G - 1) / p.G, h = hk * p.G + row - tok * p.G;
-    if (i < tiles) {
+    int all = 0, even = 0, odd = 0;   // key tiles, and steps of each half, before this segment
+    bool ok = true;
+    for (int g = 0; ok && g < (kCut ? sm.n_segments : 1); ++g) {
+      const Segment job = list[g];
+      const int t0 = job.t0, n_sub = job.steps(), tiles0 = all;
+      all += job.n;
+      if (i * kRows >= job.rows) continue;
+      const int row = job.row0 + i * kRows + r;
+      const bool mine = i * kRows + r < job.rows;
+      const int tok = min(row, job.row0 + job.rows - 1) / p.G, h = job.hk * p.G + row - tok * p.G;
       // The row of Q: scaled, in the codes' order, into the swizzled tile.
       float cs = fabsf(p.scale) * kLog2e * (kCap ? 2.f / p.softcap : 1.f);
       if (p.scale == 0.f) cs = 1.f;
-      {
+      if (n_sub > 0) {
         uint4 raw[D / 8];
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)(job.sq.t0 + tok) * p.ldq + (size_t)h * D);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)(job.q0 + tok) * p.ldq + (size_t)h * D);
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
@@ -582,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
         if (lane == 0) mbar_arrive(&sm.q_full[i]);
       }
       // Keys first .. end - 1 are the row's.
-      const int pos = job.sq.len - job.sq.nq + tok;
-      const int end = p.causal ? min(job.sq.len, pos + 1) : job.sq.len;
+      const int pos = job.len - job.nq + tok;
+      const int end = p.causal ? min(job.len, pos + 1) : job.len;
       const int first = p.window ? max(0, pos - p.window + 1) : 0;
       const float cap_log2 = p.softcap * kLog2e;
       const uint32_t s_col = tmem + lane_base + i * kKeys, o_at = tmem + lane_base + o_col + i * D;
@@ -592,10 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       const int free_hi = __reduce_min_sync(0xffffffffu, end) / kSub - 2 * t0;
       float m = kNoScore;
       float2 l = make_float2(0.f, 0.f);
-      bool ok = true;
       for (int t = 0; t < n_sub; ++t) {
         const int h = t & 1;
-        if (!(ok = wait_all(&sm.s_full[i][h], (t >> 1) & 1, &sm.abort, p.status))) break;
+        if (!(ok = wait_all(&sm.s_full[i][h], ((h ? odd : even) + (t >> 1)) & 1, &sm.abort, p.status))) break;
         tc_fence_after();
         const uint32_t at = s_col + h * kSub;
         float s[kSub];
@@ -611,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
             s[c] = rcp_approx(e.x), s[c + 1] = rcp_approx(e.y);
           }
         }
-        const uint32_t holes = *reinterpret_cast<const volatile uint16_t *>(&sm.holes[(t >> 1) & 3][2 * h]);
+        const uint32_t holes = *reinterpret_cast<const volatile uint16_t *>(&sm.holes[(tiles0 + (t >> 1)) & 3][2 * h]);
         if (t < free_lo || t >= free_hi || holes) {
           const int k0 = t0 * kKeys + t * kSub, a = first - k0, b = end - k0;
 #pragma unroll
@@ -642,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
           if (t > 0) {
             // The outputs so far: the last step's MMAs are done first.  (Step t - 3's are:
             // these scores came after step t - 2's.)
-            if (!(ok = wait_all(&sm.o_done[i][h ^ 1], ((t - 1) >> 1) & 1, &sm.abort, p.status))) break;
+            if (!(ok = wait_all(&sm.o_done[i][h ^ 1], ((h ? even : odd) + ((t - 1) >> 1)) & 1, &sm.abort, p.status))) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
@@ -669,13 +774,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[i][h]);
       }
-      if (ok && n_sub > 0) ok = wait_all(&sm.o_done[i][(n_sub - 1) & 1], ((n_sub - 1) >> 1) & 1, &sm.abort, p.status);
+      if (!ok) break;
+      even += (n_sub + 1) >> 1, odd += n_sub >> 1;
+      // The last step is its half's last.
+      if (n_sub > 0) ok = wait_all(&sm.o_done[i][(n_sub - 1) & 1], ((n_sub & 1 ? even : odd) - 1) & 1, &sm.abort, p.status);
       if (ok) {
         tc_fence_after();
         const float sum = l.x + l.y;
-        if (job.parts == 1) {
+        if (job.slot < 0) {
           const float f = sum != 0.f ? 1.f / sum : 0.f;
-          __nv_bfloat16 *dst = p.out + (size_t)(job.sq.t0 + tok) * p.ldo + (size_t)h * D;
+          __nv_bfloat16 *dst = p.out + (size_t)(job.q0 + tok) * p.ldo + (size_t)h * D;
 #pragma unroll
           for (int c = 0; c < D; c += 16) {
             float o[16];
@@ -694,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
             }
           }
         } else {
-          const size_t at = ((size_t)unit * nsplit + part) * kBlockRows + i * kRows + r;
+          const size_t at = (size_t)job.slot * kBlockRows + i * kRows + r;
           float *dst = p.part_o + at * D;
 #pragma unroll
           for (int c = 0; c < D; c += 16) {
@@ -714,13 +822,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
   } else if (warp < 12) {
     // -------------------------------------------------------------- decode
     fewer_regs<kDecodeRegs>();
-    decode_tiles<D>(p, job, sm, k_s, v_s, hk, t0, n_tiles, warp - 8);
+    if (p.wait_ns == 0) {   // a limit of 0 is there to show the way out: the first operands come late
+      const unsigned long long start = globaltimer();
+      while (globaltimer() - start < 20000ull) {
+      }
+    }
+    int done = 0;
+    for (int g = 0; g < (kCut ? sm.n_segments : 1); ++g) {
+      const Segment job = list[g];
+      if (!decode_tiles<D>(p, job, sm, k_s, v_s, done, warp - 8)) break;
+      done += job.n;
+    }
   } else {
     // --------------------------------------------------------------- issue
     fewer_regs<kIssueRegs>();
     // A warp for each tile of rows: they wait for their own softmax only.
-    if (warp == 12 && elect_one()) issue_tile<D, 0>(p, sm, q_s, k_s, v_s, n_sub);
-    if (warp == 13 && tiles > 1 && elect_one()) issue_tile<D, 1>(p, sm, q_s, k_s, v_s, n_sub);
+    if (warp == 12 && elect_one()) issue_tile<D, 0, kCut>(p, sm, q_s, k_s, v_s, list);
+    if (warp == 13 && elect_one()) issue_tile<D, 1, kCut>(p, sm, q_s, k_s, v_s, list);
     __syncwarp();
   }
   tc_fence_before();
@@ -731,65 +849,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
   }
 }
 
-// Joins the parts of four rows of a block, a warp each.
+// Joins the parts of what block blockIdx.x began, a warp a row.
+constexpr int kJoinWarps = 8, kJoinBlocks = 8;
 template <int D>
-__global__ void __launch_bounds__(128) kv4_many_join_kernel(const AttendParams p, int nsplit) {
-  const int unit = blockIdx.x, u = unit / p.b.Hkv, hk = unit - u * p.b.Hkv;
-  Job job;
-  const bool any = find_job(p, u, nsplit, job) && job.parts > 1;
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_many_join_kernel(const AttendParams p) {
   // Every block waits: this grid must not be over before the one it joins.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (!any || job.row0 + r >= job.sq.rows * p.G) return;
-  const int row = job.row0 + r;
+  const int4 *plan = reinterpret_cast<const int4 *>(after_wait(p.plan)) + 2 * blockIdx.x;
+  const int4 what = __ldcg(plan), span = __ldcg(plan + 1);   // q0, hk, row0, rows; first, last, slot
+  if (span.y <= span.x) return;
+  const int lane = threadIdx.x & 31;
   const float *po = after_wait(p.part_o);
   const float2 *pml = after_wait(p.part_ml);
-  const size_t first = (size_t)unit * nsplit * kBlockRows + r;
-  RowPart rp;
-  for (int i = 0; i < job.parts; i += 8)
-    rp.take<8, D>(po, pml, job.parts - i, lane, [&](int k) { return first + (size_t)(i + k) * kBlockRows; });
-  if (lane >= D / 4) return;
-  const int tok = row / p.G, h = hk * p.G + row - tok * p.G;
-  *reinterpret_cast<uint2 *>(p.out + (size_t)(job.sq.t0 + tok) * p.ldo + (size_t)h * D + lane * 4) = rp.result();
+  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < what.w; r += gridDim.y * kJoinWarps) {
+    RowPart rp;
+    for (int b = span.x; b <= span.y; b += 8)
+      rp.take<8, D>(po, pml, span.y - b + 1, lane, [&](int k) {
+        return (size_t)(b + k == span.x ? span.z : 2 * (b + k)) * kBlockRows + r;
+      });
+    if (lane >= D / 4) continue;
+    const int row = what.z + r, tok = row / p.G, h = what.y * p.G + row - tok * p.G;
+    *reinterpret_cast<uint2 *>(p.out + (size_t)(what.x + tok) * p.ldo + (size_t)h * D + lane * 4) = rp.result();
+  }
 }
 
-// Places of all sequences' tiles of rows, and the parts that keys may be cut into.
+// Places of all sequences' tiles of rows.
 long long places(const AttendParams &p) {
   const long long rows = (p.b.q_off ? (long long)p.b.T : p.b.n_seq) * p.G;
   return rows / kBlockRows + p.b.n_seq;
 }
-int split_of(const AttendParams &p) {
-  const long long keys = (long long)p.b.max_pages << p.b.log_page;
-  const long long most = std::max<long long>(1, (keys + kKeys - 1) / kKeys / kMinPart);
-  return (int)std::max<long long>(1, std::min<long long>(kSms / (places(p) * p.b.Hkv), most));
+bool cuts(const AttendParams &p) {
+  return places(p) * p.b.Hkv <= kCutUnits && ((long long)p.b.max_pages << p.b.log_page) > kMinPart * kKeys;
 }
 
-template <int D, bool kCap>
+template <int D, bool kCap, bool kCut>
 cudaError_t launch(const AttendParams &p, cudaStream_t st) {
-  auto kernel = kv4_many_kernel<D, kCap>;
+  auto kernel = kv4_many_kernel<D, kCap, kCut>;
   static DeviceOnce once;
   cudaError_t err = once.run([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   });
   if (err != cudaSuccess) return err;
-  const int nsplit = split_of(p);
-  const unsigned units = (unsigned)(places(p) * p.b.Hkv);
-  err = launch_k(false, kernel, dim3(units, nsplit), dim3(kThreads), Smem<D>::kBytes, st, p, nsplit);
-  if (err != cudaSuccess || nsplit == 1) return err;
-  return launch_k(true, kv4_many_join_kernel<D>, dim3(units, kBlockRows / 4), dim3(128), 0, st, p, nsplit);
+  const int n = (int)places(p);
+  err = launch_k(false, kernel, dim3(kCut ? kSms : (unsigned)n * p.b.Hkv), dim3(kThreads), Smem<D>::kBytes, st, p, n);
+  if (err != cudaSuccess || !kCut) return err;
+  // Rows that a tile may have.
+  const long long rows = (long long)(p.max_q ? std::min(p.max_q, p.b.T) : p.b.T) * p.G;
+  const int ny = (int)std::min<long long>(kJoinBlocks, (rows + kJoinWarps - 1) / kJoinWarps);
+  return launch_k(true, kv4_many_join_kernel<D>, dim3(kSms, ny), dim3(kJoinWarps * 32), 0, st, p);
+}
+template <int D>
+cudaError_t launch(const AttendParams &p, cudaStream_t st) {
+  if (cuts(p)) return p.softcap > 0.f ? launch<D, true, true>(p, st) : launch<D, false, true>(p, st);
+  return p.softcap > 0.f ? launch<D, true, false>(p, st) : launch<D, false, false>(p, st);
 }
 
 }  // namespace
 
 // Partial results of a call, in rows of D and of (maximum, sum).
 size_t many_rows(const AttendParams &p) {
-  const int nsplit = split_of(p);
-  return nsplit == 1 ? 0 : (size_t)places(p) * p.b.Hkv * nsplit * kBlockRows;
+  return cuts(p) ? (size_t)2 * kSms * kBlockRows : 0;
+}
+
+// Bytes of what a call's blocks tell the joining ones.
+size_t many_plan_bytes(const AttendParams &p) {
+  static_assert(sizeof(Joint) == 2 * sizeof(int4), "as the joining kernel reads it");
+  return cuts(p) ? kSms * sizeof(Joint) : 0;
 }
 
 cudaError_t launch_many(const AttendParams &p, int D, cudaStream_t st) {
-  if (D == 64) return p.softcap > 0.f ? launch<64, true>(p, st) : launch<64, false>(p, st);
-  return p.softcap > 0.f ? launch<128, true>(p, st) : launch<128, false>(p, st);
+  return D == 64 ? launch<64>(p, st) : launch<128>(p, st);
 }
 
 }  // namespace moe
