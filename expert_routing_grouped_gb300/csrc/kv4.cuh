@@ -94,7 +94,6 @@ struct AttendParams {
   float scale, softcap;
   float *part_o;             // [slot][column][D] partial outputs
   float2 *part_ml;           // [slot][column] (maximum, sum)
-  void *plan;                // what the blocks of kv4_many.cu tell the joining ones
   int target;                // blocks that a batch is spread over
   int32_t *status;
   unsigned long long wait_ns;
@@ -118,7 +117,6 @@ size_t few_slots(const AttendParams &p);
 cudaError_t launch_few(const AttendParams &p, int D, cudaStream_t st);
 
 size_t many_rows(const AttendParams &p);
-size_t many_plan_bytes(const AttendParams &p);
 cudaError_t launch_many(const AttendParams &p, int D, cudaStream_t st);
 
 static __device__ __forceinline__ uint2 pack_out(float4 v) {

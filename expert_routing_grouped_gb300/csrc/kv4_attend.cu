@@ -27,7 +27,7 @@ bool may_have_many(const AttendParams &p) {
 
 // Where the partial results of a call lie in its workspace.
 struct Scratch {
-  size_t o, ml, plan, bytes;
+  size_t o, ml, bytes;
 };
 Scratch workspace_of(const AttendParams &p, int D) {
   // The kernels run one after the other: one area serves both.
@@ -36,8 +36,7 @@ Scratch workspace_of(const AttendParams &p, int D) {
   Scratch w;
   w.o = 0;
   w.ml = rows * D * sizeof(float);
-  w.plan = w.ml + rows * sizeof(float2);
-  w.bytes = w.plan + (may_have_many(p) ? many_plan_bytes(p) : 0);
+  w.bytes = w.ml + rows * sizeof(float2);
   return w;
 }
 
@@ -105,7 +104,6 @@ extern "C" __attribute__((visibility("default"))) int moe_kv4_attention(
   if (w.bytes) {
     p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.o);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + w.ml);
-    p.plan = static_cast<uint8_t *>(workspace) + w.plan;
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err = cudaSuccess;

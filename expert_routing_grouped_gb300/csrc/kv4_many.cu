@@ -32,9 +32,9 @@
 // The 8 dimensions of a word of codes lie in the order 0 4 1 5 2 6 3 7 (pairs of
 // nibbles i and i + 4 decode together), in Q as in K; the output puts V's back.
 //
-// A call of few tiles of rows has their key tiles in one line that is cut into equal
-// spans, one for each SM; a second kernel joins what was cut.  Larger calls have a
-// block for each tile of rows.
+// Where a call has fewer blocks than SMs the keys are cut into parts, whose results
+// a second kernel joins.  (One line of all key tiles cut into equal spans, as for few
+// rows, was slower: 512 rows of 32/8 heads over 16384 keys 163 us against 133.)
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -48,14 +48,8 @@ constexpr int kKeys = 128;      // keys of a tile
 constexpr int kSub = 64;        // keys of a softmax step
 constexpr int kBlockRows = 2 * kRows;
 constexpr int kThreads = 512;
-constexpr int kMinPart = 4;     // key tiles of a span, at least
+constexpr int kMinPart = 4;     // key tiles of a part, at least
 constexpr int kSms = 152;
-// Tiles of rows (times KV heads) up to which the line is cut, one for each SM: 32 of
-// 128 key tiles take 57 us cut and 182 whole, 176 of 4 to 11 57 us cut and 45 whole
-// (joining is 7 to 10 us of a call).
-constexpr int kCutUnits = kSms;
-// What a tile of rows costs beside its key tiles, in those.
-constexpr int kSegmentCost = 2;
 
 // Registers a thread: 512 x 128 at launch, then by warpgroup; the shares add up to
 // what the block was launched with.
@@ -70,13 +64,14 @@ struct Smem {
   static constexpr int kBytes = 2 * kQ + 4 * kK;                 // two stages of K and V
 };
 
-// Some key tiles of a tile of rows.
-struct Segment {
+// What a block works out: some key tiles of a tile of rows.
+struct Job {
   int s, hk;          // sequence, KV head
   int q0, nq, len;    // the sequence's first row of q, its rows, its tokens
   int row0, rows;     // the first row (token x head of the KV head), how many
-  int t0, n, end;     // key tiles t0 .. t0 + n - 1; the last key's successor, of all
-  int slot;           // of the partial result; -1: whole, and so final
+  int t0, n, end;     // key tiles t0 .. t0 + n - 1; the last key's successor, of all parts
+  int parts;
+  // Steps of 64 keys.
   __device__ __forceinline__ int steps() const { return min(n * 2, max(0, (end - t0 * kKeys + kSub - 1) / kSub)); }
 };
 
@@ -86,7 +81,6 @@ struct Bars {
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
-  int n_segments;
   uint8_t holes[4][4];   // [tile % 4][decoding warp]: two bits, 16 tokens each without a page
 };
 
@@ -269,8 +263,8 @@ __device__ __forceinline__ long long tile_base(const AttendParams &p, int s) {
 
 // The tile of rows at place u, of sequence s (the last that starts at or before it),
 // with all its key tiles; rows 0: none.
-__device__ __forceinline__ Segment tile_at(const AttendParams &p, int s, int u) {
-  Segment g{};
+__device__ __forceinline__ Job tile_at(const AttendParams &p, int s, int u) {
+  Job g{};
   if (s < 0 || s >= p.b.n_seq) return g;
   const AttendSeq sq = attend_seq_at(p, s);
   const int rows = sq.rows * p.G;
@@ -283,7 +277,6 @@ __device__ __forceinline__ Segment tile_at(const AttendParams &p, int s, int u) 
   g.end = p.causal ? min(sq.len, max(0, pos1 + 1)) : sq.len;
   g.t0 = p.window ? max(0, pos0 - p.window + 1) / kKeys : 0;
   g.n = max(0, (g.end + kKeys - 1) / kKeys - g.t0);
-  g.slot = -1;
   return g;
 }
 
@@ -302,76 +295,24 @@ __device__ __forceinline__ int seq_of_place(const AttendParams &p, int u) {
   return base - 1 + __popc(__ballot_sync(0xffffffffu, lane < n && tile_base(p, base + lane) <= u));
 }
 
-// What a block joins: the parts of one tile of rows, of the blocks first .. last.
-struct Joint {
-  int q0, hk, row0, rows;
-  int first, last, slot, pad;   // last <= first: nothing; the first one's slot
-};
-
-// The segments of this block's span into the list, in any order; scratch: shared
-// memory for a number for each place and one more.  At most two of them are partial:
-// slot 2 b for one that goes on from an earlier span, 2 b + 1 for one that starts in
-// this one and goes on in the next.
-__device__ __forceinline__ void cut_line(const AttendParams &p, int n_places, Bars &sm, Segment *list,
-                                         long long *scratch) {
-  __shared__ long long sums[kThreads / 32];
-  const int u = threadIdx.x, lane = u & 31, warp = u >> 5, b = blockIdx.x;
-  for (int s = u; s <= p.b.n_seq; s += kThreads) scratch[s] = tile_base(p, s);
-  if (u == 0) sm.n_segments = 0;
-  Joint *joint = reinterpret_cast<Joint *>(p.plan) + b;
-  if (u == 0) joint->first = 0, joint->last = 0;
-  __syncthreads();
-  Segment g{};
-  if (u < n_places) {
-    int lo = 0, hi = p.b.n_seq + 1;   // the last base at or before u is in lo .. hi - 1, if any is
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (scratch[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    g = tile_at(p, scratch[lo] <= u ? lo : -1, u);
-  }
-  const int tiles = max(g.n, 1), span = g.rows ? tiles + kSegmentCost : 0;
-  long long x = (long long)span * p.b.Hkv;
-  const long long mine = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += a;
-  }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  long long start = x - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) start += sums[w];
-    total += sums[w];
-  }
-  const long long len = max((total + kSms - 1) / kSms, (long long)kMinPart), begin = len * b, end = begin + len;
-  if (span && start < end && start + mine > begin) {
-    for (int hk = begin > start ? (int)((begin - start) / span) : 0; hk < p.b.Hkv; ++hk) {
-      const long long at = start + (long long)hk * span;   // this head's tiles: at .. at + tiles
-      if (at >= end) break;
-      const int a = (int)max(begin - at, 0ll), z = (int)min(end - at, (long long)tiles);
-      if (a >= z) continue;
-      Segment h = g;
-      h.hk = hk;
-      h.t0 += a, h.n = min(z, g.n) - a;
-      if (a > 0 || z < tiles) h.slot = 2 * b + (at > begin);
-      if (a == 0 && z < tiles)
-        *joint = Joint{g.q0, hk, g.row0, g.rows, b, (int)((at + tiles - 1) / len), h.slot, 0};
-      list[atomicAdd(&sm.n_segments, 1)] = h;
-    }
-  }
-  __syncthreads();
+// The block's job: part `part` of the tile of rows at place u; rows 0: none.
+__device__ __forceinline__ Job find_job(const AttendParams &p, int u, int hk, int nsplit, int part) {
+  Job job = tile_at(p, seq_of_place(p, u), u);
+  job.hk = hk;
+  job.parts = min(nsplit, max(1, job.n / kMinPart));
+  if (part >= job.parts) job.rows = 0;
+  const int n = job.n;
+  const long long a = (long long)n * part / job.parts, z = (long long)n * (part + 1) / job.parts;
+  job.t0 += (int)a, job.n = (int)(z - a);
+  return job;
 }
 
-// The codes' role, a warpgroup (wd the warp in it): a segment's key tiles, decoded into
-// their stages (done: tiles before them).  It sets the pace of a prompt: what it need
-// not wait for is asked for a tile ahead.  false: gave up.
+// The codes' role, a warpgroup (wd the warp in it): the key tiles, decoded into their
+// stages.  It sets the pace of a prompt: what it need not wait for is asked for a tile
+// ahead.
 template <int D>
-__device__ __forceinline__ bool decode_tiles(const AttendParams &p, const Segment &job, Bars &sm, uint8_t *k_s,
-                                             uint8_t *v_s, int done, int wd) {
+__device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &job, Bars &sm, uint8_t *k_s,
+                                             uint8_t *v_s, int wd) {
   const int t0 = job.t0, n_tiles = job.n;
   // A warp has 32 tokens of the tile, in rounds of 512 neighbouring bytes of codes: a
   // lane has 16 of them, 32 dimensions of one token.
@@ -447,7 +388,7 @@ __device__ __forceinline__ bool decode_tiles(const AttendParams &p, const Segmen
   load(0, page, 0, k);
   load(0, page, 1, v);
   for (int j = 0; j < n_tiles; ++j) {
-    const int all = done + j, st = all & 1, parity = ((all >> 1) & 1) ^ 1;
+    const int st = j & 1, parity = ((j >> 1) & 1) ^ 1;
     // A token whose V holds a NaN: its K becomes NaN, its V zeros, so that only the
     // rows that see it know.
     bool nan = false;
@@ -461,17 +402,17 @@ __device__ __forceinline__ bool decode_tiles(const AttendParams &p, const Segmen
       }
     }
     // (The issuers order what is written here before the MMAs.)
-    if (!wait_all(&sm.k_empty[st], parity, &sm.abort, p.status)) return false;
+    if (!wait_all(&sm.k_empty[st], parity, &sm.abort, p.status)) return;
     if (lane == 0) {
       const int left = job.len - (t0 + j) * kKeys - w0, y = lp > 4 ? page.x : page.y;
-      sm.holes[all & 3][wd] = (left > 0 && (unsigned)page.x >= (unsigned)p.b.n_pages ? 1 : 0) |
+      sm.holes[j & 3][wd] = (left > 0 && (unsigned)page.x >= (unsigned)p.b.n_pages ? 1 : 0) |
                             (left > 16 && (unsigned)y >= (unsigned)p.b.n_pages ? 2 : 0);
     }
     write(k_s + st * Smem<D>::kK, k);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.k_full[st]);
     load(j + 1, next, 0, k);
-    if (!wait_all(&sm.v_empty[st], parity, &sm.abort, p.status)) return false;
+    if (!wait_all(&sm.v_empty[st], parity, &sm.abort, p.status)) return;
     write(v_s + st * Smem<D>::kK, v);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.v_full[st]);
@@ -479,13 +420,12 @@ __device__ __forceinline__ bool decode_tiles(const AttendParams &p, const Segmen
     page = next;
     next = pages_of(j + 2);
   }
-  return true;
 }
 
 // The MMAs of tile i of rows, issued by one thread.
-template <int D, int i, bool kCut>
+template <int D, int i>
 __device__ __forceinline__ void issue_tile(const AttendParams &p, Bars &sm, uint8_t *q_s, uint8_t *k_s, uint8_t *v_s,
-                                           const Segment *list) {
+                                           int n_tiles, int n_sub) {
   // Everything that differs between the MMAs of two steps is a constant: they take 32
   // to 64 clocks each, and the issue of one, beside three busy warps of the scheduler,
   // takes about as long.
@@ -519,20 +459,17 @@ __device__ __forceinline__ void issue_tile(const AttendParams &p, Bars &sm, uint
   };
   constexpr Int<0> c0{};
   constexpr Int<1> c1{};
-  // What a barrier has been through, over all segments: key tiles, each half's steps, Q.
-  int all = 0, halves[2] = {0, 0}, queries = 0;
-  // Key tile j of a segment, in stage st: its outputs, and the scores of the next one
-  // (stage nx) in its place.
-  auto tile = [&](int j, int n_tiles, int n_sub, auto st_, auto nx_) {
+  // Key tile j, in stage st: its outputs, and the scores of the next one (stage nx) in
+  // its place.
+  auto tile = [&](int j, auto st_, auto nx_) {
     constexpr int st = decltype(st_)::value, nx = decltype(nx_)::value;
-    wait(&sm.v_full[st], (all >> 1) & 1);
-    if (j + 1 < n_tiles) wait(&sm.k_full[nx], ((all + 1) >> 1) & 1);
+    wait(&sm.v_full[st], (j >> 1) & 1);
+    if (j + 1 < n_tiles) wait(&sm.k_full[nx], ((j + 1) >> 1) & 1);
     fence_proxy_async();
     auto half = [&](auto h_) {
       constexpr int h = decltype(h_)::value;
       const int t = 2 * j + h;
-      if (t >= n_sub || !wait(&sm.p_full[i][h], halves[h] & 1)) return;
-      ++halves[h];
+      if (t >= n_sub || !wait(&sm.p_full[i][h], j & 1)) return;
       tc_fence_after();
       outputs(st_, h_, t);
       if (t + 2 < n_sub) scores(nx_, h_);
@@ -541,71 +478,43 @@ __device__ __forceinline__ void issue_tile(const AttendParams &p, Bars &sm, uint
     half(c1);
     mma_commit(&sm.v_empty[st]);
     if (j + 1 < n_tiles) mma_commit(&sm.k_empty[nx]);
-    ++all;
   };
-  auto first = [&](int n_sub, auto st_) {
-    constexpr int st = decltype(st_)::value;
-    if (!wait(&sm.k_full[st], (all >> 1) & 1) || !wait(&sm.q_full[i], queries & 1)) return;
-    ++queries;
+  if (n_tiles > 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[i], 0)) {
     fence_proxy_async();
     tc_fence_after();
-    scores(st_, c0);
-    if (n_sub > 1) scores(st_, c1);
-    mma_commit(&sm.k_empty[st]);
-  };
-  for (int g = 0; ok && g < (kCut ? sm.n_segments : 1); ++g) {
-    const Segment &job = list[g];
-    const int n = job.n;
-    if (i == 1 && job.rows <= kRows) {   // no second tile of rows: its stages are let go
-      for (int j = 0; ok && j < n; ++j, ++all) {
-        const int st = all & 1, parity = (all >> 1) & 1;
-        if (wait(&sm.k_full[st], parity)) mbar_arrive(&sm.k_empty[st]);
-        if (wait(&sm.v_full[st], parity)) mbar_arrive(&sm.v_empty[st]);
-      }
-      continue;
-    }
-    if (n == 0) continue;
-    const int n_sub = job.steps();
-    if (all & 1) first(n_sub, c1);
-    else first(n_sub, c0);
-    for (int j = 0; ok && j < n; ++j) {
-      if (all & 1) tile(j, n, n_sub, c1, c0);
-      else tile(j, n, n_sub, c0, c1);
-    }
+    scores(c0, c0);
+    if (n_sub > 1) scores(c0, c1);
+    mma_commit(&sm.k_empty[0]);
+  }
+  for (int j = 0; ok && j < n_tiles; j += 2) {
+    tile(j, c0, c1);
+    if (ok && j + 1 < n_tiles) tile(j + 1, c1, c0);
   }
   // One more commit covers every MMA issued; tensor memory is freed after it.
   mma_commit(&sm.drain[i]);
   drain_bar(&sm.drain[i], 0, globaltimer());
 }
 
-// kCut: a block takes a span of the line; otherwise one tile of rows.
-template <int D, bool kCap, bool kCut>
-__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int n_places) {
+template <int D, bool kCap>
+__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int nsplit) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Bars sm;
-  __shared__ Segment list[kCut ? kCutUnits : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if constexpr (kCut) {
-    cut_line(p, n_places, sm, list, reinterpret_cast<long long *>(smem));
-    if (sm.n_segments == 0) return;
-  } else {
-    // Heads of one place are neighbours, the last places (of a prompt: the rows that
-    // see most keys) come first.
-    const int unit = gridDim.x - 1 - blockIdx.x, u = unit / p.b.Hkv;
-    Segment g = tile_at(p, seq_of_place(p, u), u);
-    g.hk = unit - u * p.b.Hkv;
-    if (g.rows == 0) return;
-    if (threadIdx.x == 0) list[0] = g;
-  }
+  // Heads of one place are neighbours, the last places (of a prompt: the rows that
+  // see most keys) come first.
+  const int unit = gridDim.x - 1 - blockIdx.x, u = unit / p.b.Hkv, part = blockIdx.y;
+  const Job job = find_job(p, u, unit - u * p.b.Hkv, nsplit, part);
+  if (job.rows == 0) return;
+  const int tiles = job.rows > kRows ? 2 : 1;   // tiles of rows
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.k_full[i], 4);
-      mbar_init(&sm.k_empty[i], 2);
+      mbar_init(&sm.k_empty[i], tiles);
       mbar_init(&sm.v_full[i], 4);
-      mbar_init(&sm.v_empty[i], 2);
+      mbar_init(&sm.v_empty[i], tiles);
       mbar_init(&sm.s_full[i][0], 1);
       mbar_init(&sm.s_full[i][1], 1);
       mbar_init(&sm.p_full[i][0], 4);
@@ -634,18 +543,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
   if (warp < 8) {
     // ------------------------------------------------------------- softmax
     more_regs<kSoftmaxRegs>();
+    const int n_sub = job.steps();
     const int i = warp >> 2, r = (warp & 3) * 32 + lane;   // tile, row of the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    int all = 0, even = 0, odd = 0;   // key tiles, and steps of each half, before this segment
+    const int row = job.row0 + i * kRows + r;
+    const bool mine = row < job.row0 + job.rows;
+    const int tok = min(row, job.row0 + job.rows - 1) / p.G, h = job.hk * p.G + row - tok * p.G;
     bool ok = true;
-    for (int g = 0; ok && g < (kCut ? sm.n_segments : 1); ++g) {
-      const Segment job = list[g];
-      const int t0 = job.t0, n_sub = job.steps(), tiles0 = all;
-      all += job.n;
-      if (i * kRows >= job.rows) continue;
-      const int row = job.row0 + i * kRows + r;
-      const bool mine = i * kRows + r < job.rows;
-      const int tok = min(row, job.row0 + job.rows - 1) / p.G, h = job.hk * p.G + row - tok * p.G;
+    if (i < tiles) {
       // The row of Q: scaled, in the codes' order, into the swizzled tile.
       float cs = fabsf(p.scale) * kLog2e * (kCap ? 2.f / p.softcap : 1.f);
       if (p.scale == 0.f) cs = 1.f;
@@ -694,13 +599,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       const float cap_log2 = p.softcap * kLog2e;
       const uint32_t s_col = tmem + lane_base + i * kKeys, o_at = tmem + lane_base + o_col + i * D;
       // Steps free_lo .. free_hi - 1 of the part hide nothing from this warp's rows.
-      const int free_lo = (__reduce_max_sync(0xffffffffu, first) + kSub - 1) / kSub - 2 * t0;
-      const int free_hi = __reduce_min_sync(0xffffffffu, end) / kSub - 2 * t0;
+      const int free_lo = (__reduce_max_sync(0xffffffffu, first) + kSub - 1) / kSub - 2 * job.t0;
+      const int free_hi = __reduce_min_sync(0xffffffffu, end) / kSub - 2 * job.t0;
       float m = kNoScore;
       float2 l = make_float2(0.f, 0.f);
       for (int t = 0; t < n_sub; ++t) {
         const int h = t & 1;
-        if (!(ok = wait_all(&sm.s_full[i][h], ((h ? odd : even) + (t >> 1)) & 1, &sm.abort, p.status))) break;
+        if (!(ok = wait_all(&sm.s_full[i][h], (t >> 1) & 1, &sm.abort, p.status))) break;
         tc_fence_after();
         const uint32_t at = s_col + h * kSub;
         float s[kSub];
@@ -716,9 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
             s[c] = rcp_approx(e.x), s[c + 1] = rcp_approx(e.y);
           }
         }
-        const uint32_t holes = *reinterpret_cast<const volatile uint16_t *>(&sm.holes[(tiles0 + (t >> 1)) & 3][2 * h]);
+        const uint32_t holes = *reinterpret_cast<const volatile uint16_t *>(&sm.holes[(t >> 1) & 3][2 * h]);
         if (t < free_lo || t >= free_hi || holes) {
-          const int k0 = t0 * kKeys + t * kSub, a = first - k0, b = end - k0;
+          const int k0 = job.t0 * kKeys + t * kSub, a = first - k0, b = end - k0;
 #pragma unroll
           for (int c = 0; c < kSub; ++c) {
             const bool see = c >= a && c < b && !(holes >> (c / 32 * 8 + c / 16 % 2) & 1);
@@ -745,9 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
           m = now;
           l.x *= f, l.y *= f;
           if (t > 0) {
-            // The outputs so far: the last step's MMAs are done first.  (Step t - 3's are:
-            // these scores came after step t - 2's.)
-            if (!(ok = wait_all(&sm.o_done[i][h ^ 1], ((h ? even : odd) + ((t - 1) >> 1)) & 1, &sm.abort, p.status))) break;
+            // The outputs so far: the last step's MMAs are done first.  (The one before's are:
+            // these scores came after them.)
+            if (!(ok = wait_all(&sm.o_done[i][h ^ 1], ((t - 1) >> 1) & 1, &sm.abort, p.status))) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
@@ -774,49 +679,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[i][h]);
       }
-      if (!ok) break;
-      even += (n_sub + 1) >> 1, odd += n_sub >> 1;
-      // The last step is its half's last.
-      if (n_sub > 0) ok = wait_all(&sm.o_done[i][(n_sub - 1) & 1], ((n_sub & 1 ? even : odd) - 1) & 1, &sm.abort, p.status);
+      if (ok && n_sub > 0) ok = wait_all(&sm.o_done[i][(n_sub - 1) & 1], ((n_sub - 1) >> 1) & 1, &sm.abort, p.status);
       if (ok) {
         tc_fence_after();
         const float sum = l.x + l.y;
-        if (job.slot < 0) {
-          const float f = sum != 0.f ? 1.f / sum : 0.f;
-          __nv_bfloat16 *dst = p.out + (size_t)(job.q0 + tok) * p.ldo + (size_t)h * D;
+        const bool whole = job.parts == 1;
+        const float f = !whole ? 1.f : sum != 0.f ? 1.f / sum : 0.f;
+        const size_t at = ((size_t)unit * nsplit + part) * kBlockRows + i * kRows + r;
+        float *const po = p.part_o + (whole ? 0 : at * D);
+        __nv_bfloat16 *const dst = p.out + (size_t)(job.q0 + tok) * p.ldo + (size_t)h * D;
 #pragma unroll
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            if (n_sub > 0) {
-              tmem_ld16(o_at + c, o);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              // columns 0 4 1 5 2 6 3 7
-              const uint2 x = pack_out(make_float4(o[e] * f, o[e + 2] * f, o[e + 4] * f, o[e + 6] * f));
-              const uint2 y = pack_out(make_float4(o[e + 1] * f, o[e + 3] * f, o[e + 5] * f, o[e + 7] * f));
-              if (mine) *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(x.x, x.y, y.x, y.y);
-            }
-          }
-        } else {
-          const size_t at = (size_t)job.slot * kBlockRows + i * kRows + r;
-          float *dst = p.part_o + at * D;
-#pragma unroll
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          if (n_sub > 0) {
             tmem_ld16(o_at + c, o);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              if (!mine) continue;
-              *reinterpret_cast<float4 *>(dst + c + e) = make_float4(o[e], o[e + 2], o[e + 4], o[e + 6]);
-              *reinterpret_cast<float4 *>(dst + c + e + 4) = make_float4(o[e + 1], o[e + 3], o[e + 5], o[e + 7]);
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            // columns 0 4 1 5 2 6 3 7
+            const float4 x = make_float4(o[e] * f, o[e + 2] * f, o[e + 4] * f, o[e + 6] * f);
+            const float4 y = make_float4(o[e + 1] * f, o[e + 3] * f, o[e + 5] * f, o[e + 7] * f);
+            if (!mine) continue;
+            if (whole) {
+              const uint2 v = pack_out(x), w = pack_out(y);
+              *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(v.x, v.y, w.x, w.y);
+            } else {
+              *reinterpret_cast<float4 *>(po + c + e) = x;
+              *reinterpret_cast<float4 *>(po + c + e + 4) = y;
             }
           }
-          if (mine) p.part_ml[at] = make_float2(m, sum);
         }
+        if (!whole && mine) p.part_ml[at] = make_float2(m, sum);
       }
     }
   } else if (warp < 12) {
@@ -827,18 +723,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       while (globaltimer() - start < 20000ull) {
       }
     }
-    int done = 0;
-    for (int g = 0; g < (kCut ? sm.n_segments : 1); ++g) {
-      const Segment job = list[g];
-      if (!decode_tiles<D>(p, job, sm, k_s, v_s, done, warp - 8)) break;
-      done += job.n;
-    }
+    decode_tiles<D>(p, job, sm, k_s, v_s, warp - 8);
   } else {
     // --------------------------------------------------------------- issue
     fewer_regs<kIssueRegs>();
     // A warp for each tile of rows: they wait for their own softmax only.
-    if (warp == 12 && elect_one()) issue_tile<D, 0, kCut>(p, sm, q_s, k_s, v_s, list);
-    if (warp == 13 && elect_one()) issue_tile<D, 1, kCut>(p, sm, q_s, k_s, v_s, list);
+    if (warp == 12 && elect_one()) issue_tile<D, 0>(p, sm, q_s, k_s, v_s, job.n, job.steps());
+    if (warp == 13 && tiles > 1 && elect_one()) issue_tile<D, 1>(p, sm, q_s, k_s, v_s, job.n, job.steps());
     __syncwarp();
   }
   tc_fence_before();
@@ -849,76 +740,68 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
   }
 }
 
-// Joins the parts of what block blockIdx.x began, a warp a row.
+// Joins the parts of a block's rows, a warp a row.
 constexpr int kJoinWarps = 8, kJoinBlocks = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv4_many_join_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_many_join_kernel(const AttendParams p, int nsplit) {
+  const int unit = blockIdx.x, u = unit / p.b.Hkv, lane = threadIdx.x & 31;
+  const Job job = find_job(p, u, unit - u * p.b.Hkv, nsplit, 0);
   // Every block waits: this grid must not be over before the one it joins.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 *plan = reinterpret_cast<const int4 *>(after_wait(p.plan)) + 2 * blockIdx.x;
-  const int4 what = __ldcg(plan), span = __ldcg(plan + 1);   // q0, hk, row0, rows; first, last, slot
-  if (span.y <= span.x) return;
-  const int lane = threadIdx.x & 31;
+  if (job.rows == 0 || job.parts == 1) return;
   const float *po = after_wait(p.part_o);
   const float2 *pml = after_wait(p.part_ml);
-  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < what.w; r += gridDim.y * kJoinWarps) {
+  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < job.rows; r += gridDim.y * kJoinWarps) {
+    const size_t first = (size_t)unit * nsplit * kBlockRows + r;
     RowPart rp;
-    for (int b = span.x; b <= span.y; b += 8)
-      rp.take<8, D>(po, pml, span.y - b + 1, lane, [&](int k) {
-        return (size_t)(b + k == span.x ? span.z : 2 * (b + k)) * kBlockRows + r;
-      });
+    for (int i = 0; i < job.parts; i += 8)
+      rp.take<8, D>(po, pml, job.parts - i, lane, [&](int k) { return first + (size_t)(i + k) * kBlockRows; });
     if (lane >= D / 4) continue;
-    const int row = what.z + r, tok = row / p.G, h = what.y * p.G + row - tok * p.G;
-    *reinterpret_cast<uint2 *>(p.out + (size_t)(what.x + tok) * p.ldo + (size_t)h * D + lane * 4) = rp.result();
+    const int row = job.row0 + r, tok = row / p.G, h = job.hk * p.G + row - tok * p.G;
+    *reinterpret_cast<uint2 *>(p.out + (size_t)(job.q0 + tok) * p.ldo + (size_t)h * D + lane * 4) = rp.result();
   }
 }
 
-// Places of all sequences' tiles of rows.
+// Places of all sequences' tiles of rows, and the parts that keys may be cut into.
 long long places(const AttendParams &p) {
   const long long rows = (p.b.q_off ? (long long)p.b.T : p.b.n_seq) * p.G;
   return rows / kBlockRows + p.b.n_seq;
 }
-bool cuts(const AttendParams &p) {
-  return places(p) * p.b.Hkv <= kCutUnits && ((long long)p.b.max_pages << p.b.log_page) > kMinPart * kKeys;
+int split_of(const AttendParams &p) {
+  const long long keys = (long long)p.b.max_pages << p.b.log_page;
+  const long long most = std::max<long long>(1, (keys + kKeys - 1) / kKeys / kMinPart);
+  return (int)std::max<long long>(1, std::min<long long>(kSms / (places(p) * p.b.Hkv), most));
 }
 
-template <int D, bool kCap, bool kCut>
+template <int D, bool kCap>
 cudaError_t launch(const AttendParams &p, cudaStream_t st) {
-  auto kernel = kv4_many_kernel<D, kCap, kCut>;
+  auto kernel = kv4_many_kernel<D, kCap>;
   static DeviceOnce once;
   cudaError_t err = once.run([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   });
   if (err != cudaSuccess) return err;
-  const int n = (int)places(p);
-  err = launch_k(false, kernel, dim3(kCut ? kSms : (unsigned)n * p.b.Hkv), dim3(kThreads), Smem<D>::kBytes, st, p, n);
-  if (err != cudaSuccess || !kCut) return err;
+  const int nsplit = split_of(p);
+  const unsigned units = (unsigned)(places(p) * p.b.Hkv);
+  err = launch_k(false, kernel, dim3(units, nsplit), dim3(kThreads), Smem<D>::kBytes, st, p, nsplit);
+  if (err != cudaSuccess || nsplit == 1) return err;
   // Rows that a tile may have.
   const long long rows = (long long)(p.max_q ? std::min(p.max_q, p.b.T) : p.b.T) * p.G;
   const int ny = (int)std::min<long long>(kJoinBlocks, (rows + kJoinWarps - 1) / kJoinWarps);
-  return launch_k(true, kv4_many_join_kernel<D>, dim3(kSms, ny), dim3(kJoinWarps * 32), 0, st, p);
-}
-template <int D>
-cudaError_t launch(const AttendParams &p, cudaStream_t st) {
-  if (cuts(p)) return p.softcap > 0.f ? launch<D, true, true>(p, st) : launch<D, false, true>(p, st);
-  return p.softcap > 0.f ? launch<D, true, false>(p, st) : launch<D, false, false>(p, st);
+  return launch_k(true, kv4_many_join_kernel<D>, dim3(units, ny), dim3(kJoinWarps * 32), 0, st, p, nsplit);
 }
 
 }  // namespace
 
 // Partial results of a call, in rows of D and of (maximum, sum).
 size_t many_rows(const AttendParams &p) {
-  return cuts(p) ? (size_t)2 * kSms * kBlockRows : 0;
-}
-
-// Bytes of what a call's blocks tell the joining ones.
-size_t many_plan_bytes(const AttendParams &p) {
-  static_assert(sizeof(Joint) == 2 * sizeof(int4), "as the joining kernel reads it");
-  return cuts(p) ? kSms * sizeof(Joint) : 0;
+  const int nsplit = split_of(p);
+  return nsplit == 1 ? 0 : (size_t)places(p) * p.b.Hkv * nsplit * kBlockRows;
 }
 
 cudaError_t launch_many(const AttendParams &p, int D, cudaStream_t st) {
-  return D == 64 ? launch<64>(p, st) : launch<128>(p, st);
+  if (D == 64) return p.softcap > 0.f ? launch<64, true>(p, st) : launch<64, false>(p, st);
+  return p.softcap > 0.f ? launch<128, true>(p, st) : launch<128, false>(p, st);
 }
 
 }  // namespace moe
