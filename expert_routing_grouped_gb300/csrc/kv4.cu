@@ -229,8 +229,10 @@ extern "C" __attribute__((visibility("default"))) int moe_kv4_append(
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err;
   if (dtype == MOE_F32)
-    err = head_dim == 64 ? launch_append<MOE_F32, 64>(p, n_kv_heads, st) : launch_append<MOE_F32, 128>(p, n_kv_heads, st);
+    err = head_dim == 64 ? launch_append<MOE_F32, 64>(p, n_kv_heads, st)
+                         : launch_append<MOE_F32, 128>(p, n_kv_heads, st);
   else
-    err = head_dim == 64 ? launch_append<MOE_BF16, 64>(p, n_kv_heads, st) : launch_append<MOE_BF16, 128>(p, n_kv_heads, st);
+    err = head_dim == 64 ? launch_append<MOE_BF16, 64>(p, n_kv_heads, st)
+                         : launch_append<MOE_BF16, 128>(p, n_kv_heads, st);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }

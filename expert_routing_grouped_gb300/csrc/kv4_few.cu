@@ -31,7 +31,7 @@
 //
 // The floor is the cache, 9/16 bytes an element; what bounds it is instructions: 818
 // for 32 tokens of 16 columns, issued at 2.0 a clock and SM.  One token of 96 query
-// and 8 KV heads over 131072 tokens: 47.5 us (3.2 TB/s); 64 tokens of 32 and 8 heads
+// and 8 KV heads over 131072 tokens: 47.7 us (3.2 TB/s); 64 tokens of 32 and 8 heads
 // over up to 8192 each: 49.5 us (3.8 TB/s); one over 4096: 10.6 us, mostly launches,
 // the plan and the joining.  An earlier form (52.5 us over 131072) took 34.6 us with
 // the copies alone.  Tried: codes in 16 mantissa bits and V's scales on the values
@@ -396,13 +396,15 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
         for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            jn.q[nt][gr][i][lane] = make_uint4(qb[0][gr][4 * i], qb[0][gr][4 * i + 1], qb[0][gr][4 * i + 2], qb[0][gr][4 * i + 3]);
+            jn.q[nt][gr][i][lane] =
+                make_uint4(qb[0][gr][4 * i], qb[0][gr][4 * i + 1], qb[0][gr][4 * i + 2], qb[0][gr][4 * i + 3]);
       }
     }
     // from column g's lanes to those of the accumulators' columns 2 t4, 2 t4 + 1
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr)
-      qsum[nt][gr] = make_float2(__shfl_sync(0xffffffffu, sum[gr], 8 * t4), __shfl_sync(0xffffffffu, sum[gr], 8 * t4 + 4));
+      qsum[nt][gr] =
+          make_float2(__shfl_sync(0xffffffffu, sum[gr], 8 * t4), __shfl_sync(0xffffffffu, sum[gr], 8 * t4 + 4));
     cs[nt] = make_float2(__shfl_sync(0xffffffffu, back, 8 * t4), __shfl_sync(0xffffffffu, back, 8 * t4 + 4));
   }
   if constexpr (NT > 1) __syncthreads();

@@ -15,14 +15,17 @@
 //   warps 12, 13     issue the MMAs of tile 0 and 1: scores run two steps ahead of
 //                    the softmax, in two buffers of tensor memory
 //
-// 8192 tokens of 32 query and 8 KV heads, causal: 434 us, 1268 TFLOP/s of what
-// counts (0.66 of a large matrix product's rate); the tensor pipe is busy 55 % of the
-// clocks, the schedulers 53 %.  Clocks read inside an earlier form (441 us) showed the
+// 8192 tokens of 32 query and 8 KV heads, causal: 426 us, 1291 TFLOP/s of what
+// counts (0.67 of a large matrix product's rate); the tensor pipe is busy 55 % of the
+// clocks, the schedulers 54 %.  Clocks read inside an earlier form (441 us) showed the
 // codes' role at work for 3760 of the 3836 that a tile of 128 keys takes: it sets the
 // pace, and shares its schedulers with the softmax.  So neither more warps for it
 // (481 us against 450) nor more for the softmax (516 against 441) helped, nor codes
 // shared by two blocks of a cluster (824 against 441: remote stores), nor two tiles
-// of codes in flight in registers (625 against 450: spills).
+// of codes in flight in registers (625 against 450: spills), nor both softmax groups
+// on one tile of rows where there is only one (57.9 against 56.5 for 4 rows of 96/8
+// heads in each of 4 sequences of 16384), nor blocks that work through several tiles
+// of rows, the next one's decoding beside the last one's end (447 against 426).
 //
 // The running maximum moves only when a score passes it by 8: weights up to 2^8 are
 // float16 as well as those up to 1, and the outputs in tensor memory need scaling
@@ -34,7 +37,7 @@
 //
 // Where a call has fewer blocks than SMs the keys are cut into parts, whose results
 // a second kernel joins.  (One line of all key tiles cut into equal spans, as for few
-// rows, was slower: 512 rows of 32/8 heads over 16384 keys 163 us against 133.)
+// rows, was slower: 512 rows of 32/8 heads over 16384 keys 163 us against 125.)
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -368,7 +371,8 @@ __device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &j
   const int row = w0 + tk;
   uint32_t at[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) at[e] = g * (kKeys * 128) + row * 128 + ((((pc & 1) * 4 + (e ^ (2 * g))) ^ (row & 7)) * 16);
+  for (int e = 0; e < 4; ++e)
+    at[e] = g * (kKeys * 128) + row * 128 + ((((pc & 1) * 4 + (e ^ (2 * g))) ^ (row & 7)) * 16);
   auto write = [&](uint8_t *dst, const Codes &x) {
 #pragma unroll
     for (int c = 0; c < kRounds; ++c) {

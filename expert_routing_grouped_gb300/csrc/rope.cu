@@ -13,9 +13,9 @@
 // of the block's heads.
 //
 // The floor is one read and one write.  4096 tokens of 40 heads of 128, bfloat16:
-// 18.1 us (4.6 TB/s, DRAM reads at the floor); half the warps' slots are taken and the
+// 18.0 us (4.7 TB/s, DRAM reads at the floor); half the warps' slots are taken and the
 // schedulers are half busy, so it is latency that is left.  104 heads of one token:
-// 2.1 us, a launch and one trip to memory.
+// 2.2 us, a launch and one trip to memory.
 #include <algorithm>
 #include <cmath>
 
