@@ -31,8 +31,8 @@
 //
 // The floor is the cache, 9/16 bytes an element; what bounds it is instructions: 818
 // for 32 tokens of 16 columns, issued at 2.0 a clock and SM.  One token of 96 query
-// and 8 KV heads over 131072 tokens: 47.7 us (3.2 TB/s); 64 tokens of 32 and 8 heads
-// over up to 8192 each: 49.5 us (3.8 TB/s); one over 4096: 10.6 us, mostly launches,
+// and 8 KV heads over 131072 tokens: 46.9 us (3.2 TB/s); 64 tokens of 32 and 8 heads
+// over up to 8192 each: 49.4 us (3.9 TB/s); one over 4096: 10.0 us, mostly launches,
 // the plan and the joining.  An earlier form (52.5 us over 131072) took 34.6 us with
 // the copies alone.  Tried: codes in 16 mantissa bits and V's scales on the values
 // (57.9 us against 52.8), the codes as the A side of tcgen05 MMAs (69 against 53),
@@ -174,8 +174,18 @@ struct Line {
 };
 
 // With seq < 0 the sequence in which block `block`'s span starts, else that of
-// sequence seq.  line.s < 0: none.
+// sequence seq.  line.s < 0: none.  kOne: there is one sequence only, and nothing to add
+// up (a token over 4096 takes 10.0 us for 10.4).
+template <bool kOne>
 __device__ __forceinline__ Line find_line(const AttendParams &p, int block, int seq) {
+  if constexpr (kOne) {
+    Line line;
+    line.total = (long long)span_of(tiles_of(p, attend_seq_at(p, 0))) * p.b.Hkv;
+    line.cut = max((line.total + p.target - 1) / p.target, (long long)kMinTiles);
+    line.s = seq >= 0 || line.cut * block < line.total ? 0 : -1;
+    line.start = 0;
+    return line;
+  }
   __shared__ long long sums[32];
   __shared__ long long start;
   __shared__ int where;
@@ -673,7 +683,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 }
 
 // kCut: blocks take equal spans of the line; otherwise block u is (sequence, head) u.
-template <int D, int NT, bool kCut>
+template <int D, int NT, bool kCut, bool kOne>
 __global__ void __launch_bounds__(kWarps * 32, kBlocks<NT>) kv4_few_kernel(const AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Joined<NT> jn;
@@ -686,7 +696,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks<NT>) kv4_few_kernel(const
     g.first = t.first, g.n = t.n, g.slot = 0, g.whole = true;
     do_segment<D, NT>(p, g, smem, jn);
   } else {
-    const Line line = find_line(p, blockIdx.x, -1);
+    const Line line = find_line<kOne>(p, blockIdx.x, -1);
     if (line.s < 0) return;
     const long long begin = line.cut * blockIdx.x, end = min(begin + line.cut, line.total);
     long long u = begin, start = line.start;   // start: of sequence s in the line
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks<NT>) kv4_few_kernel(const
 // Joins the parts of rows and query heads of one sequence, WR warps to each: a warp
 // takes eight parts in one go.
 constexpr int kJoinWarps = 8;
-template <int D, int WR>
+template <int D, int WR, bool kOne>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const AttendParams p, int max_cols) {
   __shared__ float4 ys[kJoinWarps][D / 4];
   __shared__ float2 mls[kJoinWarps];
@@ -726,7 +736,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const AttendP
   Line line{};
   long long head = 0;
   if (t.n > 0) {   // the whole block
-    line = find_line(p, 0, s);
+    line = find_line<kOne>(p, 0, s);
     head = line.start + (long long)hk * span_of(t);
     b0 = (int)(head / line.cut), b1 = (int)((head + t.n - 1) / line.cut);
   }
@@ -762,9 +772,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const AttendP
   *reinterpret_cast<uint2 *>(p.out + (size_t)(sq.t0 + i) * p.ldo + (size_t)h * D + lane * 4) = row.result();
 }
 
-template <int D, int NT, bool kCut>
+template <int D, int NT, bool kCut, bool kOne>
 cudaError_t launch(const AttendParams &p, int grid, cudaStream_t st) {
-  auto kernel = kv4_few_kernel<D, NT, kCut>;
+  auto kernel = kv4_few_kernel<D, NT, kCut, kOne>;
   static DeviceOnce once;
   const cudaError_t err = once.run([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>);
@@ -775,16 +785,20 @@ cudaError_t launch(const AttendParams &p, int grid, cudaStream_t st) {
 
 template <int D, int NT>
 cudaError_t launch(AttendParams p, bool cut, int max_cols, cudaStream_t st) {
-  if (!cut) return launch<D, NT, false>(p, p.b.n_seq * p.b.Hkv, st);
+  if (!cut) return launch<D, NT, false, false>(p, p.b.n_seq * p.b.Hkv, st);
   p.target = kFewSms * kBlocks<NT>;
-  const cudaError_t err = launch<D, NT, true>(p, p.target, st);
+  const bool one = p.b.n_seq == 1;
+  const cudaError_t err =
+      one ? launch<D, NT, true, true>(p, p.target, st) : launch<D, NT, true, false>(p, p.target, st);
   if (err != cudaSuccess) return err;
   // Eight warps to a row where its parts are many (one or two heads have a good part
   // of all blocks), else one.
   const int per_seq = p.b.Hkv * max_cols;
   const bool wide = p.target >= 4 * p.b.n_seq * p.b.Hkv;
   const int blocks_seq = wide ? per_seq : (per_seq + kJoinWarps - 1) / kJoinWarps;
-  return launch_k(true, wide ? kv4_join_kernel<D, kJoinWarps> : kv4_join_kernel<D, 1>,
+  auto join = one ? (wide ? kv4_join_kernel<D, kJoinWarps, true> : kv4_join_kernel<D, 1, true>)
+                  : (wide ? kv4_join_kernel<D, kJoinWarps, false> : kv4_join_kernel<D, 1, false>);
+  return launch_k(true, join,
                   dim3((unsigned)(p.b.n_seq * blocks_seq)), dim3(kJoinWarps * 32), 0, st, p, max_cols);
 }
 
