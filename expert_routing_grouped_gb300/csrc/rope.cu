@@ -13,9 +13,11 @@
 // of the block's heads.
 //
 // The floor is one read and one write.  4096 tokens of 40 heads of 128, bfloat16:
-// 18.0 us (4.7 TB/s, DRAM reads at the floor); half the warps' slots are taken and the
-// schedulers are half busy, so it is latency that is left.  104 heads of one token:
-// 2.2 us, a launch and one trip to memory.
+// 15.8 us (5.3 TB/s), in place 15.3; 17.9 and 18.0 without streaming loads, which leave
+// L2 to what is written.  Half the warps' slots are taken; capping registers for more
+// blocks an SM (18.4 us and up), 128 threads (16.2) and, before the streaming loads,
+// one or four units a thread (18.8, 23.5 against 17.9) were slower.  104 heads of one
+// token: 2.1 us, a launch and one trip to memory.
 #include <algorithm>
 #include <cmath>
 
@@ -75,7 +77,7 @@ struct Piece {
     const Word *p = reinterpret_cast<const Word *>(reinterpret_cast<const char *>(base) +
                                                    i * (DT == MOE_BF16 ? 2 : 4));
 #pragma unroll
-    for (int c = 0; c < kBytes / kWord; ++c) w[c] = p[c];
+    for (int c = 0; c < kBytes / kWord; ++c) w[c] = __ldcs(p + c);   // read once
   }
   __device__ __forceinline__ void store(void *base, long long i) const {
     Word *p = reinterpret_cast<Word *>(reinterpret_cast<char *>(base) + i * (DT == MOE_BF16 ? 2 : 4));
