@@ -9,9 +9,10 @@
 // place (sequence, length, page) is looked up while its values are on the way.
 //
 // The floor is the rows in and 9/32 of a bfloat16's bytes out.  8192 rows of 8 heads
-// of 128: 14.5 us (3.0 TB/s), bound by instructions (quotients are to nearest; with
-// them one at a time 15.3 us, the schedulers 75 % busy); with one group at a time in a warp and
-// unpacked conversions it was 24.3.  64 rows: 1.8 us.
+// of 128: 13.7 us (3.1 TB/s), bound by instructions.  Rows are read once, past what L2
+// holds (14.6 us with plain loads); two exact quotients share an instruction (15.3 us
+// one at a time, the schedulers 75 % busy); several groups a warp and packed
+// conversions (24.3 us without).  64 rows: 1.9 us.
 #include <algorithm>
 #include <cmath>
 
@@ -75,10 +76,10 @@ struct Raw8 {
   uint4 v[DT == MOE_BF16 ? 1 : 2];
   __device__ __forceinline__ void load(const void *src, size_t at) {
     if constexpr (DT == MOE_BF16) {
-      v[0] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(src) + at);
+      v[0] = __ldcs(reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(src) + at));
     } else {
       const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(src) + at);
-      v[0] = p[0], v[1] = p[1];
+      v[0] = __ldcs(p), v[1] = __ldcs(p + 1);
     }
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
