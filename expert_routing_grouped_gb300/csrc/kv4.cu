@@ -11,7 +11,7 @@
 // The floor is the rows in and 9/32 of a bfloat16's bytes out.  8192 rows of 8 heads
 // of 128: 13.7 us (3.1 TB/s), bound by instructions.  Rows are read once, past what L2
 // holds (14.6 us with plain loads); two exact quotients share an instruction (15.3 us
-// one at a time, the schedulers 75 % busy); several groups a warp and packed
+// one at a time); several groups a warp and packed
 // conversions (24.3 us without).  64 rows: 1.9 us.
 #include <algorithm>
 #include <cmath>

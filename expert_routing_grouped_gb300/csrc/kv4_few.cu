@@ -29,10 +29,10 @@
 // The tiles of all sequences and KV heads lie in one line that is cut into equal
 // spans, one for each block, whatever the lengths; a second kernel joins what was cut.
 //
-// The floor is the cache, 9/16 bytes an element; what bounds it is instructions: 818
+// The floor is the cache, 9/16 bytes an element; what bounds it is instructions: 809
 // for 32 tokens of 16 columns, issued at 2.0 a clock and SM.  One token of 96 query
-// and 8 KV heads over 131072 tokens: 46.9 us (3.2 TB/s); 64 tokens of 32 and 8 heads
-// over up to 8192 each: 49.4 us (3.9 TB/s); one over 4096: 10.0 us, mostly launches,
+// and 8 KV heads over 131072 tokens: 47.0 us (3.2 TB/s); 64 tokens of 32 and 8 heads
+// over up to 8192 each: 49.5 us (3.8 TB/s); one over 4096: 10.0 us, mostly launches,
 // the plan and the joining.  An earlier form (52.5 us over 131072) took 34.6 us with
 // the copies alone.  Tried: codes in 16 mantissa bits and V's scales on the values
 // (57.9 us against 52.8), the codes as the A side of tcgen05 MMAs (69 against 53),

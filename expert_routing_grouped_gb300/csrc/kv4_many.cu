@@ -15,7 +15,7 @@
 //   warps 12, 13     issue the MMAs of tile 0 and 1: scores run two steps ahead of
 //                    the softmax, in two buffers of tensor memory
 //
-// 8192 tokens of 32 query and 8 KV heads, causal: 426 us, 1291 TFLOP/s of what
+// 8192 tokens of 32 query and 8 KV heads, causal: 427 us, 1287 TFLOP/s of what
 // counts (0.67 of a large matrix product's rate); the tensor pipe is busy 55 % of the
 // clocks, the schedulers 54 %.  Clocks read inside an earlier form (441 us) showed the
 // codes' role at work for 3760 of the 3836 that a tile of 128 keys takes: it sets the
