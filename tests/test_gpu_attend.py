@@ -722,3 +722,36 @@ def test_offsets_out_of_order(moe):
     new = [10] * n
     off, o = batch(new, c)
     check(run(moe, q, c, new, off), q, c, o)
+
+
+@pytest.mark.parametrize("H,Hkv,D,new,have", [
+    (1024, 1024, 64, [1], [20]), (1024, 1, 64, [2, 1], [70, 300]), (1024, 1, 128, [1], [40]),
+    (1024, 64, 128, [1, 1], [90, 3]), (1008, 63, 64, [2], [33])])
+def test_most_heads(moe, H, Hkv, D, new, have):
+    """As many query heads as a call takes, each with its own KV head or all with one."""
+    g = gen(22)
+    c = ref.Cache(g, have, Hkv, D, 16)
+    off, o = batch(new, c)
+    q = randn(g, o[-1], H, D).bfloat16()
+    check(run(moe, q, c, new, off), q, c, o)
+
+
+def test_most_sequences(moe):
+    """65535 sequences of one token each, appended and attended: each sees itself alone."""
+    g = gen(23)
+    n, H, D, page = 65535, 2, 64, 16
+    pages = torch.randperm(n, generator=g, device="cuda").to(torch.int32)[:, None].contiguous()
+    cache = torch.full((n, moe.kv4_page_bytes(page, 1, D)), 255, dtype=torch.uint8, device="cuda")
+    length = torch.ones(n, dtype=torch.int32, device="cuda")
+    x = randn(g, 2, n, 1, D).bfloat16()
+    moe.kv4_append(x[0], x[1], cache, pages, length, n, 1, D, page, n, 1)
+    q = randn(g, n, H, D).bfloat16()
+    out = torch.empty_like(q)
+    need = moe.kv4_workspace(n, n, H, 1, D, page, 1)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    moe.kv4_attention(q, cache, pages, length, n, H, 1, D, page, n, 1, out, work)
+    v = ref.values(*ref.quantise(x[1].float())).expand(n, H, D)
+    # weight 1, so step c rounds as in attend's bound; V and the result round once
+    least = v.amin(2, keepdim=True)
+    tol = (2.0 ** -10 + 2.0 ** -8) * v.abs() * 1.01 + 2.0 ** -11 * (v - least) + 2.0 ** -24
+    assert bool(((out.double() - v).abs() <= tol).all())
