@@ -15,16 +15,19 @@
 //      for each group: s = sum_g step_g acc_g + lo_g sum(q of g), no rounding of K.
 //   q: float16 after a power of two per column that brings its largest just under
 //      2^15: exact to 2^-25 of that.
-//   P: for each group w step, rounded to float16 (2^-11 at most), in the
-//      accumulator's layout, transposed by movmatrix: the B operand.  V's codes are
-//      exact, and sum w lo is kept beside in f32.
+//   P: for each group w step times a power of two, rounded to float16 (2^-11 at
+//      most), in the accumulator's layout, transposed by movmatrix: the B operand.
+//      V's codes are exact, and sum w lo is kept beside in f32.
 //
 // Each warp streams its own tiles of 32 tokens through a private ring in shared
 // memory by cp.async (no barrier, no waiting but its own), with a running
-// maximum that moves only when a score passes it by 8 (weights up to 2^8 are
-// float16 as well as those up to 1), so most tiles exchange nothing.  The maximum
-// also holds a power of two that keeps w step in float16's range whatever the size
-// of V: it moves when a step passes it by 8.  The block's warps join at the end.
+// maximum that moves only when a score passes it by 8, so most tiles exchange
+// nothing.  The power of two of w step is each column's and group's own: it brings
+// the largest product that the column has met to 2^7 .. 2^15, so that what other
+// groups hold, or tokens of little weight or that the column does not see, takes no
+// bits from it (2^-25 of float16's subnormals is 2^-32 of the largest product).
+// Maxima are whole numbers: where one moves, the powers move with it and the
+// outputs stay as they are.  The block's warps join at the end.
 //
 // The tiles of all sequences and KV heads lie in one line that is cut into equal
 // spans, one for each block, whatever the lengths; a second kernel joins what was cut.
@@ -49,6 +52,7 @@ constexpr int kMinTiles = 4;                // tiles of a span, at least: one fo
 constexpr int kPlanSeqs = 1024;             // sequences of a batch that is cut into spans
 constexpr int kColumns = kFewColumns;
 constexpr int kFewSms = 152;                // blocks are sized for the GB300's SMs
+constexpr int kMostUp = 100;                // the largest exponent of w step's factors
 
 template <int D>
 struct Slot {
@@ -115,6 +119,9 @@ __device__ __forceinline__ uint32_t max2_f16(uint32_t a, uint32_t b) {
   asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// 2^e and back (of a normal number: the exponent below; of 0: -127).
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int exponent(float v) { return (__float_as_int(v) >> 23) - 127; }
 __device__ __forceinline__ float2 unpack_f16(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
@@ -389,15 +396,15 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
   if (p.causal) all_hi = max(0, sq.len - sq.nq + 1);
   if (p.window) all_lo = max(0, sq.len - p.window);
 
-  float2 nm[NT], l[NT];   // less the running maxima and the exponent below; the sums
+  float2 nm[NT], l[NT];   // less the running maxima, whole numbers; the sums
   float2 low[NG][NT];     // sums of w lo
+  float2 up[NG][NT];      // powers of two: w step enters the product times this
   float o[MT][NT][4];
-  int step_e = -150;      // no step so far is more than 8 times 2^step_e
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     nm[nt] = both(-kNoScore), l[nt] = both(0.f);
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr) low[gr][nt] = both(0.f);
+    for (int gr = 0; gr < NG; ++gr) low[gr][nt] = both(0.f), up[gr][nt] = both(pow2(kMostUp));
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -511,38 +518,18 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
             }
         }
     }
-    // V's scales of the S rows' tokens.
-    uint32_t vsc[2][2][NG];
-    uint32_t steps = 0;
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t *vs = reinterpret_cast<const uint32_t *>(sl + Slot<D>::kVs) +
-                             (16 * mt + 8 * r + (g >> 1) + 4 * (g & 1)) * NG;
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          vsc[mt][r][gr] = vs[gr];
-          steps = max2_f16(steps, vs[gr]);
-        }
-      }
-    // The running maxima, when some score or step passes theirs by 8.
-    const float step = __low2float(*reinterpret_cast<const __half2 *>(&steps));
-    bool over = __float_as_int(step) > (step_e + 130) << 23;
-    const float room = 8.f - (float)step_e;
+    // The running maxima, when some score passes theirs by 8: whole numbers, so that what
+    // is kept needs no scaling for them but the factors `up` move along.
+    bool over = false;
     float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       top[nt][0] = fmaxf(fmaxf(s[0][nt][0].x, s[0][nt][1].x), fmaxf(s[1][nt][0].x, s[1][nt][1].x));
       top[nt][1] = fmaxf(fmaxf(s[0][nt][0].y, s[0][nt][1].y), fmaxf(s[1][nt][0].y, s[1][nt][1].y));
       const float2 x = add_2(make_float2(top[nt][0], top[nt][1]), nm[nt]);
-      over |= x.x > room || x.y > room;
+      over |= x.x > 8.f || x.y > 8.f;
     }
     if (__any_sync(0xffffffffu, over)) {
-      // The power of two at or above the largest step.
-      const int sb = (int)__reduce_max_sync(0xffffffffu, __float_as_uint(step));
-      const int was = step_e;
-      step_e = max(max(was, -24), ((sb + 0x7FFFFF) >> 23) - 127);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -551,34 +538,87 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
           float &nmj = j ? nm[nt].y : nm[nt].x;
-          const float now = -fmaxf(x, -nmj - (float)was) - (float)step_e;
-          const float f = ex2(now - nmj);   // first time: ex2(-3e38) = 0
+          const float now = fminf(nmj, -ceilf(x)), by = nmj - now;   // first time: 3e38
+          const float f = ex2(-by);
           nmj = now;
           (j ? l[nt].y : l[nt].x) *= f;
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) (j ? low[gr][nt].y : low[gr][nt].x) *= f;
+          for (int gr = 0; gr < NG; ++gr) {
+            (j ? low[gr][nt].y : low[gr][nt].x) *= f;
+            float &u = j ? up[gr][nt].y : up[gr][nt].x;
+            const int e = exponent(u);
+            const float rise = fminf(by, (float)(kMostUp - e)), held = ex2(rise - by);   // 1 but at kMostUp
+            u = pow2(e + (int)rise);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) o[i][nt][j] *= f, o[i][nt][2 + j] *= f;
+            for (int i = 4 * gr; i < 4 * gr + 4; ++i) o[i][nt][j] *= held, o[i][nt][2 + j] *= held;
+          }
         }
     }
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      // Weights, and for each group their B operands.
+      // Weights, their sums and those of w lo.
+      float2 w[2][NT];
+      uint32_t vsc[2][NG];   // V's scales of the S rows' tokens
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t *vs = reinterpret_cast<const uint32_t *>(sl + Slot<D>::kVs) +
+                             (16 * mt + 8 * r + (g >> 1) + 4 * (g & 1)) * NG;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) vsc[r][gr] = vs[gr];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 x = add_2(s[mt][nt][r], nm[nt]);
+          w[r][nt] = make_float2(ex2(x.x), ex2(x.y));
+          l[nt] = add_2(l[nt], w[r][nt]);
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) low[gr][nt] = fma_2(w[r][nt], both(unpack_f16(vsc[r][gr]).y), low[gr][nt]);
+        }
+      }
+      // For each group w step as float16: the B operands, before they are transposed.
       uint32_t pb[NG][NT][2];
+      auto products = [&] {
+        uint32_t most = 0;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float2 ws = mul_2(mul_2(w[r][nt], both(unpack_f16(vsc[r][gr]).x)), up[gr][nt]);
+              pb[gr][nt][r] = pack_f16(ws.x, ws.y);
+              most = max2_f16(most, pb[gr][nt][r]);
+            }
+        return most;
+      };
+      // Where one reaches 2^15 (0x7800), the factors fall: the largest is then under 2^8.
+      if (__any_sync(0xffffffffu, ((products() + 0x08000800u) & 0x80008000u) != 0)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float x = 0.f;
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                x = fmaxf(x, (j ? w[r][nt].y : w[r][nt].x) * unpack_f16(vsc[r][gr]).x);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+              float &u = j ? up[gr][nt].y : up[gr][nt].x;
+              const int e = exponent(u), to = min(e, 7 - exponent(x));
+              const float f = ex2((float)(to - e));
+              u = pow2(to);
+#pragma unroll
+              for (int i = 4 * gr; i < 4 * gr + 4; ++i) o[i][nt][j] *= f, o[i][nt][2 + j] *= f;
+            }
+        products();
+      }
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float2 x = add_2(s[mt][nt][r], nm[nt]), w = make_float2(ex2(x.x), ex2(x.y));
-          l[nt] = add_2(l[nt], w);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            const float2 sc = unpack_f16(vsc[mt][r][gr]);
-            low[gr][nt] = fma_2(w, both(sc.y), low[gr][nt]);
-            const float2 ws = mul_2(w, both(sc.x));
-            pb[gr][nt][r] = transpose8x8(pack_f16(ws.x, ws.y));
-          }
-        }
+          for (int gr = 0; gr < NG; ++gr) pb[gr][nt][r] = transpose8x8(pb[gr][nt][r]);
       // V: the k-pairs are tokens t4, t4 + 4 (rows 2 t4, 2 t4 + 1) and 8 further; a lane
       // holds dimensions 8 g .. 8 g + 7 of each group.
 #pragma unroll
@@ -642,10 +682,11 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 #pragma unroll
       for (int w = 1; w < W; ++w) top = fmaxf(top, jn.m[w][c]);
       const float f = ex2(-(j ? nm[nt].y : nm[nt].x) - top);
-      const float f24 = f * 16777216.f, f20 = f * 1048576.f;   // the codes' 2^-24 and 2^-20
       float *dst = joined + (warp * 8 * NT + c) * kRow + g * 8;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
+        // the codes' 2^-24 and 2^-20, and w step's factor
+        const float f24 = f * pow2(24 - exponent(j ? up[gr][nt].y : up[gr][nt].x)), f20 = f24 * 0.0625f;
         const float lo = (j ? low[gr][nt].y : low[gr][nt].x) * f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
