@@ -173,10 +173,20 @@ static __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// cap tanh(x / cap) in units of log2 e, from x 2 log2(e) / cap: an absolute error
-// of a few units of cap, which is what a score's error counts as.
-static __device__ __forceinline__ float capped(float x2, float cap_log2) {
-  return cap_log2 - 2.f * cap_log2 * rcp_approx(1.f + ex2(x2));
+// cap tanh(x / cap) of two scores, x and the result in units of log2 e; with z = 2 x / cap
+// in these units it is
+//   x (1 + a z^2 + b z^4 + c z^6)      |z| < 1: tanh(y) / y to 4e-8 where y < 0.35
+//   cap - 2 cap / (1 + 2^z)            else; there it is a third of cap at least
+// so that it is off by at most 2^-20 of itself, however large the cap is.
+static __device__ __forceinline__ float2 capped_2(float2 x, float two_by_cap, float cap_log2) {
+  const float2 one = make_float2(1.f, 1.f), z = mul_2(x, make_float2(two_by_cap, two_by_cap)), t = mul_2(z, z);
+  float2 p = fma_2(t, make_float2(-8.51692959e-05f, -8.51692959e-05f), make_float2(0.00191879156f, 0.00191879156f));
+  p = fma_2(p, t, make_float2(-0.0400369462f, -0.0400369462f));
+  p = mul_2(x, fma_2(p, t, one));
+  const float2 e = add_2(make_float2(ex2(z.x), ex2(z.y)), one);
+  const float2 far = fma_2(make_float2(rcp_approx(e.x), rcp_approx(e.y)), make_float2(-2.f * cap_log2, -2.f * cap_log2),
+                           make_float2(cap_log2, cap_log2));
+  return make_float2(fabsf(z.x) < 1.f ? p.x : far.x, fabsf(z.y) < 1.f ? p.y : far.y);
 }
 
 // A running (maximum, sum, output) of one row, four dimensions of it in a lane.

@@ -99,7 +99,9 @@ extern "C" __attribute__((visibility("default"))) int moe_kv4_attention(
   p.b = KvBatch{pages, q_off, kv_len, T, n_seq, kv4_log2(page_size), n_pages, max_pages, n_kv_heads};
   p.ldq = ldq, p.ldo = ldo, p.H = n_heads, p.G = n_heads / n_kv_heads, p.max_q = max_q;
   // Tokens end before 2^30: no window shows more, and positions less it stay in 32 bits.
-  p.window = std::min(window, 1 << 30), p.causal = causal != 0, p.scale = scale, p.softcap = softcap, p.status = status;
+  p.window = std::min(window, 1 << 30), p.causal = causal != 0, p.scale = scale, p.status = status;
+  // A cap past 10^38 (whose product with log2 e leaves f32) moves no score below 10^34.
+  p.softcap = softcap <= 1e38f ? softcap : 0.f;
   const Scratch w = workspace_of(p, head_dim);
   if (w.bytes) {
     p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.o);

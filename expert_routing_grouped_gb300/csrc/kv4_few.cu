@@ -353,7 +353,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
     const int eb = (int)(top >> 23);
     const int up = eb == 255 ? 0 : min(15 + 126 - max(eb, 1), 127);
     const float f = __int_as_float((up + 127) << 23), f16th = f * 0.0625f;
-    float back = p.scale * kLog2e * (p.softcap > 0.f ? 2.f / p.softcap : 1.f) * 16777216.f;   // 2^24
+    float back = p.scale * kLog2e * 16777216.f;   // 2^24
     back = up > 100 ? back * 7.888609052210118e-31f * __int_as_float((227 - up) << 23)   // 2^-100
                     : back * __int_as_float((127 - up) << 23);
     back = finite(back);
@@ -410,7 +410,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
   }
-  const float cap_log2 = p.softcap * kLog2e;
+  const float cap_log2 = p.softcap * kLog2e, two_by_cap = finite(2.f / p.softcap);
 
   for (int it = 0; it < n_mine; ++it) {
     copy_wait<NS - 1>();
@@ -498,7 +498,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
 #pragma unroll
       for (int i = 0; i < 4 * NT; ++i) {
         float2 &x = s[i / (2 * NT)][i / 2 % NT][i & 1];
-        x = make_float2(capped(x.x, cap_log2), capped(x.y, cap_log2));
+        x = capped_2(x, two_by_cap, cap_log2);
       }
     }
     if (tok < all_lo || tok + kTile > all_hi || hole) {

@@ -54,6 +54,13 @@ constexpr int kThreads = 512;
 constexpr int kMinPart = 4;     // key tiles of a part, at least
 constexpr int kSms = 152;
 
+// Capped scores.  cap - 2 cap / (1 + e^(2 x / cap)) is off by up to cap 2^-22: 2^-16 at
+// the most for a near cap, where the keys' rounding to float16 costs a score far more.
+// Past it capped_2 (kv4.cuh), off by 2^-20 of the score, however large the cap (a prompt
+// of 4096, 32/8 heads: 248 us against 194 us for a near cap, 131 without one).
+enum Cap { kNoCap, kNearCap, kFarCap };
+constexpr float kMostNear = 64.f;
+
 // Registers a thread: 512 x 128 at launch, then by warpgroup; the shares add up to
 // what the block was launched with.
 constexpr int kSoftmaxRegs = 176, kDecodeRegs = 112, kIssueRegs = 48;
@@ -467,7 +474,7 @@ __device__ __forceinline__ void issue_tile(const AttendParams &p, Bars &sm, uint
   drain_bar(&sm.drain[i], 0, globaltimer());
 }
 
-template <int D, bool kCap>
+template <int D, Cap kCap>
 __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParams p, int nsplit) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Bars sm;
@@ -524,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
     bool ok = true;
     if (i < tiles) {
       // The row of Q: scaled, in the codes' order, into the swizzled tile.
-      float cs = fabsf(p.scale) * kLog2e * (kCap ? 2.f / p.softcap : 1.f);
+      float cs = fabsf(p.scale) * kLog2e * (kCap == kNearCap ? 2.f / p.softcap : 1.f);
       if (p.scale == 0.f) cs = 1.f;
       if (n_sub > 0) {
         uint4 raw[D / 8];
@@ -568,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
       const int pos = job.len - job.nq + tok;
       const int end = p.causal ? min(job.len, pos + 1) : job.len;
       const int first = p.window ? max(0, pos - p.window + 1) : 0;
-      const float cap_log2 = p.softcap * kLog2e;
+      const float cap_log2 = p.softcap * kLog2e, two_by_cap = finite(2.f / p.softcap);
       const uint32_t s_col = tmem + lane_base + i * kKeys, o_at = tmem + lane_base + o_col + i * D;
       // Steps free_lo .. free_hi - 1 of the part hide nothing from this warp's rows.
       const int free_lo = (__reduce_max_sync(0xffffffffu, first) + kSub - 1) / kSub - 2 * job.t0;
@@ -582,15 +589,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
         const uint32_t at = s_col + h * kSub;
         float s[kSub];
         tmem_ld64(at, s);
-        // Capped: cap tanh(x / cap) = cap - 2 cap r, r = 1 / (1 + e^(2 x / cap)), so r stands
+        // A near cap: cap tanh(x / cap) = cap - 2 cap r, r = 1 / (1 + e^(2 x / cap)), so r stands
         // for the score, and the least r for the largest.
-        constexpr float kUnseen = kCap ? INFINITY : -INFINITY;
-        if constexpr (kCap) {
+        constexpr float kUnseen = kCap == kNearCap ? INFINITY : -INFINITY;
+        if constexpr (kCap != kNoCap) {
 #pragma unroll
           for (int c = 0; c < kSub; c += 2) {
-            const float2 x = mul_2(make_float2(s[c], s[c + 1]), make_float2(cs, cs));
-            const float2 e = add_2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
-            s[c] = rcp_approx(e.x), s[c + 1] = rcp_approx(e.y);
+            float2 x = mul_2(make_float2(s[c], s[c + 1]), make_float2(cs, cs));
+            if constexpr (kCap == kNearCap) {
+              x = add_2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
+              x = make_float2(rcp_approx(x.x), rcp_approx(x.y));
+            } else {
+              x = capped_2(x, two_by_cap, cap_log2);
+            }
+            s[c] = x.x, s[c + 1] = x.y;
           }
         }
         const uint32_t holes = *reinterpret_cast<const volatile uint16_t *>(&sm.holes[(t >> 1) & 3][2 * h]);
@@ -602,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
             s[c] = see ? s[c] : kUnseen;
           }
         }
-        auto most = [](float a, float b, float c) { return kCap ? min3(a, b, c) : max3(a, b, c); };
+        auto most = [](float a, float b, float c) { return kCap == kNearCap ? min3(a, b, c) : max3(a, b, c); };
         float t8[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) t8[e] = most(s[e], s[e + 8], s[e + 16]);
@@ -614,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const AttendParam
         for (int e = 0; e < 8; ++e) t8[e] = most(t8[e], t8[e], s[e + 56]);
         const float far = most(most(t8[0], t8[1], t8[2]), most(t8[3], t8[4], t8[5]), most(t8[6], t8[7], t8[7]));
         // A score is scale s + base.
-        const float scale = kCap ? -2.f * cap_log2 : cs, base = kCap ? cap_log2 : 0.f;
+        const float scale = kCap == kNearCap ? -2.f * cap_log2 : kCap == kFarCap ? 1.f : cs;
+        const float base = kCap == kNearCap ? cap_log2 : 0.f;
         const float top = fmaf(far, scale, base);
         const bool over = top > m + 8.f;
         if (__any_sync(0xffffffffu, over)) {
@@ -745,7 +758,7 @@ int split_of(const AttendParams &p) {
   return (int)std::max<long long>(1, std::min<long long>(kSms / (places(p) * p.b.Hkv), most));
 }
 
-template <int D, bool kCap>
+template <int D, Cap kCap>
 cudaError_t launch(const AttendParams &p, cudaStream_t st) {
   auto kernel = kv4_many_kernel<D, kCap>;
   static DeviceOnce once;
@@ -772,8 +785,14 @@ size_t many_rows(const AttendParams &p) {
 }
 
 cudaError_t launch_many(const AttendParams &p, int D, cudaStream_t st) {
-  if (D == 64) return p.softcap > 0.f ? launch<64, true>(p, st) : launch<64, false>(p, st);
-  return p.softcap > 0.f ? launch<128, true>(p, st) : launch<128, false>(p, st);
+  const Cap cap = p.softcap == 0.f ? kNoCap : p.softcap <= kMostNear ? kNearCap : kFarCap;
+  if (D == 64)
+    return cap == kNoCap     ? launch<64, kNoCap>(p, st)
+           : cap == kNearCap ? launch<64, kNearCap>(p, st)
+                             : launch<64, kFarCap>(p, st);
+  return cap == kNoCap     ? launch<128, kNoCap>(p, st)
+         : cap == kNearCap ? launch<128, kNearCap>(p, st)
+                           : launch<128, kFarCap>(p, st);
 }
 
 }  // namespace moe

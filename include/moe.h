@@ -601,6 +601,8 @@ int moe_kv4_append(const void *k, const void *v, void *cache, const int32_t *pag
  *            limits the waits of both)
  * Sums and softmax statistics are f32; keys, values and weights enter the
  * products as float16 (queries scaled by powers of two), out is rounded once.
+ * A cap of any size leaves a score right to 2^-20 of itself, or to 2^-16 where
+ * that is more and the cap at most 64.
  * Scores past 2^24 leave their differences, and so the weights, no precision in
  * f32, and results there may be infinite.
  * q, out and cache 16-byte aligned, strides a multiple of 8 and at most 2^31;

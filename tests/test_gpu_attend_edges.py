@@ -149,3 +149,19 @@ def test_maximum_that_moves(moe, rise, n, H, D):
         put_row(c, 0, 0, torch.full((1, D), 30 * D ** 0.5 / mean, device="cuda"), torch.zeros(1, D, device="cuda"))
     off, _ = batch([n], c)
     close(run(moe, q, c, [n], off), q, c, 0)
+
+
+@pytest.mark.parametrize("softcap,scale", [
+    (5.0, 0.1), (30.0, 0.1), (30.0, 2.0), (1e3, 0.1), (1e3, 20.0), (1e4, 0.1), (1e5, 0.1), (1e6, 0.1), (1e6, 8.0),
+    (1e9, 0.1), (1e20, 0.1), (1e30, 0.1), (1e38, 0.1), (3e38, 0.1), (1e-3, 0.1)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,H", [(1, 4), (3, 4), (9, 4)])
+def test_caps_of_any_size(moe, n, H, D, softcap, scale):
+    """A cap costs a score 2^-20 of itself, not of the cap: one far above all scores
+    changes nothing that counts."""
+    g = gen(34)
+    c = ref.Cache(g, [300], 1, D, 16)
+    q = (1.5 * randn(g, n, H, D)).bfloat16()
+    off, _ = batch([n], c)
+    kw = dict(softcap=softcap, scale=scale)
+    close(run(moe, q, c, [n], off, **kw), q, c, 0, **kw)
