@@ -5,7 +5,9 @@
 // Angles: f_i / (2 pi) is kept as a 64-bit fraction of a turn, so that pos times
 // it, modulo 2^64, is the angle modulo a turn without any reduction: off by
 // 2^-64 turns for each position and by the double's own 2^-53, where an f32
-// product at position 10^6 is off by a sixteenth of a radian.
+// product at position 10^6 is off by a sixteenth of a radian.  The two highest bits are
+// the quadrant; the sine and cosine of what is left come as a float and what the float
+// lacks, so that mscale times them is rounded once: in all half a unit and 2^-25.4.
 //
 // A block turns some heads of one token.  Its threads first ask for their
 // elements, then work out the token's sines and cosines once into shared
@@ -44,19 +46,53 @@ struct RopeParams {
   bool inverse;
 };
 
-// f radians as a fraction of a turn, in 2^-64 (two's complement, modulo 1).
+// f radians as a fraction of a turn, in 2^-64 (two's complement, modulo 1): right to that,
+// and to 2^-127 of f where f is many turns.
 __device__ __forceinline__ unsigned long long turn_fraction(double f) {
   const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
   const int e = (int)(bits >> 52) & 0x7FF;
   if (e == 0) return 0ull;   // zero, and subnormals: less than 2^-64 turns at any position
   // f = m 2^(e - 1086) with m's top bit set; times 2^66 / (2 pi) is m k 2^(e - 1086).
   const unsigned long long m = (1ull << 63) | (bits << 11);
-  const unsigned long long k = 0xA2F9836E4E44152Aull;   // round(2^66 / (2 pi))
-  const unsigned long long hi = __umul64hi(m, k);       // m k 2^-64
-  const int shift = e - 1024;                           // 2^64 turns = hi 2^(e - 1024)
-  const unsigned long long r =
-      shift <= -64 ? 0ull : shift < 0 ? hi >> -shift : shift < 64 ? hi << shift : 0ull;
+  // k: 2^66 / (2 pi) in 64 bits and 64 more.
+  const unsigned long long k = 0xA2F9836E4E441529ull, k_low = 0xFC2757D1F534DDC0ull;
+  const unsigned long long more = __umul64hi(m, k_low), lo = m * k + more;
+  const unsigned long long hi = __umul64hi(m, k) + (lo < more);   // hi, lo: m k 2^-64
+  const int shift = e - 1024;                                     // 2^64 turns = hi 2^(e - 1024)
+  const unsigned long long r = shift <= -64 ? 0ull
+                               : shift <= 0 ? hi >> -shift
+                               : shift < 64 ? hi << shift | lo >> (64 - shift)
+                               : shift < 128 ? lo << (shift - 64)
+                                             : 0ull;
   return bits >> 63 ? 0ull - r : r;
+}
+
+// m cos and m sin of turn 2^-64 turns.  The angle beyond the nearest quarter turn is
+// a + b, a float and what it lacks; Taylor's series to a^11 and a^10 (2e-9 at an eighth
+// of a turn), each result a float and what it lacks until m is in it.
+__device__ __forceinline__ float2 turn_cos_sin(unsigned long long turn, float m) {
+  const unsigned long long q = (turn + (1ull << 61)) >> 62;
+  const unsigned long long r = turn - (q << 62);   // -2^61 .. 2^61
+  const int top = (int)(r >> 32);
+  const float h = (float)top, l = (float)(top - (int)h) + (float)(uint32_t)r * 2.3283064365386963e-10f;
+  const float k = 1.46291807927e-9f, k_low = -4.07094027e-17f;   // 2 pi 2^-32
+  const float a = h * k, b = fmaf(h, k, -a) + fmaf(h, k_low, l * k);
+  const float z = a * a;
+  float p = fmaf(z, -2.5052108e-8f, 2.7557319e-6f);
+  p = fmaf(p, z, -1.9841270e-4f);
+  p = fmaf(p, z, 8.3333333e-3f);
+  p = fmaf(p, z, -0.16666667f);
+  const float t = fmaf(p * z, a, fmaf(-0.5f * z, b, b));
+  const float s = a + t, s_low = (a - s) + t;
+  const float w = fmaf(-0.5f, z, 1.f), left = fmaf(-0.5f, z, 1.f - w);
+  p = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+  p = fmaf(p, z, -1.3888889e-3f);
+  p = fmaf(p, z, 0.041666667f);
+  const float u = fmaf(z * z, p, left) - fmaf(0.5f, fmaf(a, a, -z), a * b);
+  const float c = w + u, c_low = (w - c) + u;
+  const float mc = fmaf(m, c, m * c_low), ms = fmaf(m, s, m * s_low);
+  const float x = q & 1 ? ms : mc, y = q & 1 ? mc : ms;
+  return make_float2((q + 1) & 2 ? -x : x, q & 2 ? -y : y);
 }
 
 template <int B>
@@ -133,12 +169,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       for (int i = threadIdx.x; i < p.R / 2; i += blockDim.x) {
         const double f = __ldg(p.freqs + i);
         const unsigned long long turn = turn_fraction(f) * (unsigned long long)pos;
-        // [-1/2, 1/2) turns = [-1, 1) half turns
-        float x = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, s, c;
-        if (!isfinite(f)) x = __int_as_float(0x7fffffff);
-        sincospif(x, &s, &c);
-        cs[i] = c * p.mscale;
-        sn[i] = (p.inverse ? -s : s) * p.mscale;
+        float2 t = turn_cos_sin(turn, p.mscale);
+        if (!isfinite(f)) t.x = t.y = __int_as_float(0x7fffffff);
+        cs[i] = t.x;
+        sn[i] = p.inverse ? -t.y : t.y;
       }
       __syncthreads();
     }

@@ -499,8 +499,10 @@ size_t moe_balance_workspace(int T, int num_experts, int n_seq);
  *   pos      [T] int32, any values
  *   freqs    [R / 2] doubles on the device: radians per position, e.g. from
  *            moe_rope_freqs
- * Angles are taken modulo a turn in 64-bit fixed point, so a position as far as
- * 2^31 turns as exactly as a near one; the rotation is f32, rounded once.
+ * Angles are taken modulo a turn in 64-bit fixed point (off by pos 2^-64 turns), so
+ * a position as far as 2^31 turns as exactly as a near one.  mscale times a sine or
+ * cosine is f32, off by half a unit and mscale 2^-25.4; so are the products and their
+ * sum, which is rounded to the output once.
  * n_heads * head_dim <= 2^20, head_dim <= 1024, R even and <= head_dim, T <=
  * 2^24, strides <= 2^32; elements aligned to their own size (16-byte aligned
  * rows are faster).  T == 0 checks what it can and launches nothing.
