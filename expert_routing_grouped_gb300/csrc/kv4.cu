@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv4_append_kernel(const App
   const long long w = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int t = (int)(w / p.warps_row);
   if (t >= p.b.T) return;
+  // Rows of no sequence are not read: they lie before the first offset or from the last on.
+  if (p.b.q_off && (t < __ldg(p.b.q_off) || t >= __ldg(p.b.q_off + p.b.n_seq))) return;
   const int groups = p.b.Hkv * NG;   // of K, then as many of V
   const int u0 = (int)(w - (long long)t * p.warps_row) * 4 * NU + (lane >> 3);
   Raw8<DT> raw[NU];
