@@ -362,12 +362,19 @@ def kv4_page_bytes(page_size, n_kv_heads, head_dim):
     return lib.moe_kv4_page_bytes(page_size, n_kv_heads, head_dim)
 
 
+def _n_seq(n_seq, q_off, T):
+    """The sequences of a batch: as given, or what q_off describes; one a row without it."""
+    if n_seq is not None:
+        return n_seq
+    return T if q_off is None else q_off.shape[0] - 1
+
+
 def kv4_append(k, v, cache, pages, kv_len, T, n_kv_heads, head_dim, page_size, n_pages, max_pages,
                q_off=None, n_seq=None, dtype=BF16, k_stride=0, v_stride=0, stream=None):
     """moe_kv4_append: the T rows of K and V into the 4-bit cache; without q_off
-    one row for each of T sequences."""
+    one row for each of T sequences, with it n_seq (default: all that q_off holds)."""
     return _check(lib.moe_kv4_append(_ptr(k), _ptr(v), _ptr(cache), _ptr(pages), _ptr(q_off),
-                                     _ptr(kv_len), T, T if n_seq is None else n_seq, n_kv_heads,
+                                     _ptr(kv_len), T, _n_seq(n_seq, q_off, T), n_kv_heads,
                                      head_dim, page_size, n_pages, max_pages, dtype, k_stride,
                                      v_stride, _stream(stream)), "moe_kv4_append")
 
@@ -382,12 +389,12 @@ def kv4_attention(q, cache, pages, kv_len, T, n_heads, n_kv_heads, head_dim, pag
                   softcap=0.0, window=0, causal=True, q_stride=0, out_stride=0, status=None,
                   stream=None):
     """moe_kv4_attention: attention of the batch's rows over the 4-bit cache.
-    scale defaults to head_dim ** -0.5; workspace is a tensor or array of at
+    scale defaults to head_dim ** -0.5, n_seq as kv4_append's; workspace is a tensor or array of at
     least kv4_workspace(...) bytes, or None where that is 0."""
     if scale is None:
         scale = head_dim ** -0.5
     return _check(lib.moe_kv4_attention(_ptr(q), _ptr(cache), _ptr(pages), _ptr(q_off),
-                                        _ptr(kv_len), T, T if n_seq is None else n_seq, max_q,
+                                        _ptr(kv_len), T, _n_seq(n_seq, q_off, T), max_q,
                                         n_heads, n_kv_heads, head_dim, page_size, n_pages,
                                         max_pages, scale, softcap, window, int(causal), _ptr(out),
                                         q_stride, out_stride, _ptr(workspace),
