@@ -9,10 +9,11 @@
 // place (sequence, length, page) is looked up while its values are on the way.
 //
 // The floor is the rows in and 9/32 of a bfloat16's bytes out.  8192 rows of 8 heads
-// of 128: 13.7 us (3.1 TB/s), bound by instructions.  Rows are read once, past what L2
-// holds (14.6 us with plain loads); two exact quotients share an instruction (15.3 us
-// one at a time); several groups a warp and packed
-// conversions (24.3 us without).  64 rows: 1.9 us.
+// of 128: 14.2 us (3.0 TB/s), bound by instructions (schedulers 69 % busy).  Rows are read
+// once, past what L2 holds (13.7 us against 14.6 with plain loads, before the look at the
+// offsets that keeps rows of no sequence unread, 0.4 us); two exact quotients share an
+// instruction (15.3 us one at a time); several groups a warp and packed conversions (24.3
+// us without).  64 rows: 1.9 us.
 #include <algorithm>
 #include <cmath>
 
@@ -35,12 +36,12 @@ struct AppendParams {
 // x held in float16 terms: +-60000 leaves room for lo + 15 step.
 __device__ __forceinline__ float kv_clamp(float x) { return fminf(fmaxf(x, -60000.f), 60000.f); }
 
-__device__ __forceinline__ float min3(float a, float b, float c) {
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
   float d;
   asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
@@ -143,12 +144,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv4_append_kernel(const App
       for (int i = 0; i < 8; ++i) x[i] = 0.f;
     }
     // A NaN stays in the smallest and the largest.
-    float lo = min3(min3(min3(x[0], x[1], x[2]), x[3], x[4]), min3(x[5], x[6], x[7]), x[5]);
-    float hi = max3(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]), x[5]);
+    float lo = min3_nan(min3_nan(min3_nan(x[0], x[1], x[2]), x[3], x[4]), min3_nan(x[5], x[6], x[7]), x[5]);
+    float hi = max3_nan(max3_nan(max3_nan(x[0], x[1], x[2]), x[3], x[4]), max3_nan(x[5], x[6], x[7]), x[5]);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
       const float a = __shfl_xor_sync(0xffffffffu, lo, o), c = __shfl_xor_sync(0xffffffffu, hi, o);
-      lo = min3(lo, a, a), hi = max3(hi, c, c);
+      lo = min3_nan(lo, a, a), hi = max3_nan(hi, c, c);
     }
     if (!mine) continue;
     bool nan = false;

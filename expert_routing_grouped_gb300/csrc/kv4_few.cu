@@ -4,7 +4,8 @@
 //   S^T[token][column] = K . q^T,  O^T[dim][column] = V^T . P^T
 //
 // on warp-level MMAs (m16n8k16, float16): 16 tokens, then 16 dimensions, are the
-// rows, columns the 8-wide side, so 8 query heads waste nothing.
+// rows, columns the 8-wide side: 8 query heads of a KV head waste nothing, one alone
+// uses an eighth.
 //
 //   Codes: a code in the lowest bits of a float16 is the subnormal number c 2^-24,
 //      four bits further up c 2^-20: one AND makes a pair of exact operands, with
@@ -32,17 +33,21 @@
 // The tiles of all sequences and KV heads lie in one line that is cut into equal
 // spans, one for each block, whatever the lengths; a second kernel joins what was cut.
 //
-// The floor is the cache, 9/16 bytes an element; what bounds it is instructions: 809
-// for 32 tokens of 16 columns, issued at 2.0 a clock and SM.  One token of 96 query
-// and 8 KV heads over 131072 tokens: 47.0 us (3.2 TB/s); 64 tokens of 32 and 8 heads
-// over up to 8192 each: 49.5 us (3.8 TB/s); one over 4096: 10.0 us, mostly launches,
-// the plan and the joining.  An earlier form (52.5 us over 131072) took 34.6 us with
-// the copies alone.  Tried: codes in 16 mantissa bits and V's scales on the values
-// (57.9 us against 52.8), the codes as the A side of tcgen05 MMAs (69 against 53),
-// four blocks an SM with shorter rings for 16 columns (67.2 against 52.7).
+// The floor is the cache, 9/16 bytes an element; what bounds it is latency: 878
+// instructions for 32 tokens of 16 columns, issued at 2.1 of the 4 a clock and SM by
+// three warps a scheduler (four with 8 columns), too few to cover one another's chains.
+// One token of 96 query and 8 KV heads over 131072 tokens: 50.2 us (3.0 TB/s); 64 tokens
+// of 32 and 8 heads over up to 8192 each: 52.6 us (3.6 TB/s); one over 4096: 10.8 us,
+// mostly launches, the plan and the joining.  One power of two for both groups and all
+// tokens took 46.9, 49.4 and 10.2 us and lost small values beside large ones.  An
+// earlier form (52.5 us over 131072) took 34.6 us with the copies alone.  Tried: codes
+// in 16 mantissa bits and V's scales on the values (57.9 us against 52.8), the codes as
+// the A side of tcgen05 MMAs (69 against 53), four blocks an SM with shorter rings for
+// 16 columns (67.2 against 52.7).
 #include <algorithm>
 
 #include "kv4.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -69,9 +74,6 @@ constexpr int kRing = D == 64 ? 6 : 3;      // slots of a warp
 template <int D>
 constexpr int kSmem = kWarps * kRing<D> * Slot<D>::kBytes;
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -248,7 +250,7 @@ __device__ __forceinline__ void do_segment(const AttendParams &p, const Segment 
   // ---- the ring: this warp's tiles are first + warp, + W, ...
   const int n_mine = part.n > warp ? (part.n - warp + W - 1) / W : 0;
   uint8_t *ring = smem + warp * (NS * SB);
-  const uint32_t ring_s = smem_addr(ring);
+  const uint32_t ring_s = smem_u32(ring);
   const int32_t *pages = p.b.pages + (size_t)part.s * p.b.max_pages;
   const uint8_t *head = p.cache + (size_t)part.hk * KvBlock<D>::bytes(lp);
   const size_t page_bytes = KvBlock<D>::bytes(lp) * p.b.Hkv;

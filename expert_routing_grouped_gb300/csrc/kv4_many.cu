@@ -15,17 +15,19 @@
 //   warps 12, 13     issue the MMAs of tile 0 and 1: scores run two steps ahead of
 //                    the softmax, in two buffers of tensor memory
 //
-// 8192 tokens of 32 query and 8 KV heads, causal: 427 us, 1287 TFLOP/s of what
+// 8192 tokens of 32 query and 8 KV heads, causal: 429 us, 1282 TFLOP/s of what
 // counts (0.67 of a large matrix product's rate); the tensor pipe is busy 55 % of the
-// clocks, the schedulers 54 %.  Clocks read inside an earlier form (441 us) showed the
-// codes' role at work for 3760 of the 3836 that a tile of 128 keys takes: it sets the
-// pace, and shares its schedulers with the softmax.  So neither more warps for it
-// (481 us against 450) nor more for the softmax (516 against 441) helped, nor codes
-// shared by two blocks of a cluster (824 against 441: remote stores), nor two tiles
-// of codes in flight in registers (625 against 450: spills), nor both softmax groups
-// on one tile of rows where there is only one (57.9 against 56.5 for 4 rows of 96/8
-// heads in each of 4 sequences of 16384), nor blocks that work through several tiles
-// of rows, the next one's decoding beside the last one's end (447 against 426).
+// clocks, the schedulers 54 %.  No single part bounds it.  In an earlier form (441 us)
+// the codes' role was at work for 3760 of the 3836 clocks of a tile of 128 keys, beside
+// the softmax on the same schedulers and with shared memory's pipe 75 to 90 % busy; it took
+// 404 us without the exponentials, 419 without the masks, 340 without the softmax's
+// arithmetic and the decoded tiles' stores.  Slower: more warps for the codes (481 us
+// against 450) or for the softmax (516 against 441), codes shared by two blocks of a
+// cluster (824 against 441: remote stores), two tiles of codes in flight in registers
+// (625 against 450: spills), both softmax groups on one tile of rows where there is only
+// one (57.9 against 56.5 for 4 rows of 96/8 heads in each of 4 sequences of 16384),
+// blocks that work through several tiles of rows, the next one's decoding beside the last
+// one's end (447 against 426).
 //
 // The running maximum moves only when a score passes it by 8: weights up to 2^8 are
 // float16 as well as those up to 1, and the outputs in tensor memory need scaling
@@ -36,7 +38,9 @@
 // nibbles i and i + 4 decode together), in Q as in K; the output puts V's back.
 //
 // Where a call has fewer blocks than SMs the keys are cut into parts, whose results
-// a second kernel joins.  (One line of all key tiles cut into equal spans, as for few
+// a second kernel joins: as many as fit the SMs, counting a place too many for each
+// sequence, also for those that kv4_few.cu takes, so batches of many short sequences
+// beside a long one are not cut.  (One line of all key tiles cut into equal spans, as for few
 // rows, was slower: 512 rows of 32/8 heads over 16384 keys 163 us against 125.)
 #include <algorithm>
 
@@ -113,7 +117,9 @@ __device__ __forceinline__ bool wait_one(uint64_t *bar, uint32_t parity, int *ab
                                          unsigned long long limit_ns) {
   return mbar_test_wait(bar, parity) || wait_loop(bar, parity, abort, status, limit_ns);
 }
-// A whole warp's: the lanes vote, for what follows is warp-collective.
+// A whole warp's: the lanes vote, for what follows is warp-collective.  All these are for
+// MMAs that an issuer has committed or is about to: the issuers' limit is the caller's,
+// these have the full one and leave when an issuer has given up.
 __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, int *abort, int32_t *status) {
   const bool ok = mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort, status, kWaitNs);
   return __all_sync(0xffffffffu, ok);
@@ -286,8 +292,8 @@ __device__ __forceinline__ Job find_job(const AttendParams &p, int u, int hk, in
 }
 
 // The codes' role, a warpgroup (wd the warp in it): the key tiles, decoded into their
-// stages.  It sets the pace of a prompt: what it need not wait for is asked for a tile
-// ahead.
+// stages.  It is busy nearly all of a prompt: what it need not wait for is asked for a
+// tile ahead.
 template <int D>
 __device__ __forceinline__ void decode_tiles(const AttendParams &p, const Job &job, Bars &sm, uint8_t *k_s,
                                              uint8_t *v_s, int wd) {

@@ -15,9 +15,9 @@
 // of the block's heads.
 //
 // The floor is one read and one write.  4096 tokens of 40 heads of 128, bfloat16:
-// 15.8 us (5.3 TB/s), in place 15.3; 17.9 and 18.0 without streaming loads, which leave
+// 15.7 us (5.3 TB/s), in place 15.3; 17.9 and 18.0 without streaming loads, which leave
 // L2 to what is written.  Half the warps' slots are taken; capping registers for more
-// blocks an SM (18.4 us and up), 128 threads (16.2) and, before the streaming loads,
+// blocks an SM (18.4 us and up), 128 threads (16.2 against 15.8) and, before the streaming loads,
 // one or four units a thread (18.8, 23.5 against 17.9) were slower.  104 heads of one
 // token: 2.1 us, a launch and one trip to memory.
 #include <algorithm>

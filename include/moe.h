@@ -405,14 +405,16 @@ int moe_linear_status(int32_t *status);
 /*
  * The time limit, in microseconds, of the waits between the pipelined roles of
  * a product, and of attention with more than 16 columns, for the calls that the
- * calling host thread makes from now on (default 2000000).  A wait that is not
- * complete when its limit has passed gives up: the kernel stops its roles, waits
- * (with the full 2 s limit) for its own copies and MMAs in flight, frees its
- * tensor memory and returns, so the next call runs normally; the status word
- * holds 2, and the call returned MOE_OK (the launch succeeded).  0 makes every wait that is not
- * complete when first tested give up at once, and the first operands come late
- * enough for one to do so: a way to exercise that recovery path without a fault
- * or a hang, as MOE_OPT_WAIT_LIMIT_US is for the layer.  Products of at most
+ * calling host thread makes from now on (default 2000000).  It is the limit of the
+ * roles that issue copies and MMAs, which wait for all the others; the others wait
+ * for MMAs, with the full 2 s, and stop when an issuing role has given up.  A wait
+ * that is not complete when its limit has passed gives up: the kernel stops its
+ * roles, waits (with the full 2 s limit) for its own copies and MMAs in flight,
+ * frees its tensor memory and returns, so the next call runs normally; the status
+ * word holds 2, and the call returned MOE_OK (the launch succeeded).  0 makes every
+ * wait that is not complete when first tested give up at once, and the first
+ * operands come late enough for one to do so: a way to exercise that recovery path
+ * without a fault or a hang, as MOE_OPT_WAIT_LIMIT_US is for the layer.  Products of at most
  * 16 tokens have no such waits.  A captured call keeps the limit that it was
  * captured with.  Returns MOE_OK, or MOE_ERR_ARG for a negative limit.
  */
@@ -518,7 +520,10 @@ int moe_rope(const void *x, const int32_t *pos, const double *freqs, int T, int 
  * `context`.  By parts: a pair that makes r = context freqs[i] / (2 pi) turns
  * keeps its frequency for r >= beta_fast, is divided by factor for r <= beta_slow
  * and mixed in between by (r - beta_slow) / (beta_fast - beta_slow); *mscale is
- * then 0.1 ln(factor) + 1 (1 for the other scalings; mscale may be NULL).
+ * then 0.1 ln(factor) + 1 (1 for the other scalings; mscale may be NULL).  This is the
+ * paper's ramp, linear in the turns r.  Models trained with a ramp that is linear in
+ * the pair's index between two rounded bounds have other frequencies in between: give
+ * moe_rope those.
  * context, beta_fast and beta_slow are read by parts only.  Returns MOE_OK or
  * MOE_ERR_ARG (rot_dim not even or outside 2 .. 1024, theta or factor not finite
  * or below 1, by base with rot_dim 2, by parts with context < 1 or not
@@ -593,7 +598,8 @@ int moe_kv4_append(const void *k, const void *v, void *cache, const int32_t *pag
  *            n_heads head_dim)
  *   max_q    the most rows that any one sequence has, where the caller knows it;
  *            0: not known.  Rows of a sequence past the first max_q are left as
- *            they were.
+ *            they were.  With q_off and no max_q a step of single tokens also
+ *            launches the kernel for many rows, which finds none.
  *   workspace  at least moe_kv4_workspace(...) bytes, 16-byte aligned, not shared
  *            with a call that may overlap this one; nothing in it needs clearing
  *   status   int32 on the device: set to 2 when a bounded wait of the kernel
@@ -601,8 +607,11 @@ int moe_kv4_append(const void *k, const void *v, void *cache, const int32_t *pag
  *            such a call sets the device's own word (moe_linear_status, which
  *            reports products and attention alike, as moe_linear_wait_limit
  *            limits the waits of both)
- * Sums and softmax statistics are f32; keys, values and weights enter the
- * products as float16 (queries scaled by powers of two), out is rounded once.
+ * Sums and softmax statistics are f32, out is rounded once.  Queries enter the
+ * products as float16, scaled by powers of two.  Of sequences with at most 16 columns
+ * (rows times query heads of a KV head) keys and codes are exact, and weight times
+ * step of 64 values is rounded to float16, scaled by a power of two of each column;
+ * of larger ones keys, values and weights are float16.
  * A cap of any size leaves a score right to 2^-20 of itself, or to 2^-16 where
  * that is more and the cap at most 64.
  * Scores past 2^24 leave their differences, and so the weights, no precision in
