@@ -562,7 +562,8 @@ int moe_rope_freqs(int rot_dim, double theta, int scaling, double factor, double
  * Values are taken as they are at run time (a graph's replays may change them).
  * Offsets and lengths out of range are clamped (offsets to T and to their
  * predecessor, lengths to max_pages page_size): memory outside the operands is
- * never touched.
+ * never touched.  Of offsets out of order no more is promised: which rows they name
+ * is open.
  */
 size_t moe_kv4_page_bytes(int page_size, int n_kv_heads, int head_dim);
 
